@@ -74,8 +74,11 @@ enum pd_device_flag {
   PD_DEV_BAD_SLOT = 4,    /* slot_mapping[t] >= num_blocks*block_size: token skipped */
   PD_DEV_TIMEOUT = 8,     /* a bounded wait inside a kernel gave up: that output is invalid */
   PD_DEV_BAD_PLAN = 16,   /* a balanced-plan entry was out of range: that piece skipped */
-  PD_DEV_BAD_SMEM = 32    /* a kernel found its shared memory off the 1024-byte boundary
+  PD_DEV_BAD_SMEM = 32,   /* a kernel found its shared memory off the 1024-byte boundary
                              its swizzled tiles need: it wrote nothing */
+  PD_DEV_BAD_POSITION = 64, /* a position outside the rotation table: clamped into it */
+  PD_DEV_BAD_TREE = 128   /* an accepted path that is not strictly increasing node indices of
+                             its sequence's tree: nothing of that sequence was moved */
 };
 
 /* Human-readable name of a pd_status value (static string, never NULL). */
@@ -433,6 +436,121 @@ int pd_prefill(const void* q, int64_t q_stride, const int32_t* cu_q, const void*
                int32_t sliding_window, int32_t kv_dtype, float k_scale, float v_scale,
                void* stream);
 
+/* ---- Draft and verify: several drafted tokens per sequence ----
+ * One step of decoding with drafted tokens: pd_qk_norm_rope_cache takes the
+ * drafted tokens' fused QKV rows (norm, rotation, cache write), pd_decode_tree
+ * attends every node of each sequence's token tree over the cache, and after
+ * the model has chosen a path pd_compact_tree makes its rows consecutive. */
+
+/* The rotation table pd_qk_norm_rope_cache reads: cos_sin, device fp32
+ * [max_position][rot_dim], row p = the rot_dim / 2 cosines and then the
+ * rot_dim / 2 sines of the angles p * base^(-2 i / rot_dim), computed in 64
+ * bits and rounded once. rot_dim a multiple of 16 in [16, 512]; base finite
+ * and > 1; max_position >= 0. A one-off call. */
+int pd_rope_table(float* cos_sin, int32_t max_position, int32_t rot_dim, double base,
+                  void* stream);
+
+/* RMS norm of each q and k head, rotation by the token's position and the
+ * cache write of K and V, in one pass over fused rows.
+ *   qkv         device bf16; token t's row at element t * qkv_stride (0 =
+ *               packed): num_q_heads q heads, num_kv_heads k heads, then
+ *               num_kv_heads v heads of head_dim values.
+ *   q_weight,   device bf16 [head_dim] each, or both NULL: no norm. A head x
+ *   k_weight    becomes x_i / sqrt(mean(x^2) + eps) * (weight_offset + w_i)
+ *               (weight_offset 1 for models that keep weights around zero).
+ *   cos_sin     device fp32 [max_position][rot_dim] as pd_rope_table writes.
+ *               A pair (a, b) of the head's first rot_dim elements becomes
+ *               (a cos - b sin, b cos + a sin): elements (i, i + rot_dim / 2),
+ *               or (2 i, 2 i + 1) when interleaved != 0. The rest pass.
+ *   positions   device int32 [num_tokens]; one outside [0, max_position) is
+ *               clamped and flagged PD_DEV_BAD_POSITION.
+ *   slot_mapping, caches, kv_dtype, scales: as pd_reshape_and_cache; a token
+ *               with a negative slot still gets its q row.
+ *   q_out       device bf16, token t's q heads at element t * q_out_stride
+ *               (0 = packed). May be qkv itself (with its stride): in place.
+ * All arithmetic in fp32 in this order, each operation rounded once: the sum of
+ * squares as a balanced binary tree over neighbouring elements, times
+ * 1 / head_dim, plus eps, square root, reciprocal, x times it, times (offset +
+ * w); then the two products of each rotated element and their sum; one
+ * rounding to bf16. K is quantised from that bf16 value as
+ * pd_reshape_and_cache does, so cache bytes are reproducible bit for bit.
+ * head_dim in {64, 128, 256, 512}; block_size in {16, 32}; rot_dim a multiple
+ * of 16 in [16, head_dim]; strides multiples of 8; eps > 0 (read with weights
+ * only). */
+int pd_qk_norm_rope_cache(const void* qkv, int64_t qkv_stride, const void* q_weight,
+                          const void* k_weight, float eps, float weight_offset,
+                          const float* cos_sin, int32_t max_position, int32_t rot_dim,
+                          int32_t interleaved, const int32_t* positions,
+                          const int32_t* slot_mapping, void* q_out, int64_t q_out_stride,
+                          void* k_cache, void* v_cache, int32_t num_tokens, int32_t num_q_heads,
+                          int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                          int64_t num_blocks, int32_t kv_dtype, float k_scale, float v_scale,
+                          void* stream);
+
+/* Most nodes of one sequence's tree in pd_decode_tree, and most accepted
+ * nodes of one sequence in pd_compact_tree. */
+#define PD_MAX_TREE_NODES 64
+
+/* Workspace bytes of pd_decode_tree on a device of num_sms SMs; depends on no
+ * length. 0 for shapes the call refuses. Host only, no CUDA call. */
+size_t pd_decode_tree_workspace_bytes(int32_t max_q_len, int32_t num_q_heads,
+                                      int32_t num_kv_heads, int32_t head_dim, int32_t kv_dtype,
+                                      int32_t num_sms);
+
+/* Attention of each sequence's draft tree over the paged cache.
+ *   q, out      device bf16, total_q rows of num_q_heads x head_dim values at
+ *               element i * q_stride / i * out_stride (0 = packed).
+ *   cu_q        device int32 [num_seqs + 1]: sequence b's nodes are rows
+ *               [cu_q[b], cu_q[b+1]), n_b of them, n_b <= max_q_len <= 64.
+ *   seq_lens    device int32: L_b cached rows, the nodes' K and V already
+ *               written as the last n_b of them, in node order; prefix
+ *               p_b = L_b - n_b rows belong to the sequence proper.
+ *   tree_mask   device uint64 [total_q]: bit j of node i's word = node i sees
+ *               node j of its sequence (itself only if its own bit is set;
+ *               bits >= n_b are ignored). NULL: every node sees itself and
+ *               the nodes before it (a chain; one node is plain decode).
+ *               A node's depth is the number of nodes it sees minus one (0
+ *               if none), its position p_b + depth.
+ *   sliding_window, num_sinks   W > 0 hides the rows whose position is W or
+ *               more before the node's, except positions below num_sinks,
+ *               the first tokens that stay visible. W = 0: everything stays.
+ * out = softmax(scale q k) v over what the node sees, fp32 softmax; a node
+ * that sees nothing gets a zero row. Cache rows that no node of the sequence
+ * sees may hold anything; rows that one does see are taken to be finite.
+ * A sequence whose counts do not fit (n_b > max_q_len, L_b < n_b, L_b beyond
+ * the block table, rows beyond total_q) raises PD_DEV_BAD_SEQ_LEN and its
+ * rows are not written. workspace: pd_decode_tree_workspace_bytes, not shared
+ * by calls that overlap. head_dim in {64, 128, 256, 512}; block_size 16 or
+ * 32; num_q_heads / num_kv_heads <= 16. */
+int pd_decode_tree(const void* q, int64_t q_stride, const int32_t* cu_q,
+                   const uint64_t* tree_mask, const void* k_cache, const void* v_cache,
+                   const int32_t* block_tables, const int32_t* seq_lens, void* out,
+                   int64_t out_stride, int32_t num_seqs, int32_t total_q, int32_t max_q_len,
+                   int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                   int32_t block_size, int32_t max_blocks_per_seq, int64_t num_blocks,
+                   float scale, int32_t sliding_window, int32_t num_sinks, int32_t kv_dtype,
+                   float k_scale, float v_scale, void* workspace, size_t workspace_bytes,
+                   void* stream);
+
+/* Make each sequence's accepted nodes its newest tokens: in every layer's K
+ * and V caches row p_b + i <- row p_b + accepted[b][i] for i <
+ * num_accepted[b], and new_seq_lens[b] = p_b + num_accepted[b].
+ *   k_caches,   device, num_layers caches of pd_cache_bytes(...) bytes, layer
+ *   v_caches    l's at byte l * layer_bytes (a multiple of 16; 0 = packed).
+ *   accepted    device int32 [num_seqs][max_accepted], max_accepted <= 64: the
+ *               accepted path's node indices, strictly increasing (root
+ *               first); entries past num_accepted[b] are not read. A path
+ *               that is not so raises PD_DEV_BAD_TREE and moves nothing
+ *               (new_seq_lens[b] = p_b).
+ *   seq_lens, cu_q, block_tables   as pd_decode_tree; new_seq_lens is another
+ *               array. */
+int pd_compact_tree(void* k_caches, void* v_caches, int64_t layer_bytes, int32_t num_layers,
+                    const int32_t* block_tables, const int32_t* seq_lens, const int32_t* cu_q,
+                    const int32_t* accepted, const int32_t* num_accepted, int32_t max_accepted,
+                    int32_t* new_seq_lens, int32_t num_seqs, int32_t num_kv_heads,
+                    int32_t head_dim, int32_t block_size, int32_t max_blocks_per_seq,
+                    int64_t num_blocks, int32_t kv_dtype, void* stream);
+
 /* ---- Cross-check kernels ----
  * Independent second implementations of two steps, kept to test the fast
  * kernels against: same arguments, same results up to fp32 summation order.
@@ -460,6 +578,19 @@ int pd_prefill_crosscheck(const void* q, int64_t q_stride, const int32_t* cu_q,
                           int32_t max_blocks_per_seq, int64_t num_blocks, float scale,
                           int32_t causal, int32_t sliding_window, int32_t kv_dtype,
                           float k_scale, float v_scale, void* stream);
+
+/* pd_decode_tree on CUDA cores, one CTA per (node, q head): same arguments,
+ * the workspace unused. */
+int pd_decode_tree_crosscheck(const void* q, int64_t q_stride, const int32_t* cu_q,
+                              const uint64_t* tree_mask, const void* k_cache,
+                              const void* v_cache, const int32_t* block_tables,
+                              const int32_t* seq_lens, void* out, int64_t out_stride,
+                              int32_t num_seqs, int32_t total_q, int32_t max_q_len,
+                              int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                              int32_t block_size, int32_t max_blocks_per_seq,
+                              int64_t num_blocks, float scale, int32_t sliding_window,
+                              int32_t num_sinks, int32_t kv_dtype, float k_scale, float v_scale,
+                              void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---- Test hooks ----
  * For the library's own tests; a serving process has no reason to call them. */

@@ -10,6 +10,7 @@ raises ImportError when libpd.so has not been built
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -86,6 +87,23 @@ _lib.pd_decode_balanced.restype = ctypes.c_int
 _lib.pd_decode_balanced_strided.argtypes = ([_P, _i64] + _lib.pd_decode_balanced.argtypes[1:7] +
                                             [_i64] + _lib.pd_decode_balanced.argtypes[7:])
 _lib.pd_decode_balanced_strided.restype = ctypes.c_int
+_lib.pd_rope_table.argtypes = [_P, _i32, _i32, ctypes.c_double, _P]
+_lib.pd_rope_table.restype = ctypes.c_int
+_lib.pd_qk_norm_rope_cache.argtypes = [_P, _i64, _P, _P, _f32, _f32, _P, _i32, _i32, _i32, _P, _P,
+                                       _P, _i64, _P, _P, _i32, _i32, _i32, _i32, _i32, _i64, _i32,
+                                       _f32, _f32, _P]
+_lib.pd_qk_norm_rope_cache.restype = ctypes.c_int
+_lib.pd_decode_tree_workspace_bytes.argtypes = [_i32] * 6
+_lib.pd_decode_tree_workspace_bytes.restype = _sz
+_lib.pd_decode_tree.argtypes = [_P, _i64, _P, _P, _P, _P, _P, _P, _P, _i64, _i32, _i32, _i32, _i32,
+                                _i32, _i32, _i32, _i32, _i64, _f32, _i32, _i32, _i32, _f32, _f32,
+                                _P, _sz, _P]
+_lib.pd_decode_tree.restype = ctypes.c_int
+_lib.pd_decode_tree_crosscheck.argtypes = _lib.pd_decode_tree.argtypes
+_lib.pd_decode_tree_crosscheck.restype = ctypes.c_int
+_lib.pd_compact_tree.argtypes = [_P, _P, _i64, _i32, _P, _P, _P, _P, _P, _i32, _P, _i32, _i32, _i32,
+                                 _i32, _i32, _i64, _i32, _P]
+_lib.pd_compact_tree.restype = ctypes.c_int
 for _fn in ("pd_decode_balanced_partial", "pd_decode_balanced_combine"):
     getattr(_lib, _fn).argtypes = _lib.pd_decode_balanced.argtypes
     getattr(_lib, _fn).restype = ctypes.c_int
@@ -589,3 +607,200 @@ def pd_prefill_strided(q_rows, cu_q, k_cache, v_cache, block_tables, seq_lens, o
         float(k_scale), float(v_scale), _stream(stream))
     _check(fn, rc)
     return out_rows
+
+
+# ---- draft and verify -------------------------------------------------------
+PD_MAX_TREE_NODES = 64
+
+
+def pd_rope_table(cos_sin, base=10000.0, stream=None):
+    """Fill the rotation table cos_sin (float32 [max_position, rot_dim]): row p
+    holds the cosines and then the sines of p * base^(-2 i / rot_dim)."""
+    if cos_sin.dim() != 2:
+        raise ValueError("cos_sin must be float32 [max_position, rot_dim]")
+    rc = _lib.pd_rope_table(_dev(cos_sin, "cos_sin", torch.float32), cos_sin.shape[0],
+                            cos_sin.shape[1], float(base), _stream(stream))
+    _check("pd_rope_table", rc)
+    return cos_sin
+
+
+def _norm_rope(qkv, q_out, q_out_stride, hq, d, k_cache, v_cache, positions, slot_mapping, cos_sin,
+               num_kv_heads, block_size, num_blocks, q_weight, k_weight, eps, weight_offset,
+               interleaved, kv_dtype, k_scale, v_scale, stream):
+    if qkv.dim() != 2 or qkv.shape[1] < (hq + 2 * num_kv_heads) * d:
+        raise ValueError("qkv must be bf16 [num_tokens, row], a row its q, k and v heads")
+    T, row = qkv.shape
+    if positions.shape != (T,) or slot_mapping.shape != (T,):
+        raise ValueError("positions and slot_mapping must be [num_tokens]")
+    if cos_sin.dim() != 2:
+        raise ValueError("cos_sin must be float32 [max_position, rot_dim]")
+    dev = qkv.device
+    qw = kw = None
+    if q_weight is not None or k_weight is not None:
+        if q_weight is None or k_weight is None:
+            raise ValueError("q_weight and k_weight go together")
+        if q_weight.shape != (d,) or k_weight.shape != (d,):
+            raise ValueError("q_weight and k_weight must be [head_dim]")
+        qw = _dev(q_weight, "q_weight", torch.bfloat16, dev)
+        kw = _dev(k_weight, "k_weight", torch.bfloat16, dev)
+    rc = _lib.pd_qk_norm_rope_cache(
+        _dev(qkv, "qkv", torch.bfloat16, dev), row, qw, kw, eps, weight_offset,
+        _dev(cos_sin, "cos_sin", torch.float32, dev), cos_sin.shape[0], cos_sin.shape[1],
+        int(bool(interleaved)), _dev(positions, "positions", torch.int32, dev),
+        _dev(slot_mapping, "slot_mapping", torch.int32, dev),
+        _dev(q_out, "q_out", torch.bfloat16, dev), q_out_stride,
+        _dev(k_cache, "k_cache", None, dev), _dev(v_cache, "v_cache", None, dev), T, hq,
+        num_kv_heads, d, block_size, num_blocks, _dtype_code(kv_dtype), k_scale, v_scale,
+        _stream(stream))
+    _check("pd_qk_norm_rope_cache", rc)
+
+
+def pd_qk_norm_rope_cache(qkv, q_out, k_cache, v_cache, positions, slot_mapping, cos_sin, *,
+                          num_kv_heads, block_size, num_blocks, q_weight=None, k_weight=None,
+                          eps=1e-6, weight_offset=0.0, interleaved=False, kv_dtype=PD_KV_BF16,
+                          k_scale=1.0, v_scale=1.0, stream=None):
+    """Norm and rotate the q and k heads of fused rows, write K and V to the cache.
+
+    qkv: contiguous bf16 [T, row], a row = q heads, k heads, v heads (and
+    possibly more). q_out: contiguous bf16 [T, Hq, D]. positions, slot_mapping:
+    int32 [T]. cos_sin: float32 [max_position, rot_dim] from pd_rope_table.
+    Without weights only the rotation is applied."""
+    if q_out.dim() != 3 or q_out.shape[0] != qkv.shape[0]:
+        raise ValueError("q_out must be bf16 [num_tokens, num_q_heads, head_dim]")
+    _norm_rope(qkv, q_out, 0, q_out.shape[1], q_out.shape[2], k_cache, v_cache, positions,
+               slot_mapping, cos_sin, num_kv_heads, block_size, num_blocks, q_weight, k_weight,
+               eps, weight_offset, interleaved, kv_dtype, k_scale, v_scale, stream)
+    return q_out
+
+
+def pd_qk_norm_rope_cache_(qkv, k_cache, v_cache, positions, slot_mapping, cos_sin, *, num_q_heads,
+                           num_kv_heads, head_dim, block_size, num_blocks, q_weight=None,
+                           k_weight=None, eps=1e-6, weight_offset=0.0, interleaved=False,
+                           kv_dtype=PD_KV_BF16, k_scale=1.0, v_scale=1.0, stream=None):
+    """pd_qk_norm_rope_cache in place: the q heads of the fused rows are
+    replaced by their rotated form, ready for pd_decode_tree_strided."""
+    _norm_rope(qkv, qkv, qkv.shape[-1], num_q_heads, head_dim, k_cache, v_cache, positions,
+               slot_mapping, cos_sin, num_kv_heads, block_size, num_blocks, q_weight, k_weight,
+               eps, weight_offset, interleaved, kv_dtype, k_scale, v_scale, stream)
+    return qkv
+
+
+@functools.lru_cache(maxsize=None)
+def _num_sms(device_index) -> int:
+    return torch.cuda.get_device_properties(device_index).multi_processor_count
+
+
+def pd_decode_tree_workspace_bytes(max_q_len, num_q_heads, num_kv_heads, head_dim, kv_dtype,
+                                   num_sms) -> int:
+    """Workspace bytes of pd_decode_tree; they depend on no length."""
+    n = int(_lib.pd_decode_tree_workspace_bytes(max_q_len, num_q_heads, num_kv_heads, head_dim,
+                                                _dtype_code(kv_dtype), num_sms))
+    if n == 0:
+        raise ValueError("unsupported tree shape")
+    return n
+
+
+def _decode_tree(fn, q, q_stride, cu_q, tree_mask, k_cache, v_cache, block_tables, seq_lens, out,
+                 out_stride, T, hq, d, max_q_len, num_kv_heads, block_size, num_blocks, scale,
+                 sliding_window, num_sinks, kv_dtype, k_scale, v_scale, workspace, stream):
+    dev = q.device
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq]")
+    B, mbs = block_tables.shape
+    if seq_lens.shape != (B,) or cu_q.shape != (B + 1,):
+        raise ValueError("seq_lens must be [num_seqs] and cu_q [num_seqs + 1]")
+    mask = None
+    if tree_mask is not None:
+        if tree_mask.shape != (T,):
+            raise ValueError("tree_mask must be int64 [total_q]")
+        mask = _dev(tree_mask, "tree_mask", torch.int64, dev)
+    code = _dtype_code(kv_dtype)
+    if workspace is None:
+        # 0 for refused shapes: the call below says why
+        n = int(_lib.pd_decode_tree_workspace_bytes(max_q_len, hq, num_kv_heads, d, code,
+                                                    _num_sms(dev.index)))
+        workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
+    rc = getattr(_lib, fn)(
+        _dev(q, "q", torch.bfloat16, dev), q_stride, _dev(cu_q, "cu_q", torch.int32, dev), mask,
+        _dev(k_cache, "k_cache", None, dev), _dev(v_cache, "v_cache", None, dev),
+        _dev(block_tables, "block_tables", torch.int32, dev),
+        _dev(seq_lens, "seq_lens", torch.int32, dev), _dev(out, "out", torch.bfloat16, dev),
+        out_stride, B, T, max_q_len, hq, num_kv_heads, d, block_size, mbs, num_blocks, scale,
+        sliding_window, num_sinks, code, k_scale, v_scale,
+        _dev(workspace, "workspace", None, dev), workspace.numel() * workspace.element_size(),
+        _stream(stream))
+    _check(fn, rc)
+
+
+def pd_decode_tree(q, cu_q, k_cache, v_cache, block_tables, seq_lens, out, *, max_q_len,
+                   num_kv_heads, block_size, num_blocks, scale, tree_mask=None, sliding_window=0,
+                   num_sinks=0, kv_dtype=PD_KV_BF16, k_scale=1.0, v_scale=1.0, workspace=None,
+                   stream=None, crosscheck=False):
+    """Attention of each sequence's draft tree over the cache, into out.
+
+    q, out: contiguous bf16 [total_q, Hq, D]; cu_q: int32 [B + 1] node offsets;
+    seq_lens: int32 [B] cached rows, the nodes' own last; tree_mask: int64
+    [total_q] words of visible nodes (None: a chain); max_q_len: host int, the
+    most nodes of a sequence (at most PD_MAX_TREE_NODES); num_sinks: first
+    positions that a sliding_window does not hide. workspace: a CUDA uint8
+    tensor of pd_decode_tree_workspace_bytes, allocated here when None.
+    crosscheck: call pd_decode_tree_crosscheck (CUDA cores)."""
+    if q.dim() != 3 or out.shape != q.shape:
+        raise ValueError("q and out must be bf16 [total_q, num_q_heads, head_dim]")
+    T, hq, d = q.shape
+    _decode_tree("pd_decode_tree_crosscheck" if crosscheck else "pd_decode_tree", q, 0, cu_q,
+                 tree_mask, k_cache, v_cache, block_tables, seq_lens, out, 0, T, hq, d, max_q_len,
+                 num_kv_heads, block_size, num_blocks, scale, sliding_window, num_sinks, kv_dtype,
+                 k_scale, v_scale, workspace, stream)
+    return out
+
+
+def pd_decode_tree_strided(q_rows, cu_q, k_cache, v_cache, block_tables, seq_lens, out_rows, *,
+                           num_q_heads, head_dim, max_q_len, num_kv_heads, block_size, num_blocks,
+                           scale, tree_mask=None, sliding_window=0, num_sinks=0,
+                           kv_dtype=PD_KV_BF16, k_scale=1.0, v_scale=1.0, workspace=None,
+                           stream=None, crosscheck=False):
+    """pd_decode_tree with each node's Hq * D values in the first Hq * D of a
+    row of a wider buffer (q_rows / out_rows: contiguous bf16 [total_q, row])."""
+    T, stride = _strided_rows(q_rows, num_q_heads, head_dim, "q_rows")
+    To, ostride = _strided_rows(out_rows, num_q_heads, head_dim, "out_rows")
+    if To != T:
+        raise ValueError("q_rows and out_rows have different numbers of rows")
+    _decode_tree("pd_decode_tree_crosscheck" if crosscheck else "pd_decode_tree", q_rows, stride,
+                 cu_q, tree_mask, k_cache, v_cache, block_tables, seq_lens, out_rows, ostride, T,
+                 num_q_heads, head_dim, max_q_len, num_kv_heads, block_size, num_blocks, scale,
+                 sliding_window, num_sinks, kv_dtype, k_scale, v_scale, workspace, stream)
+    return out_rows
+
+
+def pd_compact_tree(k_caches, v_caches, block_tables, seq_lens, cu_q, accepted, num_accepted,
+                    new_seq_lens, *, num_kv_heads, head_dim, block_size, num_blocks,
+                    kv_dtype=PD_KV_BF16, stream=None):
+    """Move the accepted nodes' K and V rows to consecutive positions.
+
+    k_caches, v_caches: one layer's cache (1-D), or all layers' as [layers,
+    cache_bytes]. accepted: int32 [B, max_accepted] strictly increasing node
+    indices, num_accepted: int32 [B], new_seq_lens: int32 [B], written."""
+    if k_caches.shape != v_caches.shape or k_caches.dim() not in (1, 2):
+        raise ValueError("k_caches and v_caches must be [cache_bytes] or [layers, cache_bytes]")
+    layers = k_caches.shape[0] if k_caches.dim() == 2 else 1
+    if block_tables.dim() != 2 or accepted.dim() != 2:
+        raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq] and accepted "
+                         "[num_seqs, max_accepted]")
+    B, mbs = block_tables.shape
+    if (accepted.shape[0] != B or num_accepted.shape != (B,) or seq_lens.shape != (B,) or
+            cu_q.shape != (B + 1,) or new_seq_lens.shape != (B,)):
+        raise ValueError("accepted, num_accepted, seq_lens, cu_q and new_seq_lens must match "
+                         "block_tables' sequences")
+    dev = k_caches.device
+    layer_bytes = k_caches.shape[-1] * k_caches.element_size()
+    rc = _lib.pd_compact_tree(
+        _dev(k_caches, "k_caches", None, dev), _dev(v_caches, "v_caches", None, dev), layer_bytes,
+        layers, _dev(block_tables, "block_tables", torch.int32, dev),
+        _dev(seq_lens, "seq_lens", torch.int32, dev), _dev(cu_q, "cu_q", torch.int32, dev),
+        _dev(accepted, "accepted", torch.int32, dev),
+        _dev(num_accepted, "num_accepted", torch.int32, dev), accepted.shape[1],
+        _dev(new_seq_lens, "new_seq_lens", torch.int32, dev), B, num_kv_heads, head_dim,
+        block_size, mbs, num_blocks, _dtype_code(kv_dtype), _stream(stream))
+    _check("pd_compact_tree", rc)
+    return new_seq_lens

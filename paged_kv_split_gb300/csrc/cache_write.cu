@@ -8,13 +8,6 @@ namespace {
 
 constexpr int kWriteThreads = 256;
 
-// x / s with IEEE division (no fast-math reciprocal). A NaN x goes through
-// unchanged: the GPU's NaN results are canonical (positive), and the code of
-// a NaN input takes the input's own sign.
-__device__ __forceinline__ float quotient(float x, float s) {
-  return (x != x) ? x : __fdiv_rn(x, s);
-}
-
 // BF16: byte copy of the token's [Hkv][D] row into page slot/bs, row slot%bs.
 __device__ __forceinline__ void copy_row_bf16(const uint16_t* src, uint8_t* dst, int row_elems) {
   const uint4* s = reinterpret_cast<const uint4*>(src);

@@ -998,6 +998,240 @@ int pd_decode_e4m3_out(const void* q, const void* k_cache, const void* v_cache,
                       workspace_bytes, stream, 0, 0, false, out_scale);
 }
 
+int pd_rope_table(float* cos_sin, int32_t max_position, int32_t rot_dim, double base,
+                  void* stream) {
+  if (max_position < 0 || !isfinite(base) || base <= 1.0) return PD_ERR_INVALID_ARG;
+  if (rot_dim < 16 || rot_dim > 512 || rot_dim % 16 != 0) return PD_ERR_UNSUPPORTED;
+  if (max_position == 0) return PD_OK;
+  if (!dev_ptr_ok(cos_sin)) return PD_ERR_INVALID_ARG;
+  return cuda_status(launch_rope_table(cos_sin, max_position, rot_dim, base,
+                                       static_cast<cudaStream_t>(stream)));
+}
+
+int pd_qk_norm_rope_cache(const void* qkv, int64_t qkv_stride, const void* q_weight,
+                          const void* k_weight, float eps, float weight_offset,
+                          const float* cos_sin, int32_t max_position, int32_t rot_dim,
+                          int32_t interleaved, const int32_t* positions,
+                          const int32_t* slot_mapping, void* q_out, int64_t q_out_stride,
+                          void* k_cache, void* v_cache, int32_t num_tokens, int32_t num_q_heads,
+                          int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                          int64_t num_blocks, int32_t kv_dtype, float k_scale, float v_scale,
+                          void* stream) {
+  if (num_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0) return PD_ERR_INVALID_ARG;
+  if (num_q_heads > 65535 || num_kv_heads > 65535) return PD_ERR_UNSUPPORTED;
+  if (!head_dim_ok(head_dim) || !block_size_ok(block_size) || !dtype_ok(kv_dtype))
+    return PD_ERR_UNSUPPORTED;
+  if (rot_dim < 16 || rot_dim > head_dim || rot_dim % 16 != 0) return PD_ERR_UNSUPPORTED;
+  if (num_blocks <= 0 || num_blocks * block_size > INT32_MAX || max_position <= 0)
+    return PD_ERR_INVALID_ARG;
+  if ((q_weight == nullptr) != (k_weight == nullptr)) return PD_ERR_INVALID_ARG;
+  if (q_weight != nullptr && !(isfinite(eps) && eps > 0.0f && isfinite(weight_offset)))
+    return PD_ERR_INVALID_ARG;
+  if (kv_dtype == PD_KV_FP8_E4M3 && !(scale_ok(k_scale) && scale_ok(v_scale)))
+    return PD_ERR_INVALID_ARG;
+  if (!q_stride_ok(qkv_stride, num_q_heads + 2 * num_kv_heads, head_dim) ||
+      !q_stride_ok(q_out_stride, num_q_heads, head_dim))
+    return PD_ERR_INVALID_ARG;
+  if (num_tokens == 0) return PD_OK;
+  if (!dev_ptr_ok(qkv) || !dev_ptr_ok(cos_sin) || !dev_ptr_ok(positions) ||
+      !dev_ptr_ok(slot_mapping) || !dev_ptr_ok(q_out) || !dev_ptr_ok(k_cache) ||
+      !dev_ptr_ok(v_cache) || !aligned16(q_weight) || !aligned16(k_weight))
+    return PD_ERR_INVALID_ARG;
+  DeviceInfo* dev = nullptr;
+  if (current_device(&dev) != cudaSuccess) return PD_ERR_CUDA;
+  NormRopeArgs a;
+  a.qkv = static_cast<const uint16_t*>(qkv);
+  a.qkv_stride =
+      qkv_stride ? qkv_stride : static_cast<int64_t>(num_q_heads + 2 * num_kv_heads) * head_dim;
+  a.q_weight = static_cast<const uint16_t*>(q_weight);
+  a.k_weight = static_cast<const uint16_t*>(k_weight);
+  a.cos_sin = cos_sin;
+  a.positions = positions;
+  a.slots = slot_mapping;
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.q_out_stride = q_out_stride ? q_out_stride : static_cast<int64_t>(num_q_heads) * head_dim;
+  a.k_cache = static_cast<uint8_t*>(k_cache);
+  a.v_cache = static_cast<uint8_t*>(v_cache);
+  a.flags = dev->flags;
+  a.num_blocks = num_blocks;
+  a.page_bytes = page_bytes_of(kv_dtype, block_size, num_kv_heads, head_dim);
+  a.data_bytes = nvfp4_data_bytes(block_size, num_kv_heads, head_dim);
+  a.num_tokens = num_tokens;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.block_size = block_size;
+  a.max_position = max_position;
+  a.rot_dim = rot_dim;
+  a.interleaved = interleaved != 0;
+  a.eps = eps;
+  a.weight_offset = weight_offset;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  return cuda_status(launch_qk_norm_rope_cache(a, head_dim, kv_dtype, dev->num_sms,
+                                               static_cast<cudaStream_t>(stream)));
+}
+
+size_t pd_decode_tree_workspace_bytes(int32_t max_q_len, int32_t num_q_heads,
+                                      int32_t num_kv_heads, int32_t head_dim, int32_t kv_dtype,
+                                      int32_t num_sms) {
+  if (max_q_len < 0 || max_q_len > kMaxTreeNodes || num_sms < 1) return 0;
+  if (num_kv_heads <= 0 || num_q_heads <= 0 || num_q_heads % num_kv_heads != 0 ||
+      num_q_heads / num_kv_heads > kMaxGroup || !head_dim_ok(head_dim) || !dtype_ok(kv_dtype))
+    return 0;
+  return 16;
+}
+
+}  // extern "C"
+
+namespace {
+int decode_tree_impl(const void* q, int64_t q_stride, const int32_t* cu_q,
+                     const uint64_t* tree_mask, const void* k_cache, const void* v_cache,
+                     const int32_t* block_tables, const int32_t* seq_lens, void* out,
+                     int64_t out_stride, int32_t num_seqs, int32_t total_q, int32_t max_q_len,
+                     int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                     int32_t block_size, int32_t max_blocks_per_seq, int64_t num_blocks,
+                     float scale, int32_t sliding_window, int32_t num_sinks, int32_t kv_dtype,
+                     float k_scale, float v_scale, void* workspace, size_t workspace_bytes,
+                     void* stream, bool simple) {
+  const DecodeShape sh{num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                       max_blocks_per_seq, 1, sliding_window, kv_dtype, num_blocks};
+  const int rc = check_decode_shape(sh, k_scale, v_scale);
+  if (rc != PD_OK) return rc;
+  if (num_kv_heads > 65535 / kMaxGroup) return PD_ERR_UNSUPPORTED;
+  if (total_q < 0 || max_q_len < 0 || num_sinks < 0 || !isfinite(scale)) return PD_ERR_INVALID_ARG;
+  if (max_q_len > kMaxTreeNodes) return PD_ERR_UNSUPPORTED;
+  if (!q_stride_ok(q_stride, num_q_heads, head_dim) ||
+      !q_stride_ok(out_stride, num_q_heads, head_dim))
+    return PD_ERR_INVALID_ARG;
+  if (num_seqs == 0 || total_q == 0 || max_q_len == 0) return PD_OK;
+  if (!dev_ptr_ok(q) || !dev_ptr_ok(cu_q) || !aligned16(tree_mask) || !dev_ptr_ok(k_cache) ||
+      !dev_ptr_ok(v_cache) || !dev_ptr_ok(block_tables) || !dev_ptr_ok(seq_lens) ||
+      !dev_ptr_ok(out) || !dev_ptr_ok(workspace))
+    return PD_ERR_INVALID_ARG;
+  DeviceInfo* dev = nullptr;
+  if (current_device(&dev) != cudaSuccess) return PD_ERR_CUDA;
+  if (workspace_bytes < pd_decode_tree_workspace_bytes(max_q_len, num_q_heads, num_kv_heads,
+                                                       head_dim, kv_dtype, dev->num_sms))
+    return PD_ERR_WORKSPACE_TOO_SMALL;
+  TreeArgs a;
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_stride = q_stride ? q_stride : static_cast<int64_t>(num_q_heads) * head_dim;
+  a.cu_q = cu_q;
+  a.tree_mask = tree_mask;
+  a.k_cache = static_cast<const uint8_t*>(k_cache);
+  a.v_cache = static_cast<const uint8_t*>(v_cache);
+  a.block_tables = block_tables;
+  a.seq_lens = seq_lens;
+  a.out = static_cast<uint16_t*>(out);
+  a.out_stride = out_stride ? out_stride : static_cast<int64_t>(num_q_heads) * head_dim;
+  a.flags = dev->flags;
+  a.num_blocks = num_blocks;
+  a.page_bytes = page_bytes_of(kv_dtype, block_size, num_kv_heads, head_dim);
+  a.data_bytes = nvfp4_data_bytes(block_size, num_kv_heads, head_dim);
+  a.num_seqs = num_seqs;
+  a.total_q = total_q;
+  a.max_q_len = max_q_len;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.group = num_q_heads / num_kv_heads;
+  a.block_size = block_size;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.sliding_window = sliding_window;
+  a.num_sinks = num_sinks;
+  a.scale_log2 = scale * kLog2e;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  (void)simple;
+  return cuda_status(launch_tree_simple(a, head_dim, kv_dtype, static_cast<cudaStream_t>(stream)));
+}
+}  // namespace
+
+extern "C" {
+
+#define PD_TREE_ARGS                                                                             \
+  q, q_stride, cu_q, tree_mask, k_cache, v_cache, block_tables, seq_lens, out, out_stride,       \
+      num_seqs, total_q, max_q_len, num_q_heads, num_kv_heads, head_dim, block_size,             \
+      max_blocks_per_seq, num_blocks, scale, sliding_window, num_sinks, kv_dtype, k_scale,       \
+      v_scale, workspace, workspace_bytes, stream
+
+int pd_decode_tree(const void* q, int64_t q_stride, const int32_t* cu_q,
+                   const uint64_t* tree_mask, const void* k_cache, const void* v_cache,
+                   const int32_t* block_tables, const int32_t* seq_lens, void* out,
+                   int64_t out_stride, int32_t num_seqs, int32_t total_q, int32_t max_q_len,
+                   int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                   int32_t block_size, int32_t max_blocks_per_seq, int64_t num_blocks,
+                   float scale, int32_t sliding_window, int32_t num_sinks, int32_t kv_dtype,
+                   float k_scale, float v_scale, void* workspace, size_t workspace_bytes,
+                   void* stream) {
+  return decode_tree_impl(PD_TREE_ARGS, false);
+}
+
+int pd_decode_tree_crosscheck(const void* q, int64_t q_stride, const int32_t* cu_q,
+                              const uint64_t* tree_mask, const void* k_cache,
+                              const void* v_cache, const int32_t* block_tables,
+                              const int32_t* seq_lens, void* out, int64_t out_stride,
+                              int32_t num_seqs, int32_t total_q, int32_t max_q_len,
+                              int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                              int32_t block_size, int32_t max_blocks_per_seq,
+                              int64_t num_blocks, float scale, int32_t sliding_window,
+                              int32_t num_sinks, int32_t kv_dtype, float k_scale, float v_scale,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+  return decode_tree_impl(PD_TREE_ARGS, true);
+}
+#undef PD_TREE_ARGS
+
+int pd_compact_tree(void* k_caches, void* v_caches, int64_t layer_bytes, int32_t num_layers,
+                    const int32_t* block_tables, const int32_t* seq_lens, const int32_t* cu_q,
+                    const int32_t* accepted, const int32_t* num_accepted, int32_t max_accepted,
+                    int32_t* new_seq_lens, int32_t num_seqs, int32_t num_kv_heads,
+                    int32_t head_dim, int32_t block_size, int32_t max_blocks_per_seq,
+                    int64_t num_blocks, int32_t kv_dtype, void* stream) {
+  if (num_seqs < 0 || num_seqs > 65535 || num_layers < 0 || num_layers > 65535)
+    return PD_ERR_INVALID_ARG;
+  if (num_kv_heads <= 0 || max_blocks_per_seq <= 0 || num_blocks <= 0 || max_accepted < 0)
+    return PD_ERR_INVALID_ARG;
+  if (!head_dim_ok(head_dim) || !block_size_ok(block_size) || !dtype_ok(kv_dtype) ||
+      max_accepted > kMaxTreeNodes)
+    return PD_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(max_blocks_per_seq) * block_size > (int64_t{1} << 30) ||
+      num_blocks * block_size > INT32_MAX)
+    return PD_ERR_INVALID_ARG;
+  const int64_t page_bytes = page_bytes_of(kv_dtype, block_size, num_kv_heads, head_dim);
+  if (layer_bytes != 0 && (layer_bytes < num_blocks * page_bytes || layer_bytes % 16 != 0))
+    return PD_ERR_INVALID_ARG;
+  if (num_seqs == 0 || num_layers == 0) return PD_OK;
+  if (!dev_ptr_ok(k_caches) || !dev_ptr_ok(v_caches) || !dev_ptr_ok(block_tables) ||
+      !dev_ptr_ok(seq_lens) || !dev_ptr_ok(cu_q) || !dev_ptr_ok(num_accepted) ||
+      !dev_ptr_ok(new_seq_lens) || new_seq_lens == seq_lens)
+    return PD_ERR_INVALID_ARG;
+  if (max_accepted > 0 && !dev_ptr_ok(accepted)) return PD_ERR_INVALID_ARG;
+  DeviceInfo* dev = nullptr;
+  if (current_device(&dev) != cudaSuccess) return PD_ERR_CUDA;
+  CompactArgs a;
+  a.k_caches = static_cast<uint8_t*>(k_caches);
+  a.v_caches = static_cast<uint8_t*>(v_caches);
+  a.layer_bytes = layer_bytes ? layer_bytes : num_blocks * page_bytes;
+  a.block_tables = block_tables;
+  a.seq_lens = seq_lens;
+  a.cu_q = cu_q;
+  a.accepted = accepted;
+  a.num_accepted = num_accepted;
+  a.new_seq_lens = new_seq_lens;
+  a.flags = dev->flags;
+  a.num_blocks = num_blocks;
+  a.page_bytes = page_bytes;
+  a.data_bytes = nvfp4_data_bytes(block_size, num_kv_heads, head_dim);
+  a.num_seqs = num_seqs;
+  a.num_layers = num_layers;
+  a.max_accepted = max_accepted;
+  a.num_kv_heads = num_kv_heads;
+  a.head_dim = head_dim;
+  a.block_size = block_size;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.kv_dtype = kv_dtype;
+  return cuda_status(launch_compact_tree(a, static_cast<cudaStream_t>(stream)));
+}
+
 float pd_fp8_scale(float absmax) { return absmax > 0.0f ? absmax / 448.0f : 1.0f; }
 
 int pd_fp8_scales_from_absmax(const float* absmax, float* scales, int32_t count, void* stream) {

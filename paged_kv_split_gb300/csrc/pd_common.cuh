@@ -84,6 +84,13 @@ __device__ __forceinline__ float e2m1_decode(uint32_t c) {
   return (c & 0x8u) ? -mag : mag;
 }
 
+// x / s with IEEE division (no fast-math reciprocal). A NaN x goes through
+// unchanged: the GPU's NaN results are canonical (positive), and the code of
+// a NaN input takes the input's own sign.
+__device__ __forceinline__ float quotient(float x, float s) {
+  return (x != x) ? x : __fdiv_rn(x, s);
+}
+
 // ---------------------------------------------------------------------------
 // Cache geometry.
 __host__ __device__ __forceinline__ int64_t page_bytes_of(int kv_dtype, int bs, int hkv, int d) {
@@ -207,6 +214,67 @@ struct PrefillArgs {
   float k_scale, v_scale;        // FP8 per-tensor scales
 };
 
+// Norm + rotation + cache write (pd_qk_norm_rope_cache): token t's fused row
+// [Hq q heads | Hkv k heads | Hkv v heads] at t * qkv_stride elements.
+struct NormRopeArgs {
+  const uint16_t* qkv;
+  int64_t qkv_stride;
+  const uint16_t* q_weight;      // [D] bf16, or null: no norm
+  const uint16_t* k_weight;
+  const float* cos_sin;          // [max_position][rot_dim]: cosines, then sines
+  const int32_t* positions;      // [T]
+  const int32_t* slots;          // [T]
+  uint16_t* q_out;               // token t's q heads at t * q_out_stride
+  int64_t q_out_stride;
+  uint8_t* k_cache;
+  uint8_t* v_cache;
+  int* flags;
+  int64_t num_blocks, page_bytes, data_bytes;
+  int num_tokens, num_q_heads, num_kv_heads, block_size;
+  int max_position, rot_dim, interleaved;
+  float eps, weight_offset, k_scale, v_scale;
+};
+
+// Draft-tree attention (pd_decode_tree). Sequence b's nodes are query rows
+// cu_q[b] .. cu_q[b+1]-1, its keys the first seq_lens[b] rows of the cache, the
+// last cu_q[b+1] - cu_q[b] of them the nodes' own.
+constexpr int kMaxTreeNodes = PD_MAX_TREE_NODES;
+struct TreeArgs {
+  const uint16_t* q;
+  int64_t q_stride;
+  const int32_t* cu_q;           // [B + 1]
+  const uint64_t* tree_mask;     // [total_q], or null: every node sees those before it
+  const uint8_t* k_cache;
+  const uint8_t* v_cache;
+  const int32_t* block_tables;   // [B][MBS]
+  const int32_t* seq_lens;       // [B]
+  uint16_t* out;
+  int64_t out_stride;
+  int* flags;
+  int64_t num_blocks, page_bytes, data_bytes;
+  int num_seqs, total_q, max_q_len, num_q_heads, num_kv_heads, group, block_size;
+  int max_blocks_per_seq, sliding_window, num_sinks;
+  float scale_log2;              // scale * log2(e)
+  float k_scale, v_scale;
+};
+
+// Moving accepted rows (pd_compact_tree); layer l's caches at l * layer_bytes.
+struct CompactArgs {
+  uint8_t* k_caches;
+  uint8_t* v_caches;
+  int64_t layer_bytes;
+  const int32_t* block_tables;
+  const int32_t* seq_lens;
+  const int32_t* cu_q;
+  const int32_t* accepted;       // [B][max_accepted]
+  const int32_t* num_accepted;   // [B]
+  int32_t* new_seq_lens;         // [B]
+  int* flags;
+  int64_t num_blocks, page_bytes, data_bytes;
+  int num_seqs, num_layers, max_accepted, num_kv_heads, head_dim, block_size;
+  int max_blocks_per_seq, kv_dtype;
+};
+
 // Sequence length as the kernels use it: clamped to the block table, with a
 // flag raised for values outside [0, MBS*bs].
 __device__ __forceinline__ int checked_seq_len(const int32_t* seq_lens, int b, int mbs, int bs,
@@ -218,6 +286,64 @@ __device__ __forceinline__ int checked_seq_len(const int32_t* seq_lens, int b, i
     L = L < 0 ? 0 : cap;
   }
   return L;
+}
+
+// A sequence of a draft-tree batch: its first node row q0, node count n and key
+// count L, or n = 0 with a flag raised when they do not fit the batch's arrays.
+struct TreeSeq {
+  int q0, n, L;
+};
+__device__ __forceinline__ TreeSeq tree_seq(const int32_t* cu_q, const int32_t* seq_lens, int b,
+                                            int total_q, int max_nodes, int mbs, int bs,
+                                            int* flags) {
+  TreeSeq s;
+  s.q0 = cu_q[b];
+  const int q1 = cu_q[b + 1];
+  s.n = q1 - s.q0;
+  s.L = seq_lens[b];
+  const bool ok = s.q0 >= 0 && q1 >= s.q0 && q1 <= total_q && s.n <= max_nodes && s.L >= s.n &&
+                  s.L <= mbs * bs;
+  if (!ok) {
+    if (flags) atomicOr(flags, PD_DEV_BAD_SEQ_LEN);
+    s.n = 0;
+  }
+  return s;
+}
+// Node i's visible nodes among the sequence's n (bit j: node j), before the window.
+__device__ __forceinline__ uint64_t tree_bits(const uint64_t* mask, int q0, int i, int n) {
+  const uint64_t all = n >= 64 ? ~0ull : (1ull << n) - 1ull;
+  const uint64_t chain = i >= 63 ? ~0ull : (2ull << i) - 1ull;
+  return (mask ? mask[q0 + i] : chain) & all;
+}
+__device__ __forceinline__ int tree_depth(uint64_t bits) {
+  const int c = __popcll(bits);
+  return c > 0 ? c - 1 : 0;
+}
+// What node i sees: cached rows r < prefix with r >= lo or r < sinks, and the
+// nodes of `bits`. A window narrower than 64 can also hide nodes (two nodes'
+// depths differ by at most 63).
+struct NodeView {
+  int lo;
+  uint64_t bits;
+};
+__device__ __forceinline__ NodeView node_view(const uint64_t* mask, const TreeSeq& s, int i, int W,
+                                              int sinks) {
+  NodeView v;
+  v.bits = tree_bits(mask, s.q0, i, s.n);
+  v.lo = 0;
+  if (W > 0) {
+    const int prefix = s.L - s.n;
+    const int depth = tree_depth(v.bits);
+    v.lo = prefix + depth + 1 - W;
+    if (v.lo < 0) v.lo = 0;
+    if (W < kMaxTreeNodes) {
+      for (int j = 0; j < s.n; ++j) {
+        const int dj = tree_depth(tree_bits(mask, s.q0, j, s.n));
+        if (depth - dj >= W && prefix + dj >= sinks) v.bits &= ~(1ull << j);
+      }
+    }
+  }
+  return v;
 }
 
 }  // namespace pd
@@ -271,4 +397,11 @@ cudaError_t launch_prefill_pair(const PrefillArgs& a, const void* k_cache, const
                                 int head_dim, int max_q_len, cudaStream_t st);
 cudaError_t launch_prefill_umma(const PrefillArgs& a, const void* k_cache, const void* v_cache,
                                 int head_dim, int max_q_len, cudaStream_t st);
+// The table pd_rope_table writes: [max_position][rot_dim] fp32.
+cudaError_t launch_rope_table(float* cos_sin, int max_position, int rot_dim, double base,
+                              cudaStream_t st);
+cudaError_t launch_qk_norm_rope_cache(const NormRopeArgs& a, int head_dim, int kv_dtype,
+                                      int num_sms, cudaStream_t st);
+cudaError_t launch_tree_simple(const TreeArgs& a, int head_dim, int kv_dtype, cudaStream_t st);
+cudaError_t launch_compact_tree(const CompactArgs& a, cudaStream_t st);
 }  // namespace pd
