@@ -12,6 +12,7 @@
 #include <vector>
 
 #include "pd_common.cuh"
+#include "tree_plan.cuh"
 
 namespace pd {
 namespace {
@@ -1078,7 +1079,9 @@ size_t pd_decode_tree_workspace_bytes(int32_t max_q_len, int32_t num_q_heads,
   if (num_kv_heads <= 0 || num_q_heads <= 0 || num_q_heads % num_kv_heads != 0 ||
       num_q_heads / num_kv_heads > kMaxGroup || !head_dim_ok(head_dim) || !dtype_ok(kv_dtype))
     return 0;
-  return 16;
+  if (head_dim > 128) return 16;
+  return tree_umma_workspace(max_q_len, num_q_heads / num_kv_heads, head_dim, num_sms, nullptr,
+                             nullptr);
 }
 
 }  // extern "C"
@@ -1141,7 +1144,12 @@ int decode_tree_impl(const void* q, int64_t q_stride, const int32_t* cu_q,
   a.scale_log2 = scale * kLog2e;
   a.k_scale = k_scale;
   a.v_scale = v_scale;
-  (void)simple;
+  if (!simple && head_dim <= 128) {
+    TreeWork w;
+    tree_umma_workspace(max_q_len, a.group, head_dim, dev->num_sms, &w, workspace);
+    return cuda_status(
+        launch_tree_umma(a, w, head_dim, kv_dtype, static_cast<cudaStream_t>(stream)));
+  }
   return cuda_status(launch_tree_simple(a, head_dim, kv_dtype, static_cast<cudaStream_t>(stream)));
 }
 }  // namespace

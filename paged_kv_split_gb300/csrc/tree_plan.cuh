@@ -1,0 +1,268 @@
+// How draft-tree attention is dealt to CTAs, worked out on the device.
+//
+// An item is (sequence, kv head, tile of the sequence's nodes); its keys are a
+// line of key tiles: the tiles that hold the first tokens that stay visible,
+// then those from the window's first page on (or all of them). All items, laid
+// end to end (sequence, then kv head, then node tile: the node tiles of a head
+// run side by side and share its keys in L2), make one line of units, a unit a
+// key tile, with `ov` units of slack after each item for what a piece costs
+// beside its tiles. CTA c takes units [c S, (c + 1) S). So every CTA streams the
+// same number of tiles whatever the lengths, an item cut by a share's end
+// becomes pieces whose partials a second kernel joins, and at most one item
+// begins in a CTA and goes on in the next: the partials need two slots a CTA.
+// Every CTA sums the line from cu_q and seq_lens itself, so the host needs no
+// lengths and a captured graph follows them.
+#pragma once
+
+#include "pd_common.cuh"
+
+namespace pd {
+namespace tree {
+
+// One sequence's tiles.
+struct SeqPlan {
+  TreeSeq s;
+  int nst;   // leading tiles, from key 0, for the first tokens
+  int base;  // first key of the other tiles (page aligned)
+  int nt;    // tiles
+  int rts;   // node tiles
+};
+__device__ __forceinline__ SeqPlan seq_plan(const TreeArgs& a, int b, int tpc, int kt, int* flags) {
+  SeqPlan p;
+  p.s = tree_seq(a.cu_q, a.seq_lens, b, a.total_q, a.max_q_len, a.max_blocks_per_seq, a.block_size,
+                 flags);
+  p.nst = p.base = p.nt = p.rts = 0;
+  if (p.s.n == 0) return p;
+  const int prefix = p.s.L - p.s.n;
+  if (a.sliding_window > 0) {
+    const int lo = max(0, prefix + 1 - a.sliding_window);  // a node of depth 0 sees the most
+    p.base = lo / a.block_size * a.block_size;
+    p.nst = (min(a.num_sinks, p.s.L) + kt - 1) / kt;
+    if (p.base <= p.nst * kt) p.nst = p.base = 0;  // the two ranges meet
+  }
+  p.nt = p.nst + (p.s.L - p.base + kt - 1) / kt;
+  p.rts = (p.s.n + tpc - 1) / tpc;
+  return p;
+}
+// First key of tile j.
+__device__ __forceinline__ int tile_key(const SeqPlan& p, int j, int kt) {
+  return j < p.nst ? j * kt : p.base + (j - p.nst) * kt;
+}
+// Keys of tile j end here (the first tokens' last tile stops at num_sinks).
+__device__ __forceinline__ int tile_end(const SeqPlan& p, int j, int kt, int sinks) {
+  return j < p.nst ? min((j + 1) * kt, sinks) : min(p.base + (j - p.nst + 1) * kt, p.s.L);
+}
+
+// A CTA's share of the line.
+struct Share {
+  long long units;  // S
+  long long x0;     // first unit
+  int b, k, off;    // its sequence, item there and unit in the item; b < 0: nothing
+};
+struct ShareScratch {
+  long long warp_sum[32];
+  long long units;
+  int b, k, off;
+};
+// Called by all threads of the CTA, one barrier pair. `per_cta_min`: a share is at
+// least that long.
+__device__ __forceinline__ Share make_share(const TreeArgs& a, int tpc, int kt, int ov,
+                                            int per_cta_min, ShareScratch* sh) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int nthreads = blockDim.x;
+  const int per = (a.num_seqs + nthreads - 1) / nthreads;
+  const int b0 = min(tid * per, a.num_seqs), b1 = min(b0 + per, a.num_seqs);
+  int* flags = blockIdx.x == 0 ? a.flags : nullptr;
+  long long sum = 0;
+  for (int b = b0; b < b1; ++b) {
+    const SeqPlan p = seq_plan(a, b, tpc, kt, flags);
+    sum += static_cast<long long>(p.rts) * a.num_kv_heads * (p.nt + ov);
+  }
+  long long incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) sh->warp_sum[warp] = incl;
+  if (tid == 0) sh->b = -1;
+  __syncthreads();
+  long long before = 0, total = 0;
+  const int warps = nthreads >> 5;
+  for (int w = 0; w < warps; ++w) {
+    if (w == warp) before = total;
+    total += sh->warp_sum[w];
+  }
+  Share r;
+  r.units = (total + gridDim.x - 1) / gridDim.x;
+  if (r.units < per_cta_min) r.units = per_cta_min;
+  r.x0 = r.units * blockIdx.x;
+  long long at = before + incl - sum;  // first unit of this thread's sequences
+  if (r.x0 >= at && r.x0 < at + sum) {
+    for (int b = b0; b < b1; ++b) {
+      const SeqPlan p = seq_plan(a, b, tpc, kt, nullptr);
+      const long long cost = static_cast<long long>(p.rts) * a.num_kv_heads * (p.nt + ov);
+      if (r.x0 < at + cost) {
+        const int item = p.nt + ov;
+        sh->b = b;
+        sh->k = static_cast<int>((r.x0 - at) / item);
+        sh->off = static_cast<int>((r.x0 - at) % item);
+        break;
+      }
+      at += cost;
+    }
+  }
+  __syncthreads();
+  r.b = sh->b;
+  r.k = sh->k;
+  r.off = sh->off;
+  return r;
+}
+
+// A CTA's part of one item.
+struct Piece {
+  SeqPlan p;
+  int b, g, rt;
+  int j0, j1;     // its tiles
+  bool begins;    // holds the item's first tile
+  bool whole;     // and its last: writes the output itself
+  int slot;       // else its partial's slot
+};
+// Goes through a share's pieces; every warp role that needs them runs its own.
+struct Walker {
+  const TreeArgs& a;
+  int tpc, kt, ov;
+  long long units, x, end;
+  int b, k, off;
+  SeqPlan p;
+
+  __device__ __forceinline__ Walker(const TreeArgs& args, const Share& s, int tpc_, int kt_, int ov_)
+      : a(args), tpc(tpc_), kt(kt_), ov(ov_), units(s.units), x(s.x0), end(s.x0 + s.units), b(s.b),
+        k(s.k), off(s.off) {
+    p = seq_plan(a, b, tpc, kt, nullptr);
+  }
+  __device__ __forceinline__ bool next(Piece& q) {
+    while (x < end && b < a.num_seqs) {
+      const int items = p.rts * a.num_kv_heads;
+      if (k >= items) {
+        k = 0;
+        if (++b < a.num_seqs) p = seq_plan(a, b, tpc, kt, nullptr);
+        continue;
+      }
+      const int take = static_cast<int>(min(static_cast<long long>(p.nt + ov - off), end - x));
+      const int j0 = off, j1 = min(off + take, p.nt);
+      x += take;
+      q.g = k / p.rts;
+      q.rt = k % p.rts;
+      if (off + take == p.nt + ov) {
+        ++k;
+        off = 0;
+      } else {
+        off += take;
+      }
+      if (j0 >= j1) continue;  // slack only
+      q.p = p;
+      q.b = b;
+      q.j0 = j0;
+      q.j1 = j1;
+      q.begins = j0 == 0;
+      q.whole = j0 == 0 && j1 == p.nt;
+      q.slot = 2 * static_cast<int>(blockIdx.x) + (q.begins ? 1 : 0);
+      return true;
+    }
+    return false;
+  }
+  // pieces of the item whose first j1 tiles end this share
+  __device__ __forceinline__ int pieces_of_last(int j1) const {
+    const long long s = end - j1;  // the item's first unit
+    return static_cast<int>((s + p.nt - 1) / units - (end - 1) / units) + 1;
+  }
+};
+
+// What a CTA leaves for the join: the item that begins in it and goes on, or
+// pieces = 0.
+struct JoinRecord {
+  int b, g, rt, pieces;
+};
+
+// Workspace: records [ctas], then (m, l) [2 ctas][rows], then O
+// [2 ctas][D / 4][rows][4] fp32, rows the padded rows of an item. m in log2
+// units, l and O not divided.
+struct WorkLayout {
+  size_t ml, o, bytes;
+};
+__host__ __device__ inline WorkLayout work_layout(int ctas, int rows, int d) {
+  WorkLayout w;
+  w.ml = (static_cast<size_t>(ctas) * sizeof(JoinRecord) + 255) / 256 * 256;
+  w.o = w.ml + (static_cast<size_t>(2) * ctas * rows * sizeof(float2) + 255) / 256 * 256;
+  w.bytes = w.o + static_cast<size_t>(2) * ctas * rows * d * sizeof(float);
+  return w;
+}
+
+// The workspace as the kernels see it.
+}  // namespace tree
+struct TreeWork {
+  tree::JoinRecord* records;  // [ctas]
+  float2* ml;
+  float* o;
+  int ctas, rows, item_nodes, min_units;
+};
+size_t tree_umma_workspace(int max_q_len, int group, int head_dim, int num_sms, TreeWork* w,
+                           void* workspace);
+cudaError_t launch_tree_umma(const TreeArgs& a, const TreeWork& w, int head_dim, int kv_dtype,
+                             cudaStream_t st);
+namespace tree {
+
+// Which cached rows and nodes a node (or, merged, any node) sees.
+struct RowView {
+  int lo, prefix, sinks;  // rows [lo, prefix) and [0, sinks), sinks <= prefix
+  uint64_t bits;
+};
+// Bits [a, b) of a word.
+__device__ __forceinline__ uint32_t range32(int a, int b) {
+  a = max(a, 0);
+  b = min(b, 32);
+  if (a >= b) return 0u;
+  return (b - a == 32 ? 0xFFFFFFFFu : ((1u << (b - a)) - 1u)) << a;
+}
+// Bit i: row k0 + i is seen.
+__device__ __forceinline__ uint32_t seen32(const RowView& v, int k0) {
+  uint32_t w = range32(v.lo - k0, v.prefix - k0) | range32(-k0, v.sinks - k0);
+  const int s = k0 - v.prefix;
+  if (s >= 0) {
+    if (s < 64) w |= static_cast<uint32_t>(v.bits >> s);
+  } else if (s > -32) {
+    w |= static_cast<uint32_t>(v.bits << -s);
+  }
+  return w;
+}
+__device__ __forceinline__ RowView row_view(const TreeArgs& a, const TreeSeq& s, int i) {
+  const NodeView n = node_view(a.tree_mask, s, i, a.sliding_window, a.num_sinks);
+  RowView v;
+  v.prefix = s.L - s.n;
+  v.lo = min(n.lo, v.prefix);
+  v.sinks = a.sliding_window > 0 ? min(a.num_sinks, v.prefix) : 0;
+  v.bits = n.bits;
+  return v;
+}
+// What any node of the sequence sees (all lanes of a warp together).
+__device__ __forceinline__ RowView any_view(const TreeArgs& a, const TreeSeq& s, int lane) {
+  RowView u;
+  u.prefix = s.L - s.n;
+  u.lo = u.prefix;
+  u.sinks = a.sliding_window > 0 ? min(a.num_sinks, u.prefix) : 0;
+  u.bits = 0;
+  for (int i = lane; i < s.n; i += 32) {
+    const RowView v = row_view(a, s, i);
+    u.lo = min(u.lo, v.lo);
+    u.bits |= v.bits;
+  }
+  u.lo = __reduce_min_sync(0xFFFFFFFFu, u.lo);
+  const uint32_t lo32 = __reduce_or_sync(0xFFFFFFFFu, static_cast<uint32_t>(u.bits));
+  const uint32_t hi32 = __reduce_or_sync(0xFFFFFFFFu, static_cast<uint32_t>(u.bits >> 32));
+  u.bits = (static_cast<uint64_t>(hi32) << 32) | lo32;
+  return u;
+}
+
+}  // namespace tree
+}  // namespace pd

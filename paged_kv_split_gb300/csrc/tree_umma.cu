@@ -1,0 +1,925 @@
+// Draft-tree attention on the 5th-generation tensor cores, head_dim 64 and 128,
+// and the join of the partials.
+//
+// The rows of one kv head are the nodes times its G q heads, so every key byte
+// serves n G rows: at 4 D bytes a key (BF16) and 4 D n G operations the keys'
+// bytes bound the kernel up to some 290 rows, and padding the rows to the
+// tensor core's 128 costs nothing that matters. What has to hold is that the
+// chain scores -> softmax -> weighted values keeps up with the memory.
+//
+//  * One CTA an SM takes an equal share of all key tiles (tree_plan.cuh). A
+//    tile is 128 keys. Two groups of four softmax warps, one thread a row:
+//    up to 128 rows the groups take alternate tiles of the same rows and merge
+//    at the end; above, each takes 128 rows of every tile.
+//  * TMEM holds per group S (128 columns fp32), over which P is written as
+//    16-bit pairs, and O (D columns). P is then the A operand from TMEM, so
+//    shared memory carries K, V and Q only.
+//  * The producer warp copies K and V units (128 keys of one head) by TMA into
+//    a ring, in the order in which they are used. FP8 and NVFP4 units land raw
+//    and four more warps widen them to f16 (exact: every E4M3 value and every
+//    E2M1 x E4M3 product is an f16); q is then scaled by a power of two a row.
+//  * A row's P is taken against a running reference that moves only when a
+//    tile passes it by more than 2^8, in one pass over the scores; tiles that
+//    are masked (the window's edge, the nodes, the first of a piece) take the
+//    maximum first. Sums and O are fp32; P is rounded to bf16 (BF16 caches) or
+//    f16.
+//  * V rows that no node sees are zeroed, so stale bytes never meet a weight.
+//  * Every wait is bounded (2 s): on time-out the CTA raises PD_DEV_TIMEOUT,
+//    waits for its copies and MMAs in flight, frees its TMEM and ends.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cudaTypedefs.h>
+
+#include <cstring>
+
+#include "mma_common.cuh"
+#include "pd_common.cuh"
+#include "tree_plan.cuh"
+#include "umma_common.cuh"
+
+namespace pd {
+namespace {
+
+using namespace ::pd::mma;
+using namespace ::pd::umma;
+using namespace ::pd::tree;
+
+constexpr float kTreeRescale = 8.0f;  // P <= 2^8 between moves of the reference
+constexpr int kTreeKT = 128;          // keys of a tile
+constexpr int kTreeSlack = 1;         // units a piece costs beside its tiles
+constexpr int kTreeSoftWarps = 8;
+constexpr int kTreeProd = 8;
+constexpr int kTreeMma = 9;
+constexpr int kTreeConv = 10;         // warps 10..13 widen quantised units
+constexpr int kTreeTmemCols = 512;
+constexpr int kTreeBadRing = 32;      // tiles whose page masks are kept
+
+template <int FMT, int D, int BS>
+struct TreeCfg {
+  static constexpr bool kQuant = FMT != PD_KV_BF16;
+  static constexpr int kThreads = (kQuant ? 14 : 10) * 32;
+  static constexpr int kCopies = kTreeKT / BS;            // pages of a tile
+  static constexpr int kQBytes = 128 * D * 2;             // one Q tile, chunk-major
+  static constexpr int kUnitBytes = kTreeKT * D * 2;      // one 16-bit K or V unit, chunk-major
+  static constexpr int kUnits = (kQuant ? 96 : 160) * 1024 / kUnitBytes;
+  // a raw quantised unit: rows [128][row bytes], then NVFP4 scales [128][D / 16]
+  static constexpr int kRowBytes = FMT == PD_KV_FP8_E4M3 ? D : D / 2;
+  static constexpr int kRawData = kTreeKT * kRowBytes;
+  static constexpr int kRawScales = FMT == PD_KV_NVFP4 ? kTreeKT * (D / 16) : 0;
+  static constexpr int kRawBytes = kQuant ? (kRawData + kRawScales + 1023) / 1024 * 1024 : 0;
+  static constexpr int kRaws = kQuant ? 64 * 1024 / kRawBytes : 0;
+  static constexpr int kUnitOff = 2 * kQBytes;
+  static constexpr int kRawOff = kUnitOff + kUnits * kUnitBytes;
+  static constexpr int kBarOff = kRawOff + kRaws * kRawBytes;
+  // unit full / empty, raw full / empty, s_full[2], p_full[2], o_done[2],
+  // ml_full[2], q_full, fin
+  static constexpr int kNumBars = 2 * kUnits + 2 * kRaws + 10;
+  static constexpr int kBadOff = kBarOff + kNumBars * 8;
+  static constexpr int kMlOff = kBadOff + kTreeBadRing * 4;
+  static constexpr int kPageOff = kMlOff + 2 * 128 * 8;
+  static constexpr int kHolderOff = kPageOff + 4 * kCopies * 4;  // pages of the last four tiles
+  static constexpr int kSmemBytes = kHolderOff + 16;
+  static_assert(kUnitBytes % 1024 == 0 && kRawBytes % 1024 == 0, "aligned tiles");
+  static_assert(kSmemBytes <= 227 * 1024, "one CTA's shared memory");
+};
+
+// Order in which a piece of T tiles uses its 2 T units: dual (each group has its
+// own rows) K0 V0 K1 V1 ..; alternating groups K0 K1 V0 K2 V1 ...
+__device__ __forceinline__ void unit_at(int t, int T, bool dual, bool& is_v, int& j) {
+  if (dual) {
+    is_v = t & 1;
+    j = t >> 1;
+  } else if (t == 2 * T - 1) {
+    is_v = true;
+    j = T - 1;
+  } else if (t >= 2 && (t & 1) == 0) {
+    is_v = true;
+    j = (t - 2) >> 1;
+  } else {
+    is_v = false;
+    j = (t + 1) >> 1;
+  }
+}
+__device__ __forceinline__ int k_unit(int j, bool dual) {
+  return dual ? 2 * j : (j < 2 ? j : 2 * j - 1);
+}
+__device__ __forceinline__ int v_unit(int j, int T, bool dual) {
+  return dual ? 2 * j + 1 : (j == T - 1 ? 2 * T - 1 : 2 * j + 2);
+}
+
+// The page mask of a 32-key chunk from the tile's bad pages.
+template <int BS>
+__device__ __forceinline__ uint32_t bad32(uint32_t bad, int chunk) {
+  if constexpr (BS == 32) return ((bad >> chunk) & 1u) ? 0xFFFFFFFFu : 0u;
+  return (((bad >> (2 * chunk)) & 1u) ? 0x0000FFFFu : 0u) |
+         (((bad >> (2 * chunk + 1)) & 1u) ? 0xFFFF0000u : 0u);
+}
+
+// A raw unit widened to f16 in the swizzled operand layout (chunk-major
+// 128-byte rows) by 128 threads; rows whose `keep` bit is off become zeros.
+// Lanes take neighbouring 16-byte pieces of the raw rows, and the lanes of odd
+// chunks store their pieces in rotated order: no bank conflicts either way.
+template <int FMT, int D>
+__device__ __forceinline__ void widen_unit(uint32_t raw, uint32_t op, int warp, int lane,
+                                           const uint32_t (&keep)[4]) {
+  constexpr int kRow = FMT == PD_KV_FP8_E4M3 ? D : D / 2;
+  constexpr int kLanes = kRow / 16;       // lanes of a row
+  constexpr int kRows = 32 / kLanes;      // rows of a warp's step
+  constexpr int kElems = FMT == PD_KV_FP8_E4M3 ? 16 : 32;
+  constexpr int kP = kElems / 8;          // 16-byte f16 pieces of a lane
+  const int sub = lane % kLanes;
+  const int e0 = sub * kElems;
+  const int ch = e0 / 64;
+  const int p0 = (e0 % 64) / 8;
+#pragma unroll
+  for (int it = 0; it < 32 / kRows; ++it) {
+    const int row = warp * 32 + it * kRows + lane / kLanes;
+    uint4 w = lds128(raw + row * kRow + sub * 16);
+    uint32_t f[kP][4];
+    if constexpr (FMT == PD_KV_FP8_E4M3) {
+      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        f[k >> 1][2 * (k & 1)] = e4m3x2_f16x2(u[k] & 0xFFFFu);
+        f[k >> 1][2 * (k & 1) + 1] = e4m3x2_f16x2(u[k] >> 16);
+      }
+    } else {
+      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+      const uint32_t sc = raw + kTreeKT * kRow + row * (D / 16) + e0 / 16;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t s = lds_u8(sc + k / 2);
+        const uint32_t s2 = e4m3x2_f16x2(s | (s << 8));
+        uint32_t x[4];
+        e2m1x8_f16x2(u[k], x);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) f[k][q] = hmul2_u32(x[q], s2);
+      }
+    }
+    const bool on = (keep[warp] >> (row & 31)) & 1u;
+    const uint32_t dst = op + ch * (kTreeKT * 128);
+#pragma unroll
+    for (int k = 0; k < kP; ++k) {
+      const int kk = (ch & 1) ? (k + kP / 2) % kP : k;
+      uint32_t a = 0, b = 0, c = 0, d = 0;
+#pragma unroll
+      for (int q = 0; q < kP; ++q)
+        if (q == kk && on) {
+          a = f[q][0];
+          b = f[q][1];
+          c = f[q][2];
+          d = f[q][3];
+        }
+      sts128(dst + swz128(row * 128 + (p0 + kk) * 16), a, b, c, d);
+    }
+  }
+}
+
+template <int FMT, int D, int BS>
+__global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
+    tree_umma_kernel(const __grid_constant__ CUtensorMap tm_k,
+                     const __grid_constant__ CUtensorMap tm_v,
+                     const __grid_constant__ CUtensorMap tm_ks,
+                     const __grid_constant__ CUtensorMap tm_vs, const TreeArgs a,
+                     const TreeWork w) {
+  using C = TreeCfg<FMT, D, BS>;
+  constexpr bool kQuant = C::kQuant;
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int G = a.group;
+  const int TPG = 128 / G;  // nodes of one group's 128 rows
+  const int tid = threadIdx.x;
+  const int warp = tid >> 5;
+  const int lane = tid & 31;
+
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const uint32_t s0 = smem_u32(smem);
+  // (scratch where Q will be)
+  const Share share = make_share(a, 2 * TPG, kTreeKT, kTreeSlack, w.min_units,
+                                 reinterpret_cast<ShareScratch*>(smem));
+  if (tid == 0) w.records[blockIdx.x] = JoinRecord{0, 0, 0, 0};
+  if (share.b < 0) return;
+  if (s0 & 1023u) {  // the swizzled tiles need 1024-byte alignment: refuse, do not guess
+    if (tid == 0) atomicOr(a.flags, PD_DEV_BAD_SMEM);
+    return;
+  }
+
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
+  uint64_t* u_full = bars;
+  uint64_t* u_empty = u_full + C::kUnits;
+  uint64_t* r_full = u_empty + C::kUnits;
+  uint64_t* r_empty = r_full + C::kRaws;
+  uint64_t* s_full = r_empty + C::kRaws;
+  uint64_t* p_full = s_full + 2;
+  uint64_t* o_done = p_full + 2;
+  uint64_t* ml_full = o_done + 2;
+  uint64_t* q_full = ml_full + 2;
+  uint64_t* fin = q_full + 1;
+  uint32_t* bad_s = reinterpret_cast<uint32_t*>(smem + C::kBadOff);
+  float2* ml_s = reinterpret_cast<float2*>(smem + C::kMlOff);  // [2][128]
+  int* page_s = reinterpret_cast<int*>(smem + C::kPageOff);    // [4][kCopies]
+  uint32_t* holder = reinterpret_cast<uint32_t*>(smem + C::kHolderOff);
+  volatile int* abort_s = reinterpret_cast<volatile int*>(holder + 1);
+
+  if (tid == 0) {
+    for (int i = 0; i < C::kNumBars; ++i) {
+      const uint64_t* b = bars + i;
+      uint32_t count = 1;
+      if (kQuant && b >= u_full && b < u_full + C::kUnits) count = 4;      // widening warps
+      if (kQuant && b >= r_empty && b < r_empty + C::kRaws) count = 4;
+      if (b == p_full || b == p_full + 1 || b == ml_full || b == ml_full + 1) count = 4;
+      if (b == q_full) count = kTreeSoftWarps;
+      mbar_init(smem_u32(b), count);
+    }
+    *abort_s = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kTreeMma) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(holder)),
+                 "n"(kTreeTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *holder;
+  // S (and P) of group X at X * 128, O at 256 + X * D
+  const uint32_t unit_s = s0 + C::kUnitOff;
+  const uint32_t raw_s = s0 + C::kRawOff;
+  Walker walk(a, share, 2 * TPG, kTreeKT, kTreeSlack);
+  Piece q;
+  bool failed = false;
+  auto give_up = [&](bool say) {
+    if (say && *abort_s == 0) atomicOr(a.flags, PD_DEV_TIMEOUT);
+    *abort_s = 1;
+    failed = true;
+  };
+
+  if (warp == kTreeProd) {
+    // =========================== producer =================================
+    constexpr int kSlots = kQuant ? C::kRaws : C::kUnits;
+    uint64_t* full = kQuant ? r_full : u_full;
+    uint64_t* empty = kQuant ? r_empty : u_empty;
+    const int pool_rows = static_cast<int>(a.num_blocks * BS);
+    int u0 = 0;     // units of the pieces before
+    int issued = 0;
+    int tile0 = 0;  // tiles before this piece
+    while (!failed && walk.next(q)) {
+      if (lane == 0 && q.begins && !q.whole)
+        w.records[blockIdx.x] = JoinRecord{q.b, q.g, q.rt, walk.pieces_of_last(q.j1)};
+      const int nodes = min(2 * TPG, q.p.s.n - q.rt * 2 * TPG);
+      const bool dual = nodes > TPG;
+      const int T = q.j1 - q.j0;
+      const int32_t* bt = a.block_tables + static_cast<int64_t>(q.b) * a.max_blocks_per_seq;
+      // block-table entries [win, win + 32) and the 32 after them, one a lane
+      int win = -(1 << 30), cur = -1, nxt = -1;
+      auto load = [&](int e) { return e < a.max_blocks_per_seq ? bt[e] : -1; };
+      for (int t = 0; t < 2 * T; ++t) {
+        bool is_v;
+        int j;
+        unit_at(t, T, dual, is_v, j);
+        const int t0 = tile_key(q.p, q.j0 + j, kTreeKT);
+        const int tile = tile0 + j;
+        if (!is_v) {  // the tile's pages, once for K and V
+          const int first = t0 / BS;
+          if (first - win >= 32 && first - win < 64) {
+            win += 32;
+            cur = nxt;
+            nxt = load(win + 32 + lane);
+          } else if (first < win || first - win >= 64) {
+            win = first;
+            cur = load(win + lane);
+            nxt = load(win + 32 + lane);
+          }
+          // a tile's kCopies pages may cross from cur into nxt
+          const int at = first - win + lane;
+          const int ec = __shfl_sync(0xFFFFFFFFu, cur, at & 31);
+          int en = -1;
+          if (first - win + C::kCopies > 32) en = __shfl_sync(0xFFFFFFFFu, nxt, at & 31);
+          const int end = tile_end(q.p, q.j0 + j, kTreeKT, a.num_sinks);
+          int pg = -1;
+          bool bad = false;
+          if (lane < C::kCopies && t0 + lane * BS < end) {
+            pg = at < 32 ? ec : en;
+            if (pg < 0 || pg >= a.num_blocks) {
+              bad = true;
+              pg = -1;
+            }
+          }
+          const uint32_t bm = __ballot_sync(0xFFFFFFFFu, bad);
+          if (lane == 0) {
+            if (bm) atomicOr(a.flags, PD_DEV_BAD_PAGE);
+            bad_s[tile % kTreeBadRing] = bm;
+          }
+          if (lane < C::kCopies) page_s[(tile & 3) * C::kCopies + lane] = pg;
+          __syncwarp();
+        }
+        const int u = u0 + t;
+        const int slot = u % kSlots;
+        if (u >= kSlots && !warp_wait(smem_u32(&empty[slot]), ((u / kSlots) - 1) & 1, abort_s)) {
+          give_up(lane == 0);
+          break;
+        }
+        const uint32_t fb = smem_u32(&full[slot]);
+        const int* pages = page_s + (tile & 3) * C::kCopies;
+        const CUtensorMap* tm = is_v ? &tm_v : &tm_k;
+        if constexpr (FMT == PD_KV_BF16) {
+          if (lane == 0) mbar_arrive_expect_tx(fb, C::kUnitBytes);
+          __syncwarp();
+          if (lane < C::kCopies) {
+            const int pg = pages[lane];
+            const int z = pg >= 0 ? pg * BS : pool_rows;  // past the pool: zeros
+            const uint32_t dst = unit_s + slot * C::kUnitBytes + lane * (BS * 128);
+#pragma unroll
+            for (int ch = 0; ch < D / 64; ++ch)
+              tma_load_3d(dst + ch * (kTreeKT * 128), tm, ch * 64, q.g, z, fb);
+          }
+        } else if constexpr (FMT == PD_KV_FP8_E4M3) {
+          if (lane == 0) mbar_arrive_expect_tx(fb, C::kRawData);
+          __syncwarp();
+          if (lane < C::kCopies) {
+            const int pg = pages[lane];
+            const int z = pg >= 0 ? pg * BS : pool_rows;
+            tma_load_3d(raw_s + slot * C::kRawBytes + lane * (BS * D), tm, 0, q.g, z, fb);
+          }
+        } else if constexpr (BS == 16) {
+          // four gathers of four pages: codes and scales, two each
+          constexpr int kSlabWords = 16 * (D / 2) / 4, kScaleWords = 16 * (D / 16) / 4;
+          if (lane == 0) mbar_arrive_expect_tx(fb, C::kRawData + C::kRawScales);
+          __syncwarp();
+          if (lane < 4) {
+            const int h = (lane & 1) * 4;
+            const bool sc = lane >= 2;
+            const int oob = static_cast<int>(a.num_blocks);
+            int r[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) r[k] = pages[h + k] >= 0 ? pages[h + k] : oob;
+            const CUtensorMap* m = sc ? (is_v ? &tm_vs : &tm_ks) : tm;
+            const uint32_t dst = raw_s + slot * C::kRawBytes +
+                                 (sc ? C::kRawData + h * (16 * (D / 16)) : h * (16 * (D / 2)));
+            const int x = sc ? static_cast<int>(a.data_bytes / 4) + q.g * kScaleWords
+                             : q.g * kSlabWords;
+            tma_gather4(dst, m, x, r[0], r[1], r[2], r[3], fb);
+          }
+        } else {
+          constexpr uint32_t db = BS * (D / 2), sb = BS * (D / 16);
+          const uint32_t have = __ballot_sync(0xFFFFFFFFu, lane < C::kCopies && pages[lane % C::kCopies] >= 0);
+          if (lane == 0) mbar_arrive_expect_tx(fb, __popc(have) * (db + sb));
+          __syncwarp();
+          if (lane < C::kCopies && pages[lane] >= 0) {
+            const uint8_t* pg = (is_v ? a.v_cache : a.k_cache) + pages[lane] * a.page_bytes;
+            const int64_t line = static_cast<int64_t>(q.g) * BS;
+            const uint32_t dst = raw_s + slot * C::kRawBytes;
+            bulk_load(dst + lane * db, pg + line * (D / 2), db, fb);
+            bulk_load(dst + C::kRawData + lane * sb, pg + a.data_bytes + line * (D / 16), sb, fb);
+          }
+        }
+        __syncwarp();
+        ++issued;
+      }
+      u0 += 2 * T;
+      tile0 += T;
+    }
+    // every copy issued lands before the CTA can end
+    for (int u = max(0, issued - kSlots); u < issued; ++u)
+      (void)mbar_wait(smem_u32(&full[u % kSlots]), (u / kSlots) & 1);
+  } else if (warp == kTreeMma) {
+    // =========================== MMA issuer ===============================
+    if (lane == 0) {
+      constexpr uint32_t idS = kQuant ? umma_idesc_f16(128, kTreeKT, 0) : umma_idesc(128, kTreeKT, 0);
+      constexpr uint32_t idO = kQuant ? umma_idesc_f16(128, D, 1) : umma_idesc(128, D, 1);
+      const uint64_t dq0 = umma_desc(s0, 16, 1024);
+      const uint64_t dk0 = umma_desc(unit_s, 16, 1024);
+      const uint64_t dv0 = umma_desc(unit_s, kTreeKT * 128, 1024);
+      int u0 = 0, piece = 0;
+      int cs0 = 0, cs1 = 0;  // S tiles issued by group (its P, O counts follow)
+      bool ok = true;
+      auto wait = [&](const uint64_t* bar, int parity) {
+        return mbar_wait_or_abort(smem_u32(bar), parity & 1, abort_s);
+      };
+      while (ok && walk.next(q)) {
+        const int nodes = min(2 * TPG, q.p.s.n - q.rt * 2 * TPG);
+        const bool dual = nodes > TPG;
+        const int T = q.j1 - q.j0;
+        const int n0 = dual ? T : (T + 1) / 2, n1 = dual ? T : T / 2;
+        if (!(ok = wait(q_full, piece))) break;
+        tc_fence_after();
+        // S_X of its i-th tile
+        auto issue_s = [&](int X, int i) -> bool {
+          const int j = dual ? i : 2 * i + X;
+          const int u = u0 + k_unit(j, dual), slot = u % C::kUnits;
+          if (!wait(&u_full[slot], u / C::kUnits)) return false;
+          tc_fence_after();
+          const uint64_t qa = dq0 + static_cast<uint64_t>(dual && X ? C::kQBytes >> 4 : 0);
+          const uint64_t kb = dk0 + static_cast<uint64_t>((slot * C::kUnitBytes) >> 4);
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t off = ((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4;
+            umma_f16(tmem + X * 128, qa + off, kb + off, idS, ks > 0 ? 1u : 0u);
+          }
+          umma_commit(smem_u32(&s_full[X]));
+          if (!dual || X == 1) umma_commit(smem_u32(&u_empty[slot]));
+          if (X) ++cs1;
+          else ++cs0;
+          return true;
+        };
+        ok = issue_s(0, 0);
+        if (ok && n1 > 0) ok = issue_s(1, 0);
+        for (int i = 0; i < n0 && ok; ++i) {
+          for (int X = 0; X < 2; ++X) {
+            const int nX = X ? n1 : n0;
+            if (i >= nX) continue;
+            const int c = X ? cs1 : cs0;  // this tile is the group's c-th
+            const int j = dual ? i : 2 * i + X;
+            const int u = u0 + v_unit(j, T, dual), slot = u % C::kUnits;
+            if (!(ok = wait(&u_full[slot], u / C::kUnits) && wait(&p_full[X], c - 1))) break;
+            tc_fence_after();
+            const uint64_t vb = dv0 + static_cast<uint64_t>((slot * C::kUnitBytes) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < kTreeKT / 16; ++kk)
+              umma_f16_ts(tmem + 256 + X * D, tmem + X * 128 + kk * 8, vb + ((kk * 2048) >> 4), idO,
+                          (i > 0 || kk > 0) ? 1u : 0u);
+            umma_commit(smem_u32(&o_done[X]));
+            if (!dual || X == 1) umma_commit(smem_u32(&u_empty[slot]));
+            if (i + 1 < nX) {
+              // the next scores overwrite P: the product that reads it is done first
+              if (!(ok = wait(&o_done[X], c - 1))) break;
+              tc_fence_after();
+              if (!(ok = issue_s(X, i + 1))) break;
+            }
+          }
+        }
+        u0 += 2 * T;
+        ++piece;
+      }
+      if (!ok) give_up(true);
+      // every MMA issued has completed before TMEM is freed
+      umma_commit(smem_u32(fin));
+      (void)mbar_wait(smem_u32(fin), 0);
+    }
+    __syncwarp();
+  } else if (kQuant && warp >= kTreeConv) {
+    // =========================== widening warps ===========================
+    if constexpr (kQuant) {
+      const int cw = warp - kTreeConv;
+      int u0 = 0, tile0 = 0;
+      while (!failed && walk.next(q)) {
+        const int nodes = min(2 * TPG, q.p.s.n - q.rt * 2 * TPG);
+        const bool dual = nodes > TPG;
+        const int T = q.j1 - q.j0;
+        const RowView any = any_view(a, q.p.s, lane);
+        for (int t = 0; t < 2 * T; ++t) {
+          bool is_v;
+          int j;
+          unit_at(t, T, dual, is_v, j);
+          const int u = u0 + t;
+          const int rs = u % C::kRaws, us = u % C::kUnits;
+          if (!warp_wait(smem_u32(&r_full[rs]), (u / C::kRaws) & 1, abort_s) ||
+              (u >= C::kUnits &&
+               !warp_wait(smem_u32(&u_empty[us]), ((u / C::kUnits) - 1) & 1, abort_s))) {
+            give_up(lane == 0);
+            break;
+          }
+          const int t0 = tile_key(q.p, q.j0 + j, kTreeKT);
+          const uint32_t bad = bad_s[(tile0 + j) % kTreeBadRing];
+          uint32_t keep[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) keep[c] = seen32(any, t0 + 32 * c) & ~bad32<BS>(bad, c);
+          widen_unit<FMT, D>(raw_s + rs * C::kRawBytes, unit_s + us * C::kUnitBytes, cw, lane, keep);
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(smem_u32(&u_full[us]));
+            mbar_arrive(smem_u32(&r_empty[rs]));
+          }
+        }
+        u0 += 2 * T;
+        tile0 += T;
+      }
+    }
+  } else {
+    // =========================== softmax warps ============================
+    const int X = warp >> 2;
+    const int m = (warp & 3) * 32 + lane;  // row of the group's tile = TMEM lane
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_tm = tmem + lane_base + X * 128;
+    const uint32_t o_tm = tmem + lane_base + 256;  // + group * D
+    const float vmul = FMT == PD_KV_FP8_E4M3 ? a.v_scale : 1.0f;
+    int u0 = 0, tile0 = 0, piece = 0;
+    int c0 = 0, c1 = 0;  // tiles the groups have finished
+    while (!failed && walk.next(q)) {
+      const TreeSeq& s = q.p.s;
+      const int node0 = q.rt * 2 * TPG;
+      const int nodes = min(2 * TPG, s.n - node0);
+      const bool dual = nodes > TPG;
+      const int T = q.j1 - q.j0;
+      const int n0 = dual ? T : (T + 1) / 2, n1 = dual ? T : T / 2;
+      const int nX = X ? n1 : n0;
+      // ---- this row: node, head, what it sees ----
+      const int i = m / G + (dual ? X * TPG : 0);
+      const bool rvalid = m < TPG * G && i < nodes;
+      const RowView any = any_view(a, s, lane);
+      RowView view = any;
+      if (rvalid) view = row_view(a, s, node0 + i);
+      const int qh = q.g * G + m % G;
+      const int64_t qrow = static_cast<int64_t>(s.q0 + node0 + (rvalid ? i : 0));
+      // ---- Q into its tile (alternating groups: half a row each) ----
+      float sl2 = a.scale_log2 * (FMT == PD_KV_FP8_E4M3 ? a.k_scale : 1.0f);
+      {
+        const uint16_t* src = a.q + qrow * a.q_stride + static_cast<int64_t>(qh) * D;
+        const uint32_t q_s = s0 + (dual ? X * C::kQBytes : 0);
+        uint4 v[D / 8];
+#pragma unroll
+        for (int p = 0; p < D / 8; ++p)
+          v[p] = rvalid ? *reinterpret_cast<const uint4*>(src + p * 8) : make_uint4(0u, 0u, 0u, 0u);
+        if constexpr (kQuant) {
+          // f16 times a power of two: the row's largest |q| in [2^14, 2^15) (exact)
+          float mq = 0.0f;
+#pragma unroll
+          for (int p = 0; p < D / 8; ++p) {
+            const uint32_t x[4] = {v[p].x, v[p].y, v[p].z, v[p].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mq = fmaxf(mq, fmaxf(fabsf(bf16_lo(x[k])), fabsf(bf16_hi(x[k]))));
+          }
+          const float down = exp2i(14 - ilog2f(mq));
+          sl2 *= exp2i(ilog2f(mq) - 14);
+#pragma unroll
+          for (int p = 0; p < D / 8; ++p) {
+            uint32_t x[4] = {v[p].x, v[p].y, v[p].z, v[p].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[k] = pack_f16x2(bf16_lo(x[k]) * down, bf16_hi(x[k]) * down);
+            v[p] = make_uint4(x[0], x[1], x[2], x[3]);
+          }
+        }
+#pragma unroll
+        for (int p = 0; p < D / 8; ++p)
+          if (dual || (p < D / 16) == (X == 0))
+            sts128(q_s + (p / 8) * (128 * 128) + swz128(m * 128 + (p % 8) * 16), v[p].x, v[p].y,
+                   v[p].z, v[p].w);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(q_full));
+      }
+      // a padding row runs along as a full one against reference 0
+      float m_run = rvalid ? -INFINITY : 0.0f, l_run = 0.0f;
+      // warps whose 32 rows are all padding only keep the barriers going
+      const bool idle = !__any_sync(0xFFFFFFFFu, rvalid);
+      for (int jl = 0; jl < nX; ++jl) {
+        const int j = dual ? jl : 2 * jl + X;
+        const int t0 = tile_key(q.p, q.j0 + j, kTreeKT);
+        const int vu = u0 + v_unit(j, T, dual), vslot = vu % C::kUnits;
+        const int cnt = (X ? c1 : c0) + jl;
+        if (!warp_wait(smem_u32(&u_full[vslot]), (vu / C::kUnits) & 1, abort_s) ||
+            !warp_wait(smem_u32(&s_full[X]), cnt & 1, abort_s)) {
+          give_up(lane == 0);
+          break;
+        }
+        tc_fence_after();
+        const uint32_t bad = bad_s[(tile0 + j) % kTreeBadRing];
+        if constexpr (!kQuant) {
+          // V rows no node sees: zeros, by the group that uses the tile first
+          const uint32_t keep = seen32(any, t0 + (warp & 3) * 32) & ~bad32<BS>(bad, warp & 3);
+          if (keep != 0xFFFFFFFFu && (!dual || X == 0)) {
+            if (!((keep >> lane) & 1u)) {
+              const uint32_t vrow = unit_s + vslot * C::kUnitBytes;
+#pragma unroll
+              for (int p = 0; p < D / 8; ++p)
+                sts128(vrow + (p / 8) * (kTreeKT * 128) + swz128(m * 128 + (p % 8) * 16), 0u, 0u, 0u,
+                       0u);
+            }
+            fence_async_smem();
+          }
+        }
+        if (!idle) {
+          const bool full = !rvalid || (bad == 0u && t0 >= view.lo && t0 + kTreeKT <= view.prefix);
+          uint32_t pk[kTreeKT / 2];
+          float mn = m_run, alpha = 1.0f, sum = 0.0f;
+          bool redo = true;
+          uint32_t valid[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
+          auto pack = [](float x, float y) { return kQuant ? pack_f16x2(x, y) : pack_bf16x2(x, y); };
+          if (__all_sync(0xFFFFFFFFu, full && m_run != -INFINITY)) {
+            const float nref = -m_run;
+            float mx[2] = {-INFINITY, -INFINITY}, ls[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            uint32_t v[2][16];
+            tmem_ld16(s_tm, v[0]);
+#pragma unroll
+            for (int c = 0; c < kTreeKT / 16; ++c) {
+              tmem_wait_ld();
+              if (c + 1 < kTreeKT / 16) tmem_ld16(s_tm + (c + 1) * 16, v[(c + 1) & 1]);
+#pragma unroll
+              for (int k = 0; k < 16; k += 2) {
+                const float x = fmaf(__uint_as_float(v[c & 1][k]), sl2, nref);
+                const float y = fmaf(__uint_as_float(v[c & 1][k + 1]), sl2, nref);
+                mx[0] = fmaxf(mx[0], x);
+                mx[1] = fmaxf(mx[1], y);
+                const float px = ex2(x), py = ex2(y);
+                ls[(k >> 1) & 1] += px;
+                ls[2 + ((k >> 1) & 1)] += py;
+                pk[c * 8 + k / 2] = pack(px, py);
+              }
+            }
+            const float top = fmaxf(mx[0], mx[1]);  // above the reference
+            sum = (ls[0] + ls[1]) + (ls[2] + ls[3]);
+            redo = top > kTreeRescale;
+            if (redo) {
+              mn = m_run + top;
+              alpha = ex2(-top);
+            }
+          } else {
+            float mx = -INFINITY;
+            if (!full) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c) valid[c] = seen32(view, t0 + 32 * c) & ~bad32<BS>(bad, c);
+            }
+#pragma unroll
+            for (int c = 0; c < kTreeKT / 16; ++c) {
+              uint32_t v[16];
+              tmem_ld16(s_tm + c * 16, v);
+              tmem_wait_ld();
+              const uint32_t vw = valid[c / 2] >> ((c & 1) * 16);
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                if ((vw >> k) & 1u) mx = fmaxf(mx, __uint_as_float(v[k]) * sl2);
+            }
+            if (mx > m_run + kTreeRescale || m_run == -INFINITY) {
+              mn = rvalid ? mx : 0.0f;
+              alpha = m_run == -INFINITY ? 0.0f : ex2(m_run - mn);
+            }
+          }
+          if (__any_sync(0xFFFFFFFFu, redo)) {
+            // P against mn; a row that has seen nothing yet has no valid key
+            const float nref = mn == -INFINITY ? 0.0f : -mn;
+            float ls[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (int c = 0; c < kTreeKT / 16; ++c) {
+              uint32_t v[16];
+              tmem_ld16(s_tm + c * 16, v);
+              tmem_wait_ld();
+              const uint32_t vw = valid[c / 2] >> ((c & 1) * 16);
+#pragma unroll
+              for (int k = 0; k < 16; k += 2) {
+                const float px =
+                    ((vw >> k) & 1u) ? ex2(fmaf(__uint_as_float(v[k]), sl2, nref)) : 0.0f;
+                const float py =
+                    ((vw >> (k + 1)) & 1u) ? ex2(fmaf(__uint_as_float(v[k + 1]), sl2, nref)) : 0.0f;
+                ls[0] += px;
+                ls[1] += py;
+                pk[c * 8 + k / 2] = pack(px, py);
+              }
+            }
+            sum = ls[0] + ls[1];
+          }
+          l_run = l_run * alpha + sum;
+          m_run = mn;
+          // O against the new reference (the previous product is done: these
+          // scores were issued after it)
+          if (jl > 0 && __any_sync(0xFFFFFFFFu, alpha != 1.0f)) {
+#pragma unroll
+            for (int h = 0; h < D / 16; ++h) {
+              uint32_t v[16];
+              tmem_ld16(o_tm + X * D + h * 16, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha);
+              tmem_st16(o_tm + X * D + h * 16, v);
+            }
+          }
+          // P over the scores
+#pragma unroll
+          for (int c = 0; c < kTreeKT / 32; ++c) {
+            uint32_t v[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[k] = pk[c * 16 + k];
+            tmem_st16(s_tm + c * 16, v);
+          }
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&p_full[X]));
+      }
+      if (failed) break;
+      // ---- end of the piece: both groups' products, the other's (m, l) ----
+      c0 += n0;
+      c1 += n1;
+      ml_s[X * 128 + m] = make_float2(m_run, l_run);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ml_full[X]));
+      if (!warp_wait(smem_u32(&o_done[0]), (c0 - 1) & 1, abort_s) ||
+          (n1 > 0 && !warp_wait(smem_u32(&o_done[1]), (c1 - 1) & 1, abort_s)) ||
+          !warp_wait(smem_u32(&ml_full[1 - X]), piece & 1, abort_s)) {
+        give_up(lane == 0);
+        break;
+      }
+      tc_fence_after();
+      const bool both = !dual && n1 > 0;  // the other group holds tiles of the same rows
+      float f_own = 1.0f, f_other = 0.0f, M = m_run, L = l_run;
+      if (!dual) {
+        const float2 o = ml_s[(1 - X) * 128 + m];
+        M = fmaxf(m_run, o.x);
+        f_own = m_run == -INFINITY ? 0.0f : ex2(m_run - M);
+        f_other = o.x == -INFINITY ? 0.0f : ex2(o.x - M);
+        if (X == 1 && n1 == 0) f_own = 0.0f;
+        L = l_run * f_own + o.y * f_other;
+      }
+      const float f0 = X ? f_other : f_own, f1 = X ? f_own : f_other;
+      const int r = (dual ? X * TPG * G : 0) + m;  // row of the item
+      const float mul = q.whole ? vmul / fmaxf(L, 1e-20f) : vmul;
+      uint16_t* orow = a.out + qrow * a.out_stride + static_cast<int64_t>(qh) * D;
+      float* part = w.o + (static_cast<int64_t>(q.slot) * (D / 4) * w.rows + r) * 4;
+      const int cols = dual ? D : D / 2, col0 = dual ? 0 : X * (D / 2);
+      if (!idle) {
+        for (int cg = 0; cg < cols; cg += 16) {
+          uint32_t va[16], vb[16];
+          tmem_ld16(o_tm + (dual ? X * D : 0) + col0 + cg, va);
+          if (both) tmem_ld16(o_tm + D + col0 + cg, vb);
+          tmem_wait_ld();
+          float x[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            x[k] = __uint_as_float(va[k]) * (dual ? 1.0f : f0);
+            if (both) x[k] = fmaf(__uint_as_float(vb[k]), f1, x[k]);
+            x[k] *= mul;
+          }
+          if (rvalid) {
+            if (q.whole) {
+              uint32_t y[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) y[k] = pack_bf16x2(x[2 * k], x[2 * k + 1]);
+              uint4* dst = reinterpret_cast<uint4*>(orow + col0 + cg);
+              dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
+              dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                *reinterpret_cast<float4*>(part + static_cast<int64_t>((col0 + cg) / 4 + k) *
+                                                      w.rows * 4) =
+                    make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+            }
+          }
+        }
+        if (rvalid && !q.whole && (dual || X == 0))
+          w.ml[static_cast<int64_t>(q.slot) * w.rows + r] = make_float2(M, L);
+      }
+      tc_fence_before();
+      u0 += 2 * T;
+      tile0 += T;
+      ++piece;
+    }
+  }
+
+  // ---- free the TMEM columns once every warp is done with them ----
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kTreeMma) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "n"(kTreeTmemCols)
+                 : "memory");
+  }
+}
+
+// The items that were cut: out = sum_p O_p 2^(m_p - M) / sum_p l_p 2^(m_p - M),
+// the pieces in key order. A warp takes 4 rows x 32 head_dim columns, so that
+// partials are read and outputs written in whole 64-byte pieces.
+template <int D>
+__global__ void __launch_bounds__(256) tree_join_kernel(const TreeArgs a, const TreeWork w) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const JoinRecord rec = w.records[blockIdx.x];
+  if (rec.pieces == 0) return;
+  constexpr int kColBlocks = D / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int d4 = (blockIdx.y % kColBlocks) * 8 + (lane & 7);
+  const int r = (blockIdx.y / kColBlocks) * 32 + warp * 4 + (lane >> 3);
+  const int q0 = a.cu_q[rec.b], n = a.cu_q[rec.b + 1] - q0;
+  const int node = rec.rt * w.item_nodes + r / a.group;
+  if (r >= w.item_nodes * a.group || node >= n) return;
+  auto slot = [&](int p) {
+    return 2 * (static_cast<int64_t>(blockIdx.x) + p) + (p == 0 ? 1 : 0);
+  };
+  float M = -INFINITY;
+  for (int p = 0; p < rec.pieces; ++p) M = fmaxf(M, w.ml[slot(p) * w.rows + r].x);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.0f;
+#pragma unroll 4
+  for (int p = 0; p < rec.pieces; ++p) {
+    const float2 ml = w.ml[slot(p) * w.rows + r];
+    const float4 o = *reinterpret_cast<const float4*>(
+        w.o + ((slot(p) * (D / 4) + d4) * w.rows + r) * 4);
+    const float f = ml.x == -INFINITY ? 0.0f : ex2(ml.x - M);
+    l = fmaf(ml.y, f, l);
+    acc.x = fmaf(o.x, f, acc.x);
+    acc.y = fmaf(o.y, f, acc.y);
+    acc.z = fmaf(o.z, f, acc.z);
+    acc.w = fmaf(o.w, f, acc.w);
+  }
+  const float inv = 1.0f / fmaxf(l, 1e-20f);
+  const int qh = rec.g * a.group + r % a.group;
+  uint16_t* out = a.out + static_cast<int64_t>(q0 + node) * a.out_stride +
+                  static_cast<int64_t>(qh) * D + d4 * 4;
+  *reinterpret_cast<uint2*>(out) =
+      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+}
+
+template <class... A>
+cudaError_t launch_dependent(dim3 grid, int threads, int smem, cudaStream_t st, void (*kern)(A...),
+                             const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <int FMT, int D, int BS>
+cudaError_t launch_umma_cfg(const TreeArgs& a, const TreeWork& w, cudaStream_t st) {
+  using C = TreeCfg<FMT, D, BS>;
+  CUtensorMap tk, tv, tks, tvs;
+  std::memset(&tk, 0, sizeof(tk));
+  std::memset(&tv, 0, sizeof(tv));
+  std::memset(&tks, 0, sizeof(tks));
+  std::memset(&tvs, 0, sizeof(tvs));
+  const int64_t rows = a.num_blocks * BS;
+  if constexpr (FMT == PD_KV_NVFP4) {
+    if constexpr (BS == 16) {
+      constexpr int kSlab = 16 * (D / 2), kScales = 16 * (D / 16);
+      if (!encode_nvfp4_gather_map(&tk, a.k_cache, a.page_bytes, a.num_blocks, kSlab) ||
+          !encode_nvfp4_gather_map(&tv, a.v_cache, a.page_bytes, a.num_blocks, kSlab) ||
+          !encode_nvfp4_gather_map(&tks, a.k_cache, a.page_bytes, a.num_blocks, kScales) ||
+          !encode_nvfp4_gather_map(&tvs, a.v_cache, a.page_bytes, a.num_blocks, kScales))
+        return cudaErrorInvalidValue;
+    }
+  } else {
+    constexpr int kInner = FMT == PD_KV_BF16 ? 64 : D;
+    constexpr bool kSwz = FMT == PD_KV_BF16;
+    if (!encode_cache_map(&tk, a.k_cache, FMT, D, a.num_kv_heads, rows, kInner, BS, kSwz) ||
+        !encode_cache_map(&tv, a.v_cache, FMT, D, a.num_kv_heads, rows, kInner, BS, kSwz))
+      return cudaErrorInvalidValue;
+  }
+  auto kern = tree_umma_kernel<FMT, D, BS>;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  static bool attr_set[64] = {};  // per device; setting it twice is harmless
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!attr_set[dev]) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
+  }
+  e = launch_dependent(dim3(w.ctas), C::kThreads, C::kSmemBytes, st, kern, tk, tv, tks, tvs, a, w);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(w.ctas, (w.rows + 31) / 32 * (D / 32));
+  return launch_dependent(grid, 256, 0, st, tree_join_kernel<D>, a, w);
+}
+
+template <int FMT, int D>
+cudaError_t launch_umma_bs(const TreeArgs& a, const TreeWork& w, cudaStream_t st) {
+  return a.block_size == 16 ? launch_umma_cfg<FMT, D, 16>(a, w, st)
+                            : launch_umma_cfg<FMT, D, 32>(a, w, st);
+}
+
+template <int FMT>
+cudaError_t launch_umma_fmt(const TreeArgs& a, const TreeWork& w, int D, cudaStream_t st) {
+  return D == 64 ? launch_umma_bs<FMT, 64>(a, w, st) : launch_umma_bs<FMT, 128>(a, w, st);
+}
+
+}  // namespace
+
+size_t tree_umma_workspace(int max_q_len, int group, int head_dim, int num_sms, TreeWork* w,
+                           void* workspace) {
+  const int item_nodes = 2 * (128 / group);
+  const int nodes = max_q_len < item_nodes ? (max_q_len < 1 ? 1 : max_q_len) : item_nodes;
+  const int rows = (nodes * group + 7) / 8 * 8;
+  const WorkLayout l = work_layout(num_sms, rows, head_dim);
+  if (w) {
+    uint8_t* p = static_cast<uint8_t*>(workspace);
+    w->records = reinterpret_cast<JoinRecord*>(p);
+    w->ml = reinterpret_cast<float2*>(p + l.ml);
+    w->o = reinterpret_cast<float*>(p + l.o);
+    w->ctas = num_sms;
+    w->rows = rows;
+    w->item_nodes = item_nodes;
+    w->min_units = 1;
+  }
+  return l.bytes;
+}
+
+cudaError_t launch_tree_umma(const TreeArgs& a, const TreeWork& w, int head_dim, int kv_dtype,
+                             cudaStream_t st) {
+  switch (kv_dtype) {
+    case PD_KV_BF16: return launch_umma_fmt<PD_KV_BF16>(a, w, head_dim, st);
+    case PD_KV_FP8_E4M3: return launch_umma_fmt<PD_KV_FP8_E4M3>(a, w, head_dim, st);
+    default: return launch_umma_fmt<PD_KV_NVFP4>(a, w, head_dim, st);
+  }
+}
+
+}  // namespace pd
