@@ -50,14 +50,19 @@ constexpr int kTreeSlack = 1;         // units a piece costs beside its tiles
 constexpr int kTreeSoftWarps = 8;
 constexpr int kTreeProd = 8;
 constexpr int kTreeMma = 9;
-constexpr int kTreeConv = 10;         // warps 10..13 widen quantised units
+constexpr int kTreeConv = 12;         // warps 12..15 widen quantised units
 constexpr int kTreeTmemCols = 512;
 constexpr int kTreeBadRing = 32;      // tiles whose page masks are kept
 
 template <int FMT, int D, int BS>
 struct TreeCfg {
   static constexpr bool kQuant = FMT != PD_KV_BF16;
-  static constexpr int kThreads = (kQuant ? 14 : 10) * 32;
+  // whole warpgroups, since registers are dealt by warpgroup: the softmax
+  // threads hold a row's P, the other warps give theirs up (the launch has
+  // 64512 registers with 384 threads of 168, 65536 with 512 of 128)
+  static constexpr int kThreads = kQuant ? 512 : 384;
+  static constexpr int kSoftRegs = kQuant ? 176 : 208;
+  static constexpr int kOtherRegs = kQuant ? 80 : 88;
   static constexpr int kCopies = kTreeKT / BS;            // pages of a tile
   static constexpr int kQBytes = 128 * D * 2;             // one Q tile, chunk-major
   static constexpr int kUnitBytes = kTreeKT * D * 2;      // one 16-bit K or V unit, chunk-major
@@ -116,61 +121,67 @@ __device__ __forceinline__ uint32_t bad32(uint32_t bad, int chunk) {
 }
 
 // A raw unit widened to f16 in the swizzled operand layout (chunk-major
-// 128-byte rows) by 128 threads; rows whose `keep` bit is off become zeros.
+// 128-byte rows) by four warps of 32 rows; rows whose `keep` bit is off become zeros.
 // Lanes take neighbouring 16-byte pieces of the raw rows, and the lanes of odd
 // chunks store their pieces in rotated order: no bank conflicts either way.
 template <int FMT, int D>
 __device__ __forceinline__ void widen_unit(uint32_t raw, uint32_t op, int warp, int lane,
-                                           const uint32_t (&keep)[4]) {
+                                           uint32_t keep) {
   constexpr int kRow = FMT == PD_KV_FP8_E4M3 ? D : D / 2;
   constexpr int kLanes = kRow / 16;       // lanes of a row
   constexpr int kRows = 32 / kLanes;      // rows of a warp's step
   constexpr int kElems = FMT == PD_KV_FP8_E4M3 ? 16 : 32;
   constexpr int kP = kElems / 8;          // 16-byte f16 pieces of a lane
+  constexpr int kSteps = 32 / kRows;
   const int sub = lane % kLanes;
   const int e0 = sub * kElems;
   const int ch = e0 / 64;
   const int p0 = (e0 % 64) / 8;
+  const int turn = (ch & 1) ? kP / 2 : 0;
+  const int row0 = warp * 32 + lane / kLanes;
+  uint4 w[kSteps];
+  uint32_t sc[kSteps];
 #pragma unroll
-  for (int it = 0; it < 32 / kRows; ++it) {
-    const int row = warp * 32 + it * kRows + lane / kLanes;
-    uint4 w = lds128(raw + row * kRow + sub * 16);
+  for (int it = 0; it < kSteps; ++it) {
+    const int row = row0 + it * kRows;
+    w[it] = lds128(raw + row * kRow + sub * 16);
+    if constexpr (FMT == PD_KV_NVFP4) {
+      uint32_t s;
+      asm volatile("ld.shared.u16 %0, [%1];" : "=r"(s) : "r"(raw + kTreeKT * kRow + row * (D / 16) + e0 / 16));
+      sc[it] = s;
+    }
+  }
+#pragma unroll
+  for (int it = 0; it < kSteps; ++it) {
+    const int row = row0 + it * kRows;
+    const bool on = (keep >> (row & 31)) & 1u;
+    const uint32_t u[4] = {on ? w[it].x : 0u, on ? w[it].y : 0u, on ? w[it].z : 0u,
+                           on ? w[it].w : 0u};
     uint32_t f[kP][4];
     if constexpr (FMT == PD_KV_FP8_E4M3) {
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         f[k >> 1][2 * (k & 1)] = e4m3x2_f16x2(u[k] & 0xFFFFu);
         f[k >> 1][2 * (k & 1) + 1] = e4m3x2_f16x2(u[k] >> 16);
       }
     } else {
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-      const uint32_t sc = raw + kTreeKT * kRow + row * (D / 16) + e0 / 16;
+      const uint32_t both = e4m3x2_f16x2(on ? sc[it] : 0u);  // the two groups' scales
+      const uint32_t s2[2] = {__byte_perm(both, both, 0x1010), __byte_perm(both, both, 0x3232)};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const uint32_t s = lds_u8(sc + k / 2);
-        const uint32_t s2 = e4m3x2_f16x2(s | (s << 8));
         uint32_t x[4];
         e2m1x8_f16x2(u[k], x);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) f[k][q] = hmul2_u32(x[q], s2);
+        for (int q = 0; q < 4; ++q) f[k][q] = hmul2_u32(x[q], s2[k >> 1]);
       }
     }
-    const bool on = (keep[warp] >> (row & 31)) & 1u;
     const uint32_t dst = op + ch * (kTreeKT * 128);
 #pragma unroll
-    for (int k = 0; k < kP; ++k) {
-      const int kk = (ch & 1) ? (k + kP / 2) % kP : k;
-      uint32_t a = 0, b = 0, c = 0, d = 0;
-#pragma unroll
-      for (int q = 0; q < kP; ++q)
-        if (q == kk && on) {
-          a = f[q][0];
-          b = f[q][1];
-          c = f[q][2];
-          d = f[q][3];
-        }
-      sts128(dst + swz128(row * 128 + (p0 + kk) * 16), a, b, c, d);
+    for (int k = 0; k < kP; ++k) {  // lanes of odd chunks begin half way round
+      const int kr = (k + kP / 2) % kP;
+      const bool r = turn != 0;
+      sts128(dst + swz128(row * 128 + (p0 + (r ? kr : k)) * 16), r ? f[kr][0] : f[k][0],
+             r ? f[kr][1] : f[k][1], r ? f[kr][2] : f[k][2], r ? f[kr][3] : f[k][3]);
     }
   }
 }
@@ -259,6 +270,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
 
   if (warp == kTreeProd) {
     // =========================== producer =================================
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
     constexpr int kSlots = kQuant ? C::kRaws : C::kUnits;
     uint64_t* full = kQuant ? r_full : u_full;
     uint64_t* empty = kQuant ? r_empty : u_empty;
@@ -387,6 +399,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
       (void)mbar_wait(smem_u32(&full[u % kSlots]), (u / kSlots) & 1);
   } else if (warp == kTreeMma) {
     // =========================== MMA issuer ===============================
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
     if (lane == 0) {
       constexpr uint32_t idS = kQuant ? umma_idesc_f16(128, kTreeKT, 0) : umma_idesc(128, kTreeKT, 0);
       constexpr uint32_t idO = kQuant ? umma_idesc_f16(128, D, 1) : umma_idesc(128, D, 1);
@@ -462,6 +475,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
     __syncwarp();
   } else if (kQuant && warp >= kTreeConv) {
     // =========================== widening warps ===========================
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
     if constexpr (kQuant) {
       const int cw = warp - kTreeConv;
       int u0 = 0, tile0 = 0;
@@ -484,9 +498,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
           }
           const int t0 = tile_key(q.p, q.j0 + j, kTreeKT);
           const uint32_t bad = bad_s[(tile0 + j) % kTreeBadRing];
-          uint32_t keep[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) keep[c] = seen32(any, t0 + 32 * c) & ~bad32<BS>(bad, c);
+          const uint32_t keep = seen32(any, t0 + 32 * cw) & ~bad32<BS>(bad, cw);
           widen_unit<FMT, D>(raw_s + rs * C::kRawBytes, unit_s + us * C::kUnitBytes, cw, lane, keep);
           fence_async_smem();
           __syncwarp();
@@ -499,8 +511,9 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
         tile0 += T;
       }
     }
-  } else {
+  } else if (warp < kTreeSoftWarps) {
     // =========================== softmax warps ============================
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftRegs));
     const int X = warp >> 2;
     const int m = (warp & 3) * 32 + lane;  // row of the group's tile = TMEM lane
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -768,6 +781,8 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
       tile0 += T;
       ++piece;
     }
+  } else {  // completes its warpgroup
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
   }
 
   // ---- free the TMEM columns once every warp is done with them ----
