@@ -48,8 +48,10 @@ constexpr float kTreeRescale = 8.0f;  // P <= 2^8 between moves of the reference
 constexpr int kTreeKT = 128;          // keys of a tile
 constexpr int kTreeSlack = 1;         // units a piece costs beside its tiles
 constexpr int kTreeSoftWarps = 8;
-constexpr int kTreeProd = 8;
+constexpr int kTreeProd = 8;          // and 10: the copies, alternate units
 constexpr int kTreeMma = 9;
+constexpr int kTreeProd2 = 10;
+constexpr int kTreeQ = 11;            // the next piece's q rows and what they see
 constexpr int kTreeConv = 12;         // warps 12..15 widen quantised units
 constexpr int kTreeTmemCols = 512;
 constexpr int kTreeBadRing = 32;      // tiles whose page masks are kept
@@ -77,12 +79,14 @@ struct TreeCfg {
   static constexpr int kRawOff = kUnitOff + kUnits * kUnitBytes;
   static constexpr int kBarOff = kRawOff + kRaws * kRawBytes;
   // unit full / empty, raw full / empty, s_full[2], p_full[2], o_done[2],
-  // ml_full[2], q_full, fin
-  static constexpr int kNumBars = 2 * kUnits + 2 * kRaws + 10;
-  static constexpr int kBadOff = kBarOff + kNumBars * 8;
-  static constexpr int kMlOff = kBadOff + kTreeBadRing * 4;
-  static constexpr int kPageOff = kMlOff + 2 * 128 * 8;
-  static constexpr int kHolderOff = kPageOff + 4 * kCopies * 4;  // pages of the last four tiles
+  // ml_full[2], q_full[2], q_empty[2], v_empty, o_free, q_raw, fin
+  static constexpr int kNumBars = 2 * kUnits + 2 * kRaws + 16;
+  // what the piece's nodes see: bits[64], lo[64], any node's bits and lo; the
+  // rows' score multipliers [256]; page masks
+  static constexpr int kViewOff = kBarOff + (kNumBars + 1) / 2 * 16;
+  static constexpr int kMulOff = kViewOff + 64 * 12 + 16;
+  static constexpr int kBadOff = kMulOff + 256 * 4;
+  static constexpr int kHolderOff = kBadOff + kTreeBadRing * 4;
   static constexpr int kSmemBytes = kHolderOff + 16;
   static_assert(kUnitBytes % 1024 == 0 && kRawBytes % 1024 == 0, "aligned tiles");
   static_assert(kSmemBytes <= 227 * 1024, "one CTA's shared memory");
@@ -191,7 +195,8 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
     tree_umma_kernel(const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v,
                      const __grid_constant__ CUtensorMap tm_ks,
-                     const __grid_constant__ CUtensorMap tm_vs, const TreeArgs a,
+                     const __grid_constant__ CUtensorMap tm_vs,
+                     const __grid_constant__ CUtensorMap tm_q, const TreeArgs a,
                      const TreeWork w) {
   using C = TreeCfg<FMT, D, BS>;
   constexpr bool kQuant = C::kQuant;
@@ -225,10 +230,15 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
   uint64_t* o_done = p_full + 2;
   uint64_t* ml_full = o_done + 2;
   uint64_t* q_full = ml_full + 2;
-  uint64_t* fin = q_full + 1;
+  uint64_t* q_empty = q_full + 2;
+  uint64_t* v_empty = q_empty + 2;
+  uint64_t* o_free = v_empty + 1;
+  uint64_t* q_raw = o_free + 1;
+  uint64_t* fin = q_raw + 1;
+  uint64_t* bits_s = reinterpret_cast<uint64_t*>(smem + C::kViewOff);  // [64], [64]: any node
+  int* lo_s = reinterpret_cast<int*>(bits_s + 65);                     // [64], [64]: any node
+  float* mul_s = reinterpret_cast<float*>(smem + C::kMulOff);          // [256]
   uint32_t* bad_s = reinterpret_cast<uint32_t*>(smem + C::kBadOff);
-  float2* ml_s = reinterpret_cast<float2*>(smem + C::kMlOff);  // [2][128]
-  int* page_s = reinterpret_cast<int*>(smem + C::kPageOff);    // [4][kCopies]
   uint32_t* holder = reinterpret_cast<uint32_t*>(smem + C::kHolderOff);
   volatile int* abort_s = reinterpret_cast<volatile int*>(holder + 1);
 
@@ -239,7 +249,8 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
       if (kQuant && b >= u_full && b < u_full + C::kUnits) count = 4;      // widening warps
       if (kQuant && b >= r_empty && b < r_empty + C::kRaws) count = 4;
       if (b == p_full || b == p_full + 1 || b == ml_full || b == ml_full + 1) count = 4;
-      if (b == q_full) count = kTreeSoftWarps;
+      if (b >= q_empty && b <= o_free) count = kTreeSoftWarps;
+      if (!kQuant && (b == q_full || b == q_full + 1)) count = 2;  // the copy, what rows see
       mbar_init(smem_u32(b), count);
     }
     *abort_s = 0;
@@ -256,7 +267,9 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *holder;
-  // S (and P) of group X at X * 128, O at 256 + X * D
+  // S (and P) of group X at X * 128, O at 256 + X * D. Q: two tiles; while no
+  // piece has more than 128 rows they are two buffers, piece by piece
+  const int nbuf = w.rows <= 128 ? 2 : 1;
   const uint32_t unit_s = s0 + C::kUnitOff;
   const uint32_t raw_s = s0 + C::kRawOff;
   Walker walk(a, share, 2 * TPG, kTreeKT, kTreeSlack);
@@ -268,66 +281,58 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
     failed = true;
   };
 
-  if (warp == kTreeProd) {
-    // =========================== producer =================================
+  if (warp == kTreeProd || warp == kTreeProd2) {
+    // =========================== producers ================================
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
     constexpr int kSlots = kQuant ? C::kRaws : C::kUnits;
     uint64_t* full = kQuant ? r_full : u_full;
     uint64_t* empty = kQuant ? r_empty : u_empty;
     const int pool_rows = static_cast<int>(a.num_blocks * BS);
-    int u0 = 0;     // units of the pieces before
-    int issued = 0;
-    int tile0 = 0;  // tiles before this piece
+    const int mine = warp == kTreeProd2 ? 1 : 0;
+    if (lane == 0) {
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_v)) : "memory");
+    }
+    int u0 = 0;        // units of the pieces before (even: a piece has 2 T)
+    int tile0 = 0;     // tiles before
+    int last = -1;     // last unit issued here
     while (!failed && walk.next(q)) {
-      if (lane == 0 && q.begins && !q.whole)
+      if (lane == 0 && mine == 0 && q.begins && !q.whole)
         w.records[blockIdx.x] = JoinRecord{q.b, q.g, q.rt, walk.pieces_of_last(q.j1)};
       const int nodes = min(2 * TPG, q.p.s.n - q.rt * 2 * TPG);
       const bool dual = nodes > TPG;
       const int T = q.j1 - q.j0;
       const int32_t* bt = a.block_tables + static_cast<int64_t>(q.b) * a.max_blocks_per_seq;
-      // block-table entries [win, win + 32) and the 32 after them, one a lane
+      // block-table entries [win, win + 32) and the 32 after them, one a lane; units
+      // go back by two tiles at most, so the window moves on three quarters in
       int win = -(1 << 30), cur = -1, nxt = -1;
       auto load = [&](int e) { return e < a.max_blocks_per_seq ? bt[e] : -1; };
-      for (int t = 0; t < 2 * T; ++t) {
+      for (int t = mine; t < 2 * T; t += 2) {
         bool is_v;
         int j;
         unit_at(t, T, dual, is_v, j);
         const int t0 = tile_key(q.p, q.j0 + j, kTreeKT);
-        const int tile = tile0 + j;
-        if (!is_v) {  // the tile's pages, once for K and V
-          const int first = t0 / BS;
-          if (first - win >= 32 && first - win < 64) {
-            win += 32;
-            cur = nxt;
-            nxt = load(win + 32 + lane);
-          } else if (first < win || first - win >= 64) {
-            win = first;
-            cur = load(win + lane);
-            nxt = load(win + 32 + lane);
-          }
-          // a tile's kCopies pages may cross from cur into nxt
-          const int at = first - win + lane;
-          const int ec = __shfl_sync(0xFFFFFFFFu, cur, at & 31);
-          int en = -1;
-          if (first - win + C::kCopies > 32) en = __shfl_sync(0xFFFFFFFFu, nxt, at & 31);
-          const int end = tile_end(q.p, q.j0 + j, kTreeKT, a.num_sinks);
-          int pg = -1;
-          bool bad = false;
-          if (lane < C::kCopies && t0 + lane * BS < end) {
-            pg = at < 32 ? ec : en;
-            if (pg < 0 || pg >= a.num_blocks) {
-              bad = true;
-              pg = -1;
-            }
-          }
-          const uint32_t bm = __ballot_sync(0xFFFFFFFFu, bad);
-          if (lane == 0) {
-            if (bm) atomicOr(a.flags, PD_DEV_BAD_PAGE);
-            bad_s[tile % kTreeBadRing] = bm;
-          }
-          if (lane < C::kCopies) page_s[(tile & 3) * C::kCopies + lane] = pg;
-          __syncwarp();
+        const int first = t0 / BS;
+        if (first < win || first - win >= 64) {
+          win = first;
+          cur = load(win + lane);
+          nxt = load(win + 32 + lane);
+        } else if (first - win >= 48) {
+          win += 32;
+          cur = nxt;
+          nxt = load(win + 32 + lane);
         }
+        const int at = first - win + lane;
+        int pg = __shfl_sync(0xFFFFFFFFu, cur, at & 31);
+        if (first - win + C::kCopies > 32) {
+          const int far = __shfl_sync(0xFFFFFFFFu, nxt, at & 31);
+          if (at >= 32) pg = far;
+        }
+        const bool in = lane < C::kCopies &&
+                        t0 + lane * BS < tile_end(q.p, q.j0 + j, kTreeKT, a.num_sinks);
+        const bool ok_page = in && pg >= 0 && pg < a.num_blocks;
+        const uint32_t bad = __ballot_sync(0xFFFFFFFFu, in && !ok_page);
+        if (!ok_page) pg = -1;
         const int u = u0 + t;
         const int slot = u % kSlots;
         if (u >= kSlots && !warp_wait(smem_u32(&empty[slot]), ((u / kSlots) - 1) & 1, abort_s)) {
@@ -335,68 +340,164 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
           break;
         }
         const uint32_t fb = smem_u32(&full[slot]);
-        const int* pages = page_s + (tile & 3) * C::kCopies;
         const CUtensorMap* tm = is_v ? &tm_v : &tm_k;
-        if constexpr (FMT == PD_KV_BF16) {
-          if (lane == 0) mbar_arrive_expect_tx(fb, C::kUnitBytes);
-          __syncwarp();
-          if (lane < C::kCopies) {
-            const int pg = pages[lane];
-            const int z = pg >= 0 ? pg * BS : pool_rows;  // past the pool: zeros
-            const uint32_t dst = unit_s + slot * C::kUnitBytes + lane * (BS * 128);
+        if (lane == 0) {
+          if (bad) atomicOr(a.flags, PD_DEV_BAD_PAGE);
+          bad_s[(tile0 + j) % kTreeBadRing] = bad;  // K and V of a tile: the same word
+        }
+        // one lane issues all copies: a copy a lane would be issued one after
+        // another all the same, with a loop over the lanes around it
+        if constexpr (FMT != PD_KV_NVFP4) {
+          // pages that are not read land as zeros, from past the pool
+          const int z = pg >= 0 ? pg * BS : pool_rows;
+          int zs[C::kCopies];
 #pragma unroll
-            for (int ch = 0; ch < D / 64; ++ch)
-              tma_load_3d(dst + ch * (kTreeKT * 128), tm, ch * 64, q.g, z, fb);
-          }
-        } else if constexpr (FMT == PD_KV_FP8_E4M3) {
-          if (lane == 0) mbar_arrive_expect_tx(fb, C::kRawData);
-          __syncwarp();
-          if (lane < C::kCopies) {
-            const int pg = pages[lane];
-            const int z = pg >= 0 ? pg * BS : pool_rows;
-            tma_load_3d(raw_s + slot * C::kRawBytes + lane * (BS * D), tm, 0, q.g, z, fb);
+          for (int k = 0; k < C::kCopies; ++k) zs[k] = __shfl_sync(0xFFFFFFFFu, z, k);
+          if (lane == 0) {
+            if constexpr (FMT == PD_KV_BF16) {
+              mbar_arrive_expect_tx(fb, C::kUnitBytes);
+              const uint32_t dst = unit_s + slot * C::kUnitBytes;
+#pragma unroll
+              for (int k = 0; k < C::kCopies; ++k)
+#pragma unroll
+                for (int ch = 0; ch < D / 64; ++ch)
+                  tma_load_3d(dst + ch * (kTreeKT * 128) + k * (BS * 128), tm, ch * 64, q.g, zs[k],
+                              fb);
+            } else {
+              mbar_arrive_expect_tx(fb, C::kRawData);
+              const uint32_t dst = raw_s + slot * C::kRawBytes;
+#pragma unroll
+              for (int k = 0; k < C::kCopies; ++k) tma_load_3d(dst + k * (BS * D), tm, 0, q.g, zs[k], fb);
+            }
           }
         } else if constexpr (BS == 16) {
-          // four gathers of four pages: codes and scales, two each
+          // gathers of four pages, their codes and their scales
           constexpr int kSlabWords = 16 * (D / 2) / 4, kScaleWords = 16 * (D / 16) / 4;
-          if (lane == 0) mbar_arrive_expect_tx(fb, C::kRawData + C::kRawScales);
-          __syncwarp();
-          if (lane < 4) {
-            const int h = (lane & 1) * 4;
-            const bool sc = lane >= 2;
-            const int oob = static_cast<int>(a.num_blocks);
-            int r[4];
+          const int z = pg >= 0 ? pg : static_cast<int>(a.num_blocks);
+          int zs[C::kCopies];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) r[k] = pages[h + k] >= 0 ? pages[h + k] : oob;
-            const CUtensorMap* m = sc ? (is_v ? &tm_vs : &tm_ks) : tm;
-            const uint32_t dst = raw_s + slot * C::kRawBytes +
-                                 (sc ? C::kRawData + h * (16 * (D / 16)) : h * (16 * (D / 2)));
-            const int x = sc ? static_cast<int>(a.data_bytes / 4) + q.g * kScaleWords
-                             : q.g * kSlabWords;
-            tma_gather4(dst, m, x, r[0], r[1], r[2], r[3], fb);
+          for (int k = 0; k < C::kCopies; ++k) zs[k] = __shfl_sync(0xFFFFFFFFu, z, k);
+          if (lane == 0) {
+            mbar_arrive_expect_tx(fb, C::kRawData + C::kRawScales);
+            const CUtensorMap* ts = is_v ? &tm_vs : &tm_ks;
+            const uint32_t dst = raw_s + slot * C::kRawBytes;
+            const int x = static_cast<int>(a.data_bytes / 4) + q.g * kScaleWords;
+#pragma unroll
+            for (int h = 0; h < C::kCopies; h += 4) {
+              tma_gather4(dst + h * (16 * (D / 2)), tm, q.g * kSlabWords, zs[h], zs[h + 1],
+                          zs[h + 2], zs[h + 3], fb);
+              tma_gather4(dst + C::kRawData + h * (16 * (D / 16)), ts, x, zs[h], zs[h + 1],
+                          zs[h + 2], zs[h + 3], fb);
+            }
           }
         } else {
           constexpr uint32_t db = BS * (D / 2), sb = BS * (D / 16);
-          const uint32_t have = __ballot_sync(0xFFFFFFFFu, lane < C::kCopies && pages[lane % C::kCopies] >= 0);
+          const uint32_t have = __ballot_sync(0xFFFFFFFFu, pg >= 0);
           if (lane == 0) mbar_arrive_expect_tx(fb, __popc(have) * (db + sb));
           __syncwarp();
-          if (lane < C::kCopies && pages[lane] >= 0) {
-            const uint8_t* pg = (is_v ? a.v_cache : a.k_cache) + pages[lane] * a.page_bytes;
+          if (pg >= 0) {
+            const uint8_t* src = (is_v ? a.v_cache : a.k_cache) + pg * a.page_bytes;
             const int64_t line = static_cast<int64_t>(q.g) * BS;
             const uint32_t dst = raw_s + slot * C::kRawBytes;
-            bulk_load(dst + lane * db, pg + line * (D / 2), db, fb);
-            bulk_load(dst + C::kRawData + lane * sb, pg + a.data_bytes + line * (D / 16), sb, fb);
+            bulk_load(dst + lane * db, src + line * (D / 2), db, fb);
+            bulk_load(dst + C::kRawData + lane * sb, src + a.data_bytes + line * (D / 16), sb, fb);
           }
         }
         __syncwarp();
-        ++issued;
+        last = u;
       }
       u0 += 2 * T;
       tile0 += T;
     }
     // every copy issued lands before the CTA can end
-    for (int u = max(0, issued - kSlots); u < issued; ++u)
-      (void)mbar_wait(smem_u32(&full[u % kSlots]), (u / kSlots) & 1);
+    // (a slot's last unit only: an earlier phase could not be told from a later)
+    const int end = failed ? last + 1 : u0;
+    for (int u = end - 1; u >= 0 && u >= end - kSlots; --u)
+      if ((u & 1) == mine) (void)mbar_wait(smem_u32(&full[u % kSlots]), (u / kSlots) & 1);
+  } else if (warp == kTreeQ) {
+    // =========================== q rows ===================================
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
+    int piece = 0;
+    while (!failed && walk.next(q)) {
+      const TreeSeq& s = q.p.s;
+      const int node0 = q.rt * 2 * TPG;
+      const int nodes = min(2 * TPG, s.n - node0);
+      const int rows = nodes * G;
+      const int buf = piece % nbuf;
+      const bool dual = nodes > TPG;
+      if (piece >= nbuf &&
+          !warp_wait(smem_u32(&q_empty[buf]), (piece / nbuf - 1) & 1, abort_s)) {
+        give_up(lane == 0);
+        break;
+      }
+      // one box a chunk: TPG tokens of G heads, rows in (node, head) order
+      const uint32_t q_bar = smem_u32(kQuant ? q_raw : &q_full[buf]);
+      if (lane == 0) {
+        mbar_arrive_expect_tx(q_bar, (dual ? 2 : 1) * static_cast<uint32_t>(TPG * G * D * 2));
+        for (int x = 0; x < (dual ? 2 : 1); ++x)
+#pragma unroll
+          for (int ch = 0; ch < D / 64; ++ch)
+            tma_load_3d(s0 + (buf + x) * C::kQBytes + ch * (128 * 128), &tm_q, ch * 64, q.g * G,
+                        s.q0 + node0 + x * TPG, q_bar);
+      }
+      const RowView any = any_view(a, s, lane);
+      RowView v[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (lane + 32 * k < nodes) v[k] = row_view(a, s, node0 + lane + 32 * k);
+      if (piece > 0 && !warp_wait(smem_u32(v_empty), (piece - 1) & 1, abort_s)) {
+        give_up(lane == 0);
+        break;
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (lane + 32 * k < nodes) {
+          bits_s[lane + 32 * k] = v[k].bits;
+          lo_s[lane + 32 * k] = v[k].lo;
+        }
+      if (lane == 0) {
+        bits_s[64] = any.bits;
+        lo_s[64] = any.lo;
+      }
+      if constexpr (kQuant) {
+        // bf16 rows to f16 times a power of two, in place, a lane a row: the row's
+        // largest |q| into [2^14, 2^15) (exact: f16 holds bf16's 8 bits)
+        if (!warp_wait(q_bar, piece & 1, abort_s)) {
+          give_up(lane == 0);
+          break;
+        }
+        const float mul = a.scale_log2 * (FMT == PD_KV_FP8_E4M3 ? a.k_scale : 1.0f);
+        for (int r = lane; r < rows; r += 32) {
+          const bool second = r >= TPG * G;
+          const int m = second ? r - TPG * G : r;
+          const uint32_t tile = s0 + (buf + (second ? 1 : 0)) * C::kQBytes;
+          auto at = [&](int p) { return tile + (p / 8) * (128 * 128) + swz128(m * 128 + (p % 8) * 16); };
+          float mq = 0.0f;
+#pragma unroll 4
+          for (int p = 0; p < D / 8; ++p) {
+            const uint4 x = lds128(at(p));
+            const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              mq = fmaxf(mq, fmaxf(fabsf(bf16_lo(y[e])), fabsf(bf16_hi(y[e]))));
+          }
+          const float down = exp2i(14 - ilog2f(mq));
+          mul_s[r] = mul * exp2i(ilog2f(mq) - 14);
+#pragma unroll 4
+          for (int p = 0; p < D / 8; ++p) {
+            const uint4 x = lds128(at(p));
+            uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = pack_f16x2(bf16_lo(y[e]) * down, bf16_hi(y[e]) * down);
+            sts128(at(p), y[0], y[1], y[2], y[3]);
+          }
+        }
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&q_full[buf]));
+      ++piece;
+    }
   } else if (warp == kTreeMma) {
     // =========================== MMA issuer ===============================
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
@@ -417,7 +518,11 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
         const bool dual = nodes > TPG;
         const int T = q.j1 - q.j0;
         const int n0 = dual ? T : (T + 1) / 2, n1 = dual ? T : T / 2;
-        if (!(ok = wait(q_full, piece))) break;
+        const int buf = piece % nbuf;
+        // q has landed; the products that read the last P are done
+        if (!(ok = wait(&q_full[buf], piece / nbuf) && (cs0 == 0 || wait(&o_done[0], cs0 - 1)) &&
+                   (cs1 == 0 || wait(&o_done[1], cs1 - 1))))
+          break;
         tc_fence_after();
         // S_X of its i-th tile
         auto issue_s = [&](int X, int i) -> bool {
@@ -425,7 +530,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
           const int u = u0 + k_unit(j, dual), slot = u % C::kUnits;
           if (!wait(&u_full[slot], u / C::kUnits)) return false;
           tc_fence_after();
-          const uint64_t qa = dq0 + static_cast<uint64_t>(dual && X ? C::kQBytes >> 4 : 0);
+          const uint64_t qa = dq0 + static_cast<uint64_t>((buf + (dual ? X : 0)) * (C::kQBytes >> 4));
           const uint64_t kb = dk0 + static_cast<uint64_t>((slot * C::kUnitBytes) >> 4);
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
@@ -440,6 +545,8 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
         };
         ok = issue_s(0, 0);
         if (ok && n1 > 0) ok = issue_s(1, 0);
+        // the last piece's O has been read
+        if (ok && piece > 0) ok = wait(o_free, piece - 1);
         for (int i = 0; i < n0 && ok; ++i) {
           for (int X = 0; X < 2; ++X) {
             const int nX = X ? n1 : n0;
@@ -520,7 +627,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
     const uint32_t s_tm = tmem + lane_base + X * 128;
     const uint32_t o_tm = tmem + lane_base + 256;  // + group * D
     const float vmul = FMT == PD_KV_FP8_E4M3 ? a.v_scale : 1.0f;
-    int u0 = 0, tile0 = 0, piece = 0;
+    int u0 = 0, tile0 = 0, piece = 0, merges = 0;
     int c0 = 0, c1 = 0;  // tiles the groups have finished
     while (!failed && walk.next(q)) {
       const TreeSeq& s = q.p.s;
@@ -530,51 +637,30 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
       const int T = q.j1 - q.j0;
       const int n0 = dual ? T : (T + 1) / 2, n1 = dual ? T : T / 2;
       const int nX = X ? n1 : n0;
+      const int buf = piece % nbuf;
       // ---- this row: node, head, what it sees ----
       const int i = m / G + (dual ? X * TPG : 0);
       const bool rvalid = m < TPG * G && i < nodes;
-      const RowView any = any_view(a, s, lane);
-      RowView view = any;
-      if (rvalid) view = row_view(a, s, node0 + i);
       const int qh = q.g * G + m % G;
       const int64_t qrow = static_cast<int64_t>(s.q0 + node0 + (rvalid ? i : 0));
-      // ---- Q into its tile (alternating groups: half a row each) ----
-      float sl2 = a.scale_log2 * (FMT == PD_KV_FP8_E4M3 ? a.k_scale : 1.0f);
-      {
-        const uint16_t* src = a.q + qrow * a.q_stride + static_cast<int64_t>(qh) * D;
-        const uint32_t q_s = s0 + (dual ? X * C::kQBytes : 0);
-        uint4 v[D / 8];
-#pragma unroll
-        for (int p = 0; p < D / 8; ++p)
-          v[p] = rvalid ? *reinterpret_cast<const uint4*>(src + p * 8) : make_uint4(0u, 0u, 0u, 0u);
-        if constexpr (kQuant) {
-          // f16 times a power of two: the row's largest |q| in [2^14, 2^15) (exact)
-          float mq = 0.0f;
-#pragma unroll
-          for (int p = 0; p < D / 8; ++p) {
-            const uint32_t x[4] = {v[p].x, v[p].y, v[p].z, v[p].w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mq = fmaxf(mq, fmaxf(fabsf(bf16_lo(x[k])), fabsf(bf16_hi(x[k]))));
-          }
-          const float down = exp2i(14 - ilog2f(mq));
-          sl2 *= exp2i(ilog2f(mq) - 14);
-#pragma unroll
-          for (int p = 0; p < D / 8; ++p) {
-            uint32_t x[4] = {v[p].x, v[p].y, v[p].z, v[p].w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) x[k] = pack_f16x2(bf16_lo(x[k]) * down, bf16_hi(x[k]) * down);
-            v[p] = make_uint4(x[0], x[1], x[2], x[3]);
-          }
-        }
-#pragma unroll
-        for (int p = 0; p < D / 8; ++p)
-          if (dual || (p < D / 16) == (X == 0))
-            sts128(q_s + (p / 8) * (128 * 128) + swz128(m * 128 + (p % 8) * 16), v[p].x, v[p].y,
-                   v[p].z, v[p].w);
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(q_full));
+      const int r = (dual ? X * TPG * G : 0) + m;  // row of the item
+      if (!warp_wait(smem_u32(&q_full[buf]), (piece / nbuf) & 1, abort_s)) {
+        give_up(lane == 0);
+        break;
       }
+      RowView any, view;
+      any.prefix = s.L - s.n;
+      any.sinks = a.sliding_window > 0 ? min(a.num_sinks, any.prefix) : 0;
+      any.lo = lo_s[64];
+      any.bits = bits_s[64];
+      view = any;
+      if (rvalid) {
+        view.lo = lo_s[i];
+        view.bits = bits_s[i];
+      }
+      const float sl2 = kQuant ? (rvalid ? mul_s[r] : 0.0f) : a.scale_log2;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(v_empty));
       // a padding row runs along as a full one against reference 0
       float m_run = rvalid ? -INFINITY : 0.0f, l_run = 0.0f;
       // warps whose 32 rows are all padding only keep the barriers going
@@ -635,7 +721,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
             }
             const float top = fmaxf(mx[0], mx[1]);  // above the reference
             sum = (ls[0] + ls[1]) + (ls[2] + ls[3]);
-            redo = top > kTreeRescale;
+            redo = rvalid && top > kTreeRescale;
             if (redo) {
               mn = m_run + top;
               alpha = ex2(-top);
@@ -717,16 +803,24 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
       // ---- end of the piece: both groups' products, the other's (m, l) ----
       c0 += n0;
       c1 += n1;
-      ml_s[X * 128 + m] = make_float2(m_run, l_run);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&ml_full[X]));
       if (!warp_wait(smem_u32(&o_done[0]), (c0 - 1) & 1, abort_s) ||
-          (n1 > 0 && !warp_wait(smem_u32(&o_done[1]), (c1 - 1) & 1, abort_s)) ||
-          !warp_wait(smem_u32(&ml_full[1 - X]), piece & 1, abort_s)) {
+          (n1 > 0 && !warp_wait(smem_u32(&o_done[1]), (c1 - 1) & 1, abort_s))) {
         give_up(lane == 0);
         break;
       }
       tc_fence_after();
+      // (m, l) are exchanged where the piece's Q was (no product reads it any more)
+      float2* ml_s = reinterpret_cast<float2*>(smem + buf * C::kQBytes);  // [2][128]
+      if (!dual) {
+        ml_s[X * 128 + m] = make_float2(m_run, l_run);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ml_full[X]));
+        if (!warp_wait(smem_u32(&ml_full[1 - X]), merges & 1, abort_s)) {
+          give_up(lane == 0);
+          break;
+        }
+        ++merges;
+      }
       const bool both = !dual && n1 > 0;  // the other group holds tiles of the same rows
       float f_own = 1.0f, f_other = 0.0f, M = m_run, L = l_run;
       if (!dual) {
@@ -738,7 +832,6 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
         L = l_run * f_own + o.y * f_other;
       }
       const float f0 = X ? f_other : f_own, f1 = X ? f_own : f_other;
-      const int r = (dual ? X * TPG * G : 0) + m;  // row of the item
       const float mul = q.whole ? vmul / fmaxf(L, 1e-20f) : vmul;
       uint16_t* orow = a.out + qrow * a.out_stride + static_cast<int64_t>(qh) * D;
       float* part = w.o + (static_cast<int64_t>(q.slot) * (D / 4) * w.rows + r) * 4;
@@ -777,6 +870,12 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
           w.ml[static_cast<int64_t>(q.slot) * w.rows + r] = make_float2(M, L);
       }
       tc_fence_before();
+      fence_async_smem();  // the next copy lands where (m, l) were
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(smem_u32(o_free));
+        mbar_arrive(smem_u32(&q_empty[buf]));
+      }
       u0 += 2 * T;
       tile0 += T;
       ++piece;
@@ -854,6 +953,23 @@ cudaError_t launch_dependent(dim3 grid, int threads, int smem, cudaStream_t st, 
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
+// 3-D map over the q rows: dims (d, q head, row), box (64, G, 128 / G): a tile's
+// rows in (node, head) order, 128-byte swizzled. Rows past total_q land as zeros.
+bool encode_q_map(CUtensorMap* m, const TreeArgs& a, int D) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(a.num_q_heads),
+                              static_cast<cuuint64_t>(a.total_q)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2,
+                                 static_cast<cuuint64_t>(a.q_stride) * 2};
+  const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(a.group),
+                             static_cast<cuuint32_t>(128 / a.group)};
+  const cuuint32_t estr[3] = {1u, 1u, 1u};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<uint16_t*>(a.q), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int FMT, int D, int BS>
 cudaError_t launch_umma_cfg(const TreeArgs& a, const TreeWork& w, cudaStream_t st) {
   using C = TreeCfg<FMT, D, BS>;
@@ -879,6 +995,8 @@ cudaError_t launch_umma_cfg(const TreeArgs& a, const TreeWork& w, cudaStream_t s
         !encode_cache_map(&tv, a.v_cache, FMT, D, a.num_kv_heads, rows, kInner, BS, kSwz))
       return cudaErrorInvalidValue;
   }
+  CUtensorMap tq;
+  if (!encode_q_map(&tq, a, D)) return cudaErrorInvalidValue;
   auto kern = tree_umma_kernel<FMT, D, BS>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -890,7 +1008,7 @@ cudaError_t launch_umma_cfg(const TreeArgs& a, const TreeWork& w, cudaStream_t s
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
-  e = launch_dependent(dim3(w.ctas), C::kThreads, C::kSmemBytes, st, kern, tk, tv, tks, tvs, a, w);
+  e = launch_dependent(dim3(w.ctas), C::kThreads, C::kSmemBytes, st, kern, tk, tv, tks, tvs, tq, a, w);
   if (e != cudaSuccess) return e;
   const dim3 grid(w.ctas, (w.rows + 31) / 32 * (D / 32));
   return launch_dependent(grid, 256, 0, st, tree_join_kernel<D>, a, w);
