@@ -19,10 +19,10 @@
 //    and four more warps widen them to f16 (exact: every E4M3 value and every
 //    E2M1 x E4M3 product is an f16); q is then scaled by a power of two a row.
 //  * A row's P is taken against a running reference that moves only when a
-//    tile passes it by more than 2^8, in one pass over the scores; tiles that
-//    are masked (the window's edge, the nodes, the first of a piece) take the
-//    maximum first. Sums and O are fp32; P is rounded to bf16 (BF16 caches) or
-//    f16.
+//    tile passes it by more than 2^8, which spares most rescalings of O. Sums
+//    and O are fp32; P is rounded to bf16 (BF16 caches) or f16. The loops over
+//    a tile stay rolled: with one or two warps a scheduler, straight-line code
+//    for 128 keys runs at the rate of instruction fetches.
 //  * V rows that no node sees are zeroed, so stale bytes never meet a weight.
 //  * Every wait is bounded (2 s): on time-out the CTA raises PD_DEV_TIMEOUT,
 //    waits for its copies and MMAs in flight, frees its TMEM and ends.
@@ -48,23 +48,21 @@ constexpr float kTreeRescale = 8.0f;  // P <= 2^8 between moves of the reference
 constexpr int kTreeKT = 128;          // keys of a tile
 constexpr int kTreeSlack = 1;         // units a piece costs beside its tiles
 constexpr int kTreeSoftWarps = 8;
-constexpr int kTreeProd = 8;          // and 10: the copies, alternate units
-constexpr int kTreeMma = 9;
-constexpr int kTreeProd2 = 10;
-constexpr int kTreeQ = 11;            // the next piece's q rows and what they see
-constexpr int kTreeConv = 12;         // warps 12..15 widen quantised units
+constexpr int kTreeMma = 8;
+constexpr int kTreeQ = 9;             // the next piece's q rows and what they see
+constexpr int kTreeProd = 10;         // from here on: the copies, units in turn
+constexpr int kTreeConv = 12;         // quantised units are widened by warps 12..15
 constexpr int kTreeTmemCols = 512;
 constexpr int kTreeBadRing = 32;      // tiles whose page masks are kept
 
 template <int FMT, int D, int BS>
 struct TreeCfg {
   static constexpr bool kQuant = FMT != PD_KV_BF16;
-  // whole warpgroups, since registers are dealt by warpgroup: the softmax
-  // threads hold a row's P, the other warps give theirs up (the launch has
-  // 64512 registers with 384 threads of 168, 65536 with 512 of 128)
-  static constexpr int kThreads = kQuant ? 512 : 384;
-  static constexpr int kSoftRegs = kQuant ? 176 : 208;
-  static constexpr int kOtherRegs = kQuant ? 80 : 88;
+  // One thread issues a 2 KB copy about every 100 cycles, a third of the rate at
+  // which an SM's share of the memory delivers BF16 units: four producers.
+  // Quantised units take half the copies or fewer.
+  static constexpr int kProds = kQuant ? 2 : 4;
+  static constexpr int kThreads = (kQuant ? kTreeConv + 4 : kTreeProd + kProds) * 32;
   static constexpr int kCopies = kTreeKT / BS;            // pages of a tile
   static constexpr int kQBytes = 128 * D * 2;             // one Q tile, chunk-major
   static constexpr int kUnitBytes = kTreeKT * D * 2;      // one 16-bit K or V unit, chunk-major
@@ -281,19 +279,18 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
     failed = true;
   };
 
-  if (warp == kTreeProd || warp == kTreeProd2) {
+  if (warp >= kTreeProd && warp < kTreeProd + C::kProds) {
     // =========================== producers ================================
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
     constexpr int kSlots = kQuant ? C::kRaws : C::kUnits;
     uint64_t* full = kQuant ? r_full : u_full;
     uint64_t* empty = kQuant ? r_empty : u_empty;
     const int pool_rows = static_cast<int>(a.num_blocks * BS);
-    const int mine = warp == kTreeProd2 ? 1 : 0;
+    const int mine = warp - kTreeProd;
     if (lane == 0) {
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_v)) : "memory");
     }
-    int u0 = 0;        // units of the pieces before (even: a piece has 2 T)
+    int u0 = 0;        // units of the pieces before
     int tile0 = 0;     // tiles before
     int last = -1;     // last unit issued here
     while (!failed && walk.next(q)) {
@@ -307,7 +304,8 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
       // go back by two tiles at most, so the window moves on three quarters in
       int win = -(1 << 30), cur = -1, nxt = -1;
       auto load = [&](int e) { return e < a.max_blocks_per_seq ? bt[e] : -1; };
-      for (int t = mine; t < 2 * T; t += 2) {
+      // this warp's units: u % kProds == mine
+      for (int t = (mine - u0) & (C::kProds - 1); t < 2 * T; t += C::kProds) {
         bool is_v;
         int j;
         unit_at(t, T, dual, is_v, j);
@@ -413,10 +411,9 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
     // (a slot's last unit only: an earlier phase could not be told from a later)
     const int end = failed ? last + 1 : u0;
     for (int u = end - 1; u >= 0 && u >= end - kSlots; --u)
-      if ((u & 1) == mine) (void)mbar_wait(smem_u32(&full[u % kSlots]), (u / kSlots) & 1);
+      if ((u & (C::kProds - 1)) == mine) (void)mbar_wait(smem_u32(&full[u % kSlots]), (u / kSlots) & 1);
   } else if (warp == kTreeQ) {
     // =========================== q rows ===================================
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
     int piece = 0;
     while (!failed && walk.next(q)) {
       const TreeSeq& s = q.p.s;
@@ -500,7 +497,6 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
     }
   } else if (warp == kTreeMma) {
     // =========================== MMA issuer ===============================
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
     if (lane == 0) {
       constexpr uint32_t idS = kQuant ? umma_idesc_f16(128, kTreeKT, 0) : umma_idesc(128, kTreeKT, 0);
       constexpr uint32_t idO = kQuant ? umma_idesc_f16(128, D, 1) : umma_idesc(128, D, 1);
@@ -582,7 +578,6 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
     __syncwarp();
   } else if (kQuant && warp >= kTreeConv) {
     // =========================== widening warps ===========================
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
     if constexpr (kQuant) {
       const int cw = warp - kTreeConv;
       int u0 = 0, tile0 = 0;
@@ -620,7 +615,6 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
     }
   } else if (warp < kTreeSoftWarps) {
     // =========================== softmax warps ============================
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftRegs));
     const int X = warp >> 2;
     const int m = (warp & 3) * 32 + lane;  // row of the group's tile = TMEM lane
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -692,90 +686,47 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
           }
         }
         if (!idle) {
-          const bool full = !rvalid || (bad == 0u && t0 >= view.lo && t0 + kTreeKT <= view.prefix);
-          uint32_t pk[kTreeKT / 2];
-          float mn = m_run, alpha = 1.0f, sum = 0.0f;
-          bool redo = true;
-          uint32_t valid[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
-          auto pack = [](float x, float y) { return kQuant ? pack_f16x2(x, y) : pack_bf16x2(x, y); };
-          if (__all_sync(0xFFFFFFFFu, full && m_run != -INFINITY)) {
-            const float nref = -m_run;
-            float mx[2] = {-INFINITY, -INFINITY}, ls[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            uint32_t v[2][16];
-            tmem_ld16(s_tm, v[0]);
+          // the chunk's keys this row sees (a padding row: all, its scores are
+          // whatever its stale q gives and go nowhere)
+          const bool open = bad == 0u && t0 >= view.lo && t0 + kTreeKT <= view.prefix;
+          const bool all_open = __all_sync(0xFFFFFFFFu, open || !rvalid);
+          auto seen = [&](int c) -> uint32_t {
+            if (open || !rvalid) return 0xFFFFFFFFu;
+            return seen32(view, t0 + 32 * c) & ~bad32<BS>(bad, c);
+          };
+          // ---- the tile's maximum ----
+          float mx = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < kTreeKT / 32; ++c) {
+            uint32_t v[32];
+            tmem_ld32(s_tm + c * 32, v);
+            tmem_wait_ld();
+            if (a.scale_log2 < 0.0f) {  // the largest score is the smallest product's
 #pragma unroll
-            for (int c = 0; c < kTreeKT / 16; ++c) {
-              tmem_wait_ld();
-              if (c + 1 < kTreeKT / 16) tmem_ld16(s_tm + (c + 1) * 16, v[(c + 1) & 1]);
+              for (int k = 0; k < 32; ++k) v[k] ^= 0x80000000u;
+            }
+            float mc[2] = {-INFINITY, -INFINITY};
+            if (all_open) {
 #pragma unroll
-              for (int k = 0; k < 16; k += 2) {
-                const float x = fmaf(__uint_as_float(v[c & 1][k]), sl2, nref);
-                const float y = fmaf(__uint_as_float(v[c & 1][k + 1]), sl2, nref);
-                mx[0] = fmaxf(mx[0], x);
-                mx[1] = fmaxf(mx[1], y);
-                const float px = ex2(x), py = ex2(y);
-                ls[(k >> 1) & 1] += px;
-                ls[2 + ((k >> 1) & 1)] += py;
-                pk[c * 8 + k / 2] = pack(px, py);
-              }
-            }
-            const float top = fmaxf(mx[0], mx[1]);  // above the reference
-            sum = (ls[0] + ls[1]) + (ls[2] + ls[3]);
-            redo = rvalid && top > kTreeRescale;
-            if (redo) {
-              mn = m_run + top;
-              alpha = ex2(-top);
-            }
-          } else {
-            float mx = -INFINITY;
-            if (!full) {
+              for (int k = 0; k < 32; ++k) mc[k & 1] = fmaxf(mc[k & 1], __uint_as_float(v[k]));
+            } else {
+              const uint32_t vw = seen(c);
 #pragma unroll
-              for (int c = 0; c < 4; ++c) valid[c] = seen32(view, t0 + 32 * c) & ~bad32<BS>(bad, c);
+              for (int k = 0; k < 32; ++k)
+                mc[k & 1] = fmaxf(mc[k & 1], (vw >> k) & 1u ? __uint_as_float(v[k]) : -INFINITY);
             }
-#pragma unroll
-            for (int c = 0; c < kTreeKT / 16; ++c) {
-              uint32_t v[16];
-              tmem_ld16(s_tm + c * 16, v);
-              tmem_wait_ld();
-              const uint32_t vw = valid[c / 2] >> ((c & 1) * 16);
-#pragma unroll
-              for (int k = 0; k < 16; ++k)
-                if ((vw >> k) & 1u) mx = fmaxf(mx, __uint_as_float(v[k]) * sl2);
-            }
-            if (mx > m_run + kTreeRescale || m_run == -INFINITY) {
-              mn = rvalid ? mx : 0.0f;
-              alpha = m_run == -INFINITY ? 0.0f : ex2(m_run - mn);
-            }
+            mx = fmaxf(mx, fmaxf(mc[0], mc[1]));
           }
-          if (__any_sync(0xFFFFFFFFu, redo)) {
-            // P against mn; a row that has seen nothing yet has no valid key
-            const float nref = mn == -INFINITY ? 0.0f : -mn;
-            float ls[2] = {0.0f, 0.0f};
-#pragma unroll
-            for (int c = 0; c < kTreeKT / 16; ++c) {
-              uint32_t v[16];
-              tmem_ld16(s_tm + c * 16, v);
-              tmem_wait_ld();
-              const uint32_t vw = valid[c / 2] >> ((c & 1) * 16);
-#pragma unroll
-              for (int k = 0; k < 16; k += 2) {
-                const float px =
-                    ((vw >> k) & 1u) ? ex2(fmaf(__uint_as_float(v[k]), sl2, nref)) : 0.0f;
-                const float py =
-                    ((vw >> (k + 1)) & 1u) ? ex2(fmaf(__uint_as_float(v[k + 1]), sl2, nref)) : 0.0f;
-                ls[0] += px;
-                ls[1] += py;
-                pk[c * 8 + k / 2] = pack(px, py);
-              }
-            }
-            sum = ls[0] + ls[1];
+          mx *= fabsf(sl2);
+          float mn = m_run, alpha = 1.0f;
+          if (rvalid && mx > m_run + kTreeRescale) {  // also the first keys it sees
+            mn = mx;
+            alpha = m_run == -INFINITY ? 0.0f : ex2(m_run - mn);
           }
-          l_run = l_run * alpha + sum;
-          m_run = mn;
           // O against the new reference (the previous product is done: these
           // scores were issued after it)
           if (jl > 0 && __any_sync(0xFFFFFFFFu, alpha != 1.0f)) {
-#pragma unroll
+#pragma unroll 1
             for (int h = 0; h < D / 16; ++h) {
               uint32_t v[16];
               tmem_ld16(o_tm + X * D + h * 16, v);
@@ -785,14 +736,32 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
               tmem_st16(o_tm + X * D + h * 16, v);
             }
           }
-          // P over the scores
-#pragma unroll
+          // ---- P, written over the scores behind the reads: the chunk's 16
+          // columns lie in a chunk that has been read ----
+          const float nref = mn == -INFINITY ? 0.0f : -mn;
+          float ls[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
           for (int c = 0; c < kTreeKT / 32; ++c) {
-            uint32_t v[16];
+            uint32_t v[32], pk[16];
+            tmem_ld32(s_tm + c * 32, v);
+            tmem_wait_ld();
+            const uint32_t vw = all_open ? 0xFFFFFFFFu : seen(c);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) v[k] = pk[c * 16 + k];
-            tmem_st16(s_tm + c * 16, v);
+            for (int k = 0; k < 32; k += 2) {
+              float px = ex2(fmaf(__uint_as_float(v[k]), sl2, nref));
+              float py = ex2(fmaf(__uint_as_float(v[k + 1]), sl2, nref));
+              if (!all_open) {
+                px = (vw >> k) & 1u ? px : 0.0f;
+                py = (vw >> (k + 1)) & 1u ? py : 0.0f;
+              }
+              ls[(k >> 1) & 1] += px;
+              ls[2 + ((k >> 1) & 1)] += py;
+              pk[k / 2] = kQuant ? pack_f16x2(px, py) : pack_bf16x2(px, py);
+            }
+            tmem_st16(s_tm + c * 16, pk);
           }
+          l_run = fmaf(l_run, alpha, (ls[0] + ls[1]) + (ls[2] + ls[3]));
+          m_run = mn;
           tmem_wait_st();
         }
         tc_fence_before();
@@ -880,8 +849,6 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
       tile0 += T;
       ++piece;
     }
-  } else {  // completes its warpgroup
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
   }
 
   // ---- free the TMEM columns once every warp is done with them ----

@@ -210,6 +210,20 @@ def test_permuted_pages_and_repeats_give_the_same_bits():
     assert B.pd_device_status() == 0
 
 
+@pytest.mark.parametrize("kv_dtype", [0, 2])
+@pytest.mark.parametrize("d,scale", [(128, -0.7), (128, 0.0), (64, 3.0), (256, -0.5)])
+def test_any_scale(d, scale, kv_dtype):
+    """A negative scale, none, and one that makes the softmax nearly one-hot."""
+    case, masks, caches, pages, scales = build([700, 130], [6, 9], 8, 2, d, 16, kv_dtype, 12)
+
+    class Scaled:
+        def __getattr__(self, name):
+            return scale if name == "scale" else getattr(case, name)
+
+    s = Scaled()
+    check(s, masks, pages, call(s, masks, caches, scales, kv_dtype), kv_dtype)
+
+
 def test_many_sequences():
     """More sequences than a CTA has threads, most of them idle or tiny."""
     rng = np.random.default_rng(4)
