@@ -90,6 +90,33 @@ struct TreeCfg {
   static_assert(kSmemBytes <= 227 * 1024, "one CTA's shared memory");
 };
 
+// The bounded waits of mma_common.cuh with a suspend-time hint: a warp that waits
+// sleeps up to 20 us at a time instead of polling. Six or more warps of a CTA wait
+// at any moment; polling, they took half the issue slots of the warps at work.
+__device__ __forceinline__ bool try_wait_long(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(20000u)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool sleep_wait(uint32_t bar, uint32_t parity,
+                                           const volatile int* abort_flag) {
+  if (try_wait_long(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  while (!try_wait_long(bar, parity)) {
+    if (*abort_flag != 0 || global_ns() - t0 > kWaitLimitNs) return false;
+  }
+  return true;
+}
+__device__ __forceinline__ bool warp_sleep_wait(uint32_t bar, uint32_t parity,
+                                                const volatile int* abort_flag) {
+  return __all_sync(0xFFFFFFFFu, sleep_wait(bar, parity, abort_flag));
+}
+
 // Order in which a piece of T tiles uses its 2 T units: dual (each group has its
 // own rows) K0 V0 K1 V1 ..; alternating groups K0 K1 V0 K2 V1 ...
 __device__ __forceinline__ void unit_at(int t, int T, bool dual, bool& is_v, int& j) {
@@ -333,7 +360,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
         if (!ok_page) pg = -1;
         const int u = u0 + t;
         const int slot = u % kSlots;
-        if (u >= kSlots && !warp_wait(smem_u32(&empty[slot]), ((u / kSlots) - 1) & 1, abort_s)) {
+        if (u >= kSlots && !warp_sleep_wait(smem_u32(&empty[slot]), ((u / kSlots) - 1) & 1, abort_s)) {
           give_up(lane == 0);
           break;
         }
@@ -423,7 +450,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
       const int buf = piece % nbuf;
       const bool dual = nodes > TPG;
       if (piece >= nbuf &&
-          !warp_wait(smem_u32(&q_empty[buf]), (piece / nbuf - 1) & 1, abort_s)) {
+          !warp_sleep_wait(smem_u32(&q_empty[buf]), (piece / nbuf - 1) & 1, abort_s)) {
         give_up(lane == 0);
         break;
       }
@@ -442,7 +469,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
 #pragma unroll
       for (int k = 0; k < 2; ++k)
         if (lane + 32 * k < nodes) v[k] = row_view(a, s, node0 + lane + 32 * k);
-      if (piece > 0 && !warp_wait(smem_u32(v_empty), (piece - 1) & 1, abort_s)) {
+      if (piece > 0 && !warp_sleep_wait(smem_u32(v_empty), (piece - 1) & 1, abort_s)) {
         give_up(lane == 0);
         break;
       }
@@ -459,7 +486,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
       if constexpr (kQuant) {
         // bf16 rows to f16 times a power of two, in place, a lane a row: the row's
         // largest |q| into [2^14, 2^15) (exact: f16 holds bf16's 8 bits)
-        if (!warp_wait(q_bar, piece & 1, abort_s)) {
+        if (!warp_sleep_wait(q_bar, piece & 1, abort_s)) {
           give_up(lane == 0);
           break;
         }
@@ -507,7 +534,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
       int cs0 = 0, cs1 = 0;  // S tiles issued by group (its P, O counts follow)
       bool ok = true;
       auto wait = [&](const uint64_t* bar, int parity) {
-        return mbar_wait_or_abort(smem_u32(bar), parity & 1, abort_s);
+        return sleep_wait(smem_u32(bar), parity & 1, abort_s);
       };
       while (ok && walk.next(q)) {
         const int nodes = min(2 * TPG, q.p.s.n - q.rt * 2 * TPG);
@@ -592,9 +619,9 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
           unit_at(t, T, dual, is_v, j);
           const int u = u0 + t;
           const int rs = u % C::kRaws, us = u % C::kUnits;
-          if (!warp_wait(smem_u32(&r_full[rs]), (u / C::kRaws) & 1, abort_s) ||
+          if (!warp_sleep_wait(smem_u32(&r_full[rs]), (u / C::kRaws) & 1, abort_s) ||
               (u >= C::kUnits &&
-               !warp_wait(smem_u32(&u_empty[us]), ((u / C::kUnits) - 1) & 1, abort_s))) {
+               !warp_sleep_wait(smem_u32(&u_empty[us]), ((u / C::kUnits) - 1) & 1, abort_s))) {
             give_up(lane == 0);
             break;
           }
@@ -638,7 +665,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
       const int qh = q.g * G + m % G;
       const int64_t qrow = static_cast<int64_t>(s.q0 + node0 + (rvalid ? i : 0));
       const int r = (dual ? X * TPG * G : 0) + m;  // row of the item
-      if (!warp_wait(smem_u32(&q_full[buf]), (piece / nbuf) & 1, abort_s)) {
+      if (!warp_sleep_wait(smem_u32(&q_full[buf]), (piece / nbuf) & 1, abort_s)) {
         give_up(lane == 0);
         break;
       }
@@ -664,8 +691,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
         const int t0 = tile_key(q.p, q.j0 + j, kTreeKT);
         const int vu = u0 + v_unit(j, T, dual), vslot = vu % C::kUnits;
         const int cnt = (X ? c1 : c0) + jl;
-        if (!warp_wait(smem_u32(&u_full[vslot]), (vu / C::kUnits) & 1, abort_s) ||
-            !warp_wait(smem_u32(&s_full[X]), cnt & 1, abort_s)) {
+        if (!warp_sleep_wait(smem_u32(&s_full[X]), cnt & 1, abort_s)) {
           give_up(lane == 0);
           break;
         }
@@ -673,16 +699,22 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
         const uint32_t bad = bad_s[(tile0 + j) % kTreeBadRing];
         if constexpr (!kQuant) {
           // V rows no node sees: zeros, by the group that uses the tile first
-          const uint32_t keep = seen32(any, t0 + (warp & 3) * 32) & ~bad32<BS>(bad, warp & 3);
-          if (keep != 0xFFFFFFFFu && (!dual || X == 0)) {
-            if (!((keep >> lane) & 1u)) {
-              const uint32_t vrow = unit_s + vslot * C::kUnitBytes;
+          if ((bad != 0u || t0 < any.lo || t0 + kTreeKT > any.prefix) && (!dual || X == 0)) {
+            const uint32_t keep = seen32(any, t0 + (warp & 3) * 32) & ~bad32<BS>(bad, warp & 3);
+            if (keep != 0xFFFFFFFFu) {
+              if (!warp_sleep_wait(smem_u32(&u_full[vslot]), (vu / C::kUnits) & 1, abort_s)) {
+                give_up(lane == 0);
+                break;
+              }
+              if (!((keep >> lane) & 1u)) {
+                const uint32_t vrow = unit_s + vslot * C::kUnitBytes;
 #pragma unroll
-              for (int p = 0; p < D / 8; ++p)
-                sts128(vrow + (p / 8) * (kTreeKT * 128) + swz128(m * 128 + (p % 8) * 16), 0u, 0u, 0u,
-                       0u);
+                for (int p = 0; p < D / 8; ++p)
+                  sts128(vrow + (p / 8) * (kTreeKT * 128) + swz128(m * 128 + (p % 8) * 16), 0u, 0u,
+                         0u, 0u);
+              }
+              fence_async_smem();
             }
-            fence_async_smem();
           }
         }
         if (!idle) {
@@ -696,26 +728,26 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
           };
           // ---- the tile's maximum ----
           float mx = -INFINITY;
+          {
+            float mc[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-          for (int c = 0; c < kTreeKT / 32; ++c) {
-            uint32_t v[32];
-            tmem_ld32(s_tm + c * 32, v);
-            tmem_wait_ld();
-            if (a.scale_log2 < 0.0f) {  // the largest score is the smallest product's
+            for (int c = 0; c < kTreeKT / 32; ++c) {
+              uint32_t v[32];
+              tmem_ld32(s_tm + c * 32, v);
+              tmem_wait_ld();
+              if (a.scale_log2 < 0.0f) {  // the largest score is the smallest product's
 #pragma unroll
-              for (int k = 0; k < 32; ++k) v[k] ^= 0x80000000u;
+                for (int k = 0; k < 32; ++k) v[k] ^= 0x80000000u;
+              }
+              if (!all_open) {
+                const uint32_t vw = seen(c);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) v[k] = (vw >> k) & 1u ? v[k] : 0xFF800000u;  // -inf
+              }
+#pragma unroll
+              for (int k = 0; k < 32; ++k) mc[k & 3] = fmaxf(mc[k & 3], __uint_as_float(v[k]));
             }
-            float mc[2] = {-INFINITY, -INFINITY};
-            if (all_open) {
-#pragma unroll
-              for (int k = 0; k < 32; ++k) mc[k & 1] = fmaxf(mc[k & 1], __uint_as_float(v[k]));
-            } else {
-              const uint32_t vw = seen(c);
-#pragma unroll
-              for (int k = 0; k < 32; ++k)
-                mc[k & 1] = fmaxf(mc[k & 1], (vw >> k) & 1u ? __uint_as_float(v[k]) : -INFINITY);
-            }
-            mx = fmaxf(mx, fmaxf(mc[0], mc[1]));
+            mx = fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3]));
           }
           mx *= fabsf(sl2);
           float mn = m_run, alpha = 1.0f;
@@ -745,18 +777,27 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
             uint32_t v[32], pk[16];
             tmem_ld32(s_tm + c * 32, v);
             tmem_wait_ld();
-            const uint32_t vw = all_open ? 0xFFFFFFFFu : seen(c);
+            if (all_open) {
 #pragma unroll
-            for (int k = 0; k < 32; k += 2) {
-              float px = ex2(fmaf(__uint_as_float(v[k]), sl2, nref));
-              float py = ex2(fmaf(__uint_as_float(v[k + 1]), sl2, nref));
-              if (!all_open) {
+              for (int k = 0; k < 32; k += 2) {
+                const float px = ex2(fmaf(__uint_as_float(v[k]), sl2, nref));
+                const float py = ex2(fmaf(__uint_as_float(v[k + 1]), sl2, nref));
+                ls[(k >> 1) & 1] += px;
+                ls[2 + ((k >> 1) & 1)] += py;
+                pk[k / 2] = kQuant ? pack_f16x2(px, py) : pack_bf16x2(px, py);
+              }
+            } else {
+              const uint32_t vw = seen(c);
+#pragma unroll
+              for (int k = 0; k < 32; k += 2) {
+                float px = ex2(fmaf(__uint_as_float(v[k]), sl2, nref));
+                float py = ex2(fmaf(__uint_as_float(v[k + 1]), sl2, nref));
                 px = (vw >> k) & 1u ? px : 0.0f;
                 py = (vw >> (k + 1)) & 1u ? py : 0.0f;
+                ls[(k >> 1) & 1] += px;
+                ls[2 + ((k >> 1) & 1)] += py;
+                pk[k / 2] = kQuant ? pack_f16x2(px, py) : pack_bf16x2(px, py);
               }
-              ls[(k >> 1) & 1] += px;
-              ls[2 + ((k >> 1) & 1)] += py;
-              pk[k / 2] = kQuant ? pack_f16x2(px, py) : pack_bf16x2(px, py);
             }
             tmem_st16(s_tm + c * 16, pk);
           }
@@ -772,8 +813,8 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
       // ---- end of the piece: both groups' products, the other's (m, l) ----
       c0 += n0;
       c1 += n1;
-      if (!warp_wait(smem_u32(&o_done[0]), (c0 - 1) & 1, abort_s) ||
-          (n1 > 0 && !warp_wait(smem_u32(&o_done[1]), (c1 - 1) & 1, abort_s))) {
+      if (!warp_sleep_wait(smem_u32(&o_done[0]), (c0 - 1) & 1, abort_s) ||
+          (n1 > 0 && !warp_sleep_wait(smem_u32(&o_done[1]), (c1 - 1) & 1, abort_s))) {
         give_up(lane == 0);
         break;
       }
@@ -784,7 +825,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
         ml_s[X * 128 + m] = make_float2(m_run, l_run);
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&ml_full[X]));
-        if (!warp_wait(smem_u32(&ml_full[1 - X]), merges & 1, abort_s)) {
+        if (!warp_sleep_wait(smem_u32(&ml_full[1 - X]), merges & 1, abort_s)) {
           give_up(lane == 0);
           break;
         }
