@@ -121,13 +121,20 @@ __device__ __forceinline__ void reset_state(TileState<C, NT>& s) {
   }
 }
 
-// One stage of keys into the running state. head_dim split: the warps sum
+// Every column of the tile sees the keys of the stage's range.
+struct SameKeys {};
+
+// One stage of keys into the running state. M: which keys a column sees -
+// SameKeys, or a type with open(key0): every column sees keys key0 .. key0 + 15
+// (the same answer in all lanes), sees(nt, j, key): this thread's column
+// 8 nt + 2 c + j sees `key`, and any(key): some column does. head_dim split: the warps sum
 // their partial scores through `red` (buffer red_buf) at named barrier 1,
 // which every consumer warp must reach.
-template <int FMT, int D, int NT, class C>
+template <int FMT, int D, int NT, class C, class M = SameKeys>
 __device__ __forceinline__ void consume_tile(TileState<C, NT>& s, const StageView& sv,
                                              const ThreadPlace& tp, const float* red_in,
-                                             int red_buf) {
+                                             int red_buf, const M& mask = M()) {
+  constexpr bool kMask = !std::is_same<M, SameKeys>::value;
   constexpr bool F16 = C::kF16;
   const int warp = tp.warp, lane = tp.lane, r = tp.r, c = tp.c, d0 = tp.d0;
   const uint32_t kst = sv.kst, vst = sv.vst;
@@ -339,7 +346,9 @@ __device__ __forceinline__ void consume_tile(TileState<C, NT>& s, const StageVie
   };
   auto key_ok = [&](int kk) {  // kk: key index within the stage
     const int kabs = t0 + kk;
-    return kabs >= t_begin && kabs < t_end && !((bad >> (kk / C::kBR)) & 1u);
+    const bool ok = kabs >= t_begin && kabs < t_end && !((bad >> (kk / C::kBR)) & 1u);
+    if constexpr (kMask) return ok && mask.any(kabs);
+    return ok;
   };
   // m-tiles this warp handles in this stage: its own kWM (keys split across
   // warps) or all of them (head_dim split across warps)
@@ -388,6 +397,7 @@ __device__ __forceinline__ void consume_tile(TileState<C, NT>& s, const StageVie
     const int key0 = mt_of(u) * 16;
     ragged[u] = (t0 + key0 < t_begin) || (t0 + key0 + 16 > t_end) ||
                 ((bad >> (key0 / C::kBR)) & 1u);
+    if constexpr (kMask) ragged[u] = ragged[u] || !mask.open(t0 + key0);
   }
   float p[kU][NT][4];
 #pragma unroll
@@ -398,10 +408,19 @@ __device__ __forceinline__ void consume_tile(TileState<C, NT>& s, const StageVie
       const int key0 = mt_of(u) * 16;
       const bool va = !ragged[u] || key_ok(key0 + r);
       const bool vb = !ragged[u] || key_ok(key0 + r + 8);
-      p[u][nt][0] = va ? sc[u][nt][0] * qmul[nt][0] : -INFINITY;
-      p[u][nt][1] = va ? sc[u][nt][1] * qmul[nt][1] : -INFINITY;
-      p[u][nt][2] = vb ? sc[u][nt][2] * qmul[nt][0] : -INFINITY;
-      p[u][nt][3] = vb ? sc[u][nt][3] * qmul[nt][1] : -INFINITY;
+      bool v[4] = {va, va, vb, vb};
+      if constexpr (kMask) {
+        if (ragged[u]) {
+          v[0] = va && mask.sees(nt, 0, t0 + key0 + r);
+          v[1] = va && mask.sees(nt, 1, t0 + key0 + r);
+          v[2] = vb && mask.sees(nt, 0, t0 + key0 + r + 8);
+          v[3] = vb && mask.sees(nt, 1, t0 + key0 + r + 8);
+        }
+      }
+      p[u][nt][0] = v[0] ? sc[u][nt][0] * qmul[nt][0] : -INFINITY;
+      p[u][nt][1] = v[1] ? sc[u][nt][1] * qmul[nt][1] : -INFINITY;
+      p[u][nt][2] = v[2] ? sc[u][nt][2] * qmul[nt][0] : -INFINITY;
+      p[u][nt][3] = v[3] ? sc[u][nt][3] * qmul[nt][1] : -INFINITY;
       mx0 = fmaxf(mx0, fmaxf(p[u][nt][0], p[u][nt][2]));
       mx1 = fmaxf(mx1, fmaxf(p[u][nt][1], p[u][nt][3]));
     }

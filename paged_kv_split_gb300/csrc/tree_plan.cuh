@@ -207,6 +207,30 @@ struct TreeWork {
   float* o;
   int ctas, rows, item_nodes, min_units;
 };
+// Launch as a programmatic dependent of the previous work on the stream.
+template <class... A>
+inline cudaError_t launch_dependent(dim3 grid, int threads, int smem, cudaStream_t st, void (*kern)(A...),
+                             const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+cudaError_t launch_tree_join(const TreeArgs& a, const TreeWork& w, int head_dim, cudaStream_t st);
+// head_dim 64 / 128 on tcgen05; 256 / 512 on mma.sync. The workspace functions
+// return its size and, with w, lay it out.
+size_t tree_split_workspace(int max_q_len, int group, int head_dim, int kv_dtype, int num_sms,
+                            TreeWork* w, void* workspace);
+cudaError_t launch_tree_split(const TreeArgs& a, const TreeWork& w, int head_dim, int kv_dtype,
+                              cudaStream_t st);
 size_t tree_umma_workspace(int max_q_len, int group, int head_dim, int num_sms, TreeWork* w,
                            void* workspace);
 cudaError_t launch_tree_umma(const TreeArgs& a, const TreeWork& w, int head_dim, int kv_dtype,
