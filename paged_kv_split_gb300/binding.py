@@ -129,8 +129,15 @@ def _check(fn: str, rc: int) -> None:
         raise PdError(fn, rc)
 
 
+# the current stream's handle without a Stream object around it (2.8 -> 0.2 us a
+# call on a Grace core, where one whole pd_* call in C takes 3 to 5)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch._C._cuda_getDevice())
         stream = torch.cuda.current_stream()
     return int(getattr(stream, "cuda_stream", stream) or 0)
 
@@ -144,6 +151,19 @@ def _dev(t: torch.Tensor, name: str, dtype=None, device=None) -> int:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return t.data_ptr()
+
+
+def _ptr(t, name, dtype, index) -> int:
+    """_dev for the calls of a decoding loop: a CUDA tensor of device `index`."""
+    if index < 0 or t.get_device() != index or t.dtype is not dtype or not t.is_contiguous():
+        return _dev(t, name, dtype, torch.device("cuda", max(index, 0)))
+    return t.data_ptr()
+
+
+def _cache_ptr(t, name, index) -> int:
+    if index < 0 or t.get_device() != index or not t.is_contiguous():
+        return _dev(t, name, None, torch.device("cuda", max(index, 0)))
     return t.data_ptr()
 
 
@@ -634,22 +654,22 @@ def _norm_rope(qkv, q_out, q_out_stride, hq, d, k_cache, v_cache, positions, slo
         raise ValueError("positions and slot_mapping must be [num_tokens]")
     if cos_sin.dim() != 2:
         raise ValueError("cos_sin must be float32 [max_position, rot_dim]")
-    dev = qkv.device
+    dev = qkv.get_device()
     qw = kw = None
     if q_weight is not None or k_weight is not None:
         if q_weight is None or k_weight is None:
             raise ValueError("q_weight and k_weight go together")
         if q_weight.shape != (d,) or k_weight.shape != (d,):
             raise ValueError("q_weight and k_weight must be [head_dim]")
-        qw = _dev(q_weight, "q_weight", torch.bfloat16, dev)
-        kw = _dev(k_weight, "k_weight", torch.bfloat16, dev)
+        qw = _ptr(q_weight, "q_weight", torch.bfloat16, dev)
+        kw = _ptr(k_weight, "k_weight", torch.bfloat16, dev)
     rc = _lib.pd_qk_norm_rope_cache(
-        _dev(qkv, "qkv", torch.bfloat16, dev), row, qw, kw, eps, weight_offset,
-        _dev(cos_sin, "cos_sin", torch.float32, dev), cos_sin.shape[0], cos_sin.shape[1],
-        int(bool(interleaved)), _dev(positions, "positions", torch.int32, dev),
-        _dev(slot_mapping, "slot_mapping", torch.int32, dev),
-        _dev(q_out, "q_out", torch.bfloat16, dev), q_out_stride,
-        _dev(k_cache, "k_cache", None, dev), _dev(v_cache, "v_cache", None, dev), T, hq,
+        _ptr(qkv, "qkv", torch.bfloat16, dev), row, qw, kw, eps, weight_offset,
+        _ptr(cos_sin, "cos_sin", torch.float32, dev), cos_sin.shape[0], cos_sin.shape[1],
+        int(bool(interleaved)), _ptr(positions, "positions", torch.int32, dev),
+        _ptr(slot_mapping, "slot_mapping", torch.int32, dev),
+        _ptr(q_out, "q_out", torch.bfloat16, dev), q_out_stride,
+        _cache_ptr(k_cache, "k_cache", dev), _cache_ptr(v_cache, "v_cache", dev), T, hq,
         num_kv_heads, d, block_size, num_blocks, _dtype_code(kv_dtype), k_scale, v_scale,
         _stream(stream))
     _check("pd_qk_norm_rope_cache", rc)
@@ -690,6 +710,9 @@ def _num_sms(device_index) -> int:
     return torch.cuda.get_device_properties(device_index).multi_processor_count
 
 
+_tree_workspace = functools.lru_cache(maxsize=4096)(_lib.pd_decode_tree_workspace_bytes)
+
+
 def pd_decode_tree_workspace_bytes(max_q_len, num_q_heads, num_kv_heads, head_dim, kv_dtype,
                                    num_sms) -> int:
     """Workspace bytes of pd_decode_tree; they depend on no length."""
@@ -703,7 +726,9 @@ def pd_decode_tree_workspace_bytes(max_q_len, num_q_heads, num_kv_heads, head_di
 def _decode_tree(fn, q, q_stride, cu_q, tree_mask, k_cache, v_cache, block_tables, seq_lens, out,
                  out_stride, T, hq, d, max_q_len, num_kv_heads, block_size, num_blocks, scale,
                  sliding_window, num_sinks, kv_dtype, k_scale, v_scale, workspace, stream):
-    dev = q.device
+    dev = q.get_device()
+    if dev < 0:
+        raise ValueError("q must be a CUDA tensor")
     if block_tables.dim() != 2:
         raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq]")
     B, mbs = block_tables.shape
@@ -713,23 +738,22 @@ def _decode_tree(fn, q, q_stride, cu_q, tree_mask, k_cache, v_cache, block_table
     if tree_mask is not None:
         if tree_mask.shape != (T,):
             raise ValueError("tree_mask must be int64 [total_q]")
-        mask = _dev(tree_mask, "tree_mask", torch.int64, dev)
+        mask = _ptr(tree_mask, "tree_mask", torch.int64, dev)
     code = _dtype_code(kv_dtype)
     if workspace is None:
         # 0 for refused shapes: the call below says why
-        n = int(_lib.pd_decode_tree_workspace_bytes(max_q_len, hq, num_kv_heads, d, code,
-                                                    _num_sms(dev.index)))
-        workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
-    rc = getattr(_lib, fn)(
-        _dev(q, "q", torch.bfloat16, dev), q_stride, _dev(cu_q, "cu_q", torch.int32, dev), mask,
-        _dev(k_cache, "k_cache", None, dev), _dev(v_cache, "v_cache", None, dev),
-        _dev(block_tables, "block_tables", torch.int32, dev),
-        _dev(seq_lens, "seq_lens", torch.int32, dev), _dev(out, "out", torch.bfloat16, dev),
+        n = _tree_workspace(max_q_len, hq, num_kv_heads, d, code, _num_sms(dev))
+        workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=q.device)
+    rc = fn(
+        _ptr(q, "q", torch.bfloat16, dev), q_stride, _ptr(cu_q, "cu_q", torch.int32, dev), mask,
+        _cache_ptr(k_cache, "k_cache", dev), _cache_ptr(v_cache, "v_cache", dev),
+        _ptr(block_tables, "block_tables", torch.int32, dev),
+        _ptr(seq_lens, "seq_lens", torch.int32, dev), _ptr(out, "out", torch.bfloat16, dev),
         out_stride, B, T, max_q_len, hq, num_kv_heads, d, block_size, mbs, num_blocks, scale,
         sliding_window, num_sinks, code, k_scale, v_scale,
-        _dev(workspace, "workspace", None, dev), workspace.numel() * workspace.element_size(),
+        _cache_ptr(workspace, "workspace", dev), workspace.numel() * workspace.element_size(),
         _stream(stream))
-    _check(fn, rc)
+    _check(fn.__name__, rc)
 
 
 def pd_decode_tree(q, cu_q, k_cache, v_cache, block_tables, seq_lens, out, *, max_q_len,
@@ -748,7 +772,7 @@ def pd_decode_tree(q, cu_q, k_cache, v_cache, block_tables, seq_lens, out, *, ma
     if q.dim() != 3 or out.shape != q.shape:
         raise ValueError("q and out must be bf16 [total_q, num_q_heads, head_dim]")
     T, hq, d = q.shape
-    _decode_tree("pd_decode_tree_crosscheck" if crosscheck else "pd_decode_tree", q, 0, cu_q,
+    _decode_tree(_lib.pd_decode_tree_crosscheck if crosscheck else _lib.pd_decode_tree, q, 0, cu_q,
                  tree_mask, k_cache, v_cache, block_tables, seq_lens, out, 0, T, hq, d, max_q_len,
                  num_kv_heads, block_size, num_blocks, scale, sliding_window, num_sinks, kv_dtype,
                  k_scale, v_scale, workspace, stream)
@@ -766,7 +790,7 @@ def pd_decode_tree_strided(q_rows, cu_q, k_cache, v_cache, block_tables, seq_len
     To, ostride = _strided_rows(out_rows, num_q_heads, head_dim, "out_rows")
     if To != T:
         raise ValueError("q_rows and out_rows have different numbers of rows")
-    _decode_tree("pd_decode_tree_crosscheck" if crosscheck else "pd_decode_tree", q_rows, stride,
+    _decode_tree(_lib.pd_decode_tree_crosscheck if crosscheck else _lib.pd_decode_tree, q_rows, stride,
                  cu_q, tree_mask, k_cache, v_cache, block_tables, seq_lens, out_rows, ostride, T,
                  num_q_heads, head_dim, max_q_len, num_kv_heads, block_size, num_blocks, scale,
                  sliding_window, num_sinks, kv_dtype, k_scale, v_scale, workspace, stream)
@@ -792,15 +816,15 @@ def pd_compact_tree(k_caches, v_caches, block_tables, seq_lens, cu_q, accepted, 
             cu_q.shape != (B + 1,) or new_seq_lens.shape != (B,)):
         raise ValueError("accepted, num_accepted, seq_lens, cu_q and new_seq_lens must match "
                          "block_tables' sequences")
-    dev = k_caches.device
+    dev = k_caches.get_device()
     layer_bytes = k_caches.shape[-1] * k_caches.element_size()
     rc = _lib.pd_compact_tree(
-        _dev(k_caches, "k_caches", None, dev), _dev(v_caches, "v_caches", None, dev), layer_bytes,
-        layers, _dev(block_tables, "block_tables", torch.int32, dev),
-        _dev(seq_lens, "seq_lens", torch.int32, dev), _dev(cu_q, "cu_q", torch.int32, dev),
-        _dev(accepted, "accepted", torch.int32, dev),
-        _dev(num_accepted, "num_accepted", torch.int32, dev), accepted.shape[1],
-        _dev(new_seq_lens, "new_seq_lens", torch.int32, dev), B, num_kv_heads, head_dim,
+        _cache_ptr(k_caches, "k_caches", dev), _cache_ptr(v_caches, "v_caches", dev), layer_bytes,
+        layers, _ptr(block_tables, "block_tables", torch.int32, dev),
+        _ptr(seq_lens, "seq_lens", torch.int32, dev), _ptr(cu_q, "cu_q", torch.int32, dev),
+        _ptr(accepted, "accepted", torch.int32, dev),
+        _ptr(num_accepted, "num_accepted", torch.int32, dev), accepted.shape[1],
+        _ptr(new_seq_lens, "new_seq_lens", torch.int32, dev), B, num_kv_heads, head_dim,
         block_size, mbs, num_blocks, _dtype_code(kv_dtype), _stream(stream))
     _check("pd_compact_tree", rc)
     return new_seq_lens

@@ -108,6 +108,31 @@ def test_bits_and_bound(orc, kv_dtype, T, hq, hkv, d, bs, rot, inter, norm, offs
     assert torch.equal(kc, kc2) and torch.equal(vc, vc2)
 
 
+@pytest.mark.parametrize("kv_dtype", [0, 1, 2])
+@pytest.mark.parametrize("scale", [1.0, 1.7, 3.14159 / 448, 2.0 ** -20, 1e6])
+def test_every_bf16_pattern_as_v(orc, kv_dtype, scale):
+    """All 65536 patterns (NaN payloads, infinities, subnormals) through the V
+    write, bit for bit as the oracle's cache write."""
+    if kv_dtype != 1 and scale != 1.0:
+        pytest.skip("the scale is FP8's")
+    B = U.pd()
+    d, bs, T = 128, 16, 512
+    v = np.arange(65536, dtype=np.uint32).astype(np.uint16).reshape(T, 1, d)
+    x = np.zeros((T, 3, d), np.uint16)
+    x[:, 2:] = v
+    nb = T // bs
+    slots = np.arange(T, dtype=np.int32)
+    kc = B.empty_cache(kv_dtype, nb, bs, 1, d).zero_()
+    vc = kc.clone()
+    out = torch.empty(T, 1, d, dtype=torch.bfloat16, device="cuda")
+    B.pd_qk_norm_rope_cache(U.bf16_dev(x.reshape(T, -1)), out, kc, vc, U.to_dev(slots * 0),
+                            U.to_dev(slots), _table(1, d), num_kv_heads=1, block_size=bs,
+                            num_blocks=nb, kv_dtype=kv_dtype, k_scale=scale, v_scale=scale)
+    okc, ovc = (np.zeros(kc.numel(), np.uint8) for _ in range(2))
+    orc.reshape_and_cache(np.zeros_like(v), v, okc, ovc, slots, 1, d, bs, nb, kv_dtype, scale, scale)
+    assert np.array_equal(vc.cpu().numpy(), ovc)
+
+
 def test_zero_rows_infinities_and_nan():
     """A zero head stays zero, a NaN element spoils its own head alone."""
     B = U.pd()
