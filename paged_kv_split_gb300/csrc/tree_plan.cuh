@@ -225,12 +225,11 @@ inline cudaError_t launch_dependent(dim3 grid, int threads, int smem, cudaStream
 }
 
 cudaError_t launch_tree_join(const TreeArgs& a, const TreeWork& w, int head_dim, cudaStream_t st);
-// head_dim 64 / 128 on tcgen05; 256 / 512 on mma.sync. The workspace functions
-// return its size and, with w, lay it out.
-size_t tree_split_workspace(int max_q_len, int group, int head_dim, int kv_dtype, int num_sms,
-                            TreeWork* w, void* workspace);
-cudaError_t launch_tree_split(const TreeArgs& a, const TreeWork& w, int head_dim, int kv_dtype,
-                              cudaStream_t st);
+// head_dim 64 to 256 on tcgen05, 512 on mma.sync. The workspace functions return
+// its size and, with w, lay it out.
+size_t tree_split_workspace(int max_q_len, int group, int kv_dtype, int num_sms, TreeWork* w,
+                            void* workspace);
+cudaError_t launch_tree_split(const TreeArgs& a, const TreeWork& w, int kv_dtype, cudaStream_t st);
 size_t tree_umma_workspace(int max_q_len, int group, int head_dim, int num_sms, TreeWork* w,
                            void* workspace);
 cudaError_t launch_tree_umma(const TreeArgs& a, const TreeWork& w, int head_dim, int kv_dtype,

@@ -1,5 +1,5 @@
-// Draft-tree attention at head_dim 256 and 512, where O alone would fill the
-// tensor memory: mma.sync tiles with keys on M and 8 or 16 rows (nodes times q
+// Draft-tree attention at head_dim 512, where O alone would fill the tensor
+// memory: mma.sync tiles with keys on M and 8 or 16 rows (nodes times q
 // heads) on N, head_dim split over four consumer warps, as decode_balanced.cu
 // has them (mma_tile.cuh). More rows than that are further node tiles, which
 // run side by side and find the keys in L2.
@@ -357,24 +357,23 @@ cudaError_t launch_split_nt(const TreeArgs& a, const TreeWork& w, cudaStream_t s
 }
 
 template <int FMT>
-int split_per_sm(int D, bool one) {
-  if (D == 256) return one ? SplitCfg<FMT, 256, 1>::kPerSm : SplitCfg<FMT, 256, 2>::kPerSm;
+int split_per_sm(bool one) {
   return one ? SplitCfg<FMT, 512, 1>::kPerSm : SplitCfg<FMT, 512, 2>::kPerSm;
 }
 
 }  // namespace
 
-size_t tree_split_workspace(int max_q_len, int group, int head_dim, int kv_dtype, int num_sms,
-                            TreeWork* w, void* workspace) {
+size_t tree_split_workspace(int max_q_len, int group, int kv_dtype, int num_sms, TreeWork* w,
+                            void* workspace) {
   // 8 rows where they hold every node of the batch, else 16
   const bool one = (max_q_len < 1 ? 1 : max_q_len) * group <= 8;
   const int item_nodes = (one ? 8 : 16) / group;
   const int rows = one ? 8 : 16;
-  const int per_sm = kv_dtype == PD_KV_BF16       ? split_per_sm<PD_KV_BF16>(head_dim, one)
-                     : kv_dtype == PD_KV_FP8_E4M3 ? split_per_sm<PD_KV_FP8_E4M3>(head_dim, one)
-                                                  : split_per_sm<PD_KV_NVFP4>(head_dim, one);
+  const int per_sm = kv_dtype == PD_KV_BF16       ? split_per_sm<PD_KV_BF16>(one)
+                     : kv_dtype == PD_KV_FP8_E4M3 ? split_per_sm<PD_KV_FP8_E4M3>(one)
+                                                  : split_per_sm<PD_KV_NVFP4>(one);
   const int ctas = num_sms * per_sm;
-  const WorkLayout l = work_layout(ctas, rows, head_dim);
+  const WorkLayout l = work_layout(ctas, rows, 512);
   if (w) {
     uint8_t* p = static_cast<uint8_t*>(workspace);
     w->records = reinterpret_cast<JoinRecord*>(p);
@@ -388,15 +387,7 @@ size_t tree_split_workspace(int max_q_len, int group, int head_dim, int kv_dtype
   return l.bytes;
 }
 
-cudaError_t launch_tree_split(const TreeArgs& a, const TreeWork& w, int head_dim, int kv_dtype,
-                              cudaStream_t st) {
-  if (head_dim == 256) {
-    switch (kv_dtype) {
-      case PD_KV_BF16: return launch_split_nt<PD_KV_BF16, 256>(a, w, st);
-      case PD_KV_FP8_E4M3: return launch_split_nt<PD_KV_FP8_E4M3, 256>(a, w, st);
-      default: return launch_split_nt<PD_KV_NVFP4, 256>(a, w, st);
-    }
-  }
+cudaError_t launch_tree_split(const TreeArgs& a, const TreeWork& w, int kv_dtype, cudaStream_t st) {
   switch (kv_dtype) {
     case PD_KV_BF16: return launch_split_nt<PD_KV_BF16, 512>(a, w, st);
     case PD_KV_FP8_E4M3: return launch_split_nt<PD_KV_FP8_E4M3, 512>(a, w, st);

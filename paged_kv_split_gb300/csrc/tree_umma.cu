@@ -1,4 +1,4 @@
-// Draft-tree attention on the 5th-generation tensor cores, head_dim 64 and 128.
+// Draft-tree attention on the 5th-generation tensor cores, head_dim 64 to 256.
 //
 // The rows of one kv head are the nodes times its G q heads, so every key byte
 // serves n G rows: at 4 D bytes a key (BF16) and 4 D n G operations the keys'
@@ -9,7 +9,8 @@
 //  * One CTA an SM takes an equal share of all key tiles (tree_plan.cuh). A
 //    tile is 128 keys. Two groups of four softmax warps, one thread a row:
 //    up to 128 rows the groups take alternate tiles of the same rows and merge
-//    at the end; above, each takes 128 rows of every tile.
+//    at the end; above, each takes 128 rows of every tile. (head_dim 256: one
+//    group, 64 keys, see kOneO.)
 //  * TMEM holds per group S (128 columns fp32), over which P is written as
 //    16-bit pairs, and O (D columns). P is then the A operand from TMEM, so
 //    shared memory carries K, V and Q only.
@@ -44,9 +45,7 @@ using namespace ::pd::umma;
 using namespace ::pd::tree;
 
 constexpr float kTreeRescale = 8.0f;  // P <= 2^8 between moves of the reference
-constexpr int kTreeKT = 128;          // keys of a tile
 constexpr int kTreeSlack = 1;         // units a piece costs beside its tiles
-constexpr int kTreeSoftWarps = 8;
 constexpr int kTreeMma = 8;
 constexpr int kTreeQ = 9;             // the next piece's q rows and what they see
 constexpr int kTreeProd = 10;         // from here on: the copies, units in turn
@@ -57,22 +56,28 @@ constexpr int kTreeBadRing = 32;      // tiles whose page masks are kept
 template <int FMT, int D, int BS>
 struct TreeCfg {
   static constexpr bool kQuant = FMT != PD_KV_BF16;
+  // head_dim 256: one O fills half the tensor memory, so a single group of
+  // softmax warps takes every tile, its scores in two buffers by turns
+  static constexpr bool kOneO = D == 256;
+  static constexpr int kKT = kOneO ? 64 : 128;            // keys of a tile
+  static constexpr int kQTiles = kOneO ? 1 : 2;
+  static constexpr int kSoftWarps = kOneO ? 4 : 8;
   // One thread issues a 2 KB copy about every 100 cycles, a third of the rate at
   // which an SM's share of the memory delivers BF16 units: four producers.
   // Quantised units take half the copies or fewer.
   static constexpr int kProds = kQuant ? 2 : 4;
   static constexpr int kThreads = (kQuant ? kTreeConv + 4 : kTreeProd + kProds) * 32;
-  static constexpr int kCopies = kTreeKT / BS;            // pages of a tile
+  static constexpr int kCopies = kKT / BS;            // pages of a tile
   static constexpr int kQBytes = 128 * D * 2;             // one Q tile, chunk-major
-  static constexpr int kUnitBytes = kTreeKT * D * 2;      // one 16-bit K or V unit, chunk-major
+  static constexpr int kUnitBytes = kKT * D * 2;      // one 16-bit K or V unit, chunk-major
   static constexpr int kUnits = (kQuant ? 96 : 160) * 1024 / kUnitBytes;
   // a raw quantised unit: rows [128][row bytes], then NVFP4 scales [128][D / 16]
   static constexpr int kRowBytes = FMT == PD_KV_FP8_E4M3 ? D : D / 2;
-  static constexpr int kRawData = kTreeKT * kRowBytes;
-  static constexpr int kRawScales = FMT == PD_KV_NVFP4 ? kTreeKT * (D / 16) : 0;
+  static constexpr int kRawData = kKT * kRowBytes;
+  static constexpr int kRawScales = FMT == PD_KV_NVFP4 ? kKT * (D / 16) : 0;
   static constexpr int kRawBytes = kQuant ? (kRawData + kRawScales + 1023) / 1024 * 1024 : 0;
   static constexpr int kRaws = kQuant ? 64 * 1024 / kRawBytes : 0;
-  static constexpr int kUnitOff = 2 * kQBytes;
+  static constexpr int kUnitOff = kQTiles * kQBytes;
   static constexpr int kRawOff = kUnitOff + kUnits * kUnitBytes;
   static constexpr int kBarOff = kRawOff + kRaws * kRawBytes;
   // unit full / empty, raw full / empty, s_full[2], p_full[2], o_done[2],
@@ -149,24 +154,25 @@ __device__ __forceinline__ uint32_t bad32(uint32_t bad, int chunk) {
 }
 
 // A raw unit widened to f16 in the swizzled operand layout (chunk-major
-// 128-byte rows) by four warps of 32 rows; rows whose `keep` bit is off become zeros.
+// 128-byte rows) by four warps; a warp's rows whose `keep` bit is off become zeros.
 // Lanes take neighbouring 16-byte pieces of the raw rows, and the lanes of odd
 // chunks store their pieces in rotated order: no bank conflicts either way.
 template <int FMT, int D>
 __device__ __forceinline__ void widen_unit(uint32_t raw, uint32_t op, int warp, int lane,
                                            uint32_t keep) {
+  constexpr int kKT = D == 256 ? 64 : 128;
   constexpr int kRow = FMT == PD_KV_FP8_E4M3 ? D : D / 2;
   constexpr int kLanes = kRow / 16;       // lanes of a row
   constexpr int kRows = 32 / kLanes;      // rows of a warp's step
   constexpr int kElems = FMT == PD_KV_FP8_E4M3 ? 16 : 32;
   constexpr int kP = kElems / 8;          // 16-byte f16 pieces of a lane
-  constexpr int kSteps = 32 / kRows;
+  constexpr int kSteps = kKT / 4 / kRows;
   const int sub = lane % kLanes;
   const int e0 = sub * kElems;
   const int ch = e0 / 64;
   const int p0 = (e0 % 64) / 8;
   const int turn = (ch & 1) ? kP / 2 : 0;
-  const int row0 = warp * 32 + lane / kLanes;
+  const int row0 = warp * (kKT / 4) + lane / kLanes;
   uint4 w[kSteps];
   uint32_t sc[kSteps];
 #pragma unroll
@@ -175,14 +181,14 @@ __device__ __forceinline__ void widen_unit(uint32_t raw, uint32_t op, int warp, 
     w[it] = lds128(raw + row * kRow + sub * 16);
     if constexpr (FMT == PD_KV_NVFP4) {
       uint32_t s;
-      asm volatile("ld.shared.u16 %0, [%1];" : "=r"(s) : "r"(raw + kTreeKT * kRow + row * (D / 16) + e0 / 16));
+      asm volatile("ld.shared.u16 %0, [%1];" : "=r"(s) : "r"(raw + kKT * kRow + row * (D / 16) + e0 / 16));
       sc[it] = s;
     }
   }
 #pragma unroll
   for (int it = 0; it < kSteps; ++it) {
     const int row = row0 + it * kRows;
-    const bool on = (keep >> (row & 31)) & 1u;
+    const bool on = (keep >> (row - warp * (kKT / 4))) & 1u;
     const uint32_t u[4] = {on ? w[it].x : 0u, on ? w[it].y : 0u, on ? w[it].z : 0u,
                            on ? w[it].w : 0u};
     uint32_t f[kP][4];
@@ -203,7 +209,7 @@ __device__ __forceinline__ void widen_unit(uint32_t raw, uint32_t op, int warp, 
         for (int q = 0; q < 4; ++q) f[k][q] = hmul2_u32(x[q], s2[k >> 1]);
       }
     }
-    const uint32_t dst = op + ch * (kTreeKT * 128);
+    const uint32_t dst = op + ch * (kKT * 128);
 #pragma unroll
     for (int k = 0; k < kP; ++k) {  // lanes of odd chunks begin half way round
       const int kr = (k + kP / 2) % kP;
@@ -224,10 +230,13 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
                      const TreeWork w) {
   using C = TreeCfg<FMT, D, BS>;
   constexpr bool kQuant = C::kQuant;
+  constexpr bool kOneO = C::kOneO;
+  constexpr int KT = C::kKT;
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int G = a.group;
-  const int TPG = 128 / G;  // nodes of one group's 128 rows
+  const int TPG = 128 / G;        // nodes of 128 rows
+  const int IN = w.item_nodes;    // nodes of an item: TPG, or with two groups 2 TPG
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
   const int lane = tid & 31;
@@ -235,7 +244,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t s0 = smem_u32(smem);
   // (scratch where Q will be)
-  const Share share = make_share(a, 2 * TPG, kTreeKT, kTreeSlack, w.min_units,
+  const Share share = make_share(a, IN, KT, kTreeSlack, w.min_units,
                                  reinterpret_cast<ShareScratch*>(smem));
   if (tid == 0) w.records[blockIdx.x] = JoinRecord{0, 0, 0, 0};
   if (share.b < 0) return;
@@ -273,7 +282,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
       if (kQuant && b >= u_full && b < u_full + C::kUnits) count = 4;      // widening warps
       if (kQuant && b >= r_empty && b < r_empty + C::kRaws) count = 4;
       if (b == p_full || b == p_full + 1 || b == ml_full || b == ml_full + 1) count = 4;
-      if (b >= q_empty && b <= o_free) count = kTreeSoftWarps;
+      if (b >= q_empty && b <= o_free) count = C::kSoftWarps;
       if (!kQuant && (b == q_full || b == q_full + 1)) count = 2;  // the copy, what rows see
       mbar_init(smem_u32(b), count);
     }
@@ -293,10 +302,10 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
   const uint32_t tmem = *holder;
   // S (and P) of group X at X * 128, O at 256 + X * D. Q: two tiles; while no
   // piece has more than 128 rows they are two buffers, piece by piece
-  const int nbuf = w.rows <= 128 ? 2 : 1;
+  const int nbuf = !kOneO && w.rows <= 128 ? 2 : 1;
   const uint32_t unit_s = s0 + C::kUnitOff;
   const uint32_t raw_s = s0 + C::kRawOff;
-  Walker walk(a, share, 2 * TPG, kTreeKT, kTreeSlack);
+  Walker walk(a, share, IN, KT, kTreeSlack);
   Piece q;
   bool failed = false;
   auto give_up = [&](bool say) {
@@ -322,7 +331,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
     while (!failed && walk.next(q)) {
       if (lane == 0 && mine == 0 && q.begins && !q.whole)
         w.records[blockIdx.x] = JoinRecord{q.b, q.g, q.rt, walk.pieces_of_last(q.j1)};
-      const int nodes = min(2 * TPG, q.p.s.n - q.rt * 2 * TPG);
+      const int nodes = min(IN, q.p.s.n - q.rt * IN);
       const bool dual = nodes > TPG;
       const int T = q.j1 - q.j0;
       const int32_t* bt = a.block_tables + static_cast<int64_t>(q.b) * a.max_blocks_per_seq;
@@ -335,7 +344,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
         bool is_v;
         int j;
         unit_at(t, T, dual, is_v, j);
-        const int t0 = tile_key(q.p, q.j0 + j, kTreeKT);
+        const int t0 = tile_key(q.p, q.j0 + j, KT);
         const int first = t0 / BS;
         if (first < win || first - win >= 64) {
           win = first;
@@ -353,7 +362,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
           if (at >= 32) pg = far;
         }
         const bool in = lane < C::kCopies &&
-                        t0 + lane * BS < tile_end(q.p, q.j0 + j, kTreeKT, a.num_sinks);
+                        t0 + lane * BS < tile_end(q.p, q.j0 + j, KT, a.num_sinks);
         const bool ok_page = in && pg >= 0 && pg < a.num_blocks;
         const uint32_t bad = __ballot_sync(0xFFFFFFFFu, in && !ok_page);
         if (!ok_page) pg = -1;
@@ -385,7 +394,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
               for (int k = 0; k < C::kCopies; ++k)
 #pragma unroll
                 for (int ch = 0; ch < D / 64; ++ch)
-                  tma_load_3d(dst + ch * (kTreeKT * 128) + k * (BS * 128), tm, ch * 64, q.g, zs[k],
+                  tma_load_3d(dst + ch * (KT * 128) + k * (BS * 128), tm, ch * 64, q.g, zs[k],
                               fb);
             } else {
               mbar_arrive_expect_tx(fb, C::kRawData);
@@ -443,8 +452,8 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
     int piece = 0;
     while (!failed && walk.next(q)) {
       const TreeSeq& s = q.p.s;
-      const int node0 = q.rt * 2 * TPG;
-      const int nodes = min(2 * TPG, s.n - node0);
+      const int node0 = q.rt * IN;
+      const int nodes = min(IN, s.n - node0);
       const int rows = nodes * G;
       const int buf = piece % nbuf;
       const bool dual = nodes > TPG;
@@ -524,11 +533,11 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
   } else if (warp == kTreeMma) {
     // =========================== MMA issuer ===============================
     if (lane == 0) {
-      constexpr uint32_t idS = kQuant ? umma_idesc_f16(128, kTreeKT, 0) : umma_idesc(128, kTreeKT, 0);
+      constexpr uint32_t idS = kQuant ? umma_idesc_f16(128, KT, 0) : umma_idesc(128, KT, 0);
       constexpr uint32_t idO = kQuant ? umma_idesc_f16(128, D, 1) : umma_idesc(128, D, 1);
       const uint64_t dq0 = umma_desc(s0, 16, 1024);
       const uint64_t dk0 = umma_desc(unit_s, 16, 1024);
-      const uint64_t dv0 = umma_desc(unit_s, kTreeKT * 128, 1024);
+      const uint64_t dv0 = umma_desc(unit_s, KT * 128, 1024);
       int u0 = 0, piece = 0;
       int cs0 = 0, cs1 = 0;  // S tiles issued by group (its P, O counts follow)
       bool ok = true;
@@ -536,7 +545,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
         return sleep_wait(smem_u32(bar), parity & 1, abort_s);
       };
       while (ok && walk.next(q)) {
-        const int nodes = min(2 * TPG, q.p.s.n - q.rt * 2 * TPG);
+        const int nodes = min(IN, q.p.s.n - q.rt * IN);
         const bool dual = nodes > TPG;
         const int T = q.j1 - q.j0;
         const int n0 = dual ? T : (T + 1) / 2, n1 = dual ? T : T / 2;
@@ -580,9 +589,10 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
             tc_fence_after();
             const uint64_t vb = dv0 + static_cast<uint64_t>((slot * C::kUnitBytes) >> 4);
 #pragma unroll
-            for (int kk = 0; kk < kTreeKT / 16; ++kk)
-              umma_f16_ts(tmem + 256 + X * D, tmem + X * 128 + kk * 8, vb + ((kk * 2048) >> 4), idO,
-                          (i > 0 || kk > 0) ? 1u : 0u);
+            for (int kk = 0; kk < KT / 16; ++kk)
+              umma_f16_ts(tmem + 256 + (kOneO ? 0 : X * D), tmem + X * 128 + kk * 8,
+                          vb + ((kk * 2048) >> 4), idO,
+                          ((kOneO ? j : i) > 0 || kk > 0) ? 1u : 0u);
             umma_commit(smem_u32(&o_done[X]));
             if (!dual || X == 1) umma_commit(smem_u32(&u_empty[slot]));
             if (i + 1 < nX) {
@@ -608,7 +618,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
       const int cw = warp - kTreeConv;
       int u0 = 0, tile0 = 0;
       while (!failed && walk.next(q)) {
-        const int nodes = min(2 * TPG, q.p.s.n - q.rt * 2 * TPG);
+        const int nodes = min(IN, q.p.s.n - q.rt * IN);
         const bool dual = nodes > TPG;
         const int T = q.j1 - q.j0;
         const RowView any = any_view(a, q.p.s, lane);
@@ -624,9 +634,11 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
             give_up(lane == 0);
             break;
           }
-          const int t0 = tile_key(q.p, q.j0 + j, kTreeKT);
+          const int t0 = tile_key(q.p, q.j0 + j, KT);
           const uint32_t bad = bad_s[(tile0 + j) % kTreeBadRing];
-          const uint32_t keep = seen32(any, t0 + 32 * cw) & ~bad32<BS>(bad, cw);
+          const int row0 = cw * (KT / 4);  // this warp's first row
+          const uint32_t keep =
+              (seen32(any, t0 + row0 / 32 * 32) & ~bad32<BS>(bad, row0 / 32)) >> (row0 % 32);
           widen_unit<FMT, D>(raw_s + rs * C::kRawBytes, unit_s + us * C::kUnitBytes, cw, lane, keep);
           fence_async_smem();
           __syncwarp();
@@ -639,24 +651,23 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
         tile0 += T;
       }
     }
-  } else if (warp < kTreeSoftWarps) {
+  } else if (warp < C::kSoftWarps) {
     // =========================== softmax warps ============================
-    const int X = warp >> 2;
+    const int X = warp >> 2;  // the group
     const int m = (warp & 3) * 32 + lane;  // row of the group's tile = TMEM lane
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t s_tm = tmem + lane_base + X * 128;
     const uint32_t o_tm = tmem + lane_base + 256;  // + group * D
     const float vmul = FMT == PD_KV_FP8_E4M3 ? a.v_scale : 1.0f;
     int u0 = 0, tile0 = 0, piece = 0, merges = 0;
     int c0 = 0, c1 = 0;  // tiles the groups have finished
     while (!failed && walk.next(q)) {
       const TreeSeq& s = q.p.s;
-      const int node0 = q.rt * 2 * TPG;
-      const int nodes = min(2 * TPG, s.n - node0);
+      const int node0 = q.rt * IN;
+      const int nodes = min(IN, s.n - node0);
       const bool dual = nodes > TPG;
       const int T = q.j1 - q.j0;
       const int n0 = dual ? T : (T + 1) / 2, n1 = dual ? T : T / 2;
-      const int nX = X ? n1 : n0;
+      const int nX = kOneO ? T : (X ? n1 : n0);
       const int buf = piece % nbuf;
       // ---- this row: node, head, what it sees ----
       const int i = m / G + (dual ? X * TPG : 0);
@@ -686,11 +697,13 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
       // warps whose 32 rows are all padding only keep the barriers going
       const bool idle = !__any_sync(0xFFFFFFFFu, rvalid);
       for (int jl = 0; jl < nX; ++jl) {
-        const int j = dual ? jl : 2 * jl + X;
-        const int t0 = tile_key(q.p, q.j0 + j, kTreeKT);
+        const int j = dual || kOneO ? jl : 2 * jl + X;
+        const int sx = kOneO ? jl & 1 : X;  // score buffer
+        const uint32_t s_tm = tmem + lane_base + sx * 128;
+        const int t0 = tile_key(q.p, q.j0 + j, KT);
         const int vu = u0 + v_unit(j, T, dual), vslot = vu % C::kUnits;
-        const int cnt = (X ? c1 : c0) + jl;
-        if (!warp_sleep_wait(smem_u32(&s_full[X]), cnt & 1, abort_s)) {
+        const int cnt = (sx ? c1 : c0) + (kOneO ? jl >> 1 : jl);
+        if (!warp_sleep_wait(smem_u32(&s_full[sx]), cnt & 1, abort_s)) {
           give_up(lane == 0);
           break;
         }
@@ -698,7 +711,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
         const uint32_t bad = bad_s[(tile0 + j) % kTreeBadRing];
         if constexpr (!kQuant) {
           // V rows no node sees: zeros, by the group that uses the tile first
-          if ((bad != 0u || t0 < any.lo || t0 + kTreeKT > any.prefix) && (!dual || X == 0)) {
+          if ((bad != 0u || t0 < any.lo || t0 + KT > any.prefix) && (!dual || X == 0) && m < KT) {
             const uint32_t keep = seen32(any, t0 + (warp & 3) * 32) & ~bad32<BS>(bad, warp & 3);
             if (keep != 0xFFFFFFFFu) {
               if (!warp_sleep_wait(smem_u32(&u_full[vslot]), (vu / C::kUnits) & 1, abort_s)) {
@@ -709,7 +722,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
                 const uint32_t vrow = unit_s + vslot * C::kUnitBytes;
 #pragma unroll
                 for (int p = 0; p < D / 8; ++p)
-                  sts128(vrow + (p / 8) * (kTreeKT * 128) + swz128(m * 128 + (p % 8) * 16), 0u, 0u,
+                  sts128(vrow + (p / 8) * (KT * 128) + swz128(m * 128 + (p % 8) * 16), 0u, 0u,
                          0u, 0u);
               }
               fence_async_smem();
@@ -719,7 +732,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
         if (!idle) {
           // the chunk's keys this row sees (a padding row: all, its scores are
           // whatever its stale q gives and go nowhere)
-          const bool open = bad == 0u && t0 >= view.lo && t0 + kTreeKT <= view.prefix;
+          const bool open = bad == 0u && t0 >= view.lo && t0 + KT <= view.prefix;
           const bool all_open = __all_sync(0xFFFFFFFFu, open || !rvalid);
           auto seen = [&](int c) -> uint32_t {
             if (open || !rvalid) return 0xFFFFFFFFu;
@@ -730,7 +743,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
           {
             float mc[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-            for (int c = 0; c < kTreeKT / 32; ++c) {
+            for (int c = 0; c < KT / 32; ++c) {
               uint32_t v[32];
               tmem_ld32(s_tm + c * 32, v);
               tmem_wait_ld();
@@ -754,9 +767,17 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
             mn = mx;
             alpha = m_run == -INFINITY ? 0.0f : ex2(m_run - mn);
           }
-          // O against the new reference (the previous product is done: these
-          // scores were issued after it)
+          // O against the new reference, once the previous product is done (with
+          // an O for each group, these scores were issued after it)
           if (jl > 0 && __any_sync(0xFFFFFFFFu, alpha != 1.0f)) {
+            if constexpr (kOneO) {
+              const int last = (sx ? c0 : c1) + ((jl - 1) >> 1);
+              if (!warp_sleep_wait(smem_u32(&o_done[1 - sx]), last & 1, abort_s)) {
+                give_up(lane == 0);
+                break;
+              }
+              tc_fence_after();
+            }
 #pragma unroll 1
             for (int h = 0; h < D / 16; ++h) {
               uint32_t v[16];
@@ -772,7 +793,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
           const float nref = mn == -INFINITY ? 0.0f : -mn;
           float ls[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 1
-          for (int c = 0; c < kTreeKT / 32; ++c) {
+          for (int c = 0; c < KT / 32; ++c) {
             uint32_t v[32], pk[16];
             tmem_ld32(s_tm + c * 32, v);
             tmem_wait_ld();
@@ -806,7 +827,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&p_full[X]));
+        if (lane == 0) mbar_arrive(smem_u32(&p_full[sx]));
       }
       if (failed) break;
       // ---- end of the piece: both groups' products, the other's (m, l) ----
@@ -820,7 +841,8 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
       tc_fence_after();
       // (m, l) are exchanged where the piece's Q was (no product reads it any more)
       float2* ml_s = reinterpret_cast<float2*>(smem + buf * C::kQBytes);  // [2][128]
-      if (!dual) {
+      const bool merge = !dual && !kOneO;  // two groups hold tiles of the same rows
+      if (merge) {
         ml_s[X * 128 + m] = make_float2(m_run, l_run);
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&ml_full[X]));
@@ -830,9 +852,9 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
         }
         ++merges;
       }
-      const bool both = !dual && n1 > 0;  // the other group holds tiles of the same rows
+      const bool both = merge && n1 > 0;
       float f_own = 1.0f, f_other = 0.0f, M = m_run, L = l_run;
-      if (!dual) {
+      if (merge) {
         const float2 o = ml_s[(1 - X) * 128 + m];
         M = fmaxf(m_run, o.x);
         f_own = m_run == -INFINITY ? 0.0f : ex2(m_run - M);
@@ -844,7 +866,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
       const float mul = q.whole ? vmul / fmaxf(L, 1e-20f) : vmul;
       uint16_t* orow = a.out + qrow * a.out_stride + static_cast<int64_t>(qh) * D;
       float* part = w.o + (static_cast<int64_t>(q.slot) * (D / 4) * w.rows + r) * 4;
-      const int cols = dual ? D : D / 2, col0 = dual ? 0 : X * (D / 2);
+      const int cols = merge ? D / 2 : D, col0 = merge ? X * (D / 2) : 0;
       if (!idle) {
         for (int cg = 0; cg < cols; cg += 16) {
           uint32_t va[16], vb[16];
@@ -854,7 +876,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
           float x[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
-            x[k] = __uint_as_float(va[k]) * (dual ? 1.0f : f0);
+            x[k] = __uint_as_float(va[k]) * (merge ? f0 : 1.0f);
             if (both) x[k] = fmaf(__uint_as_float(vb[k]), f1, x[k]);
             x[k] *= mul;
           }
@@ -875,7 +897,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
             }
           }
         }
-        if (rvalid && !q.whole && (dual || X == 0))
+        if (rvalid && !q.whole && (!merge || X == 0))
           w.ml[static_cast<int64_t>(q.slot) * w.rows + r] = make_float2(M, L);
       }
       tc_fence_before();
@@ -970,14 +992,18 @@ cudaError_t launch_umma_bs(const TreeArgs& a, const TreeWork& w, cudaStream_t st
 
 template <int FMT>
 cudaError_t launch_umma_fmt(const TreeArgs& a, const TreeWork& w, int D, cudaStream_t st) {
-  return D == 64 ? launch_umma_bs<FMT, 64>(a, w, st) : launch_umma_bs<FMT, 128>(a, w, st);
+  switch (D) {
+    case 64: return launch_umma_bs<FMT, 64>(a, w, st);
+    case 128: return launch_umma_bs<FMT, 128>(a, w, st);
+    default: return launch_umma_bs<FMT, 256>(a, w, st);
+  }
 }
 
 }  // namespace
 
 size_t tree_umma_workspace(int max_q_len, int group, int head_dim, int num_sms, TreeWork* w,
                            void* workspace) {
-  const int item_nodes = 2 * (128 / group);
+  const int item_nodes = (head_dim == 256 ? 1 : 2) * (128 / group);
   const int nodes = max_q_len < item_nodes ? (max_q_len < 1 ? 1 : max_q_len) : item_nodes;
   const int rows = (nodes * group + 7) / 8 * 8;
   const WorkLayout l = work_layout(num_sms, rows, head_dim);
