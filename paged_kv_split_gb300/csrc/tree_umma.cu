@@ -76,6 +76,8 @@ struct TreeCfg {
   static constexpr int kRawData = kKT * kRowBytes;
   static constexpr int kRawScales = FMT == PD_KV_NVFP4 ? kKT * (D / 16) : 0;
   static constexpr int kRawBytes = kQuant ? (kRawData + kRawScales + 1023) / 1024 * 1024 : 0;
+  // NVFP4 pages by gathers of four, while a head's codes of a page fit a box
+  static constexpr bool kGather = FMT == PD_KV_NVFP4 && BS == 16 && D <= 128;
   static constexpr int kRaws = kQuant ? 64 * 1024 / kRawBytes : 0;
   static constexpr int kUnitOff = kQTiles * kQBytes;
   static constexpr int kRawOff = kUnitOff + kUnits * kUnitBytes;
@@ -403,7 +405,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
               for (int k = 0; k < C::kCopies; ++k) tma_load_3d(dst + k * (BS * D), tm, 0, q.g, zs[k], fb);
             }
           }
-        } else if constexpr (BS == 16) {
+        } else if constexpr (C::kGather) {
           // gathers of four pages, their codes and their scales
           constexpr int kSlabWords = 16 * (D / 2) / 4, kScaleWords = 16 * (D / 16) / 4;
           const int z = pg >= 0 ? pg : static_cast<int>(a.num_blocks);
@@ -565,8 +567,9 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
           const uint64_t kb = dk0 + static_cast<uint64_t>((slot * C::kUnitBytes) >> 4);
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t off = ((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4;
-            umma_f16(tmem + X * 128, qa + off, kb + off, idS, ks > 0 ? 1u : 0u);
+            const uint32_t qoff = ((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4;
+            const uint32_t koff = ((ks >> 2) * (KT * 128) + (ks & 3) * 32) >> 4;
+            umma_f16(tmem + X * 128, qa + qoff, kb + koff, idS, ks > 0 ? 1u : 0u);
           }
           umma_commit(smem_u32(&s_full[X]));
           if (!dual || X == 1) umma_commit(smem_u32(&u_empty[slot]));
@@ -951,7 +954,7 @@ cudaError_t launch_umma_cfg(const TreeArgs& a, const TreeWork& w, cudaStream_t s
   std::memset(&tvs, 0, sizeof(tvs));
   const int64_t rows = a.num_blocks * BS;
   if constexpr (FMT == PD_KV_NVFP4) {
-    if constexpr (BS == 16) {
+    if constexpr (C::kGather) {
       constexpr int kSlab = 16 * (D / 2), kScales = 16 * (D / 16);
       if (!encode_nvfp4_gather_map(&tk, a.k_cache, a.page_bytes, a.num_blocks, kSlab) ||
           !encode_nvfp4_gather_map(&tv, a.v_cache, a.page_bytes, a.num_blocks, kSlab) ||
