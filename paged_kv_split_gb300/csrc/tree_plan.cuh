@@ -53,6 +53,13 @@ __device__ __forceinline__ int tile_end(const SeqPlan& p, int j, int kt, int sin
   return j < p.nst ? min((j + 1) * kt, sinks) : min(p.base + (j - p.nst + 1) * kt, p.s.L);
 }
 
+// Non-negative 64-bit quotients that are nearly always 32-bit ones.
+__device__ __noinline__ inline long long quotient64(long long a, long long b) { return a / b; }
+__device__ __forceinline__ long long quotient_of(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return quotient64(a, b);
+}
+
 // A CTA's share of the line.
 struct Share {
   long long units;  // S
@@ -94,7 +101,7 @@ __device__ __forceinline__ Share make_share(const TreeArgs& a, int tpc, int kt, 
     total += sh->warp_sum[w];
   }
   Share r;
-  r.units = (total + gridDim.x - 1) / gridDim.x;
+  r.units = quotient_of(total + gridDim.x - 1, gridDim.x);
   if (r.units < per_cta_min) r.units = per_cta_min;
   r.x0 = r.units * blockIdx.x;
   long long at = before + incl - sum;  // first unit of this thread's sequences
@@ -105,8 +112,9 @@ __device__ __forceinline__ Share make_share(const TreeArgs& a, int tpc, int kt, 
       if (r.x0 < at + cost) {
         const int item = p.nt + ov;
         sh->b = b;
-        sh->k = static_cast<int>((r.x0 - at) / item);
-        sh->off = static_cast<int>((r.x0 - at) % item);
+        const int k = static_cast<int>(quotient_of(r.x0 - at, item));
+        sh->k = k;
+        sh->off = static_cast<int>(r.x0 - at - static_cast<long long>(k) * item);
         break;
       }
       at += cost;
@@ -175,14 +183,14 @@ struct Walker {
   // pieces of the item whose first j1 tiles end this share
   __device__ __forceinline__ int pieces_of_last(int j1) const {
     const long long s = end - j1;  // the item's first unit
-    return static_cast<int>((s + p.nt - 1) / units - (end - 1) / units) + 1;
+    return static_cast<int>(quotient_of(s + p.nt - 1, units) - static_cast<int>(blockIdx.x)) + 1;
   }
 };
 
-// What a CTA leaves for the join: the item that begins in it and goes on, or
-// pieces = 0.
+// What a CTA leaves for the join: the item that begins in it and goes on (its
+// first query row, nodes, first q head), or pieces = 0.
 struct JoinRecord {
-  int b, g, rt, pieces;
+  int pieces, row0, nodes, head0;
 };
 
 // Workspace: records [ctas], then (m, l) [2 ctas][rows], then O

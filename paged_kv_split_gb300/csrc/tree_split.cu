@@ -142,7 +142,9 @@ __global__ void __launch_bounds__(kMmaThreads, (SplitCfg<FMT, D, NT>::kPerSm))
     bool ok = true;
     while (ok && walk.next(q)) {
       if (lane == 0 && q.begins && !q.whole)
-        w.records[blockIdx.x] = JoinRecord{q.b, q.g, q.rt, walk.pieces_of_last(q.j1)};
+        w.records[blockIdx.x] =
+            JoinRecord{walk.pieces_of_last(q.j1), q.p.s.q0 + q.rt * TPC,
+                       min(TPC, q.p.s.n - q.rt * TPC), q.g * G};
       const int node0 = q.rt * TPC;
       const int nodes = min(TPC, q.p.s.n - node0);
       // the rows' q: the group's heads of a node are contiguous

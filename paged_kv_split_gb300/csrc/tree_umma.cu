@@ -32,6 +32,8 @@
 
 #include <cstring>
 
+#pragma nv_diag_suppress 177  // TreeCfg<> defines every constant for every form
+
 #include "mma_common.cuh"
 #include "pd_common.cuh"
 #include "tree_plan.cuh"
@@ -83,8 +85,8 @@ struct TreeCfg {
   static constexpr int kRawOff = kUnitOff + kUnits * kUnitBytes;
   static constexpr int kBarOff = kRawOff + kRaws * kRawBytes;
   // unit full / empty, raw full / empty, s_full[2], p_full[2], o_done[2],
-  // ml_full[2], q_full[2], q_empty[2], v_empty, o_free, q_raw, fin
-  static constexpr int kNumBars = 2 * kUnits + 2 * kRaws + 16;
+  // ml_full[2], q_full[2], q_empty[2], v_empty, o_free, q_raw[2], fin
+  static constexpr int kNumBars = 2 * kUnits + 2 * kRaws + 17;
   // what the piece's nodes see: bits[64], lo[64], any node's bits and lo; the
   // rows' score multipliers [256]; page masks
   static constexpr int kViewOff = kBarOff + (kNumBars + 1) / 2 * 16;
@@ -222,6 +224,58 @@ __device__ __forceinline__ void widen_unit(uint32_t raw, uint32_t op, int warp, 
   }
 }
 
+// A piece's bf16 q rows to f16 times a power of two, in place, by four warps: a
+// row's largest |q| into [2^14, 2^15) (exact: f16 holds bf16's 8 bits). mul_s[r]
+// becomes row r's score multiplier. Rows from `second` on are the second tile's.
+template <int D>
+__device__ __forceinline__ void widen_q(uint32_t tile, int tile_bytes, int rows, int second,
+                                        float mul, float* mul_s, int warp, int lane) {
+  constexpr int kLanes = D / 8;       // lanes of a row, 16 bytes each
+  constexpr int kStep = 32 / kLanes;  // rows of a step
+  constexpr int kBatch = 4;           // steps whose latencies overlap
+  const int c = lane % kLanes;
+#pragma unroll 1
+  for (int r0 = warp * kBatch * kStep; r0 < rows; r0 += 4 * kBatch * kStep) {
+    uint32_t at[kBatch];
+    uint4 x[kBatch];
+    float mq[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int r = min(r0 + k * kStep + lane / kLanes, rows - 1);
+      const int m = r >= second ? r - second : r;
+      at[k] = tile + (r >= second ? tile_bytes : 0) + (c / 8) * (128 * 128) +
+              swz128(m * 128 + (c % 8) * 16);
+      x[k] = lds128(at[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const uint32_t y[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+      mq[k] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        mq[k] = fmaxf(mq[k], fmaxf(fabsf(bf16_lo(y[e])), fabsf(bf16_hi(y[e]))));
+    }
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1)
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        mq[k] = fmaxf(mq[k], __shfl_xor_sync(0xFFFFFFFFu, mq[k], o));
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int r = r0 + k * kStep + lane / kLanes;
+      if (r < rows) {
+        const int up = ilog2f(mq[k]);
+        const float down = exp2i(14 - up);
+        uint32_t y[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = pack_f16x2(bf16_lo(y[e]) * down, bf16_hi(y[e]) * down);
+        sts128(at[k], y[0], y[1], y[2], y[3]);
+        if (c == 0) mul_s[r] = mul * exp2i(up - 14);
+      }
+    }
+  }
+}
+
 template <int FMT, int D, int BS>
 __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
     tree_umma_kernel(const __grid_constant__ CUtensorMap tm_k,
@@ -235,7 +289,6 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
   constexpr bool kOneO = C::kOneO;
   constexpr int KT = C::kKT;
   asm volatile("griddepcontrol.launch_dependents;");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int G = a.group;
   const int TPG = 128 / G;        // nodes of 128 rows
   const int IN = w.item_nodes;    // nodes of an item: TPG, or with two groups 2 TPG
@@ -245,16 +298,6 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
 
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t s0 = smem_u32(smem);
-  // (scratch where Q will be)
-  const Share share = make_share(a, IN, KT, kTreeSlack, w.min_units,
-                                 reinterpret_cast<ShareScratch*>(smem));
-  if (tid == 0) w.records[blockIdx.x] = JoinRecord{0, 0, 0, 0};
-  if (share.b < 0) return;
-  if (s0 & 1023u) {  // the swizzled tiles need 1024-byte alignment: refuse, do not guess
-    if (tid == 0) atomicOr(a.flags, PD_DEV_BAD_SMEM);
-    return;
-  }
-
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
   uint64_t* u_full = bars;
   uint64_t* u_empty = u_full + C::kUnits;
@@ -269,7 +312,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
   uint64_t* v_empty = q_empty + 2;
   uint64_t* o_free = v_empty + 1;
   uint64_t* q_raw = o_free + 1;
-  uint64_t* fin = q_raw + 1;
+  uint64_t* fin = q_raw + 2;
   uint64_t* bits_s = reinterpret_cast<uint64_t*>(smem + C::kViewOff);  // [64], [64]: any node
   int* lo_s = reinterpret_cast<int*>(bits_s + 65);                     // [64], [64]: any node
   float* mul_s = reinterpret_cast<float*>(smem + C::kMulOff);          // [256]
@@ -285,7 +328,8 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
       if (kQuant && b >= r_empty && b < r_empty + C::kRaws) count = 4;
       if (b == p_full || b == p_full + 1 || b == ml_full || b == ml_full + 1) count = 4;
       if (b >= q_empty && b <= o_free) count = C::kSoftWarps;
-      if (!kQuant && (b == q_full || b == q_full + 1)) count = 2;  // the copy, what rows see
+      // what rows see, and the copy or the four warps that widen it
+      if (b == q_full || b == q_full + 1) count = kQuant ? 5 : 2;
       mbar_init(smem_u32(b), count);
     }
     *abort_s = 0;
@@ -298,10 +342,26 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  // what touches global memory waits for the previous work on the stream
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // (scratch where Q will be; its barriers also publish those above)
+  const Share share = make_share(a, IN, KT, kTreeSlack, w.min_units,
+                                 reinterpret_cast<ShareScratch*>(smem));
+  if (tid == 0) w.records[blockIdx.x] = JoinRecord{0, 0, 0, 0};
+  // the swizzled tiles need 1024-byte alignment: refuse, do not guess
+  if ((s0 & 1023u) && tid == 0) atomicOr(a.flags, PD_DEV_BAD_SMEM);
+  const bool work = share.b >= 0 && (s0 & 1023u) == 0;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *holder;
+  if (!work) {
+    if (warp == kTreeMma)
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                   "n"(kTreeTmemCols)
+                   : "memory");
+    return;
+  }
   // S (and P) of group X at X * 128, O at 256 + X * D. Q: two tiles; while no
   // piece has more than 128 rows they are two buffers, piece by piece
   const int nbuf = !kOneO && w.rows <= 128 ? 2 : 1;
@@ -332,7 +392,8 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
     int last = -1;     // last unit issued here
     while (!failed && walk.next(q)) {
       if (lane == 0 && mine == 0 && q.begins && !q.whole)
-        w.records[blockIdx.x] = JoinRecord{q.b, q.g, q.rt, walk.pieces_of_last(q.j1)};
+        w.records[blockIdx.x] = JoinRecord{walk.pieces_of_last(q.j1), q.p.s.q0 + q.rt * IN,
+                                           min(IN, q.p.s.n - q.rt * IN), q.g * G};
       const int nodes = min(IN, q.p.s.n - q.rt * IN);
       const bool dual = nodes > TPG;
       const int T = q.j1 - q.j0;
@@ -465,7 +526,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
         break;
       }
       // one box a chunk: TPG tokens of G heads, rows in (node, head) order
-      const uint32_t q_bar = smem_u32(kQuant ? q_raw : &q_full[buf]);
+      const uint32_t q_bar = smem_u32(kQuant ? &q_raw[buf] : &q_full[buf]);
       if (lane == 0) {
         mbar_arrive_expect_tx(q_bar, (dual ? 2 : 1) * static_cast<uint32_t>(TPG * G * D * 2));
         for (int x = 0; x < (dual ? 2 : 1); ++x)
@@ -493,41 +554,6 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
         bits_s[64] = any.bits;
         lo_s[64] = any.lo;
       }
-      if constexpr (kQuant) {
-        // bf16 rows to f16 times a power of two, in place, a lane a row: the row's
-        // largest |q| into [2^14, 2^15) (exact: f16 holds bf16's 8 bits)
-        if (!warp_sleep_wait(q_bar, piece & 1, abort_s)) {
-          give_up(lane == 0);
-          break;
-        }
-        const float mul = a.scale_log2 * (FMT == PD_KV_FP8_E4M3 ? a.k_scale : 1.0f);
-        for (int r = lane; r < rows; r += 32) {
-          const bool second = r >= TPG * G;
-          const int m = second ? r - TPG * G : r;
-          const uint32_t tile = s0 + (buf + (second ? 1 : 0)) * C::kQBytes;
-          auto at = [&](int p) { return tile + (p / 8) * (128 * 128) + swz128(m * 128 + (p % 8) * 16); };
-          float mq = 0.0f;
-#pragma unroll 4
-          for (int p = 0; p < D / 8; ++p) {
-            const uint4 x = lds128(at(p));
-            const uint32_t y[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              mq = fmaxf(mq, fmaxf(fabsf(bf16_lo(y[e])), fabsf(bf16_hi(y[e]))));
-          }
-          const float down = exp2i(14 - ilog2f(mq));
-          mul_s[r] = mul * exp2i(ilog2f(mq) - 14);
-#pragma unroll 4
-          for (int p = 0; p < D / 8; ++p) {
-            const uint4 x = lds128(at(p));
-            uint32_t y[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = pack_f16x2(bf16_lo(y[e]) * down, bf16_hi(y[e]) * down);
-            sts128(at(p), y[0], y[1], y[2], y[3]);
-          }
-        }
-      }
-      fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&q_full[buf]));
       ++piece;
@@ -619,12 +645,24 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
     // =========================== widening warps ===========================
     if constexpr (kQuant) {
       const int cw = warp - kTreeConv;
-      int u0 = 0, tile0 = 0;
+      int u0 = 0, tile0 = 0, piece = 0;
       while (!failed && walk.next(q)) {
         const int nodes = min(IN, q.p.s.n - q.rt * IN);
         const bool dual = nodes > TPG;
         const int T = q.j1 - q.j0;
         const RowView any = any_view(a, q.p.s, lane);
+        const int buf = piece % nbuf;
+        if (!warp_sleep_wait(smem_u32(&q_raw[buf]), (piece / nbuf) & 1, abort_s) ||
+            (piece > 0 && !warp_sleep_wait(smem_u32(v_empty), (piece - 1) & 1, abort_s))) {
+          give_up(lane == 0);
+          break;
+        }
+        widen_q<D>(s0 + buf * C::kQBytes, C::kQBytes, nodes * G, TPG * G,
+                   a.scale_log2 * (FMT == PD_KV_FP8_E4M3 ? a.k_scale : 1.0f), mul_s, cw, lane);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&q_full[buf]));
+        ++piece;
         for (int t = 0; t < 2 * T; ++t) {
           bool is_v;
           int j;
