@@ -158,70 +158,65 @@ __device__ __forceinline__ uint32_t bad32(uint32_t bad, int chunk) {
 }
 
 // A raw unit widened to f16 in the swizzled operand layout (chunk-major
-// 128-byte rows) by four warps; a warp's rows whose `keep` bit is off become zeros.
-// Lanes take neighbouring 16-byte pieces of the raw rows, and the lanes of odd
-// chunks store their pieces in rotated order: no bank conflicts either way.
+// 128-byte rows) by four warps; a warp's rows whose `keep` bit is off become
+// zeros. Eight lanes take a row, a lane the same 8 elements (a 16-byte f16 piece)
+// of every 64-element chunk: eight lanes store eight different pieces of a row.
+// Rows that would read from the same banks begin with another chunk.
 template <int FMT, int D>
 __device__ __forceinline__ void widen_unit(uint32_t raw, uint32_t op, int warp, int lane,
                                            uint32_t keep) {
   constexpr int kKT = D == 256 ? 64 : 128;
   constexpr int kRow = FMT == PD_KV_FP8_E4M3 ? D : D / 2;
-  constexpr int kLanes = kRow / 16;       // lanes of a row
-  constexpr int kRows = 32 / kLanes;      // rows of a warp's step
-  constexpr int kElems = FMT == PD_KV_FP8_E4M3 ? 16 : 32;
-  constexpr int kP = kElems / 8;          // 16-byte f16 pieces of a lane
-  constexpr int kSteps = kKT / 4 / kRows;
-  const int sub = lane % kLanes;
-  const int e0 = sub * kElems;
-  const int ch = e0 / 64;
-  const int p0 = (e0 % 64) / 8;
-  const int turn = (ch & 1) ? kP / 2 : 0;
-  const int row0 = warp * (kKT / 4) + lane / kLanes;
-  uint4 w[kSteps];
-  uint32_t sc[kSteps];
+  constexpr int kPiece = FMT == PD_KV_FP8_E4M3 ? 8 : 4;  // raw bytes of a piece
+  constexpr int kSteps = kKT / 4 / 4;
+  constexpr int kCh = D / 64;
+  const int p = lane & 7;
+  const int row0 = warp * (kKT / 4) + (lane >> 3);
+  const int turn = kCh == 1 ? 0 : (FMT == PD_KV_FP8_E4M3 ? (lane >> 3) & 1 : lane >> 4);
+  uint2 w[kSteps][kCh];
+  uint32_t sc[kSteps][kCh];
 #pragma unroll
-  for (int it = 0; it < kSteps; ++it) {
-    const int row = row0 + it * kRows;
-    w[it] = lds128(raw + row * kRow + sub * 16);
-    if constexpr (FMT == PD_KV_NVFP4) {
-      uint32_t s;
-      asm volatile("ld.shared.u16 %0, [%1];" : "=r"(s) : "r"(raw + kKT * kRow + row * (D / 16) + e0 / 16));
-      sc[it] = s;
-    }
-  }
+  for (int it = 0; it < kSteps; ++it)
 #pragma unroll
-  for (int it = 0; it < kSteps; ++it) {
-    const int row = row0 + it * kRows;
-    const bool on = (keep >> (row - warp * (kKT / 4))) & 1u;
-    const uint32_t u[4] = {on ? w[it].x : 0u, on ? w[it].y : 0u, on ? w[it].z : 0u,
-                           on ? w[it].w : 0u};
-    uint32_t f[kP][4];
-    if constexpr (FMT == PD_KV_FP8_E4M3) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        f[k >> 1][2 * (k & 1)] = e4m3x2_f16x2(u[k] & 0xFFFFu);
-        f[k >> 1][2 * (k & 1) + 1] = e4m3x2_f16x2(u[k] >> 16);
-      }
-    } else {
-      const uint32_t both = e4m3x2_f16x2(on ? sc[it] : 0u);  // the two groups' scales
-      const uint32_t s2[2] = {__byte_perm(both, both, 0x1010), __byte_perm(both, both, 0x3232)};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t x[4];
-        e2m1x8_f16x2(u[k], x);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) f[k][q] = hmul2_u32(x[q], s2[k >> 1]);
+    for (int k = 0; k < kCh; ++k) {
+      const int row = row0 + it * 4, piece = (k ^ turn) * 8 + p;
+      if constexpr (FMT == PD_KV_FP8_E4M3) {
+        w[it][k] = lds64(raw + row * kRow + piece * kPiece);
+      } else {
+        w[it][k].x = lds32(raw + row * kRow + piece * kPiece);
+        sc[it][k] = lds_u8(raw + kKT * kRow + row * (D / 16) + piece / 2);
       }
     }
-    const uint32_t dst = op + ch * (kKT * 128);
+  if (keep != 0xFFFFFFFFu) {
 #pragma unroll
-    for (int k = 0; k < kP; ++k) {  // lanes of odd chunks begin half way round
-      const int kr = (k + kP / 2) % kP;
-      const bool r = turn != 0;
-      sts128(dst + swz128(row * 128 + (p0 + (r ? kr : k)) * 16), r ? f[kr][0] : f[k][0],
-             r ? f[kr][1] : f[k][1], r ? f[kr][2] : f[k][2], r ? f[kr][3] : f[k][3]);
-    }
+    for (int it = 0; it < kSteps; ++it)
+      if (!((keep >> ((lane >> 3) + it * 4)) & 1u)) {
+#pragma unroll
+        for (int k = 0; k < kCh; ++k) {
+          w[it][k] = make_uint2(0u, 0u);
+          sc[it][k] = 0u;
+        }
+      }
   }
+#pragma unroll
+  for (int it = 0; it < kSteps; ++it)
+#pragma unroll
+    for (int k = 0; k < kCh; ++k) {
+      const int row = row0 + it * 4;
+      uint32_t f[4];
+      if constexpr (FMT == PD_KV_FP8_E4M3) {
+        f[0] = e4m3x2_f16x2(w[it][k].x & 0xFFFFu);
+        f[1] = e4m3x2_f16x2(w[it][k].x >> 16);
+        f[2] = e4m3x2_f16x2(w[it][k].y & 0xFFFFu);
+        f[3] = e4m3x2_f16x2(w[it][k].y >> 16);
+      } else {
+        const uint32_t s2 = e4m3x2_f16x2(sc[it][k] | (sc[it][k] << 8));
+        e2m1x8_f16x2(w[it][k].x, f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = hmul2_u32(f[e], s2);
+      }
+      sts128(op + (k ^ turn) * (kKT * 128) + swz128(row * 128 + p * 16), f[0], f[1], f[2], f[3]);
+    }
 }
 
 // A piece's bf16 q rows to f16 times a power of two, in place, by four warps: a
@@ -513,11 +508,11 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
   } else if (warp == kTreeQ) {
     // =========================== q rows ===================================
     int piece = 0;
+    bool armed = false;  // this piece's copy is on its way, its views are not written
     while (!failed && walk.next(q)) {
       const TreeSeq& s = q.p.s;
       const int node0 = q.rt * IN;
       const int nodes = min(IN, s.n - node0);
-      const int rows = nodes * G;
       const int buf = piece % nbuf;
       const bool dual = nodes > TPG;
       if (piece >= nbuf &&
@@ -527,6 +522,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
       }
       // one box a chunk: TPG tokens of G heads, rows in (node, head) order
       const uint32_t q_bar = smem_u32(kQuant ? &q_raw[buf] : &q_full[buf]);
+      armed = true;
       if (lane == 0) {
         mbar_arrive_expect_tx(q_bar, (dual ? 2 : 1) * static_cast<uint32_t>(TPG * G * D * 2));
         for (int x = 0; x < (dual ? 2 : 1); ++x)
@@ -557,6 +553,13 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&q_full[buf]));
       ++piece;
+      armed = false;
+    }
+    if (failed && armed) {  // the copy issued last lands before the CTA can end
+      const int buf = piece % nbuf;
+      __syncwarp();
+      if (!kQuant && lane == 0) mbar_arrive(smem_u32(&q_full[buf]));
+      (void)mbar_wait(smem_u32(kQuant ? &q_raw[buf] : &q_full[buf]), (piece / nbuf) & 1);
     }
   } else if (warp == kTreeMma) {
     // =========================== MMA issuer ===============================
@@ -678,8 +681,9 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
           const int t0 = tile_key(q.p, q.j0 + j, KT);
           const uint32_t bad = bad_s[(tile0 + j) % kTreeBadRing];
           const int row0 = cw * (KT / 4);  // this warp's first row
-          const uint32_t keep =
-              (seen32(any, t0 + row0 / 32 * 32) & ~bad32<BS>(bad, row0 / 32)) >> (row0 % 32);
+          uint32_t keep = 0xFFFFFFFFu;
+          if (bad != 0u || t0 < any.lo || t0 + KT > any.prefix)
+            keep = (seen32(any, t0 + row0 / 32 * 32) & ~bad32<BS>(bad, row0 / 32)) >> (row0 % 32);
           widen_unit<FMT, D>(raw_s + rs * C::kRawBytes, unit_s + us * C::kUnitBytes, cw, lane, keep);
           fence_async_smem();
           __syncwarp();
