@@ -555,12 +555,14 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
       ++piece;
       armed = false;
     }
-    if (failed && armed) {  // the copy issued last lands before the CTA can end
-      const int buf = piece % nbuf;
-      __syncwarp();
-      if (!kQuant && lane == 0) mbar_arrive(smem_u32(&q_full[buf]));
-      (void)mbar_wait(smem_u32(kQuant ? &q_raw[buf] : &q_full[buf]), (piece / nbuf) & 1);
+    // every copy issued lands before the CTA can end, whoever gave up
+    if (armed) {
+      if (!kQuant && lane == 0) mbar_arrive(smem_u32(&q_full[piece % nbuf]));
+      ++piece;
     }
+    __syncwarp();
+    for (int p = piece - 1; p >= 0 && p >= piece - nbuf; --p)
+      (void)mbar_wait(smem_u32(kQuant ? &q_raw[p % nbuf] : &q_full[p % nbuf]), (p / nbuf) & 1);
   } else if (warp == kTreeMma) {
     // =========================== MMA issuer ===============================
     if (lane == 0) {

@@ -224,6 +224,59 @@ def test_any_scale(d, scale, kv_dtype):
     check(s, masks, pages, call(s, masks, caches, scales, kv_dtype), kv_dtype)
 
 
+LONG = [
+    # lens, nodes, hq, hkv, d, bs, window, sinks: tens of tiles a CTA, many times round its buffers
+    ([9000] * 24, [3] * 24, 8, 8, 64, 16, 0, 0),
+    ([12000] * 16, [1] * 16, 16, 8, 128, 16, 0, 0),
+    ([12000] * 16, [5] * 16, 16, 8, 128, 32, 9000, 4),
+    ([20000, 16000], [64, 40], 32, 8, 128, 16, 0, 0),
+    ([9000] * 16, [5] * 16, 16, 8, 256, 16, 0, 0),
+]
+
+
+@pytest.mark.parametrize("kv_dtype", [0, 1, 2])
+@pytest.mark.parametrize("i", range(len(LONG)))
+def test_long_sequences(i, kv_dtype):
+    """Against the CUDA-core kernel, itself compared with the definition above.
+    Both are within the definition's bound: P to 16 bits and the output to bf16
+    are 2^-8 of values that average |v| <= 1 in the mean square, halved by the
+    averaging over thousands of keys; outputs here are below 2^-3."""
+    B = U.pd()
+    lens, nodes, hq, hkv, d, bs, window, sinks = LONG[i]
+    g = torch.Generator(device="cuda").manual_seed(i)
+    rng = np.random.default_rng(i)
+    pages = [(n + bs - 1) // bs for n in lens]
+    nb = sum(pages)
+    perm = rng.permutation(nb).astype(np.int32)
+    bt = np.full((len(lens), max(pages)), -1, np.int32)
+    at = 0
+    for b, p in enumerate(pages):
+        bt[b, :p] = perm[at:at + p]
+        at += p
+    caches = [B.empty_cache(kv_dtype, nb, bs, hkv, d) for _ in range(2)]
+    slots = torch.arange(nb * bs, dtype=torch.int32, device="cuda")
+    kv = [torch.randn(nb * bs, hkv, d, generator=g, device="cuda").bfloat16() for _ in range(2)]
+    B.pd_reshape_and_cache(*kv, *caches, slots, num_blocks=nb, block_size=bs, kv_dtype=kv_dtype,
+                           k_scale=0.0125, v_scale=0.0125)
+    T = sum(nodes)
+    masks = [m for n in nodes for m in V.random_tree(rng, n)[0]]
+    q = torch.randn(T, hq, d, generator=g, device="cuda").bfloat16()
+    outs = []
+    for cross in (False, True):
+        out = torch.empty_like(q)
+        B.pd_decode_tree(q, U.to_dev(np.cumsum([0] + nodes).astype(np.int32)), *caches, U.to_dev(bt),
+                         U.to_dev(np.array(lens, np.int32)), out,
+                         tree_mask=U.to_dev(V.masks_to_i64(masks)), max_q_len=max(nodes),
+                         num_kv_heads=hkv, block_size=bs, num_blocks=nb, scale=d ** -0.5,
+                         sliding_window=window, num_sinks=sinks, kv_dtype=kv_dtype, k_scale=0.0125,
+                         v_scale=0.0125, crosscheck=cross)
+        outs.append(out.float())
+    assert B.pd_device_status() == 0
+    got, want = outs
+    assert float((got - want).abs().max()) <= 2 * 2.0 ** -8 * 2.0 ** -2
+    assert float(want.abs().max()) > 2.0 ** -6
+
+
 def test_many_sequences():
     """More sequences than a CTA has threads, most of them idle or tiny."""
     rng = np.random.default_rng(4)
@@ -240,4 +293,7 @@ def test_refusals():
         call(case, masks, caches, scales, 0, most=65)
     with pytest.raises(ValueError):
         call(case, masks[:3], caches, scales, 0)
+    with pytest.raises(B.PdError):
+        call(case, masks, caches, scales, 0,
+             workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
     assert B.pd_device_status() == 0
