@@ -18,16 +18,18 @@
 //    a ring, in the order in which they are used. FP8 and NVFP4 units land raw
 //    and four more warps widen them to f16 (exact: every E4M3 value and every
 //    E2M1 x E4M3 product is an f16); q is then scaled by a power of two a row.
-//  * A row's P is taken against a running reference that moves only when a
-//    tile passes it by more than 2^8, which spares most rescalings of O. Sums
-//    and O are fp32; P is rounded to bf16 (BF16 caches) or f16. The loops over
-//    a tile stay rolled: with one or two warps a scheduler, straight-line code
-//    for 128 keys runs at the rate of instruction fetches.
+//  * A row's P is taken against a running reference: the largest of the first
+//    scores it sees. Floating-point P need no exact maximum, so a tile is read
+//    once: the reference moves, and what was computed is rescaled, only where 32
+//    keys' P add up to 2^15. Sums and O are fp32; P is rounded to bf16 (BF16
+//    caches) or f16. The loops over a tile stay rolled: with one or two warps a
+//    scheduler, straight-line code for 128 keys runs at the rate of fetches.
 //  * V rows that no node sees are zeroed, so stale bytes never meet a weight.
 //  * Every wait is bounded (2 s): on time-out the CTA raises PD_DEV_TIMEOUT,
 //    waits for its copies and MMAs in flight, frees its TMEM and ends.
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cudaTypedefs.h>
 
 #include <cstring>
@@ -46,8 +48,10 @@ using namespace ::pd::mma;
 using namespace ::pd::umma;
 using namespace ::pd::tree;
 
-constexpr float kTreeRescale = 8.0f;  // P <= 2^8 between moves of the reference
-constexpr int kTreeSlack = 1;         // units a piece costs beside its tiles
+constexpr float kTreeHigh = 32768.0f; // a row's P add up to less in 32 keys, or its reference moves
+// A piece's start and end cost about two tiles, and a CTA takes two at least (1 and 1:
+// 2 to 5% slower with batches of 32 and 64 sequences, 14.9 against 14.2 us for one short sequence).
+constexpr int kTreeSlack = 2;
 constexpr int kTreeMma = 8;
 constexpr int kTreeQ = 9;             // the next piece's q rows and what they see
 constexpr int kTreeProd = 10;         // from here on: the copies, units in turn
@@ -61,8 +65,8 @@ struct TreeCfg {
   // head_dim 256: one O fills half the tensor memory, so a single group of
   // softmax warps takes every tile, its scores in two buffers by turns
   static constexpr bool kOneO = D == 256;
-  static constexpr int kKT = kOneO ? 64 : 128;            // keys of a tile
-  static constexpr int kQTiles = kOneO ? 1 : 2;
+  static constexpr int kKT = D == 256 ? 64 : 128;            // keys of a tile
+  static constexpr int kQTiles = D == 256 ? 1 : 2;
   static constexpr int kSoftWarps = kOneO ? 4 : 8;
   // One thread issues a 2 KB copy about every 100 cycles, a third of the rate at
   // which an SM's share of the memory delivers BF16 units: four producers.
@@ -155,6 +159,14 @@ __device__ __forceinline__ uint32_t bad32(uint32_t bad, int chunk) {
   if constexpr (BS == 32) return ((bad >> chunk) & 1u) ? 0xFFFFFFFFu : 0u;
   return (((bad >> (2 * chunk)) & 1u) ? 0x0000FFFFu : 0u) |
          (((bad >> (2 * chunk + 1)) & 1u) ? 0xFFFF0000u : 0u);
+}
+
+// Both 16-bit halves (f16 or bf16) times a.
+template <bool F16>
+__device__ __forceinline__ uint32_t scale_pair(uint32_t w, float a) {
+  if constexpr (!F16) return pack_bf16x2(bf16_lo(w) * a, bf16_hi(w) * a);
+  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return pack_f16x2(x.x * a, x.y * a);
 }
 
 // A raw unit widened to f16 in the swizzled operand layout (chunk-major
@@ -564,7 +576,10 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
     for (int p = piece - 1; p >= 0 && p >= piece - nbuf; --p)
       (void)mbar_wait(smem_u32(kQuant ? &q_raw[p % nbuf] : &q_full[p % nbuf]), (p / nbuf) & 1);
   } else if (warp == kTreeMma) {
-    // =========================== MMA issuer ===============================
+    // =========================== products =================================
+    // (A second warp for the second group, both issuing at once, was slower at 256
+    // rows, 103 us against 92: the groups' products then share the tensor core, and
+    // a group waits twice as long for its own.)
     if (lane == 0) {
       constexpr uint32_t idS = kQuant ? umma_idesc_f16(128, KT, 0) : umma_idesc(128, KT, 0);
       constexpr uint32_t idO = kQuant ? umma_idesc_f16(128, D, 1) : umma_idesc(128, D, 1);
@@ -572,7 +587,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
       const uint64_t dk0 = umma_desc(unit_s, 16, 1024);
       const uint64_t dv0 = umma_desc(unit_s, KT * 128, 1024);
       int u0 = 0, piece = 0;
-      int cs0 = 0, cs1 = 0;  // S tiles issued by group (its P, O counts follow)
+      int c0 = 0, c1 = 0;  // tiles of the groups before this piece
       bool ok = true;
       auto wait = [&](const uint64_t* bar, int parity) {
         return sleep_wait(smem_u32(bar), parity & 1, abort_s);
@@ -584,8 +599,8 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
         const int n0 = dual ? T : (T + 1) / 2, n1 = dual ? T : T / 2;
         const int buf = piece % nbuf;
         // q has landed; the products that read the last P are done
-        if (!(ok = wait(&q_full[buf], piece / nbuf) && (cs0 == 0 || wait(&o_done[0], cs0 - 1)) &&
-                   (cs1 == 0 || wait(&o_done[1], cs1 - 1))))
+        if (!(ok = wait(&q_full[buf], piece / nbuf) && (c0 == 0 || wait(&o_done[0], c0 - 1)) &&
+                   (c1 == 0 || wait(&o_done[1], c1 - 1))))
           break;
         tc_fence_after();
         // S_X of its i-th tile
@@ -604,8 +619,6 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
           }
           umma_commit(smem_u32(&s_full[X]));
           if (!dual || X == 1) umma_commit(smem_u32(&u_empty[slot]));
-          if (X) ++cs1;
-          else ++cs0;
           return true;
         };
         ok = issue_s(0, 0);
@@ -616,10 +629,10 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
           for (int X = 0; X < 2; ++X) {
             const int nX = X ? n1 : n0;
             if (i >= nX) continue;
-            const int c = X ? cs1 : cs0;  // this tile is the group's c-th
+            const int c = (X ? c1 : c0) + i;  // this tile is the group's c-th
             const int j = dual ? i : 2 * i + X;
             const int u = u0 + v_unit(j, T, dual), slot = u % C::kUnits;
-            if (!(ok = wait(&u_full[slot], u / C::kUnits) && wait(&p_full[X], c - 1))) break;
+            if (!(ok = wait(&u_full[slot], u / C::kUnits) && wait(&p_full[X], c))) break;
             tc_fence_after();
             const uint64_t vb = dv0 + static_cast<uint64_t>((slot * C::kUnitBytes) >> 4);
 #pragma unroll
@@ -631,17 +644,19 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
             if (!dual || X == 1) umma_commit(smem_u32(&u_empty[slot]));
             if (i + 1 < nX) {
               // the next scores overwrite P: the product that reads it is done first
-              if (!(ok = wait(&o_done[X], c - 1))) break;
+              if (!(ok = wait(&o_done[X], c))) break;
               tc_fence_after();
               if (!(ok = issue_s(X, i + 1))) break;
             }
           }
         }
         u0 += 2 * T;
+        c0 += n0;
+        c1 += n1;
         ++piece;
       }
       if (!ok) give_up(true);
-      // every MMA issued has completed before TMEM is freed
+      // every product issued has completed before TMEM is freed
       umma_commit(smem_u32(fin));
       (void)mbar_wait(smem_u32(fin), 0);
     }
@@ -785,42 +800,89 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
             if (open || !rvalid) return 0xFFFFFFFFu;
             return seen32(view, t0 + 32 * c) & ~bad32<BS>(bad, c);
           };
-          // ---- the tile's maximum ----
-          float mx = -INFINITY;
-          {
-            float mc[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          // ---- P, written over the scores behind the reads: the chunk's 16
+          // columns lie in a chunk that has been read ----
+          bool lost = false;
+          // (scores past 2^24 round by whole steps of the reference: no end of moves)
+          int c = 0, moves = 0;
+          for (;;) {
+            const float nref = m_run == -INFINITY ? 0.0f : -m_run;
+            // rows that need another reference: at the first keys they see, and
+            // where the chunk's sum shows a P that f16 might not hold
+            bool move = false;
 #pragma unroll 1
-            for (int c = 0; c < KT / 32; ++c) {
+            for (; c < KT / 32; ++c) {
+              uint32_t v[32], pk[16];
+              float ls[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+              tmem_ld32(s_tm + c * 32, v);
+              tmem_wait_ld();
+              if (all_open) {
+#pragma unroll
+                for (int k = 0; k < 32; k += 2) {
+                  const float px = ex2(fmaf(__uint_as_float(v[k]), sl2, nref));
+                  const float py = ex2(fmaf(__uint_as_float(v[k + 1]), sl2, nref));
+                  ls[(k >> 1) & 1] += px;
+                  ls[2 + ((k >> 1) & 1)] += py;
+                  pk[k / 2] = kQuant ? pack_f16x2(px, py) : pack_bf16x2(px, py);
+                }
+                move = m_run == -INFINITY;
+              } else {
+                const uint32_t vw = seen(c);
+#pragma unroll
+                for (int k = 0; k < 32; k += 2) {
+                  float px = ex2(fmaf(__uint_as_float(v[k]), sl2, nref));
+                  float py = ex2(fmaf(__uint_as_float(v[k + 1]), sl2, nref));
+                  px = (vw >> k) & 1u ? px : 0.0f;
+                  py = (vw >> (k + 1)) & 1u ? py : 0.0f;
+                  ls[(k >> 1) & 1] += px;
+                  ls[2 + ((k >> 1) & 1)] += py;
+                  pk[k / 2] = kQuant ? pack_f16x2(px, py) : pack_bf16x2(px, py);
+                }
+                move = m_run == -INFINITY && vw != 0u;
+              }
+              const float sum = (ls[0] + ls[1]) + (ls[2] + ls[3]);
+              move = rvalid && (move || sum > kTreeHigh);
+              if (__any_sync(0xFFFFFFFFu, move) && moves < KT / 16) break;
+              l_run += sum;
+              tmem_st16(s_tm + c * 16, pk);
+            }
+            if (c == KT / 32) break;
+            ++moves;
+            // ---- the chunk's largest score as the reference; what was computed
+            // against the last one is rescaled ----
+            float mx = -INFINITY, alpha = 1.0f;
+            {
               uint32_t v[32];
               tmem_ld32(s_tm + c * 32, v);
               tmem_wait_ld();
-              if (a.scale_log2 < 0.0f) {  // the largest score is the smallest product's
+              const uint32_t vw = seen(c);
 #pragma unroll
-                for (int k = 0; k < 32; ++k) v[k] ^= 0x80000000u;
-              }
-              if (!all_open) {
-                const uint32_t vw = seen(c);
-#pragma unroll
-                for (int k = 0; k < 32; ++k) v[k] = (vw >> k) & 1u ? v[k] : 0xFF800000u;  // -inf
-              }
-#pragma unroll
-              for (int k = 0; k < 32; ++k) mc[k & 3] = fmaxf(mc[k & 3], __uint_as_float(v[k]));
+              for (int k = 0; k < 32; ++k)
+                mx = fmaxf(mx, (vw >> k) & 1u ? __uint_as_float(v[k]) * sl2 : -INFINITY);
             }
-            mx = fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3]));
-          }
-          mx *= fabsf(sl2);
-          float mn = m_run, alpha = 1.0f;
-          if (rvalid && mx > m_run + kTreeRescale) {  // also the first keys it sees
-            mn = mx;
-            alpha = m_run == -INFINITY ? 0.0f : ex2(m_run - mn);
-          }
-          // O against the new reference, once the previous product is done (with
-          // an O for each group, these scores were issued after it)
-          if (jl > 0 && __any_sync(0xFFFFFFFFu, alpha != 1.0f)) {
+            if (move) {
+              mx = fmaxf(floorf(mx), -3.0e38f);  // a whole number: the rescaling is exact
+              alpha = m_run == -INFINITY ? 0.0f : ex2(m_run - mx);
+              m_run = mx;
+              l_run *= alpha;
+            }
+            tmem_wait_st();
+#pragma unroll 1
+            for (int h = 0; h < c; ++h) {
+              uint32_t v[16];
+              tmem_ld16(s_tm + h * 16, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 16; ++k) v[k] = scale_pair<kQuant>(v[k], alpha);
+              tmem_st16(s_tm + h * 16, v);
+            }
+            if (jl == 0) continue;
+            // O, once the previous product is done (with an O for each group,
+            // these scores were issued after it)
             if constexpr (kOneO) {
               const int last = (sx ? c0 : c1) + ((jl - 1) >> 1);
               if (!warp_sleep_wait(smem_u32(&o_done[1 - sx]), last & 1, abort_s)) {
-                give_up(lane == 0);
+                lost = true;
                 break;
               }
               tc_fence_after();
@@ -828,48 +890,17 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
 #pragma unroll 1
             for (int h = 0; h < D / 16; ++h) {
               uint32_t v[16];
-              tmem_ld16(o_tm + X * D + h * 16, v);
+              tmem_ld16(o_tm + (kOneO ? 0 : X * D) + h * 16, v);
               tmem_wait_ld();
 #pragma unroll
               for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha);
-              tmem_st16(o_tm + X * D + h * 16, v);
+              tmem_st16(o_tm + (kOneO ? 0 : X * D) + h * 16, v);
             }
           }
-          // ---- P, written over the scores behind the reads: the chunk's 16
-          // columns lie in a chunk that has been read ----
-          const float nref = mn == -INFINITY ? 0.0f : -mn;
-          float ls[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 1
-          for (int c = 0; c < KT / 32; ++c) {
-            uint32_t v[32], pk[16];
-            tmem_ld32(s_tm + c * 32, v);
-            tmem_wait_ld();
-            if (all_open) {
-#pragma unroll
-              for (int k = 0; k < 32; k += 2) {
-                const float px = ex2(fmaf(__uint_as_float(v[k]), sl2, nref));
-                const float py = ex2(fmaf(__uint_as_float(v[k + 1]), sl2, nref));
-                ls[(k >> 1) & 1] += px;
-                ls[2 + ((k >> 1) & 1)] += py;
-                pk[k / 2] = kQuant ? pack_f16x2(px, py) : pack_bf16x2(px, py);
-              }
-            } else {
-              const uint32_t vw = seen(c);
-#pragma unroll
-              for (int k = 0; k < 32; k += 2) {
-                float px = ex2(fmaf(__uint_as_float(v[k]), sl2, nref));
-                float py = ex2(fmaf(__uint_as_float(v[k + 1]), sl2, nref));
-                px = (vw >> k) & 1u ? px : 0.0f;
-                py = (vw >> (k + 1)) & 1u ? py : 0.0f;
-                ls[(k >> 1) & 1] += px;
-                ls[2 + ((k >> 1) & 1)] += py;
-                pk[k / 2] = kQuant ? pack_f16x2(px, py) : pack_bf16x2(px, py);
-              }
-            }
-            tmem_st16(s_tm + c * 16, pk);
+          if (lost) {
+            give_up(lane == 0);
+            break;
           }
-          l_run = fmaf(l_run, alpha, (ls[0] + ls[1]) + (ls[2] + ls[3]));
-          m_run = mn;
           tmem_wait_st();
         }
         tc_fence_before();
@@ -877,16 +908,18 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
         if (lane == 0) mbar_arrive(smem_u32(&p_full[sx]));
       }
       if (failed) break;
-      // ---- end of the piece: both groups' products, the other's (m, l) ----
+      // ---- end of the piece: this group's products, the other's (m, l) ----
       c0 += n0;
       c1 += n1;
-      if (!warp_sleep_wait(smem_u32(&o_done[0]), (c0 - 1) & 1, abort_s) ||
-          (n1 > 0 && !warp_sleep_wait(smem_u32(&o_done[1]), (c1 - 1) & 1, abort_s))) {
+      if (((kOneO || X == 0 || n1 == 0) && !warp_sleep_wait(smem_u32(&o_done[0]), (c0 - 1) & 1, abort_s)) ||
+          ((kOneO || X == 1) && n1 > 0 &&
+           !warp_sleep_wait(smem_u32(&o_done[1]), (c1 - 1) & 1, abort_s))) {
         give_up(lane == 0);
         break;
       }
-      tc_fence_after();
-      // (m, l) are exchanged where the piece's Q was (no product reads it any more)
+      // (m, l) are exchanged where the piece's Q was: a group's last product is
+      // issued after the other's last scores, so that nothing reads it any more
+      // (a second group without tiles waits for the first's)
       float2* ml_s = reinterpret_cast<float2*>(smem + buf * C::kQBytes);  // [2][128]
       const bool merge = !dual && !kOneO;  // two groups hold tiles of the same rows
       if (merge) {
@@ -899,6 +932,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
         }
         ++merges;
       }
+      tc_fence_after();
       const bool both = merge && n1 > 0;
       float f_own = 1.0f, f_other = 0.0f, M = m_run, L = l_run;
       if (merge) {
@@ -1062,7 +1096,7 @@ size_t tree_umma_workspace(int max_q_len, int group, int head_dim, int num_sms, 
     w->ctas = num_sms;
     w->rows = rows;
     w->item_nodes = item_nodes;
-    w->min_units = 1;
+    w->min_units = kTreeSlack;
   }
   return l.bytes;
 }
