@@ -49,9 +49,11 @@ using namespace ::pd::umma;
 using namespace ::pd::tree;
 
 constexpr float kTreeHigh = 32768.0f; // a row's P add up to less in 32 keys, or its reference moves
-// A piece's start and end cost about two tiles, and a CTA takes two at least (1 and 1:
-// 2 to 5% slower with batches of 32 and 64 sequences, 14.9 against 14.2 us for one short sequence).
-constexpr int kTreeSlack = 2;
+// A piece's start and end cost about three tiles (1: 3 to 8% slower with batches of 32
+// and 64 sequences); a CTA takes two units at least (1, 3: 14.9 and 15.7 us for one short
+// sequence, against 14.2).
+constexpr int kTreeSlack = 3;
+constexpr int kTreeLeast = 2;
 constexpr int kTreeMma = 8;
 constexpr int kTreeQ = 9;             // the next piece's q rows and what they see
 constexpr int kTreeProd = 10;         // from here on: the copies, units in turn
@@ -145,9 +147,6 @@ __device__ __forceinline__ void unit_at(int t, int T, bool dual, bool& is_v, int
     is_v = false;
     j = (t + 1) >> 1;
   }
-}
-__device__ __forceinline__ int k_unit(int j, bool dual) {
-  return dual ? 2 * j : (j < 2 ? j : 2 * j - 1);
 }
 __device__ __forceinline__ int v_unit(int j, int T, bool dual) {
   return dual ? 2 * j + 1 : (j == T - 1 ? 2 * T - 1 : 2 * j + 2);
@@ -586,11 +585,22 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
       const uint64_t dq0 = umma_desc(s0, 16, 1024);
       const uint64_t dk0 = umma_desc(unit_s, 16, 1024);
       const uint64_t dv0 = umma_desc(unit_s, KT * 128, 1024);
-      int u0 = 0, piece = 0;
+      int piece = 0, slot = 0;
+      uint32_t turn = 0;   // parity of the ring's turn
       int c0 = 0, c1 = 0;  // tiles of the groups before this piece
       bool ok = true;
       auto wait = [&](const uint64_t* bar, int parity) {
         return sleep_wait(smem_u32(bar), parity & 1, abort_s);
+      };
+      // the next unit, once it has landed: units come in the order of use
+      auto take = [&](int& s) -> bool {
+        s = slot;
+        const uint32_t ph = turn;
+        if (++slot == C::kUnits) {
+          slot = 0;
+          turn ^= 1u;
+        }
+        return sleep_wait(smem_u32(&u_full[s]), ph, abort_s);
       };
       while (ok && walk.next(q)) {
         const int nodes = min(IN, q.p.s.n - q.rt * IN);
@@ -603,54 +613,49 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
                    (c1 == 0 || wait(&o_done[1], c1 - 1))))
           break;
         tc_fence_after();
-        // S_X of its i-th tile
-        auto issue_s = [&](int X, int i) -> bool {
-          const int j = dual ? i : 2 * i + X;
-          const int u = u0 + k_unit(j, dual), slot = u % C::kUnits;
-          if (!wait(&u_full[slot], u / C::kUnits)) return false;
+        int ks = 0, vs = 0;  // the last K and V unit; dual pieces use each twice
+        auto issue_s = [&](int X) -> bool {
+          if (!(dual && X == 1) && !take(ks)) return false;
           tc_fence_after();
           const uint64_t qa = dq0 + static_cast<uint64_t>((buf + (dual ? X : 0)) * (C::kQBytes >> 4));
-          const uint64_t kb = dk0 + static_cast<uint64_t>((slot * C::kUnitBytes) >> 4);
+          const uint64_t kb = dk0 + static_cast<uint64_t>((ks * C::kUnitBytes) >> 4);
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t qoff = ((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4;
-            const uint32_t koff = ((ks >> 2) * (KT * 128) + (ks & 3) * 32) >> 4;
-            umma_f16(tmem + X * 128, qa + qoff, kb + koff, idS, ks > 0 ? 1u : 0u);
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t qoff = ((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4;
+            const uint32_t koff = ((k >> 2) * (KT * 128) + (k & 3) * 32) >> 4;
+            umma_f16(tmem + X * 128, qa + qoff, kb + koff, idS, k > 0 ? 1u : 0u);
           }
           umma_commit(smem_u32(&s_full[X]));
-          if (!dual || X == 1) umma_commit(smem_u32(&u_empty[slot]));
+          if (!dual || X == 1) umma_commit(smem_u32(&u_empty[ks]));
           return true;
         };
-        ok = issue_s(0, 0);
-        if (ok && n1 > 0) ok = issue_s(1, 0);
+        ok = issue_s(0);
+        if (ok && n1 > 0) ok = issue_s(1);
         // the last piece's O has been read
         if (ok && piece > 0) ok = wait(o_free, piece - 1);
         for (int i = 0; i < n0 && ok; ++i) {
           for (int X = 0; X < 2; ++X) {
-            const int nX = X ? n1 : n0;
-            if (i >= nX) continue;
+            if (X == 1 && i >= n1) continue;
             const int c = (X ? c1 : c0) + i;  // this tile is the group's c-th
-            const int j = dual ? i : 2 * i + X;
-            const int u = u0 + v_unit(j, T, dual), slot = u % C::kUnits;
-            if (!(ok = wait(&u_full[slot], u / C::kUnits) && wait(&p_full[X], c))) break;
+            if (!(dual && X == 1) && !(ok = take(vs))) break;
+            const uint64_t vb = dv0 + static_cast<uint64_t>((vs * C::kUnitBytes) >> 4);
+            const uint32_t o_tm = tmem + 256 + (kOneO ? 0 : X * D);
+            const bool more = (kOneO ? i + X : i) > 0;
+            if (!(ok = wait(&p_full[X], c))) break;
             tc_fence_after();
-            const uint64_t vb = dv0 + static_cast<uint64_t>((slot * C::kUnitBytes) >> 4);
 #pragma unroll
-            for (int kk = 0; kk < KT / 16; ++kk)
-              umma_f16_ts(tmem + 256 + (kOneO ? 0 : X * D), tmem + X * 128 + kk * 8,
-                          vb + ((kk * 2048) >> 4), idO,
-                          ((kOneO ? j : i) > 0 || kk > 0) ? 1u : 0u);
+            for (int k = 0; k < KT / 16; ++k)
+              umma_f16_ts(o_tm, tmem + X * 128 + k * 8, vb + ((k * 2048) >> 4), idO,
+                          more || k > 0 ? 1u : 0u);
             umma_commit(smem_u32(&o_done[X]));
-            if (!dual || X == 1) umma_commit(smem_u32(&u_empty[slot]));
-            if (i + 1 < nX) {
+            if (!dual || X == 1) umma_commit(smem_u32(&u_empty[vs]));
+            if (i + 1 < (X ? n1 : n0)) {
               // the next scores overwrite P: the product that reads it is done first
               if (!(ok = wait(&o_done[X], c))) break;
-              tc_fence_after();
-              if (!(ok = issue_s(X, i + 1))) break;
+              if (!(ok = issue_s(X))) break;
             }
           }
         }
-        u0 += 2 * T;
         c0 += n0;
         c1 += n1;
         ++piece;
@@ -665,7 +670,9 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
     // =========================== widening warps ===========================
     if constexpr (kQuant) {
       const int cw = warp - kTreeConv;
-      int u0 = 0, tile0 = 0, piece = 0;
+      int tile0 = 0, piece = 0;
+      int rs = 0, us = 0;               // raw unit, and its place as an operand
+      uint32_t r_turn = 0, u_turn = 1;  // their rings' parities: an operand's first turn is free
       while (!failed && walk.next(q)) {
         const int nodes = min(IN, q.p.s.n - q.rt * IN);
         const bool dual = nodes > TPG;
@@ -683,15 +690,12 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&q_full[buf]));
         ++piece;
+        int next_k = 0, next_v = 0;
         for (int t = 0; t < 2 * T; ++t) {
-          bool is_v;
-          int j;
-          unit_at(t, T, dual, is_v, j);
-          const int u = u0 + t;
-          const int rs = u % C::kRaws, us = u % C::kUnits;
-          if (!warp_sleep_wait(smem_u32(&r_full[rs]), (u / C::kRaws) & 1, abort_s) ||
-              (u >= C::kUnits &&
-               !warp_sleep_wait(smem_u32(&u_empty[us]), ((u / C::kUnits) - 1) & 1, abort_s))) {
+          const bool is_v = next_k == T || (dual ? t & 1 : next_k - next_v == 2);  // as unit_at
+          const int j = is_v ? next_v++ : next_k++;
+          if (!warp_sleep_wait(smem_u32(&r_full[rs]), r_turn, abort_s) ||
+              !warp_sleep_wait(smem_u32(&u_empty[us]), u_turn, abort_s)) {
             give_up(lane == 0);
             break;
           }
@@ -708,8 +712,15 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
             mbar_arrive(smem_u32(&u_full[us]));
             mbar_arrive(smem_u32(&r_empty[rs]));
           }
+          if (++rs == C::kRaws) {
+            rs = 0;
+            r_turn ^= 1u;
+          }
+          if (++us == C::kUnits) {
+            us = 0;
+            u_turn ^= 1u;
+          }
         }
-        u0 += 2 * T;
         tile0 += T;
       }
     }
@@ -763,7 +774,6 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
         const int sx = kOneO ? jl & 1 : X;  // score buffer
         const uint32_t s_tm = tmem + lane_base + sx * 128;
         const int t0 = tile_key(q.p, q.j0 + j, KT);
-        const int vu = u0 + v_unit(j, T, dual), vslot = vu % C::kUnits;
         const int cnt = (sx ? c1 : c0) + (kOneO ? jl >> 1 : jl);
         if (!warp_sleep_wait(smem_u32(&s_full[sx]), cnt & 1, abort_s)) {
           give_up(lane == 0);
@@ -776,6 +786,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
           if ((bad != 0u || t0 < any.lo || t0 + KT > any.prefix) && (!dual || X == 0) && m < KT) {
             const uint32_t keep = seen32(any, t0 + (warp & 3) * 32) & ~bad32<BS>(bad, warp & 3);
             if (keep != 0xFFFFFFFFu) {
+              const int vu = u0 + v_unit(j, T, dual), vslot = vu % C::kUnits;
               if (!warp_sleep_wait(smem_u32(&u_full[vslot]), (vu / C::kUnits) & 1, abort_s)) {
                 give_up(lane == 0);
                 break;
@@ -1096,7 +1107,7 @@ size_t tree_umma_workspace(int max_q_len, int group, int head_dim, int num_sms, 
     w->ctas = num_sms;
     w->rows = rows;
     w->item_nodes = item_nodes;
-    w->min_units = kTreeSlack;
+    w->min_units = kTreeLeast;
   }
   return l.bytes;
 }
