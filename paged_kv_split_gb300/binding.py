@@ -15,13 +15,18 @@ import os
 
 import torch
 
-from .build import LIB as _LIB_PATH
+from .build import LIB as _LIB_PATH, MARSHAL as _MARSHAL_PATH
 
-if not os.path.exists(_LIB_PATH):
-    raise ImportError(f"{_LIB_PATH} is not built; run `python -m paged_kv_split_gb300.build` "
-                      "(or __graft_entry__.build()) on a machine with nvcc")
+for _path in (_LIB_PATH, _MARSHAL_PATH):
+    if not os.path.exists(_path):
+        raise ImportError(f"{_path} is not built; run `python -m paged_kv_split_gb300.build` "
+                          "(or __graft_entry__.build()) on a machine with nvcc")
 
 _lib = ctypes.CDLL(_LIB_PATH)
+
+# the draft-and-verify calls without ctypes, for the arguments they usually get:
+# a status, or None for others, which the Python below then takes or refuses
+from . import _marshal  # noqa: E402
 
 PD_OK = 0
 PD_KV_BF16, PD_KV_FP8_E4M3, PD_KV_NVFP4 = 0, 1, 2
@@ -685,6 +690,13 @@ def pd_qk_norm_rope_cache(qkv, q_out, k_cache, v_cache, positions, slot_mapping,
     possibly more). q_out: contiguous bf16 [T, Hq, D]. positions, slot_mapping:
     int32 [T]. cos_sin: float32 [max_position, rot_dim] from pd_rope_table.
     Without weights only the rotation is applied."""
+    code = _dtype_code(kv_dtype)
+    rc = _marshal.norm_rope(qkv, q_out, 0, 0, k_cache, v_cache, positions, slot_mapping, cos_sin,
+                            num_kv_heads, block_size, num_blocks, q_weight, k_weight, eps,
+                            weight_offset, interleaved, code, k_scale, v_scale, _stream(stream))
+    if rc is not None:
+        _check("pd_qk_norm_rope_cache", rc)
+        return q_out
     if q_out.dim() != 3 or q_out.shape[0] != qkv.shape[0]:
         raise ValueError("q_out must be bf16 [num_tokens, num_q_heads, head_dim]")
     _norm_rope(qkv, q_out, 0, q_out.shape[1], q_out.shape[2], k_cache, v_cache, positions,
@@ -699,6 +711,14 @@ def pd_qk_norm_rope_cache_(qkv, k_cache, v_cache, positions, slot_mapping, cos_s
                            kv_dtype=PD_KV_BF16, k_scale=1.0, v_scale=1.0, stream=None):
     """pd_qk_norm_rope_cache in place: the q heads of the fused rows are
     replaced by their rotated form, ready for pd_decode_tree_strided."""
+    code = _dtype_code(kv_dtype)
+    rc = _marshal.norm_rope(qkv, None, num_q_heads, head_dim, k_cache, v_cache, positions,
+                            slot_mapping, cos_sin, num_kv_heads, block_size, num_blocks, q_weight,
+                            k_weight, eps, weight_offset, interleaved, code, k_scale, v_scale,
+                            _stream(stream))
+    if rc is not None:
+        _check("pd_qk_norm_rope_cache", rc)
+        return qkv
     _norm_rope(qkv, qkv, qkv.shape[-1], num_q_heads, head_dim, k_cache, v_cache, positions,
                slot_mapping, cos_sin, num_kv_heads, block_size, num_blocks, q_weight, k_weight,
                eps, weight_offset, interleaved, kv_dtype, k_scale, v_scale, stream)
@@ -723,6 +743,14 @@ def pd_decode_tree_workspace_bytes(max_q_len, num_q_heads, num_kv_heads, head_di
     return n
 
 
+def _tree_scratch(q, workspace, max_q_len, hq, num_kv_heads, d, code):
+    if workspace is not None:
+        return workspace
+    # 0 for refused shapes: the call says why
+    n = _tree_workspace(max_q_len, hq, num_kv_heads, d, code, _num_sms(q.get_device()))
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=q.device)
+
+
 def _decode_tree(fn, q, q_stride, cu_q, tree_mask, k_cache, v_cache, block_tables, seq_lens, out,
                  out_stride, T, hq, d, max_q_len, num_kv_heads, block_size, num_blocks, scale,
                  sliding_window, num_sinks, kv_dtype, k_scale, v_scale, workspace, stream):
@@ -740,10 +768,7 @@ def _decode_tree(fn, q, q_stride, cu_q, tree_mask, k_cache, v_cache, block_table
             raise ValueError("tree_mask must be int64 [total_q]")
         mask = _ptr(tree_mask, "tree_mask", torch.int64, dev)
     code = _dtype_code(kv_dtype)
-    if workspace is None:
-        # 0 for refused shapes: the call below says why
-        n = _tree_workspace(max_q_len, hq, num_kv_heads, d, code, _num_sms(dev))
-        workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=q.device)
+    workspace = _tree_scratch(q, workspace, max_q_len, hq, num_kv_heads, d, code)
     rc = fn(
         _ptr(q, "q", torch.bfloat16, dev), q_stride, _ptr(cu_q, "cu_q", torch.int32, dev), mask,
         _cache_ptr(k_cache, "k_cache", dev), _cache_ptr(v_cache, "v_cache", dev),
@@ -772,6 +797,16 @@ def pd_decode_tree(q, cu_q, k_cache, v_cache, block_tables, seq_lens, out, *, ma
     if q.dim() != 3 or out.shape != q.shape:
         raise ValueError("q and out must be bf16 [total_q, num_q_heads, head_dim]")
     T, hq, d = q.shape
+    if not crosscheck and q.is_cuda:
+        code = _dtype_code(kv_dtype)
+        workspace = _tree_scratch(q, workspace, max_q_len, hq, num_kv_heads, d, code)
+        rc = _marshal.decode_tree(q, out, 0, 0, cu_q, tree_mask, k_cache, v_cache, block_tables,
+                                  seq_lens, max_q_len, num_kv_heads, block_size, num_blocks, scale,
+                                  sliding_window, num_sinks, code, k_scale, v_scale, workspace,
+                                  _stream(stream))
+        if rc is not None:
+            _check("pd_decode_tree", rc)
+            return out
     _decode_tree(_lib.pd_decode_tree_crosscheck if crosscheck else _lib.pd_decode_tree, q, 0, cu_q,
                  tree_mask, k_cache, v_cache, block_tables, seq_lens, out, 0, T, hq, d, max_q_len,
                  num_kv_heads, block_size, num_blocks, scale, sliding_window, num_sinks, kv_dtype,
@@ -786,6 +821,17 @@ def pd_decode_tree_strided(q_rows, cu_q, k_cache, v_cache, block_tables, seq_len
                            stream=None, crosscheck=False):
     """pd_decode_tree with each node's Hq * D values in the first Hq * D of a
     row of a wider buffer (q_rows / out_rows: contiguous bf16 [total_q, row])."""
+    if not crosscheck and q_rows.is_cuda:
+        code = _dtype_code(kv_dtype)
+        workspace = _tree_scratch(q_rows, workspace, max_q_len, num_q_heads, num_kv_heads, head_dim,
+                                  code)
+        rc = _marshal.decode_tree(q_rows, out_rows, num_q_heads, head_dim, cu_q, tree_mask, k_cache,
+                                  v_cache, block_tables, seq_lens, max_q_len, num_kv_heads,
+                                  block_size, num_blocks, scale, sliding_window, num_sinks, code,
+                                  k_scale, v_scale, workspace, _stream(stream))
+        if rc is not None:
+            _check("pd_decode_tree", rc)
+            return out_rows
     T, stride = _strided_rows(q_rows, num_q_heads, head_dim, "q_rows")
     To, ostride = _strided_rows(out_rows, num_q_heads, head_dim, "out_rows")
     if To != T:
@@ -805,6 +851,12 @@ def pd_compact_tree(k_caches, v_caches, block_tables, seq_lens, cu_q, accepted, 
     k_caches, v_caches: one layer's cache (1-D), or all layers' as [layers,
     cache_bytes]. accepted: int32 [B, max_accepted] strictly increasing node
     indices, num_accepted: int32 [B], new_seq_lens: int32 [B], written."""
+    rc = _marshal.compact_tree(k_caches, v_caches, block_tables, seq_lens, cu_q, accepted,
+                               num_accepted, new_seq_lens, num_kv_heads, head_dim, block_size,
+                               num_blocks, _dtype_code(kv_dtype), _stream(stream))
+    if rc is not None:
+        _check("pd_compact_tree", rc)
+        return new_seq_lens
     if k_caches.shape != v_caches.shape or k_caches.dim() not in (1, 2):
         raise ValueError("k_caches and v_caches must be [cache_bytes] or [layers, cache_bytes]")
     layers = k_caches.shape[0] if k_caches.dim() == 2 else 1

@@ -1,18 +1,21 @@
 """Build libpd.so in-tree with nvcc for sm_103a.
 
 Each .cu under csrc/ compiles to an object in parallel; the objects link into
-paged_kv_split_gb300/libpd.so against the shared CUDA runtime. A rebuild
-happens only when a source or header is newer than the library.
+paged_kv_split_gb300/libpd.so against the shared CUDA runtime; csrc/marshal.cpp
+becomes the Python module _marshal.so beside it. A rebuild happens only when a
+source or header is newer than the libraries.
 
     python -m paged_kv_split_gb300.build [--force] [--verbose-ptxas]
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,6 +23,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpd.so")
+MARSHAL_SRC = os.path.join(CSRC, "marshal.cpp")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = [
@@ -43,14 +48,14 @@ def sources():
 
 
 def _inputs():
-    return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(
+    return sources() + [MARSHAL_SRC] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(
         os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
 
 
 def is_stale() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(MARSHAL)):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(MARSHAL))
     return any(os.path.getmtime(p) > t for p in _inputs())
 
 
@@ -67,6 +72,14 @@ def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = True) 
         objs.append(obj)
         cmd = [cc, *NVCC_FLAGS, *extra, "-c", src, "-o", obj]
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    marshal_obj = os.path.join(BUILD_DIR, "marshal.cpp.o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-I", INCLUDE,
+           "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(torch_dir, "include"),
+           "-isystem", os.path.join(torch_dir, "include/torch/csrc/api/include"),
+           "-c", MARSHAL_SRC, "-o", marshal_obj]
+    procs.append((MARSHAL_SRC, subprocess.Popen(cmd, stdout=subprocess.PIPE,
+                                                stderr=subprocess.STDOUT)))
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -77,12 +90,18 @@ def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = True) 
             sys.stdout.write(text)
     if failed:
         msg = "\n".join(f"--- {s}\n{t}" for s, t in failed)
-        raise RuntimeError(f"nvcc failed:\n{msg}")
+        raise RuntimeError(f"compiling failed:\n{msg}")
     tmp = LIB + f".tmp{os.getpid()}"
     cuda_lib = os.path.join(os.path.dirname(os.path.dirname(cc)), "lib64")
     subprocess.run([cc, *ARCH, "-shared", "-cudart", "shared", "-Xlinker", f"-rpath,{cuda_lib}",
                     "-o", tmp, *objs], check=True)
     os.replace(tmp, LIB)
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    torch_lib = os.path.join(torch_dir, "lib")
+    subprocess.run(["g++", "-shared", "-o", tmp, marshal_obj, "-L", PKG, "-l:libpd.so",
+                    "-L", torch_lib, "-ltorch_python", "-ltorch_cpu", "-lc10",
+                    "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{torch_lib}"], check=True)
+    os.replace(tmp, MARSHAL)
     return LIB
 
 
