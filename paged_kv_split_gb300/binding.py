@@ -690,13 +690,14 @@ def pd_qk_norm_rope_cache(qkv, q_out, k_cache, v_cache, positions, slot_mapping,
     possibly more). q_out: contiguous bf16 [T, Hq, D]. positions, slot_mapping:
     int32 [T]. cos_sin: float32 [max_position, rot_dim] from pd_rope_table.
     Without weights only the rotation is applied."""
-    code = _dtype_code(kv_dtype)
-    rc = _marshal.norm_rope(qkv, q_out, 0, 0, k_cache, v_cache, positions, slot_mapping, cos_sin,
-                            num_kv_heads, block_size, num_blocks, q_weight, k_weight, eps,
-                            weight_offset, interleaved, code, k_scale, v_scale, _stream(stream))
-    if rc is not None:
-        _check("pd_qk_norm_rope_cache", rc)
-        return q_out
+    if qkv.is_cuda:
+        rc = _marshal.norm_rope(qkv, q_out, 0, 0, k_cache, v_cache, positions, slot_mapping,
+                                cos_sin, num_kv_heads, block_size, num_blocks, q_weight, k_weight,
+                                eps, weight_offset, interleaved, _dtype_code(kv_dtype), k_scale,
+                                v_scale, _stream(stream))
+        if rc is not None:
+            _check("pd_qk_norm_rope_cache", rc)
+            return q_out
     if q_out.dim() != 3 or q_out.shape[0] != qkv.shape[0]:
         raise ValueError("q_out must be bf16 [num_tokens, num_q_heads, head_dim]")
     _norm_rope(qkv, q_out, 0, q_out.shape[1], q_out.shape[2], k_cache, v_cache, positions,
@@ -711,14 +712,14 @@ def pd_qk_norm_rope_cache_(qkv, k_cache, v_cache, positions, slot_mapping, cos_s
                            kv_dtype=PD_KV_BF16, k_scale=1.0, v_scale=1.0, stream=None):
     """pd_qk_norm_rope_cache in place: the q heads of the fused rows are
     replaced by their rotated form, ready for pd_decode_tree_strided."""
-    code = _dtype_code(kv_dtype)
-    rc = _marshal.norm_rope(qkv, None, num_q_heads, head_dim, k_cache, v_cache, positions,
-                            slot_mapping, cos_sin, num_kv_heads, block_size, num_blocks, q_weight,
-                            k_weight, eps, weight_offset, interleaved, code, k_scale, v_scale,
-                            _stream(stream))
-    if rc is not None:
-        _check("pd_qk_norm_rope_cache", rc)
-        return qkv
+    if qkv.is_cuda:
+        rc = _marshal.norm_rope(qkv, None, num_q_heads, head_dim, k_cache, v_cache, positions,
+                                slot_mapping, cos_sin, num_kv_heads, block_size, num_blocks,
+                                q_weight, k_weight, eps, weight_offset, interleaved,
+                                _dtype_code(kv_dtype), k_scale, v_scale, _stream(stream))
+        if rc is not None:
+            _check("pd_qk_norm_rope_cache", rc)
+            return qkv
     _norm_rope(qkv, qkv, qkv.shape[-1], num_q_heads, head_dim, k_cache, v_cache, positions,
                slot_mapping, cos_sin, num_kv_heads, block_size, num_blocks, q_weight, k_weight,
                eps, weight_offset, interleaved, kv_dtype, k_scale, v_scale, stream)
@@ -851,12 +852,13 @@ def pd_compact_tree(k_caches, v_caches, block_tables, seq_lens, cu_q, accepted, 
     k_caches, v_caches: one layer's cache (1-D), or all layers' as [layers,
     cache_bytes]. accepted: int32 [B, max_accepted] strictly increasing node
     indices, num_accepted: int32 [B], new_seq_lens: int32 [B], written."""
-    rc = _marshal.compact_tree(k_caches, v_caches, block_tables, seq_lens, cu_q, accepted,
-                               num_accepted, new_seq_lens, num_kv_heads, head_dim, block_size,
-                               num_blocks, _dtype_code(kv_dtype), _stream(stream))
-    if rc is not None:
-        _check("pd_compact_tree", rc)
-        return new_seq_lens
+    if k_caches.is_cuda:
+        rc = _marshal.compact_tree(k_caches, v_caches, block_tables, seq_lens, cu_q, accepted,
+                                   num_accepted, new_seq_lens, num_kv_heads, head_dim, block_size,
+                                   num_blocks, _dtype_code(kv_dtype), _stream(stream))
+        if rc is not None:
+            _check("pd_compact_tree", rc)
+            return new_seq_lens
     if k_caches.shape != v_caches.shape or k_caches.dim() not in (1, 2):
         raise ValueError("k_caches and v_caches must be [cache_bytes] or [layers, cache_bytes]")
     layers = k_caches.shape[0] if k_caches.dim() == 2 else 1
