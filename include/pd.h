@@ -514,6 +514,8 @@ size_t pd_decode_tree_workspace_bytes(int32_t max_q_len, int32_t num_q_heads,
  *   sliding_window, num_sinks   W > 0 hides the rows whose position is W or
  *               more before the node's, except positions below num_sinks,
  *               the first tokens that stay visible. W = 0: everything stays.
+ * Lengths are read on the device only: a captured graph follows cu_q, seq_lens
+ * and the masks as they are at each replay (max_q_len is the one host bound).
  * out = softmax(scale q k) v over what the node sees, fp32 softmax; a node
  * that sees nothing gets a zero row. Cache rows that no node of the sequence
  * sees may hold anything; rows that one does see are taken to be finite.

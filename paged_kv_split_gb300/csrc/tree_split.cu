@@ -2,7 +2,8 @@
 // memory: mma.sync tiles with keys on M and 8 or 16 rows (nodes times q
 // heads) on N, head_dim split over four consumer warps, as decode_balanced.cu
 // has them (mma_tile.cuh). More rows than that are further node tiles, which
-// run side by side and find the keys in L2.
+// run side by side and find the keys in L2: single tokens and small trees run near
+// the memory's rate, 64 nodes of 8 heads at 20 times their floor.
 //
 // Keys are dealt by the device plan of tree_plan.cuh in 16-key tiles; a warp
 // produces (TMA copies for BF16 and FP8, bulk copies for NVFP4, one page a tile)
