@@ -17,7 +17,7 @@
 // CTAs stay, each with a run of (token, head group) items, the next item's rows
 // on their way while one is computed. Measured: 8192 rows of 32 + 2 x 8 heads of
 // 128 in 41.4 us, 74% of the copy rate, 65% of the issue slots taken (one chunk a
-// lane, partners by shuffle: 77 us; 4, 5 or 8 resident CTAs: 42 to 47); 832 rows
+// lane, partners by shuffle: 77 us; 4 or 8 resident CTAs: 49 and 51); 832 rows
 // into FP8 9.5 us, 8 rows 2.4 us, both a chain of latencies.
 #include "pd_common.cuh"
 
