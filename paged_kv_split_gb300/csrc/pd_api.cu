@@ -1079,7 +1079,7 @@ size_t pd_decode_tree_workspace_bytes(int32_t max_q_len, int32_t num_q_heads,
   if (num_kv_heads <= 0 || num_q_heads <= 0 || num_q_heads % num_kv_heads != 0 ||
       num_q_heads / num_kv_heads > kMaxGroup || !head_dim_ok(head_dim) || !dtype_ok(kv_dtype))
     return 0;
-  if (head_dim > 256)
+  if (!tree_on_umma(max_q_len, num_q_heads / num_kv_heads, head_dim))
     return tree_split_workspace(max_q_len, num_q_heads / num_kv_heads, kv_dtype, num_sms, nullptr,
                                 nullptr);
   return tree_umma_workspace(max_q_len, num_q_heads / num_kv_heads, head_dim, num_sms, nullptr,
@@ -1149,7 +1149,9 @@ int decode_tree_impl(const void* q, int64_t q_stride, const int32_t* cu_q,
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (simple) return cuda_status(launch_tree_simple(a, head_dim, kv_dtype, st));
   TreeWork w;
-  if (head_dim <= 256) {
+  a.half_bits = 0;
+  if (tree_on_umma(max_q_len, a.group, head_dim)) {
+    a.half_bits = head_dim > 256 ? 1 : 0;
     tree_umma_workspace(max_q_len, a.group, head_dim, dev->num_sms, &w, workspace);
     return cuda_status(launch_tree_umma(a, w, head_dim, kv_dtype, st));
   }

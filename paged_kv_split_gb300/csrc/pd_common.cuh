@@ -254,6 +254,7 @@ struct TreeArgs {
   int64_t num_blocks, page_bytes, data_bytes;
   int num_seqs, total_q, max_q_len, num_q_heads, num_kv_heads, group, block_size;
   int max_blocks_per_seq, sliding_window, num_sinks;
+  int half_bits;                 // 1: an item is half of head_dim's columns of V and O
   float scale_log2;              // scale * log2(e)
   float k_scale, v_scale;
 };

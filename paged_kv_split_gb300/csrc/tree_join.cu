@@ -13,7 +13,8 @@ using namespace ::pd::tree;
 // the pieces in key order. A warp takes 4 rows x 32 head_dim columns, so that
 // partials are read and outputs written in whole 64-byte pieces. What it costs
 // is latency (record, then partials), so kBatch pieces are read at once.
-template <int D>
+// D columns of a head's HD.
+template <int D, int HD>
 __global__ void __launch_bounds__(256) tree_join_kernel(const TreeArgs a, const TreeWork w) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const JoinRecord rec = w.records[blockIdx.x];
@@ -22,7 +23,8 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const TreeArgs a, const 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int d4 = (blockIdx.y % kColBlocks) * 8 + (lane & 7);
   const int r = (blockIdx.y / kColBlocks) * 32 + warp * 4 + (lane >> 3);
-  if (rec.pieces == 0 || r >= rec.nodes * a.group) return;
+  const int nodes = rec.nodes & 0xFFFF, col0 = (rec.nodes >> 16) * D;
+  if (rec.pieces == 0 || r >= nodes * a.group) return;
   // the first piece is its CTA's second slot, the others their CTAs' first
   const int64_t slot0 = 2 * static_cast<int64_t>(blockIdx.x);
   const float2* ml = w.ml + slot0 * w.rows + r;
@@ -67,7 +69,7 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const TreeArgs a, const 
   const float inv = 1.0f / fmaxf(l, 1e-20f);
   const int node = r / a.group;
   uint16_t* out = a.out + static_cast<int64_t>(rec.row0 + node) * a.out_stride +
-                  static_cast<int64_t>(rec.head0 + r - node * a.group) * D + d4 * 4;
+                  static_cast<int64_t>(rec.head0 + r - node * a.group) * HD + col0 + d4 * 4;
   *reinterpret_cast<uint2*>(out) =
       make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
 }
@@ -75,12 +77,15 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const TreeArgs a, const 
 }  // namespace
 
 cudaError_t launch_tree_join(const TreeArgs& a, const TreeWork& w, int head_dim, cudaStream_t st) {
-  const dim3 grid(w.ctas, (w.rows + 31) / 32 * (head_dim / 32));
+  const int cols = head_dim >> a.half_bits;
+  const dim3 grid(w.ctas, (w.rows + 31) / 32 * (cols / 32));
   switch (head_dim) {
-    case 64: return launch_dependent(grid, 256, 0, st, tree_join_kernel<64>, a, w);
-    case 128: return launch_dependent(grid, 256, 0, st, tree_join_kernel<128>, a, w);
-    case 256: return launch_dependent(grid, 256, 0, st, tree_join_kernel<256>, a, w);
-    default: return launch_dependent(grid, 256, 0, st, tree_join_kernel<512>, a, w);
+    case 64: return launch_dependent(grid, 256, 0, st, tree_join_kernel<64, 64>, a, w);
+    case 128: return launch_dependent(grid, 256, 0, st, tree_join_kernel<128, 128>, a, w);
+    case 256: return launch_dependent(grid, 256, 0, st, tree_join_kernel<256, 256>, a, w);
+    default:
+      return a.half_bits ? launch_dependent(grid, 256, 0, st, tree_join_kernel<256, 512>, a, w)
+                         : launch_dependent(grid, 256, 0, st, tree_join_kernel<512, 512>, a, w);
   }
 }
 

@@ -25,7 +25,7 @@ struct SeqPlan {
   int nst;   // leading tiles, from key 0, for the first tokens
   int base;  // first key of the other tiles (page aligned)
   int nt;    // tiles
-  int rts;   // node tiles
+  int rts;   // node tiles (times two where V's columns come in halves)
 };
 __device__ __forceinline__ SeqPlan seq_plan(const TreeArgs& a, int b, int tpc, int kt, int* flags) {
   SeqPlan p;
@@ -41,7 +41,7 @@ __device__ __forceinline__ SeqPlan seq_plan(const TreeArgs& a, int b, int tpc, i
     if (p.base <= p.nst * kt) p.nst = p.base = 0;  // the two ranges meet
   }
   p.nt = p.nst + (p.s.L - p.base + kt - 1) / kt;
-  p.rts = (p.s.n + tpc - 1) / tpc;
+  p.rts = (p.s.n + tpc - 1) / tpc << a.half_bits;
   return p;
 }
 // First key of tile j.
@@ -130,7 +130,7 @@ __device__ __forceinline__ Share make_share(const TreeArgs& a, int tpc, int kt, 
 // A CTA's part of one item.
 struct Piece {
   SeqPlan p;
-  int b, g, rt;
+  int b, g, rt, half;
   int j0, j1;     // its tiles
   bool begins;    // holds the item's first tile
   bool whole;     // and its last: writes the output itself
@@ -162,6 +162,8 @@ struct Walker {
       x += take;
       q.g = k / p.rts;
       q.rt = k % p.rts;
+      q.half = q.rt & ((1 << a.half_bits) - 1);
+      q.rt >>= a.half_bits;
       if (off + take == p.nt + ov) {
         ++k;
         off = 0;
@@ -188,7 +190,8 @@ struct Walker {
 };
 
 // What a CTA leaves for the join: the item that begins in it and goes on (its
-// first query row, nodes, first q head), or pieces = 0.
+// first query row, nodes (bit 16: the second half of head_dim), first q head), or
+// pieces = 0.
 struct JoinRecord {
   int pieces, row0, nodes, head0;
 };
@@ -233,8 +236,15 @@ inline cudaError_t launch_dependent(dim3 grid, int threads, int smem, cudaStream
 }
 
 cudaError_t launch_tree_join(const TreeArgs& a, const TreeWork& w, int head_dim, cudaStream_t st);
-// head_dim 64 to 256 on tcgen05, 512 on mma.sync. The workspace functions return
+// On tcgen05 or, where it says so, on mma.sync. The workspace functions return
 // its size and, with w, lay it out.
+// head_dim 512 in up to 32 rows (nodes times q heads of a kv head) runs on mma.sync,
+// 16 rows a pass over the keys; on tcgen05 128 rows take two passes. 8 sequences
+// over 8192 keys, mma.sync against tcgen05 in us, BF16 / FP8 / NVFP4: 32 rows 113 /
+// 120 / 113 against 109 / 123 / 139, 64 rows 213 / 220 / 200 against 112 / 128 / 145.
+inline bool tree_on_umma(int max_q_len, int group, int head_dim) {
+  return head_dim <= 256 || max_q_len * group > 32;
+}
 size_t tree_split_workspace(int max_q_len, int group, int kv_dtype, int num_sms, TreeWork* w,
                             void* workspace);
 cudaError_t launch_tree_split(const TreeArgs& a, const TreeWork& w, int kv_dtype, cudaStream_t st);

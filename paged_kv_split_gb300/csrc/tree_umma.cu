@@ -1,4 +1,4 @@
-// Draft-tree attention on the 5th-generation tensor cores, head_dim 64 to 256.
+// Draft-tree attention on the 5th-generation tensor cores, head_dim 64 to 512.
 //
 // The rows of one kv head are the nodes times its G q heads, so every key byte
 // serves n G rows: at 4 D bytes a key (BF16) and 4 D n G operations the keys'
@@ -10,7 +10,8 @@
 //    tile is 128 keys. Two groups of four softmax warps, one thread a row:
 //    up to 128 rows the groups take alternate tiles of the same rows and merge
 //    at the end; above, each takes 128 rows of every tile. (head_dim 256: one
-//    group, 64 keys, see kOneO.)
+//    group, 64 keys, see kOneO. head_dim 512: 32 keys, and an item is half of the
+//    columns of V and O, so K is read twice, the second time mostly from L2.)
 //  * TMEM holds per group S (128 columns fp32), over which P is written as
 //    16-bit pairs, and O (D columns). P is then the A operand from TMEM, so
 //    shared memory carries K, V and Q only.
@@ -30,7 +31,8 @@
 //    2 trees of 64 nodes over 32K keys 85 us (808 TFLOP/s), bound by each group's
 //    chain of scores, softmax and weighted values; 64 trees in FP8 181 us, by the
 //    same chain with the widening in it. Without the softmax these take 94, 65, 73
-//    and 141 us, with an eighth of the products 95, 66, 71 and 165.
+//    and 141 us, with an eighth of the products 95, 66, 71 and 165. head_dim 512, 64
+//    nodes of 8 heads over 28000 keys: 179 us (mma.sync 690).
 //  * Every wait is bounded (2 s): on time-out the CTA raises PD_DEV_TIMEOUT,
 //    waits for its copies and MMAs in flight, frees its TMEM and ends.
 #include <cuda.h>
@@ -70,29 +72,35 @@ constexpr int kTreeBadRing = 32;      // tiles whose page masks are kept
 template <int FMT, int D, int BS>
 struct TreeCfg {
   static constexpr bool kQuant = FMT != PD_KV_BF16;
-  // head_dim 256: one O fills half the tensor memory, so a single group of
+  // head_dim 256 and up: one O fills half the tensor memory, so a single group of
   // softmax warps takes every tile, its scores in two buffers by turns
-  static constexpr bool kOneO = D == 256;
-  static constexpr int kKT = D == 256 ? 64 : 128;            // keys of a tile
-  static constexpr int kQTiles = D == 256 ? 1 : 2;
+  static constexpr bool kOneO = D >= 256;
+  // head_dim 512: an item is one half of the columns of V and O, with all of K
+  static constexpr int kHalves = D == 512 ? 2 : 1;
+  static constexpr int kDV = D / kHalves;
+  static constexpr int kKT = D == 512 ? 32 : D == 256 ? 64 : 128;  // keys of a tile
+  static constexpr int kQTiles = kOneO ? 1 : 2;
   static constexpr int kSoftWarps = kOneO ? 4 : 8;
   // One thread issues a 2 KB copy about every 100 cycles, a third of the rate at
   // which an SM's share of the memory delivers BF16 units: four producers.
-  // Quantised units take half the copies or fewer.
-  static constexpr int kProds = kQuant ? 2 : 4;
+  // Quantised units take half the copies or fewer. (A producer must not come back
+  // to a slot whose last but one unit is still in use: no more of them than slots.)
+  static constexpr int kProds = kQuant || D == 512 ? 2 : 4;
   static constexpr int kThreads = (kQuant ? kTreeConv + 4 : kTreeProd + kProds) * 32;
   static constexpr int kCopies = kKT / BS;            // pages of a tile
   static constexpr int kQBytes = 128 * D * 2;             // one Q tile, chunk-major
   static constexpr int kUnitBytes = kKT * D * 2;      // one 16-bit K or V unit, chunk-major
-  static constexpr int kUnits = (kQuant ? 96 : 160) * 1024 / kUnitBytes;
-  // a raw quantised unit: rows [128][row bytes], then NVFP4 scales [128][D / 16]
+  static constexpr int kUnits =
+      ((kQuant ? 96 : 160) - (D == 512 ? (kQuant ? 32 : 64) : 0)) * 1024 / kUnitBytes;
+  // a raw quantised unit: rows [kKT][row bytes] (FP8: in slabs of 256 columns), then
+  // NVFP4 scales [kKT][D / 16]
   static constexpr int kRowBytes = FMT == PD_KV_FP8_E4M3 ? D : D / 2;
   static constexpr int kRawData = kKT * kRowBytes;
   static constexpr int kRawScales = FMT == PD_KV_NVFP4 ? kKT * (D / 16) : 0;
   static constexpr int kRawBytes = kQuant ? (kRawData + kRawScales + 1023) / 1024 * 1024 : 0;
   // NVFP4 pages by gathers of four, while a head's codes of a page fit a box
   static constexpr bool kGather = FMT == PD_KV_NVFP4 && BS == 16 && D <= 128;
-  static constexpr int kRaws = kQuant ? 64 * 1024 / kRawBytes : 0;
+  static constexpr int kRaws = kQuant ? (D == 512 ? 32 : 64) * 1024 / kRawBytes : 0;
   static constexpr int kUnitOff = kQTiles * kQBytes;
   static constexpr int kRawOff = kUnitOff + kUnits * kUnitBytes;
   static constexpr int kBarOff = kRawOff + kRaws * kRawBytes;
@@ -106,6 +114,7 @@ struct TreeCfg {
   static constexpr int kBadOff = kMulOff + 256 * 4;
   static constexpr int kHolderOff = kBadOff + kTreeBadRing * 4;
   static constexpr int kSmemBytes = kHolderOff + 16;
+  static_assert(kProds <= (kQuant ? kRaws : kUnits), "producers are not lapped");
   static_assert(kUnitBytes % 1024 == 0 && kRawBytes % 1024 == 0, "aligned tiles");
   static_assert(kSmemBytes <= 227 * 1024, "one CTA's shared memory");
 };
@@ -179,14 +188,15 @@ __device__ __forceinline__ uint32_t scale_pair(uint32_t w, float a) {
 // zeros. Eight lanes take a row, a lane the same 8 elements (a 16-byte f16 piece)
 // of every 64-element chunk: eight lanes store eight different pieces of a row.
 // Rows that would read from the same banks begin with another chunk.
-template <int FMT, int D>
-__device__ __forceinline__ void widen_unit(uint32_t raw, uint32_t op, int warp, int lane,
-                                           uint32_t keep) {
-  constexpr int kKT = D == 256 ? 64 : 128;
-  constexpr int kRow = FMT == PD_KV_FP8_E4M3 ? D : D / 2;
-  constexpr int kPiece = FMT == PD_KV_FP8_E4M3 ? 8 : 4;  // raw bytes of a piece
+// COLS of the row's D columns, from 64-column chunk `chunk0` on (FP8: a raw unit
+// holds these columns only, in slabs of 256).
+template <int FMT, int D, int COLS>
+__device__ __forceinline__ void widen_unit(uint32_t raw, uint32_t op, int chunk0, int warp,
+                                           int lane, uint32_t keep) {
+  constexpr int kKT = D == 512 ? 32 : D == 256 ? 64 : 128;
+  constexpr int kRow = FMT == PD_KV_FP8_E4M3 ? (D < 256 ? D : 256) : D / 2;
   constexpr int kSteps = kKT / 4 / 4;
-  constexpr int kCh = D / 64;
+  constexpr int kCh = COLS / 64;
   const int p = lane & 7;
   const int row0 = warp * (kKT / 4) + (lane >> 3);
   const int turn = kCh == 1 ? 0 : (FMT == PD_KV_FP8_E4M3 ? (lane >> 3) & 1 : lane >> 4);
@@ -196,11 +206,12 @@ __device__ __forceinline__ void widen_unit(uint32_t raw, uint32_t op, int warp, 
   for (int it = 0; it < kSteps; ++it)
 #pragma unroll
     for (int k = 0; k < kCh; ++k) {
-      const int row = row0 + it * 4, piece = (k ^ turn) * 8 + p;
+      const int row = row0 + it * 4, ch = k ^ turn;
       if constexpr (FMT == PD_KV_FP8_E4M3) {
-        w[it][k] = lds64(raw + row * kRow + piece * kPiece);
+        w[it][k] = lds64(raw + (ch >> 2) * (kKT * 256) + row * kRow + (ch & 3) * 64 + p * 8);
       } else {
-        w[it][k].x = lds32(raw + row * kRow + piece * kPiece);
+        const int piece = (chunk0 + ch) * 8 + p;
+        w[it][k].x = lds32(raw + row * kRow + piece * 4);
         sc[it][k] = lds_u8(raw + kKT * kRow + row * (D / 16) + piece / 2);
       }
     }
@@ -242,30 +253,38 @@ __device__ __forceinline__ void widen_unit(uint32_t raw, uint32_t op, int warp, 
 template <int D>
 __device__ __forceinline__ void widen_q(uint32_t tile, int tile_bytes, int rows, int second,
                                         float mul, float* mul_s, int warp, int lane) {
-  constexpr int kLanes = D / 8;       // lanes of a row, 16 bytes each
-  constexpr int kStep = 32 / kLanes;  // rows of a step
-  constexpr int kBatch = 4;           // steps whose latencies overlap
+  constexpr int kLanes = D < 256 ? D / 8 : 32;  // lanes of a row
+  constexpr int kPer = D / 8 / kLanes;          // 16-byte pieces of a lane
+  constexpr int kStep = 32 / kLanes;            // rows of a step
+  constexpr int kBatch = 4;                     // steps whose latencies overlap
   const int c = lane % kLanes;
 #pragma unroll 1
   for (int r0 = warp * kBatch * kStep; r0 < rows; r0 += 4 * kBatch * kStep) {
-    uint32_t at[kBatch];
-    uint4 x[kBatch];
+    uint32_t at[kBatch][kPer];
+    uint4 x[kBatch][kPer];
     float mq[kBatch];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const int r = min(r0 + k * kStep + lane / kLanes, rows - 1);
       const int m = r >= second ? r - second : r;
-      at[k] = tile + (r >= second ? tile_bytes : 0) + (c / 8) * (128 * 128) +
-              swz128(m * 128 + (c % 8) * 16);
-      x[k] = lds128(at[k]);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int piece = c + j * kLanes;
+        at[k][j] = tile + (r >= second ? tile_bytes : 0) + (piece / 8) * (128 * 128) +
+                   swz128(m * 128 + (piece % 8) * 16);
+        x[k][j] = lds128(at[k][j]);
+      }
     }
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      const uint32_t y[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
       mq[k] = 0.0f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        mq[k] = fmaxf(mq[k], fmaxf(fabsf(bf16_lo(y[e])), fabsf(bf16_hi(y[e]))));
+      for (int j = 0; j < kPer; ++j) {
+        const uint32_t y[4] = {x[k][j].x, x[k][j].y, x[k][j].z, x[k][j].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          mq[k] = fmaxf(mq[k], fmaxf(fabsf(bf16_lo(y[e])), fabsf(bf16_hi(y[e]))));
+      }
     }
 #pragma unroll
     for (int o = 1; o < kLanes; o <<= 1)
@@ -278,10 +297,14 @@ __device__ __forceinline__ void widen_q(uint32_t tile, int tile_bytes, int rows,
       if (r < rows) {
         const int up = ilog2f(mq[k]);
         const float down = exp2i(14 - up);
-        uint32_t y[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = pack_f16x2(bf16_lo(y[e]) * down, bf16_hi(y[e]) * down);
-        sts128(at[k], y[0], y[1], y[2], y[3]);
+        for (int j = 0; j < kPer; ++j) {
+          uint32_t y[4] = {x[k][j].x, x[k][j].y, x[k][j].z, x[k][j].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            y[e] = pack_f16x2(bf16_lo(y[e]) * down, bf16_hi(y[e]) * down);
+          sts128(at[k][j], y[0], y[1], y[2], y[3]);
+        }
         if (c == 0) mul_s[r] = mul * exp2i(up - 14);
       }
     }
@@ -300,6 +323,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
   constexpr bool kQuant = C::kQuant;
   constexpr bool kOneO = C::kOneO;
   constexpr int KT = C::kKT;
+  constexpr int DV = C::kDV;  // columns of V and O that an item has
   asm volatile("griddepcontrol.launch_dependents;");
   const int G = a.group;
   const int TPG = 128 / G;        // nodes of 128 rows
@@ -405,7 +429,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
     while (!failed && walk.next(q)) {
       if (lane == 0 && mine == 0 && q.begins && !q.whole)
         w.records[blockIdx.x] = JoinRecord{walk.pieces_of_last(q.j1), q.p.s.q0 + q.rt * IN,
-                                           min(IN, q.p.s.n - q.rt * IN), q.g * G};
+                                           min(IN, q.p.s.n - q.rt * IN) | q.half << 16, q.g * G};
       const int nodes = min(IN, q.p.s.n - q.rt * IN);
       const bool dual = nodes > TPG;
       const int T = q.j1 - q.j0;
@@ -463,19 +487,31 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
           for (int k = 0; k < C::kCopies; ++k) zs[k] = __shfl_sync(0xFFFFFFFFu, z, k);
           if (lane == 0) {
             if constexpr (FMT == PD_KV_BF16) {
-              mbar_arrive_expect_tx(fb, C::kUnitBytes);
+              const int chunks = C::kHalves > 1 && is_v ? DV / 64 : D / 64;
+              const int x0 = C::kHalves > 1 && is_v ? q.half * DV : 0;
+              mbar_arrive_expect_tx(fb, KT * 128 * chunks);
               const uint32_t dst = unit_s + slot * C::kUnitBytes;
 #pragma unroll
               for (int k = 0; k < C::kCopies; ++k)
 #pragma unroll
                 for (int ch = 0; ch < D / 64; ++ch)
-                  tma_load_3d(dst + ch * (KT * 128) + k * (BS * 128), tm, ch * 64, q.g, zs[k],
-                              fb);
+                  if (C::kHalves == 1 || ch < chunks)
+                    tma_load_3d(dst + ch * (KT * 128) + k * (BS * 128), tm, x0 + ch * 64, q.g,
+                                zs[k], fb);
             } else {
-              mbar_arrive_expect_tx(fb, C::kRawData);
+              // a box is 256 columns at most
+              constexpr int kBox = D < 256 ? D : 256;
+              const int boxes = C::kHalves > 1 && is_v ? 1 : D / kBox;
+              const int x0 = C::kHalves > 1 && is_v ? q.half * DV : 0;
+              mbar_arrive_expect_tx(fb, KT * kBox * boxes);
               const uint32_t dst = raw_s + slot * C::kRawBytes;
 #pragma unroll
-              for (int k = 0; k < C::kCopies; ++k) tma_load_3d(dst + k * (BS * D), tm, 0, q.g, zs[k], fb);
+              for (int k = 0; k < C::kCopies; ++k)
+#pragma unroll
+                for (int h = 0; h < D / kBox; ++h)
+                  if (h < boxes)
+                    tma_load_3d(dst + h * (KT * kBox) + k * (BS * kBox), tm, x0 + h * kBox, q.g,
+                                zs[k], fb);
             }
           }
         } else if constexpr (C::kGather) {
@@ -587,7 +623,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
     // a group waits twice as long for its own.)
     if (lane == 0) {
       constexpr uint32_t idS = kQuant ? umma_idesc_f16(128, KT, 0) : umma_idesc(128, KT, 0);
-      constexpr uint32_t idO = kQuant ? umma_idesc_f16(128, D, 1) : umma_idesc(128, D, 1);
+      constexpr uint32_t idO = kQuant ? umma_idesc_f16(128, DV, 1) : umma_idesc(128, DV, 1);
       const uint64_t dq0 = umma_desc(s0, 16, 1024);
       const uint64_t dk0 = umma_desc(unit_s, 16, 1024);
       const uint64_t dv0 = umma_desc(unit_s, KT * 128, 1024);
@@ -711,7 +747,11 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
           uint32_t keep = 0xFFFFFFFFu;
           if (bad != 0u || t0 < any.lo || t0 + KT > any.prefix)
             keep = (seen32(any, t0 + row0 / 32 * 32) & ~bad32<BS>(bad, row0 / 32)) >> (row0 % 32);
-          widen_unit<FMT, D>(raw_s + rs * C::kRawBytes, unit_s + us * C::kUnitBytes, cw, lane, keep);
+          const uint32_t raw = raw_s + rs * C::kRawBytes, op = unit_s + us * C::kUnitBytes;
+          if (C::kHalves > 1 && is_v)
+            widen_unit<FMT, D, DV>(raw, op, q.half * (DV / 64), cw, lane, keep);
+          else
+            widen_unit<FMT, D, D>(raw, op, 0, cw, lane, keep);
           fence_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -800,7 +840,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
               if (!((keep >> lane) & 1u)) {
                 const uint32_t vrow = unit_s + vslot * C::kUnitBytes;
 #pragma unroll
-                for (int p = 0; p < D / 8; ++p)
+                for (int p = 0; p < DV / 8; ++p)
                   sts128(vrow + (p / 8) * (KT * 128) + swz128(m * 128 + (p % 8) * 16), 0u, 0u,
                          0u, 0u);
               }
@@ -905,7 +945,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
               tc_fence_after();
             }
 #pragma unroll 1
-            for (int h = 0; h < D / 16; ++h) {
+            for (int h = 0; h < DV / 16; ++h) {
               uint32_t v[16];
               tmem_ld16(o_tm + (kOneO ? 0 : X * D) + h * 16, v);
               tmem_wait_ld();
@@ -962,9 +1002,9 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
       }
       const float f0 = X ? f_other : f_own, f1 = X ? f_own : f_other;
       const float mul = q.whole ? vmul / fmaxf(L, 1e-20f) : vmul;
-      uint16_t* orow = a.out + qrow * a.out_stride + static_cast<int64_t>(qh) * D;
-      float* part = w.o + (static_cast<int64_t>(q.slot) * (D / 4) * w.rows + r) * 4;
-      const int cols = merge ? D / 2 : D, col0 = merge ? X * (D / 2) : 0;
+      uint16_t* orow = a.out + qrow * a.out_stride + static_cast<int64_t>(qh) * D + q.half * DV;
+      float* part = w.o + (static_cast<int64_t>(q.slot) * (DV / 4) * w.rows + r) * 4;
+      const int cols = merge ? DV / 2 : DV, col0 = merge ? X * (D / 2) : 0;
       if (!idle) {
         for (int cg = 0; cg < cols; cg += 16) {
           uint32_t va[16], vb[16];
@@ -1058,7 +1098,7 @@ cudaError_t launch_umma_cfg(const TreeArgs& a, const TreeWork& w, cudaStream_t s
         return cudaErrorInvalidValue;
     }
   } else {
-    constexpr int kInner = FMT == PD_KV_BF16 ? 64 : D;
+    constexpr int kInner = FMT == PD_KV_BF16 ? 64 : (D < 256 ? D : 256);
     constexpr bool kSwz = FMT == PD_KV_BF16;
     if (!encode_cache_map(&tk, a.k_cache, FMT, D, a.num_kv_heads, rows, kInner, BS, kSwz) ||
         !encode_cache_map(&tv, a.v_cache, FMT, D, a.num_kv_heads, rows, kInner, BS, kSwz))
@@ -1093,7 +1133,8 @@ cudaError_t launch_umma_fmt(const TreeArgs& a, const TreeWork& w, int D, cudaStr
   switch (D) {
     case 64: return launch_umma_bs<FMT, 64>(a, w, st);
     case 128: return launch_umma_bs<FMT, 128>(a, w, st);
-    default: return launch_umma_bs<FMT, 256>(a, w, st);
+    case 256: return launch_umma_bs<FMT, 256>(a, w, st);
+    default: return launch_umma_bs<FMT, 512>(a, w, st);
   }
 }
 
@@ -1101,10 +1142,10 @@ cudaError_t launch_umma_fmt(const TreeArgs& a, const TreeWork& w, int D, cudaStr
 
 size_t tree_umma_workspace(int max_q_len, int group, int head_dim, int num_sms, TreeWork* w,
                            void* workspace) {
-  const int item_nodes = (head_dim == 256 ? 1 : 2) * (128 / group);
+  const int item_nodes = (head_dim >= 256 ? 1 : 2) * (128 / group);
   const int nodes = max_q_len < item_nodes ? (max_q_len < 1 ? 1 : max_q_len) : item_nodes;
   const int rows = (nodes * group + 7) / 8 * 8;
-  const WorkLayout l = work_layout(num_sms, rows, head_dim);
+  const WorkLayout l = work_layout(num_sms, rows, head_dim > 256 ? 256 : head_dim);
   if (w) {
     uint8_t* p = static_cast<uint8_t*>(workspace);
     w->records = reinterpret_cast<JoinRecord*>(p);

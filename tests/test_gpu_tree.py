@@ -90,6 +90,8 @@ SHAPES = [
     ([5, 3, 64], [5, 3, 64], 6, 3, 64, 16, 3, 1, "padded"),
     (list(range(1, 150, 5)), [min(n, 1 + n % 7) for n in range(1, 150, 5)], 8, 2, 128, 16, 0, 0,
      "tree"),
+    ([70, 333, 0, 33], [20, 64, 0, 33], 5, 5, 512, 16, 0, 0, "padded"),
+    ([901], [31], 12, 4, 512, 32, 200, 35, "tree"),
 ]
 
 
@@ -112,7 +114,8 @@ def test_a_node_that_sees_nothing_is_zero():
     assert not got[0].any() and not got[2].any() and got[1].any() and got[3].any()
 
 
-@pytest.mark.parametrize("d,hq,hkv", [(128, 32, 8), (64, 4, 2), (256, 8, 4), (512, 4, 2)])
+@pytest.mark.parametrize("d,hq,hkv", [(128, 32, 8), (64, 4, 2), (256, 8, 4), (512, 4, 2),
+                                      (512, 8, 2)])
 @pytest.mark.parametrize("kv_dtype", [0, 1])
 def test_what_no_node_sees_may_be_nan(kv_dtype, d, hq, hkv):
     """Rows past the length, before every window, and padding nodes' own rows
@@ -211,7 +214,7 @@ def test_permuted_pages_and_repeats_give_the_same_bits():
 
 
 @pytest.mark.parametrize("kv_dtype", [0, 2])
-@pytest.mark.parametrize("d,scale", [(128, -0.7), (128, 0.0), (64, 3.0), (256, -0.5)])
+@pytest.mark.parametrize("d,scale", [(128, -0.7), (128, 0.0), (64, 3.0), (256, -0.5), (512, 2.0)])
 def test_any_scale(d, scale, kv_dtype):
     """A negative scale, none, and one that makes the softmax nearly one-hot."""
     case, masks, caches, pages, scales = build([700, 130], [6, 9], 8, 2, d, 16, kv_dtype, 12)
@@ -231,6 +234,9 @@ LONG = [
     ([12000] * 16, [5] * 16, 16, 8, 128, 32, 9000, 4),
     ([20000, 16000], [64, 40], 32, 8, 128, 16, 0, 0),
     ([9000] * 16, [5] * 16, 16, 8, 256, 16, 0, 0),
+    ([6000] * 8, [9] * 8, 16, 2, 512, 16, 0, 0),
+    ([9000, 4000], [40, 64], 8, 4, 512, 32, 3000, 20),
+    ([9000] * 4, [2] * 4, 16, 2, 512, 16, 0, 0),
 ]
 
 
