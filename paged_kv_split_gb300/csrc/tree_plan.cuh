@@ -65,16 +65,73 @@ struct Share {
   long long units;  // S
   long long x0;     // first unit
   int b, k, off;    // its sequence, item there and unit in the item; b < 0: nothing
+  SeqPlan p;        // of that sequence
 };
 struct ShareScratch {
   long long warp_sum[32];
   long long units;
   int b, k, off;
 };
-// Called by all threads of the CTA, one barrier pair. `per_cta_min`: a share is at
-// least that long.
+// The start of the share [x0, ..) among the sequences [b0, b1), whose units begin at `at`.
+__device__ __forceinline__ void find_start(const TreeArgs& a, int tpc, int kt, int ov, int b0, int b1,
+                                           long long at, Share* r) {
+  for (int b = b0; b < b1; ++b) {
+    const SeqPlan p = seq_plan(a, b, tpc, kt, nullptr);
+    const long long cost = static_cast<long long>(p.rts) * a.num_kv_heads * (p.nt + ov);
+    if (r->x0 < at + cost) {
+      const int item = p.nt + ov;
+      r->b = b;
+      r->k = static_cast<int>(quotient_of(r->x0 - at, item));
+      r->off = static_cast<int>(r->x0 - at - static_cast<long long>(r->k) * item);
+      r->p = p;
+      return;
+    }
+    at += cost;
+  }
+}
+// Up to kWarpPlan sequences every warp works the share out for itself, without
+// barriers (one short sequence 14.1 -> 13.8 us, 64 sequences in FP8 181 -> 179);
+// beyond that a lane would have more than four in turn.
+constexpr int kWarpPlan = 128;
+__device__ __forceinline__ Share warp_share(const TreeArgs& a, int tpc, int kt, int ov,
+                                            int per_cta_min) {
+  const int lane = threadIdx.x & 31;
+  const int per = (a.num_seqs + 31) / 32;
+  const int b0 = min(lane * per, a.num_seqs), b1 = min(b0 + per, a.num_seqs);
+  int* flags = blockIdx.x == 0 && threadIdx.x < 32 ? a.flags : nullptr;
+  long long sum = 0;
+  for (int b = b0; b < b1; ++b) {
+    const SeqPlan p = seq_plan(a, b, tpc, kt, flags);
+    sum += static_cast<long long>(p.rts) * a.num_kv_heads * (p.nt + ov);
+  }
+  long long incl = sum;
+  for (int o = 1; o < 32 && o * per < a.num_seqs; o <<= 1) {
+    const long long v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  const long long total = __shfl_sync(0xFFFFFFFFu, incl, max(a.num_seqs - 1, 0) / max(per, 1));
+  Share r;
+  r.units = quotient_of(total + gridDim.x - 1, gridDim.x);
+  if (r.units < per_cta_min) r.units = per_cta_min;
+  r.x0 = r.units * blockIdx.x;
+  r.b = -1;
+  r.k = r.off = 0;
+  r.p.s.q0 = r.p.s.n = r.p.s.L = r.p.nst = r.p.base = r.p.nt = r.p.rts = 0;
+  const bool mine = r.x0 >= incl - sum && r.x0 < incl;
+  if (mine) find_start(a, tpc, kt, ov, b0, b1, incl - sum, &r);
+  const uint32_t who = __ballot_sync(0xFFFFFFFFu, mine);
+  if (who == 0u) return r;
+  const int src = __ffs(who) - 1;
+  int* const field[] = {&r.b, &r.k, &r.off, &r.p.s.q0, &r.p.s.n, &r.p.s.L, &r.p.nst, &r.p.base,
+                        &r.p.nt, &r.p.rts};
+#pragma unroll
+  for (int i = 0; i < 10; ++i) *field[i] = __shfl_sync(0xFFFFFFFFu, *field[i], src);
+  return r;
+}
+// Called by all threads of the CTA. `per_cta_min`: a share is at least that long.
 __device__ __forceinline__ Share make_share(const TreeArgs& a, int tpc, int kt, int ov,
                                             int per_cta_min, ShareScratch* sh) {
+  if (a.num_seqs <= kWarpPlan) return warp_share(a, tpc, kt, ov, per_cta_min);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int nthreads = blockDim.x;
   const int per = (a.num_seqs + nthreads - 1) / nthreads;
@@ -106,24 +163,16 @@ __device__ __forceinline__ Share make_share(const TreeArgs& a, int tpc, int kt, 
   r.x0 = r.units * blockIdx.x;
   long long at = before + incl - sum;  // first unit of this thread's sequences
   if (r.x0 >= at && r.x0 < at + sum) {
-    for (int b = b0; b < b1; ++b) {
-      const SeqPlan p = seq_plan(a, b, tpc, kt, nullptr);
-      const long long cost = static_cast<long long>(p.rts) * a.num_kv_heads * (p.nt + ov);
-      if (r.x0 < at + cost) {
-        const int item = p.nt + ov;
-        sh->b = b;
-        const int k = static_cast<int>(quotient_of(r.x0 - at, item));
-        sh->k = k;
-        sh->off = static_cast<int>(r.x0 - at - static_cast<long long>(k) * item);
-        break;
-      }
-      at += cost;
-    }
+    find_start(a, tpc, kt, ov, b0, b1, at, &r);
+    sh->b = r.b;
+    sh->k = r.k;
+    sh->off = r.off;
   }
   __syncthreads();
   r.b = sh->b;
   r.k = sh->k;
   r.off = sh->off;
+  if (r.b >= 0) r.p = seq_plan(a, r.b, tpc, kt, nullptr);
   return r;
 }
 
@@ -146,9 +195,7 @@ struct Walker {
 
   __device__ __forceinline__ Walker(const TreeArgs& args, const Share& s, int tpc_, int kt_, int ov_)
       : a(args), tpc(tpc_), kt(kt_), ov(ov_), units(s.units), x(s.x0), end(s.x0 + s.units), b(s.b),
-        k(s.k), off(s.off) {
-    p = seq_plan(a, b, tpc, kt, nullptr);
-  }
+        k(s.k), off(s.off), p(s.p) {}
   __device__ __forceinline__ bool next(Piece& q) {
     while (x < end && b < a.num_seqs) {
       const int items = p.rts * a.num_kv_heads;

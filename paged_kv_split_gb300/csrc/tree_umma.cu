@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
   }
   // what touches global memory waits for the previous work on the stream
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  // (scratch where Q will be; its barriers also publish those above)
+  // (scratch where Q will be)
   const Share share = make_share(a, IN, KT, kTreeSlack, w.min_units,
                                  reinterpret_cast<ShareScratch*>(smem));
   if (tid == 0) w.records[blockIdx.x] = JoinRecord{0, 0, 0, 0};
