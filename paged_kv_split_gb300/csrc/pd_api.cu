@@ -1080,8 +1080,8 @@ size_t pd_decode_tree_workspace_bytes(int32_t max_q_len, int32_t num_q_heads,
       num_q_heads / num_kv_heads > kMaxGroup || !head_dim_ok(head_dim) || !dtype_ok(kv_dtype))
     return 0;
   if (!tree_on_umma(max_q_len, num_q_heads / num_kv_heads, head_dim))
-    return tree_split_workspace(max_q_len, num_q_heads / num_kv_heads, kv_dtype, num_sms, nullptr,
-                                nullptr);
+    return tree_split_workspace(max_q_len, num_q_heads / num_kv_heads, head_dim, kv_dtype, num_sms,
+                                nullptr, nullptr);
   return tree_umma_workspace(max_q_len, num_q_heads / num_kv_heads, head_dim, num_sms, nullptr,
                              nullptr);
 }
@@ -1155,8 +1155,8 @@ int decode_tree_impl(const void* q, int64_t q_stride, const int32_t* cu_q,
     tree_umma_workspace(max_q_len, a.group, head_dim, dev->num_sms, &w, workspace);
     return cuda_status(launch_tree_umma(a, w, head_dim, kv_dtype, st));
   }
-  tree_split_workspace(max_q_len, a.group, kv_dtype, dev->num_sms, &w, workspace);
-  return cuda_status(launch_tree_split(a, w, kv_dtype, st));
+  tree_split_workspace(max_q_len, a.group, head_dim, kv_dtype, dev->num_sms, &w, workspace);
+  return cuda_status(launch_tree_split(a, w, head_dim, kv_dtype, st));
 }
 }  // namespace
 

@@ -289,12 +289,16 @@ cudaError_t launch_tree_join(const TreeArgs& a, const TreeWork& w, int head_dim,
 // 16 rows a pass over the keys; on tcgen05 128 rows take two passes. 8 sequences
 // over 8192 keys, mma.sync against tcgen05 in us, BF16 / FP8 / NVFP4: 32 rows 113 /
 // 120 / 113 against 109 / 123 / 139, 64 rows 213 / 220 / 200 against 112 / 128 / 145.
+// head_dim 256 in up to 8 rows does too: 16 sequences over 4096 keys 52 / 39 / 41
+// against 58 / 59 / 58; 16 rows 97 / 70 / 69 against 60 / 61 / 60. At 128 the two
+// are equal in 8 rows.
 inline bool tree_on_umma(int max_q_len, int group, int head_dim) {
-  return head_dim <= 256 || max_q_len * group > 32;
+  return head_dim <= 128 || max_q_len * group > (head_dim == 256 ? 8 : 32);
 }
-size_t tree_split_workspace(int max_q_len, int group, int kv_dtype, int num_sms, TreeWork* w,
-                            void* workspace);
-cudaError_t launch_tree_split(const TreeArgs& a, const TreeWork& w, int kv_dtype, cudaStream_t st);
+size_t tree_split_workspace(int max_q_len, int group, int head_dim, int kv_dtype, int num_sms,
+                            TreeWork* w, void* workspace);
+cudaError_t launch_tree_split(const TreeArgs& a, const TreeWork& w, int head_dim, int kv_dtype,
+                              cudaStream_t st);
 size_t tree_umma_workspace(int max_q_len, int group, int head_dim, int num_sms, TreeWork* w,
                            void* workspace);
 cudaError_t launch_tree_umma(const TreeArgs& a, const TreeWork& w, int head_dim, int kv_dtype,

@@ -1,5 +1,6 @@
-// Draft-tree attention at head_dim 512 in few rows, where the tcgen05 kernel would
-// go over the keys twice for a nearly empty tile: mma.sync tiles with keys on M and 8 or 16 rows (nodes times q
+// Draft-tree attention at head_dim 256 and 512 in few rows, where the tcgen05 kernel
+// would widen, score and weight for a nearly empty tile (and at 512 go over the keys
+// twice): mma.sync tiles with keys on M and 8 or 16 rows (nodes times q
 // heads) on N, head_dim split over four consumer warps, as decode_balanced.cu
 // has them (mma_tile.cuh). More rows than that are further node tiles, which
 // run side by side and find the keys in L2. Single tokens of 8 sequences over 8192
@@ -352,32 +353,39 @@ cudaError_t launch_split_cfg(const TreeArgs& a, const TreeWork& w, cudaStream_t 
   return launch_tree_join(a, w, D, st);
 }
 
-template <int FMT, int D>
-cudaError_t launch_split_nt(const TreeArgs& a, const TreeWork& w, cudaStream_t st) {
+// head_dim 256 comes here in up to 8 rows only.
+template <int FMT>
+cudaError_t launch_split_nt(const TreeArgs& a, const TreeWork& w, int head_dim, cudaStream_t st) {
   const bool one = w.item_nodes * a.group <= 8;
+  if (head_dim == 256)
+    return a.block_size == 16 ? launch_split_cfg<FMT, 256, 1, 16>(a, w, st)
+                              : launch_split_cfg<FMT, 256, 1, 32>(a, w, st);
   if (a.block_size == 16)
-    return one ? launch_split_cfg<FMT, D, 1, 16>(a, w, st) : launch_split_cfg<FMT, D, 2, 16>(a, w, st);
-  return one ? launch_split_cfg<FMT, D, 1, 32>(a, w, st) : launch_split_cfg<FMT, D, 2, 32>(a, w, st);
+    return one ? launch_split_cfg<FMT, 512, 1, 16>(a, w, st)
+               : launch_split_cfg<FMT, 512, 2, 16>(a, w, st);
+  return one ? launch_split_cfg<FMT, 512, 1, 32>(a, w, st)
+             : launch_split_cfg<FMT, 512, 2, 32>(a, w, st);
 }
 
 template <int FMT>
-int split_per_sm(bool one) {
+int split_per_sm(bool one, int head_dim) {
+  if (head_dim == 256) return SplitCfg<FMT, 256, 1>::kPerSm;
   return one ? SplitCfg<FMT, 512, 1>::kPerSm : SplitCfg<FMT, 512, 2>::kPerSm;
 }
 
 }  // namespace
 
-size_t tree_split_workspace(int max_q_len, int group, int kv_dtype, int num_sms, TreeWork* w,
-                            void* workspace) {
+size_t tree_split_workspace(int max_q_len, int group, int head_dim, int kv_dtype, int num_sms,
+                            TreeWork* w, void* workspace) {
   // 8 rows where they hold every node of the batch, else 16
   const bool one = (max_q_len < 1 ? 1 : max_q_len) * group <= 8;
   const int item_nodes = (one ? 8 : 16) / group;
   const int rows = one ? 8 : 16;
-  const int per_sm = kv_dtype == PD_KV_BF16       ? split_per_sm<PD_KV_BF16>(one)
-                     : kv_dtype == PD_KV_FP8_E4M3 ? split_per_sm<PD_KV_FP8_E4M3>(one)
-                                                  : split_per_sm<PD_KV_NVFP4>(one);
+  const int per_sm = kv_dtype == PD_KV_BF16       ? split_per_sm<PD_KV_BF16>(one, head_dim)
+                     : kv_dtype == PD_KV_FP8_E4M3 ? split_per_sm<PD_KV_FP8_E4M3>(one, head_dim)
+                                                  : split_per_sm<PD_KV_NVFP4>(one, head_dim);
   const int ctas = num_sms * per_sm;
-  const WorkLayout l = work_layout(ctas, rows, 512);
+  const WorkLayout l = work_layout(ctas, rows, head_dim);
   if (w) {
     uint8_t* p = static_cast<uint8_t*>(workspace);
     w->records = reinterpret_cast<JoinRecord*>(p);
@@ -391,11 +399,12 @@ size_t tree_split_workspace(int max_q_len, int group, int kv_dtype, int num_sms,
   return l.bytes;
 }
 
-cudaError_t launch_tree_split(const TreeArgs& a, const TreeWork& w, int kv_dtype, cudaStream_t st) {
+cudaError_t launch_tree_split(const TreeArgs& a, const TreeWork& w, int head_dim, int kv_dtype,
+                              cudaStream_t st) {
   switch (kv_dtype) {
-    case PD_KV_BF16: return launch_split_nt<PD_KV_BF16, 512>(a, w, st);
-    case PD_KV_FP8_E4M3: return launch_split_nt<PD_KV_FP8_E4M3, 512>(a, w, st);
-    default: return launch_split_nt<PD_KV_NVFP4, 512>(a, w, st);
+    case PD_KV_BF16: return launch_split_nt<PD_KV_BF16>(a, w, head_dim, st);
+    case PD_KV_FP8_E4M3: return launch_split_nt<PD_KV_FP8_E4M3>(a, w, head_dim, st);
+    default: return launch_split_nt<PD_KV_NVFP4>(a, w, head_dim, st);
   }
 }
 

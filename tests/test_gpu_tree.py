@@ -92,6 +92,8 @@ SHAPES = [
      "tree"),
     ([70, 333, 0, 33], [20, 64, 0, 33], 5, 5, 512, 16, 0, 0, "padded"),
     ([901], [31], 12, 4, 512, 32, 200, 35, "tree"),
+    ([700, 41, 0, 3], [4, 2, 0, 3], 8, 4, 256, 16, 0, 0, "padded"),
+    ([1200, 95], [1, 1], 16, 2, 256, 32, 300, 4, "chain"),
 ]
 
 
@@ -237,6 +239,7 @@ LONG = [
     ([6000] * 8, [9] * 8, 16, 2, 512, 16, 0, 0),
     ([9000, 4000], [40, 64], 8, 4, 512, 32, 3000, 20),
     ([9000] * 4, [2] * 4, 16, 2, 512, 16, 0, 0),
+    ([9000] * 6, [4] * 6, 8, 4, 256, 16, 0, 0),
 ]
 
 
