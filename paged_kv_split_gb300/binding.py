@@ -147,6 +147,27 @@ def _stream(stream) -> int:
     return int(getattr(stream, "cuda_stream", stream) or 0)
 
 
+def _torch_stream(stream, device):
+    """torch's object for a stream given as an object or a handle."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = _stream(stream)
+    if handle in (0, 1):  # the default stream, under either of its handles
+        return torch.cuda.default_stream(device)
+    return torch.cuda.ExternalStream(handle, device)
+
+
+def _scratch(nbytes, device, stream):
+    """A workspace for one call on `stream`. It comes from that stream's memory,
+    so that whatever takes the memory next, once the call has returned and
+    dropped it, runs behind the call's kernels."""
+    nbytes = max(nbytes, 16)
+    if stream is None or _stream(stream) == torch.cuda.current_stream(device).cuda_stream:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(_torch_stream(stream, device)):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 def _dev(t: torch.Tensor, name: str, dtype=None, device=None) -> int:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -325,8 +346,7 @@ def pd_decode(q, k_cache, v_cache, block_tables, seq_lens, out, *, num_kv_heads,
         if S == 0:
             S = pd_choose_num_splits(B, num_kv_heads, mbs, block_size, sliding_window, d, code,
                                      q.device.index)
-        workspace = torch.empty(max(pd_decode_workspace_bytes(B, hq, d, S), 16), dtype=torch.uint8,
-                                device=q.device)
+        workspace = _scratch(pd_decode_workspace_bytes(B, hq, d, S), q.device, stream)
     dev = q.device
     fn = "pd_decode_crosscheck" if crosscheck else "pd_decode"
     rc = getattr(_lib, fn)(
@@ -355,8 +375,7 @@ def pd_decode_e4m3_out(q, k_cache, v_cache, block_tables, seq_lens, out, *, out_
         if S == 0:
             S = pd_choose_num_splits(B, num_kv_heads, mbs, block_size, sliding_window, d, code,
                                      q.device.index)
-        workspace = torch.empty(max(pd_decode_workspace_bytes(B, hq, d, S), 16), dtype=torch.uint8,
-                                device=q.device)
+        workspace = _scratch(pd_decode_workspace_bytes(B, hq, d, S), q.device, stream)
     dev = q.device
     rc = _lib.pd_decode_e4m3_out(
         _dev(q, "q", torch.bfloat16, dev), _dev(k_cache, "k_cache", None, dev),
@@ -465,7 +484,7 @@ def pd_decode_balanced(q, k_cache, v_cache, block_tables, plan_dev, plan, out, *
     mbs = block_tables.shape[1]
     dev = q.device
     if workspace is None:
-        workspace = torch.empty(max(plan.workspace_bytes, 16), dtype=torch.uint8, device=dev)
+        workspace = _scratch(plan.workspace_bytes, dev, stream)
     rc = getattr(_lib, _fn)(
         _dev(q, "q", torch.bfloat16, dev), _dev(k_cache, "k_cache", None, dev),
         _dev(v_cache, "v_cache", None, dev), _dev(block_tables, "block_tables", torch.int32, dev),
@@ -533,8 +552,7 @@ def pd_decode_strided(q_rows, k_cache, v_cache, block_tables, seq_lens, out_rows
         if S == 0:
             S = pd_choose_num_splits(B, num_kv_heads, mbs, block_size, sliding_window, head_dim,
                                      code, dev.index)
-        workspace = torch.empty(max(pd_decode_workspace_bytes(B, num_q_heads, head_dim, S), 16),
-                                dtype=torch.uint8, device=dev)
+        workspace = _scratch(pd_decode_workspace_bytes(B, num_q_heads, head_dim, S), dev, stream)
     rc = _lib.pd_decode_strided(
         _dev(q_rows, "q_rows", torch.bfloat16, dev), stride,
         _dev(k_cache, "k_cache", None, dev), _dev(v_cache, "v_cache", None, dev),
@@ -560,7 +578,7 @@ def pd_decode_balanced_strided(q_rows, k_cache, v_cache, block_tables, plan_dev,
         raise ValueError("q_rows and out_rows have different numbers of sequences")
     dev = q_rows.device
     if workspace is None:
-        workspace = torch.empty(max(plan.workspace_bytes, 16), dtype=torch.uint8, device=dev)
+        workspace = _scratch(plan.workspace_bytes, dev, stream)
     rc = _lib.pd_decode_balanced_strided(
         _dev(q_rows, "q_rows", torch.bfloat16, dev), stride,
         _dev(k_cache, "k_cache", None, dev), _dev(v_cache, "v_cache", None, dev),
@@ -744,12 +762,12 @@ def pd_decode_tree_workspace_bytes(max_q_len, num_q_heads, num_kv_heads, head_di
     return n
 
 
-def _tree_scratch(q, workspace, max_q_len, hq, num_kv_heads, d, code):
+def _tree_scratch(q, workspace, max_q_len, hq, num_kv_heads, d, code, stream):
     if workspace is not None:
         return workspace
     # 0 for refused shapes: the call says why
     n = _tree_workspace(max_q_len, hq, num_kv_heads, d, code, _num_sms(q.get_device()))
-    return torch.empty(max(n, 16), dtype=torch.uint8, device=q.device)
+    return _scratch(n, q.device, stream)
 
 
 def _decode_tree(fn, q, q_stride, cu_q, tree_mask, k_cache, v_cache, block_tables, seq_lens, out,
@@ -769,7 +787,7 @@ def _decode_tree(fn, q, q_stride, cu_q, tree_mask, k_cache, v_cache, block_table
             raise ValueError("tree_mask must be int64 [total_q]")
         mask = _ptr(tree_mask, "tree_mask", torch.int64, dev)
     code = _dtype_code(kv_dtype)
-    workspace = _tree_scratch(q, workspace, max_q_len, hq, num_kv_heads, d, code)
+    workspace = _tree_scratch(q, workspace, max_q_len, hq, num_kv_heads, d, code, stream)
     rc = fn(
         _ptr(q, "q", torch.bfloat16, dev), q_stride, _ptr(cu_q, "cu_q", torch.int32, dev), mask,
         _cache_ptr(k_cache, "k_cache", dev), _cache_ptr(v_cache, "v_cache", dev),
@@ -800,7 +818,7 @@ def pd_decode_tree(q, cu_q, k_cache, v_cache, block_tables, seq_lens, out, *, ma
     T, hq, d = q.shape
     if not crosscheck and q.is_cuda:
         code = _dtype_code(kv_dtype)
-        workspace = _tree_scratch(q, workspace, max_q_len, hq, num_kv_heads, d, code)
+        workspace = _tree_scratch(q, workspace, max_q_len, hq, num_kv_heads, d, code, stream)
         rc = _marshal.decode_tree(q, out, 0, 0, cu_q, tree_mask, k_cache, v_cache, block_tables,
                                   seq_lens, max_q_len, num_kv_heads, block_size, num_blocks, scale,
                                   sliding_window, num_sinks, code, k_scale, v_scale, workspace,
@@ -825,7 +843,7 @@ def pd_decode_tree_strided(q_rows, cu_q, k_cache, v_cache, block_tables, seq_len
     if not crosscheck and q_rows.is_cuda:
         code = _dtype_code(kv_dtype)
         workspace = _tree_scratch(q_rows, workspace, max_q_len, num_q_heads, num_kv_heads, head_dim,
-                                  code)
+                                  code, stream)
         rc = _marshal.decode_tree(q_rows, out_rows, num_q_heads, head_dim, cu_q, tree_mask, k_cache,
                                   v_cache, block_tables, seq_lens, max_q_len, num_kv_heads,
                                   block_size, num_blocks, scale, sliding_window, num_sinks, code,
