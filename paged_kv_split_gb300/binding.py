@@ -296,12 +296,15 @@ def fp8_calibrate(key, value, stream=None):
     """Per-tensor FP8 scales for key and value: pd_absmax_bf16 of each, then
     pd_fp8_scales_from_absmax, both on the device; the two scales are read
     back once (a synchronising copy: calibration is a one-off step, not part
-    of decode)."""
+    of decode). All of it on the one stream."""
+    if stream is not None:
+        with torch.cuda.stream(_torch_stream(stream, key.device)):
+            return fp8_calibrate(key, value)
     amax = torch.zeros(2, dtype=torch.float32, device=key.device)
-    pd_absmax_bf16(key, amax[0:1], stream)
-    pd_absmax_bf16(value, amax[1:2], stream)
+    pd_absmax_bf16(key, amax[0:1])
+    pd_absmax_bf16(value, amax[1:2])
     scales = torch.empty_like(amax)
-    pd_fp8_scales_from_absmax(amax, scales, stream)
+    pd_fp8_scales_from_absmax(amax, scales)
     ks, vs = scales.cpu().tolist()
     return ks, vs
 

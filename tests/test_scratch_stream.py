@@ -125,6 +125,33 @@ def test_allocated_on_the_calls_stream(made, name, stream, handle):
     assert made == [handle]
 
 
+@pytest.mark.parametrize("stream,handle", [(Side(), 0x5150), (0x5150, 0x5150), (0, 0),
+                                           (None, 0x1000)])
+def test_calibration_runs_on_one_stream(made, monkeypatch, stream, handle):
+    """The zeroed maxima, the kernels and the copy back are in one stream's order."""
+    seen = []
+    real = torch.zeros
+
+    def here():
+        seen.append(torch.cuda.current_stream().cuda_stream)
+
+    class Scales:
+        def cpu(self):
+            here()
+            return real(2)
+
+    def zeros(n, dtype=None, device=None):
+        here()
+        return real(n, dtype=dtype)
+
+    monkeypatch.setattr(torch, "zeros", zeros)
+    monkeypatch.setattr(torch, "empty_like", lambda t: Scales())
+    monkeypatch.setattr(B, "pd_absmax_bf16", lambda x, m, s=None: seen.append(B._stream(s)))
+    monkeypatch.setattr(B, "pd_fp8_scales_from_absmax", lambda a, x, s=None: seen.append(B._stream(s)))
+    B.fp8_calibrate(T(8), T(8), stream)
+    assert seen == [handle] * 5
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("as_handle", [False, True])
 @pytest.mark.parametrize("d", [128, 512])
