@@ -52,6 +52,22 @@ def _inputs():
         os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
 
 
+def _torch_dir() -> str:
+    return os.path.dirname(importlib.util.find_spec("torch").origin)
+
+
+def marshal_cflags() -> list:
+    """g++ flags that compile csrc/marshal.cpp."""
+    inc = os.path.join(_torch_dir(), "include")
+    return ["-O2", "-std=c++17", "-fPIC", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+            "-isystem", inc, "-isystem", os.path.join(inc, "torch/csrc/api/include")]
+
+
+def marshal_ldflags() -> list:
+    lib = os.path.join(_torch_dir(), "lib")
+    return ["-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10", f"-Wl,-rpath,{lib}"]
+
+
 def is_stale() -> bool:
     if not (os.path.exists(LIB) and os.path.exists(MARSHAL)):
         return True
@@ -72,12 +88,8 @@ def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = True) 
         objs.append(obj)
         cmd = [cc, *NVCC_FLAGS, *extra, "-c", src, "-o", obj]
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
-    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
     marshal_obj = os.path.join(BUILD_DIR, "marshal.cpp.o")
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-I", INCLUDE,
-           "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(torch_dir, "include"),
-           "-isystem", os.path.join(torch_dir, "include/torch/csrc/api/include"),
-           "-c", MARSHAL_SRC, "-o", marshal_obj]
+    cmd = ["g++", *marshal_cflags(), "-c", MARSHAL_SRC, "-o", marshal_obj]
     procs.append((MARSHAL_SRC, subprocess.Popen(cmd, stdout=subprocess.PIPE,
                                                 stderr=subprocess.STDOUT)))
     failed = []
@@ -97,10 +109,8 @@ def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = True) 
                     "-o", tmp, *objs], check=True)
     os.replace(tmp, LIB)
     tmp = MARSHAL + f".tmp{os.getpid()}"
-    torch_lib = os.path.join(torch_dir, "lib")
     subprocess.run(["g++", "-shared", "-o", tmp, marshal_obj, "-L", PKG, "-l:libpd.so",
-                    "-L", torch_lib, "-ltorch_python", "-ltorch_cpu", "-lc10",
-                    "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{torch_lib}"], check=True)
+                    *marshal_ldflags(), "-Wl,-rpath,$ORIGIN"], check=True)
     os.replace(tmp, MARSHAL)
     return LIB
 

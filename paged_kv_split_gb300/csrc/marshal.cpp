@@ -5,11 +5,18 @@
 // Grace core, the call itself 4. Each function here does what binding.py's
 // function of the same purpose does, checks included, and returns its status;
 // it returns None, having done nothing, for arguments that it does not take as
-// they are, and binding.py then says what is wrong with them.
+// they are, and binding.py then says what is wrong with them. Tensors throw for
+// what they do not have (a 0-dim tensor's sizes, a vmapped one's address): no
+// exception leaves an entry, it means None too.
 #include <Python.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "pd.h"
+
+// The device whose tensors are taken; a host build of the tests has the CPU's.
+#ifndef PD_MARSHAL_DEVICE
+#define PD_MARSHAL_DEVICE at::kCUDA
+#endif
 
 namespace {
 
@@ -25,7 +32,7 @@ struct Args {
       return nullptr;
     }
     const at::Tensor& t = THPVariable_Unpack(a[i]);
-    if (!t.is_cuda() || !t.is_contiguous() || (dev >= 0 && t.get_device() != dev)) ok = false;
+    if (t.device().type() != PD_MARSHAL_DEVICE || !t.is_contiguous() || (dev >= 0 && t.get_device() != dev)) ok = false;
     if (dev < 0 && ok) dev = static_cast<int>(t.get_device());
     return ok ? &t : nullptr;
   }
@@ -76,14 +83,31 @@ struct Args {
   void* stream(int i) { return reinterpret_cast<void*>(static_cast<uintptr_t>(i64(i))); }
 };
 
-// The status of f(), made without the interpreter's lock.
+// The interpreter's lock let go.
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+// The status of f(), made without the lock.
 template <class F>
 PyObject* status(F f) {
   int rc;
-  Py_BEGIN_ALLOW_THREADS;
-  rc = f();
-  Py_END_ALLOW_THREADS;
+  {
+    Unlocked unlocked;
+    rc = f();
+  }
   return PyLong_FromLong(rc);
+}
+// An entry of N arguments: what F returns, or None where it throws.
+template <PyObject* (*F)(PyObject* const*), Py_ssize_t N>
+PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (n != N) Py_RETURN_NONE;
+  try {
+    return F(args);
+  } catch (...) {
+    PyErr_Clear();
+    Py_RETURN_NONE;
+  }
 }
 
 constexpr auto kBf16 = at::kBFloat16;
@@ -92,8 +116,7 @@ constexpr auto kI32 = at::kInt;
 // (qkv, q_out or None: in place, num_q_heads, head_dim (0: q_out's), k_cache, v_cache,
 //  positions, slot_mapping, cos_sin, num_kv_heads, block_size, num_blocks, q_weight,
 //  k_weight, eps, weight_offset, interleaved, kv_dtype, k_scale, v_scale, stream)
-PyObject* norm_rope(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  if (n != 21) Py_RETURN_NONE;
+PyObject* norm_rope(PyObject* const* args) {
   Args g{args};
   const at::Tensor* qkv = g.tensor(0);
   if (!qkv || qkv->scalar_type() != kBf16 || qkv->dim() != 2) Py_RETURN_NONE;
@@ -146,12 +169,12 @@ PyObject* norm_rope(PyObject*, PyObject* const* args, Py_ssize_t n) {
 //  tree_mask or None, k_cache, v_cache, block_tables, seq_lens, max_q_len, num_kv_heads,
 //  block_size, num_blocks, scale, sliding_window, num_sinks, kv_dtype, k_scale, v_scale,
 //  workspace, stream)
-PyObject* decode_tree(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  if (n != 22) Py_RETURN_NONE;
+PyObject* decode_tree(PyObject* const* args) {
   Args g{args};
   const at::Tensor* q = g.tensor(0);
   const at::Tensor* o = g.tensor(1);
-  if (!g.ok || q->scalar_type() != kBf16 || o->scalar_type() != kBf16) Py_RETURN_NONE;
+  if (!g.ok || q->scalar_type() != kBf16 || o->scalar_type() != kBf16 || q->dim() < 2)
+    Py_RETURN_NONE;
   int64_t hq = g.i64(2), d = g.i64(3), qs = 0, os = 0;
   const int64_t T = q->size(0);
   if (d == 0) {
@@ -198,8 +221,7 @@ PyObject* decode_tree(PyObject*, PyObject* const* args, Py_ssize_t n) {
 
 // (k_caches, v_caches, block_tables, seq_lens, cu_q, accepted, num_accepted, new_seq_lens,
 //  num_kv_heads, head_dim, block_size, num_blocks, kv_dtype, stream)
-PyObject* compact_tree(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  if (n != 14) Py_RETURN_NONE;
+PyObject* compact_tree(PyObject* const* args) {
   Args g{args};
   const at::Tensor* k = g.tensor(0);
   const at::Tensor* v = g.tensor(1);
@@ -234,14 +256,14 @@ PyObject* compact_tree(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
-PyMethodDef methods[] = {
-    {"norm_rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(norm_rope)),
-     METH_FASTCALL, nullptr},
-    {"decode_tree", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(decode_tree)),
-     METH_FASTCALL, nullptr},
-    {"compact_tree", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(compact_tree)),
-     METH_FASTCALL, nullptr},
-    {nullptr, nullptr, 0, nullptr}};
+// A method of N arguments.
+template <PyObject* (*F)(PyObject* const*), Py_ssize_t N>
+PyMethodDef method(const char* name) {
+  return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(entry<F, N>)),
+          METH_FASTCALL, nullptr};
+}
+PyMethodDef methods[] = {method<norm_rope, 21>("norm_rope"), method<decode_tree, 22>("decode_tree"),
+                         method<compact_tree, 14>("compact_tree"), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods,
                       nullptr,               nullptr,    nullptr, nullptr};
 
