@@ -822,8 +822,8 @@ def pd_decode_tree(q, cu_q, k_cache, v_cache, block_tables, seq_lens, out, *, ma
     if not crosscheck and q.is_cuda:
         code = _dtype_code(kv_dtype)
         workspace = _tree_scratch(q, workspace, max_q_len, hq, num_kv_heads, d, code, stream)
-        rc = _marshal.decode_tree(q, out, 0, 0, cu_q, tree_mask, k_cache, v_cache, block_tables,
-                                  seq_lens, max_q_len, num_kv_heads, block_size, num_blocks, scale,
+        rc = _marshal.decode_tree(q, out, None, None, cu_q, tree_mask, k_cache, v_cache,
+                                  block_tables, seq_lens, max_q_len, num_kv_heads, block_size, num_blocks, scale,
                                   sliding_window, num_sinks, code, k_scale, v_scale, workspace,
                                   _stream(stream))
         if rc is not None:
@@ -847,10 +847,10 @@ def pd_decode_tree_strided(q_rows, cu_q, k_cache, v_cache, block_tables, seq_len
         code = _dtype_code(kv_dtype)
         workspace = _tree_scratch(q_rows, workspace, max_q_len, num_q_heads, num_kv_heads, head_dim,
                                   code, stream)
-        rc = _marshal.decode_tree(q_rows, out_rows, num_q_heads, head_dim, cu_q, tree_mask, k_cache,
-                                  v_cache, block_tables, seq_lens, max_q_len, num_kv_heads,
-                                  block_size, num_blocks, scale, sliding_window, num_sinks, code,
-                                  k_scale, v_scale, workspace, _stream(stream))
+        rc = _marshal.decode_tree_rows(q_rows, out_rows, num_q_heads, head_dim, cu_q, tree_mask,
+                                       k_cache, v_cache, block_tables, seq_lens, max_q_len,
+                                       num_kv_heads, block_size, num_blocks, scale, sliding_window,
+                                       num_sinks, code, k_scale, v_scale, workspace, _stream(stream))
         if rc is not None:
             _check("pd_decode_tree", rc)
             return out_rows

@@ -113,7 +113,7 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
 constexpr auto kBf16 = at::kBFloat16;
 constexpr auto kI32 = at::kInt;
 
-// (qkv, q_out or None: in place, num_q_heads, head_dim (0: q_out's), k_cache, v_cache,
+// (qkv, q_out or None: in place, num_q_heads, head_dim (read in place only), k_cache, v_cache,
 //  positions, slot_mapping, cos_sin, num_kv_heads, block_size, num_blocks, q_weight,
 //  k_weight, eps, weight_offset, interleaved, kv_dtype, k_scale, v_scale, stream)
 PyObject* norm_rope(PyObject* const* args) {
@@ -165,27 +165,31 @@ PyObject* norm_rope(PyObject* const* args) {
   });
 }
 
-// (q, out, num_q_heads, head_dim (0: q and out are [total_q, num_q_heads, head_dim]), cu_q,
-//  tree_mask or None, k_cache, v_cache, block_tables, seq_lens, max_q_len, num_kv_heads,
-//  block_size, num_blocks, scale, sliding_window, num_sinks, kv_dtype, k_scale, v_scale,
-//  workspace, stream)
+// (q, out, num_q_heads, head_dim, cu_q, tree_mask or None, k_cache, v_cache, block_tables,
+//  seq_lens, max_q_len, num_kv_heads, block_size, num_blocks, scale, sliding_window, num_sinks,
+//  kv_dtype, k_scale, v_scale, workspace, stream): q and out [total_q, row] with ROWS, else
+//  [total_q, num_q_heads, head_dim] and None for the two numbers
+template <bool ROWS>
 PyObject* decode_tree(PyObject* const* args) {
   Args g{args};
   const at::Tensor* q = g.tensor(0);
   const at::Tensor* o = g.tensor(1);
-  if (!g.ok || q->scalar_type() != kBf16 || o->scalar_type() != kBf16 || q->dim() < 2)
+  if (!g.ok || q->scalar_type() != kBf16 || o->scalar_type() != kBf16 ||
+      q->dim() != (ROWS ? 2 : 3) || o->dim() != q->dim() || o->size(0) != q->size(0))
     Py_RETURN_NONE;
-  int64_t hq = g.i64(2), d = g.i64(3), qs = 0, os = 0;
   const int64_t T = q->size(0);
-  if (d == 0) {
-    if (q->dim() != 3 || !q->sizes().equals(o->sizes())) Py_RETURN_NONE;
-    hq = q->size(1);
-    d = q->size(2);
-  } else {
-    if (q->dim() != 2 || o->dim() != 2 || o->size(0) != T) Py_RETURN_NONE;
+  int64_t hq, d, qs = 0, os = 0;
+  if constexpr (ROWS) {
+    hq = g.i64(2);
+    d = g.i64(3);
     qs = q->size(1);
     os = o->size(1);
-    if (hq < 0 || d < 0 || qs < hq * d || os < hq * d) Py_RETURN_NONE;
+    if (!g.ok || hq < 0 || d < 0 || hq > INT32_MAX || d > INT32_MAX || qs < hq * d || os < hq * d)
+      Py_RETURN_NONE;
+  } else {
+    if (args[2] != Py_None || args[3] != Py_None || !q->sizes().equals(o->sizes())) Py_RETURN_NONE;
+    hq = q->size(1);
+    d = q->size(2);
   }
   const at::Tensor* bt = g.tensor(8);
   if (!bt || bt->scalar_type() != kI32 || bt->dim() != 2) Py_RETURN_NONE;
@@ -262,8 +266,11 @@ PyMethodDef method(const char* name) {
   return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(entry<F, N>)),
           METH_FASTCALL, nullptr};
 }
-PyMethodDef methods[] = {method<norm_rope, 21>("norm_rope"), method<decode_tree, 22>("decode_tree"),
-                         method<compact_tree, 14>("compact_tree"), {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {method<norm_rope, 21>("norm_rope"),
+                         method<decode_tree<false>, 22>("decode_tree"),
+                         method<decode_tree<true>, 22>("decode_tree_rows"),
+                         method<compact_tree, 14>("compact_tree"),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods,
                       nullptr,               nullptr,    nullptr, nullptr};
 

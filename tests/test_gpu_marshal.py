@@ -41,6 +41,15 @@ def test_rows_of_the_wrong_rank():
         strided(z(2, 256), z())
 
 
+@pytest.mark.parametrize("kw", [dict(head_dim=0), dict(head_dim=0, num_q_heads=99),
+                                dict(head_dim=None, num_q_heads=None)])
+def test_packed_tensors_are_not_rows(kw):
+    """3-D tensors belong to pd_decode_tree, whatever head_dim says."""
+    q = z(2, 4, 64)
+    with pytest.raises(ValueError, match="q_rows"):
+        strided(q, q, **kw)
+
+
 def test_tensors_without_an_address():
     """Inside vmap a tensor has no address to give."""
     with pytest.raises((ValueError, RuntimeError)):

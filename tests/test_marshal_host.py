@@ -37,7 +37,7 @@ GOOD = {
     "norm_rope": [z(2, 512, dtype=bf), z(2, 4, 64, dtype=bf), 0, 0, z(64), z(64), z(2, dtype=i32),
                   z(2, dtype=i32), z(8, 64), 2, 16, 4, z(64, dtype=bf), z(64, dtype=bf), 1e-6, 0.0,
                   False, 0, 1.0, 1.0, 0],
-    "decode_tree": [z(2, 4, 64, dtype=bf), z(2, 4, 64, dtype=bf), 0, 0, z(3, dtype=i32),
+    "decode_tree": [z(2, 4, 64, dtype=bf), z(2, 4, 64, dtype=bf), None, None, z(3, dtype=i32),
                     z(2, dtype=torch.int64), z(64), z(64), z(2, 4, dtype=i32), z(2, dtype=i32), 2, 2,
                     16, 4, 1.0, 0, 0, 0, 1.0, 1.0, z(64), 0],
     "compact_tree": [z(2, 64), z(2, 64), z(2, 4, dtype=i32), z(2, dtype=i32), z(3, dtype=i32),
@@ -50,11 +50,21 @@ def call(name, **at):
     return getattr(M, name)(*a)
 assert call("norm_rope") == 41 and call("decode_tree") == 42 and call("compact_tree") == 43
 rows = z(2, 256, dtype=bf)
+GOOD["decode_tree_rows"] = [rows, rows, 4, 64] + GOOD["decode_tree"][4:]
 """
 
 CASES = {
-    "rows": 'assert call("decode_tree", _0=rows, _1=rows, _2=4, _3=64) == 42\n'
-            'assert call("norm_rope", _1=None, _2=4, _3=64) == 41',
+    "rows": """
+assert call("decode_tree_rows") == 42
+assert call("norm_rope", _1=None, _2=4, _3=64) == 41
+# neither form of the attention takes the other's tensors
+q = GOOD["decode_tree"][0]
+for hq, d in ((4, 64), (0, 0), (9999, 0), (None, None)):
+    assert call("decode_tree_rows", _0=q, _1=q, _2=hq, _3=d) is None
+    assert call("decode_tree", _0=rows, _1=rows, _2=hq, _3=d) is None
+assert call("decode_tree_rows", _2=5) is None
+assert call("decode_tree_rows", _2=-4, _3=-64) is None
+assert call("decode_tree", _2=4, _3=64) is None""",
     "0-dim": """
 for name, args in GOOD.items():
     for i, x in enumerate(args):
@@ -64,12 +74,12 @@ for name, args in GOOD.items():
             assert r is None or x.dtype == torch.float32, (name, i, r)
 s = z((), dtype=bf)
 assert call("decode_tree", _0=s, _1=s) is None
-assert call("decode_tree", _0=s, _1=s, _2=4, _3=64) is None
-assert call("decode_tree", _0=rows, _1=s, _2=4, _3=64) is None""",
+assert call("decode_tree_rows", _0=s, _1=s) is None
+assert call("decode_tree_rows", _1=s) is None""",
     "1-dim": """
 s = z(256, dtype=bf)
 assert call("decode_tree", _0=s, _1=s) is None
-assert call("decode_tree", _0=s, _1=s, _2=4, _3=64) is None""",
+assert call("decode_tree_rows", _0=s, _1=s) is None""",
     "vmap": """
 got = []
 for name, args in GOOD.items():
@@ -79,7 +89,7 @@ for name, args in GOOD.items():
                 got.append((name, i, call(name, **{f"_{i}": y})))
                 return y
             torch.vmap(f)(torch.stack([x, x]))
-assert len(got) == 26 and all(r is None for _, _, r in got), got""",
+assert len(got) == 35 and all(r is None for _, _, r in got), got""",
     "sparse": """
 assert call("decode_tree", _0=GOOD["decode_tree"][0].to_sparse()) is None
 assert call("compact_tree", _0=z(2, 64).to_sparse(), _1=z(2, 64).to_sparse()) is None""",

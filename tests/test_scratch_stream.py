@@ -85,7 +85,8 @@ def made(monkeypatch):
     monkeypatch.setattr(B, "_lib", Lib())
     monkeypatch.setattr(B, "_tree_workspace", lambda *a: 4096)
     monkeypatch.setattr(B, "_num_sms", lambda device: 152)
-    monkeypatch.setattr(B, "_marshal", types.SimpleNamespace(decode_tree=lambda *a: 0))
+    monkeypatch.setattr(B, "_marshal", types.SimpleNamespace(decode_tree=lambda *a: 0,
+                                                               decode_tree_rows=lambda *a: 0))
     for name in ("_dev", "_ptr", "_cache_ptr"):
         monkeypatch.setattr(B, name, lambda *a: 0x100)
     return handles
