@@ -12,21 +12,36 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import warnings
 
 import torch
 
-from .build import LIB as _LIB_PATH, MARSHAL as _MARSHAL_PATH
+from .build import LIB as _LIB_PATH, MARSHAL as _MARSHAL_PATH, marshal_fits
 
-for _path in (_LIB_PATH, _MARSHAL_PATH):
-    if not os.path.exists(_path):
-        raise ImportError(f"{_path} is not built; run `python -m paged_kv_split_gb300.build` "
-                          "(or __graft_entry__.build()) on a machine with nvcc")
+if not os.path.exists(_LIB_PATH):
+    raise ImportError(f"{_LIB_PATH} is not built; run `python -m paged_kv_split_gb300.build` "
+                      "(or __graft_entry__.build()) on a machine with nvcc")
 
 _lib = ctypes.CDLL(_LIB_PATH)
 
-# the draft-and-verify calls without ctypes, for the arguments they usually get:
-# a status, or None for others, which the Python below then takes or refuses
-from . import _marshal  # noqa: E402
+
+def _load_marshal():
+    """The draft-and-verify calls without ctypes, for the arguments they usually
+    get: a status, or None for others, which the Python below then takes or
+    refuses. None where it was not built for this Python and torch: then the
+    Python below takes all calls, some 10 us slower each."""
+    why = "it was not built for this Python and torch"
+    if marshal_fits():
+        try:
+            from . import _marshal
+            return _marshal
+        except ImportError as e:
+            why = str(e)
+    warnings.warn(f"{_MARSHAL_PATH} is not used, calls take longer without it: {why}")
+    return None
+
+
+_marshal = _load_marshal()
 
 PD_OK = 0
 PD_KV_BF16, PD_KV_FP8_E4M3, PD_KV_NVFP4 = 0, 1, 2
@@ -711,7 +726,7 @@ def pd_qk_norm_rope_cache(qkv, q_out, k_cache, v_cache, positions, slot_mapping,
     possibly more). q_out: contiguous bf16 [T, Hq, D]. positions, slot_mapping:
     int32 [T]. cos_sin: float32 [max_position, rot_dim] from pd_rope_table.
     Without weights only the rotation is applied."""
-    if qkv.is_cuda:
+    if _marshal is not None and qkv.is_cuda:
         rc = _marshal.norm_rope(qkv, q_out, 0, 0, k_cache, v_cache, positions, slot_mapping,
                                 cos_sin, num_kv_heads, block_size, num_blocks, q_weight, k_weight,
                                 eps, weight_offset, interleaved, _dtype_code(kv_dtype), k_scale,
@@ -733,7 +748,7 @@ def pd_qk_norm_rope_cache_(qkv, k_cache, v_cache, positions, slot_mapping, cos_s
                            kv_dtype=PD_KV_BF16, k_scale=1.0, v_scale=1.0, stream=None):
     """pd_qk_norm_rope_cache in place: the q heads of the fused rows are
     replaced by their rotated form, ready for pd_decode_tree_strided."""
-    if qkv.is_cuda:
+    if _marshal is not None and qkv.is_cuda:
         rc = _marshal.norm_rope(qkv, None, num_q_heads, head_dim, k_cache, v_cache, positions,
                                 slot_mapping, cos_sin, num_kv_heads, block_size, num_blocks,
                                 q_weight, k_weight, eps, weight_offset, interleaved,
@@ -819,13 +834,13 @@ def pd_decode_tree(q, cu_q, k_cache, v_cache, block_tables, seq_lens, out, *, ma
     if q.dim() != 3 or out.shape != q.shape:
         raise ValueError("q and out must be bf16 [total_q, num_q_heads, head_dim]")
     T, hq, d = q.shape
-    if not crosscheck and q.is_cuda:
+    if not crosscheck and _marshal is not None and q.is_cuda:
         code = _dtype_code(kv_dtype)
         workspace = _tree_scratch(q, workspace, max_q_len, hq, num_kv_heads, d, code, stream)
         rc = _marshal.decode_tree(q, out, None, None, cu_q, tree_mask, k_cache, v_cache,
-                                  block_tables, seq_lens, max_q_len, num_kv_heads, block_size, num_blocks, scale,
-                                  sliding_window, num_sinks, code, k_scale, v_scale, workspace,
-                                  _stream(stream))
+                                  block_tables, seq_lens, max_q_len, num_kv_heads, block_size,
+                                  num_blocks, scale, sliding_window, num_sinks, code, k_scale,
+                                  v_scale, workspace, _stream(stream))
         if rc is not None:
             _check("pd_decode_tree", rc)
             return out
@@ -843,14 +858,15 @@ def pd_decode_tree_strided(q_rows, cu_q, k_cache, v_cache, block_tables, seq_len
                            stream=None, crosscheck=False):
     """pd_decode_tree with each node's Hq * D values in the first Hq * D of a
     row of a wider buffer (q_rows / out_rows: contiguous bf16 [total_q, row])."""
-    if not crosscheck and q_rows.is_cuda:
+    if not crosscheck and _marshal is not None and q_rows.is_cuda:
         code = _dtype_code(kv_dtype)
         workspace = _tree_scratch(q_rows, workspace, max_q_len, num_q_heads, num_kv_heads, head_dim,
                                   code, stream)
         rc = _marshal.decode_tree_rows(q_rows, out_rows, num_q_heads, head_dim, cu_q, tree_mask,
                                        k_cache, v_cache, block_tables, seq_lens, max_q_len,
                                        num_kv_heads, block_size, num_blocks, scale, sliding_window,
-                                       num_sinks, code, k_scale, v_scale, workspace, _stream(stream))
+                                       num_sinks, code, k_scale, v_scale, workspace,
+                                       _stream(stream))
         if rc is not None:
             _check("pd_decode_tree", rc)
             return out_rows
@@ -873,7 +889,7 @@ def pd_compact_tree(k_caches, v_caches, block_tables, seq_lens, cu_q, accepted, 
     k_caches, v_caches: one layer's cache (1-D), or all layers' as [layers,
     cache_bytes]. accepted: int32 [B, max_accepted] strictly increasing node
     indices, num_accepted: int32 [B], new_seq_lens: int32 [B], written."""
-    if k_caches.is_cuda:
+    if _marshal is not None and k_caches.is_cuda:
         rc = _marshal.compact_tree(k_caches, v_caches, block_tables, seq_lens, cu_q, accepted,
                                    num_accepted, new_seq_lens, num_kv_heads, head_dim, block_size,
                                    num_blocks, _dtype_code(kv_dtype), _stream(stream))

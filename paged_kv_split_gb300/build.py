@@ -1,9 +1,13 @@
 """Build libpd.so in-tree with nvcc for sm_103a.
 
 Each .cu under csrc/ compiles to an object in parallel; the objects link into
-paged_kv_split_gb300/libpd.so against the shared CUDA runtime; csrc/marshal.cpp
-becomes the Python module _marshal.so beside it. A rebuild happens only when a
-source or header is newer than the libraries.
+paged_kv_split_gb300/libpd.so against the shared CUDA runtime. A rebuild
+happens only when a source or header is newer than the library.
+
+csrc/marshal.cpp becomes the Python module _marshal.so beside it, against the
+headers of torch and Python. The binding works without it, its calls take some
+10 us longer: where it cannot be built there is a warning, and one built for
+another Python or torch is rebuilt, and not loaded before that.
 
     python -m paged_kv_split_gb300.build [--force] [--verbose-ptxas]
 """
@@ -12,10 +16,12 @@ from __future__ import annotations
 import glob
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -25,6 +31,7 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpd.so")
 MARSHAL_SRC = os.path.join(CSRC, "marshal.cpp")
 MARSHAL = os.path.join(PKG, "_marshal.so")
+MARSHAL_ABI = os.path.join(BUILD_DIR, "marshal.abi")  # what _marshal.so was built for
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = [
@@ -48,7 +55,7 @@ def sources():
 
 
 def _inputs():
-    return sources() + [MARSHAL_SRC] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(
+    return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(
         os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
 
 
@@ -68,16 +75,61 @@ def marshal_ldflags() -> list:
     return ["-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10", f"-Wl,-rpath,{lib}"]
 
 
+def marshal_abi() -> str:
+    """The Python and the torch that _marshal.so depends on."""
+    with open(os.path.join(_torch_dir(), "version.py")) as f:
+        torch = re.search(r"__version__ = '([^']*)'", f.read()).group(1)
+    return f"{sysconfig.get_config_var('SOABI')} torch {torch}"
+
+
+def marshal_fits() -> bool:
+    """_marshal.so is there, for this Python and this torch."""
+    try:
+        with open(MARSHAL_ABI) as f:
+            return os.path.exists(MARSHAL) and f.read() == marshal_abi()
+    except (OSError, AttributeError):
+        return False
+
+
+def _older(path, inputs) -> bool:
+    return not os.path.exists(path) or any(os.path.getmtime(p) > os.path.getmtime(path)
+                                           for p in inputs)
+
+
 def is_stale() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(MARSHAL)):
-        return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(MARSHAL))
-    return any(os.path.getmtime(p) > t for p in _inputs())
+    return _older(LIB, _inputs())
 
 
-def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = True) -> str:
-    if not (force or is_stale()):
-        return LIB
+def marshal_is_stale() -> bool:
+    return not marshal_fits() or _older(MARSHAL, [MARSHAL_SRC, os.path.abspath(__file__)] +
+                                        glob.glob(os.path.join(INCLUDE, "*.h")))
+
+
+def _build_marshal() -> bool:
+    """Build _marshal.so; without it, a warning and False."""
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    try:
+        cmd = ["g++", *marshal_cflags(), "-shared", "-o", tmp, MARSHAL_SRC, "-L", PKG,
+               "-l:libpd.so", *marshal_ldflags(), "-Wl,-rpath,$ORIGIN"]
+        r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+        why = r.stdout.decode(errors="replace") if r.returncode else None
+        abi = marshal_abi()
+    except (OSError, AttributeError) as e:  # no g++, no torch
+        why = str(e)
+    if why is not None:
+        if os.path.exists(tmp):
+            os.remove(tmp)
+        warnings.warn(f"{MARSHAL} was not built; calls take longer without it:\n{why}")
+        return False
+    if os.path.exists(MARSHAL_ABI):
+        os.remove(MARSHAL_ABI)  # never a module beside another one's mark
+    os.replace(tmp, MARSHAL)
+    with open(MARSHAL_ABI, "w") as f:
+        f.write(abi)
+    return True
+
+
+def _build_lib(verbose_ptxas: bool, quiet: bool) -> None:
     os.makedirs(BUILD_DIR, exist_ok=True)
     cc = nvcc()
     extra = ["-Xptxas", "-v"] if verbose_ptxas else []
@@ -88,10 +140,6 @@ def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = True) 
         objs.append(obj)
         cmd = [cc, *NVCC_FLAGS, *extra, "-c", src, "-o", obj]
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
-    marshal_obj = os.path.join(BUILD_DIR, "marshal.cpp.o")
-    cmd = ["g++", *marshal_cflags(), "-c", MARSHAL_SRC, "-o", marshal_obj]
-    procs.append((MARSHAL_SRC, subprocess.Popen(cmd, stdout=subprocess.PIPE,
-                                                stderr=subprocess.STDOUT)))
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -102,16 +150,20 @@ def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = True) 
             sys.stdout.write(text)
     if failed:
         msg = "\n".join(f"--- {s}\n{t}" for s, t in failed)
-        raise RuntimeError(f"compiling failed:\n{msg}")
+        raise RuntimeError(f"nvcc failed:\n{msg}")
     tmp = LIB + f".tmp{os.getpid()}"
     cuda_lib = os.path.join(os.path.dirname(os.path.dirname(cc)), "lib64")
     subprocess.run([cc, *ARCH, "-shared", "-cudart", "shared", "-Xlinker", f"-rpath,{cuda_lib}",
                     "-o", tmp, *objs], check=True)
     os.replace(tmp, LIB)
-    tmp = MARSHAL + f".tmp{os.getpid()}"
-    subprocess.run(["g++", "-shared", "-o", tmp, marshal_obj, "-L", PKG, "-l:libpd.so",
-                    *marshal_ldflags(), "-Wl,-rpath,$ORIGIN"], check=True)
-    os.replace(tmp, MARSHAL)
+
+
+def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = True) -> str:
+    if force or is_stale():
+        _build_lib(verbose_ptxas, quiet)
+    if force or marshal_is_stale():
+        os.makedirs(BUILD_DIR, exist_ok=True)
+        _build_marshal()
     return LIB
 
 
