@@ -15,7 +15,7 @@ def _cuda():
 
 
 def z(*shape, dtype=torch.bfloat16):
-    return torch.zeros(*shape, dtype=dtype, device="cuda")
+    return torch.zeros(shape, dtype=dtype, device="cuda")
 
 
 def i32(*shape):
