@@ -333,7 +333,7 @@ def pd_test_encode(fmt: int, first_bits: int, codes, stream=None) -> None:
 
 
 def pd_test_set_consumer_wait_ns(ns: int) -> int:
-    """Test hook: the decode kernels' consumer wait limit (0xFFFFFFFF = default).
+    """Test hook: the decode and tree attention kernels' consumer wait limit (0xFFFFFFFF = default).
     Returns the previous limit."""
     return int(_lib.pd_test_set_consumer_wait_ns(int(ns) & 0xFFFFFFFF))
 

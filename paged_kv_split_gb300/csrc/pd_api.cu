@@ -31,7 +31,7 @@ struct DeviceInfo {
 };
 DeviceInfo g_devices[kMaxDevices];
 
-// Limit of the decode kernels' consumer-side waits (ns). Only a test changes
+// Limit of the decode and tree attention kernels' consumer-side waits (ns). Only a test changes
 // it (pd_test_set_consumer_wait_ns), to make those waits run out on purpose.
 constexpr uint32_t kDefaultConsumerWaitNs = 2000000000u;
 std::atomic<uint32_t> g_consumer_wait_ns{kDefaultConsumerWaitNs};
@@ -1143,13 +1143,14 @@ int decode_tree_impl(const void* q, int64_t q_stride, const int32_t* cu_q,
   a.max_blocks_per_seq = max_blocks_per_seq;
   a.sliding_window = sliding_window;
   a.num_sinks = num_sinks;
+  a.consumer_wait_ns = g_consumer_wait_ns.load(std::memory_order_relaxed);
+  a.half_bits = 0;
   a.scale_log2 = scale * kLog2e;
   a.k_scale = k_scale;
   a.v_scale = v_scale;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (simple) return cuda_status(launch_tree_simple(a, head_dim, kv_dtype, st));
   TreeWork w;
-  a.half_bits = 0;
   if (tree_on_umma(max_q_len, a.group, head_dim)) {
     a.half_bits = head_dim > 256 ? 1 : 0;
     tree_umma_workspace(max_q_len, a.group, head_dim, dev->num_sms, &w, workspace);

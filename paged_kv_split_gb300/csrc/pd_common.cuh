@@ -255,6 +255,7 @@ struct TreeArgs {
   int num_seqs, total_q, max_q_len, num_q_heads, num_kv_heads, group, block_size;
   int max_blocks_per_seq, sliding_window, num_sinks;
   int half_bits;                 // 1: an item is half of head_dim's columns of V and O
+  uint32_t consumer_wait_ns;     // limit of the waits for copies (0: one probe)
   float scale_log2;              // scale * log2(e)
   float k_scale, v_scale;
 };

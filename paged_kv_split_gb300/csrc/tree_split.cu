@@ -10,7 +10,7 @@
 // Keys are dealt by the device plan of tree_plan.cuh in 16-key tiles; a warp
 // produces (TMA copies for BF16 and FP8, bulk copies for NVFP4, one page a tile)
 // and four consume. All warps walk the plan themselves. Waits are bounded as in
-// decode_balanced.cu.
+// decode_balanced.cu, the consumers' by consumer_wait_ns.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kMmaThreads, (SplitCfg<FMT, D, NT>::kPerSm))
   Walker walk(a, share, TPC, C::kKT, kSplitSlack);
   Piece q;
   int i = 0;      // tiles so far
-  int piece = 0;
+  int piece = 0;  // pieces whose q rows were copied, or used
 
   // =========================== producer warp ===============================
   if (warp == kConsumerWarps) {
@@ -162,6 +162,7 @@ __global__ void __launch_bounds__(kMmaThreads, (SplitCfg<FMT, D, NT>::kPerSm))
                   a.q + static_cast<int64_t>(q.p.s.q0 + node0 + lane) * a.q_stride +
                       static_cast<int64_t>(q.g) * G * D,
                   G * D * 2, smem_u32(q_full));
+      ++piece;
       const int32_t* bt = a.block_tables + static_cast<int64_t>(q.b) * a.max_blocks_per_seq;
       int base = -(1 << 30), entry = -1, ahead = -1;  // entries [base, base + 32), the next 32
       auto load = [&](int e) { return e < a.max_blocks_per_seq ? bt[e] : -1; };
@@ -216,13 +217,13 @@ __global__ void __launch_bounds__(kMmaThreads, (SplitCfg<FMT, D, NT>::kPerSm))
         }
         __syncwarp();
       }
-      if (ok) ++piece;
     }
     if (!ok) {
       if (lane == 0 && *abort_s == 0) atomicOr(a.flags, PD_DEV_TIMEOUT);
       *abort_s = 1;
     }
-    // every copy issued lands before the block can exit
+    // every copy issued lands before the block can exit, the q rows of a piece
+    // that was given up among them
     for (int t = max(0, i - C::kStages); t < i; ++t)
       (void)mbar_wait(smem_u32(&full_bar[t % C::kStages]), (t / C::kStages) & 1);
     if (piece > 0) (void)mbar_wait(smem_u32(q_full), (piece - 1) & 1);
@@ -267,7 +268,7 @@ __global__ void __launch_bounds__(kMmaThreads, (SplitCfg<FMT, D, NT>::kPerSm))
       }
     mask.open_lo = __reduce_max_sync(0xFFFFFFFFu, open_lo);
     // ---- q fragments ----
-    if (!agree(warp_wait(smem_u32(q_full), piece & 1, abort_s))) return;
+    if (!agree(warp_wait(smem_u32(q_full), piece & 1, abort_s, a.consumer_wait_ns))) return;
     TileState<C, NT> ts;
     load_q_fragments<FMT, D, NT>(ts, reinterpret_cast<const uint16_t*>(q_s), rows, a.scale_log2,
                                  a.k_scale, tp, qmax_s);
@@ -276,7 +277,9 @@ __global__ void __launch_bounds__(kMmaThreads, (SplitCfg<FMT, D, NT>::kPerSm))
     reset_state(ts);
     for (int j = q.j0; j < q.j1; ++j, ++i) {
       const int st = i % C::kStages;
-      if (!agree(warp_wait(smem_u32(&full_bar[st]), (i / C::kStages) & 1, abort_s))) return;
+      if (!agree(warp_wait(smem_u32(&full_bar[st]), (i / C::kStages) & 1, abort_s,
+                           a.consumer_wait_ns)))
+        return;
       const uint32_t kst = smem_u32(smem + st * C::kStageBytes);
       const int t0 = tile_key(q.p, j, C::kKT);
       consume_tile<FMT, D, NT>(
