@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kMmaThreads, (SplitCfg<FMT, D, NT>::kPerSm))
       }
     }
     if (!ok) {
-      if (lane == 0 && *abort_s == 0) atomicOr(a.flags, PD_DEV_TIMEOUT);
+      if (lane == 0) atomicOr(a.flags, PD_DEV_TIMEOUT);
       *abort_s = 1;
     }
     // every copy issued lands before the block can exit, the q rows of a piece
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kMmaThreads, (SplitCfg<FMT, D, NT>::kPerSm))
   auto agree = [&](bool ok) {
     ok = consumers_vote(ok);
     if (!ok) {
-      if (lane == 0 && *abort_s == 0) atomicOr(a.flags, PD_DEV_TIMEOUT);
+      if (lane == 0) atomicOr(a.flags, PD_DEV_TIMEOUT);
       *abort_s = 1;
     }
     return ok;

@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
   Piece q;
   bool failed = false;
   auto give_up = [&](bool say) {
-    if (say && *abort_s == 0) atomicOr(a.flags, PD_DEV_TIMEOUT);
+    if (say) atomicOr(a.flags, PD_DEV_TIMEOUT);
     *abort_s = 1;
     failed = true;
   };
