@@ -33,7 +33,7 @@
 //    same chain with the widening in it. Without the softmax these take 94, 65, 73
 //    and 141 us, with an eighth of the products 95, 66, 71 and 165. head_dim 512, 64
 //    nodes of 8 heads over 28000 keys: 179 us (mma.sync 690).
-//  * Every wait is bounded (2 s): on time-out the CTA raises PD_DEV_TIMEOUT,
+//  * Every wait is bounded (2 s, those for copies by consumer_wait_ns): on time-out the CTA raises PD_DEV_TIMEOUT,
 //    waits for its copies and MMAs in flight, frees its TMEM and ends.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -113,8 +113,9 @@ struct TreeCfg {
   static constexpr int kMulOff = kViewOff + 64 * 12 + 16;
   static constexpr int kBadOff = kMulOff + 256 * 4;
   static constexpr int kHolderOff = kBadOff + kTreeBadRing * 4;
-  static constexpr int kSmemBytes = kHolderOff + 16;
-  static_assert(kProds <= (kQuant ? kRaws : kUnits), "producers are not lapped");
+  static constexpr int kLastOff = kHolderOff + 16;  // the producers' newest units
+  static constexpr int kSmemBytes = kLastOff + 16;
+  static_assert(kProds <= (kQuant ? kRaws : kUnits) && kProds <= 4, "producers are not lapped");
   static_assert(kUnitBytes % 1024 == 0 && kRawBytes % 1024 == 0, "aligned tiles");
   static_assert(kSmemBytes <= 227 * 1024, "one CTA's shared memory");
 };
@@ -133,17 +134,20 @@ __device__ __forceinline__ bool try_wait_long(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 __device__ __forceinline__ bool sleep_wait(uint32_t bar, uint32_t parity,
-                                           const volatile int* abort_flag) {
+                                           const volatile int* abort_flag,
+                                           uint64_t limit_ns = kWaitLimitNs) {
+  if (limit_ns == 0) return mbar_test_wait(bar, parity);
   if (try_wait_long(bar, parity)) return true;
   const uint64_t t0 = global_ns();
   while (!try_wait_long(bar, parity)) {
-    if (*abort_flag != 0 || global_ns() - t0 > kWaitLimitNs) return false;
+    if (*abort_flag != 0 || global_ns() - t0 > limit_ns) return false;
   }
   return true;
 }
 __device__ __forceinline__ bool warp_sleep_wait(uint32_t bar, uint32_t parity,
-                                                const volatile int* abort_flag) {
-  return __all_sync(0xFFFFFFFFu, sleep_wait(bar, parity, abort_flag));
+                                                const volatile int* abort_flag,
+                                                uint64_t limit_ns = kWaitLimitNs) {
+  return __all_sync(0xFFFFFFFFu, sleep_wait(bar, parity, abort_flag, limit_ns));
 }
 
 // Order in which a piece of T tiles uses its 2 T units: dual (each group has its
@@ -553,11 +557,15 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
       u0 += 2 * T;
       tile0 += T;
     }
-    // every copy issued lands before the CTA can end
-    // (a slot's last unit only: an earlier phase could not be told from a later)
-    const int end = failed ? last + 1 : u0;
-    for (int u = end - 1; u >= 0 && u >= end - kSlots; --u)
-      if ((u & (C::kProds - 1)) == mine) (void)mbar_wait(smem_u32(&full[u % kSlots]), (u / kSlots) & 1);
+    // every copy issued lands before the CTA can end: each slot's newest unit, whose
+    // producer waits for it (an older unit has landed, and its phase could not be
+    // told from the next but one)
+    volatile int* last_s = reinterpret_cast<volatile int*>(smem + C::kLastOff);
+    if (lane == 0) last_s[mine] = last;
+    asm volatile("bar.sync 1, %0;" ::"n"(C::kProds * 32) : "memory");
+    for (int u = last; u >= 0 && u > last - kSlots; u -= C::kProds)
+      if (u + kSlots > last_s[(u + kSlots) & (C::kProds - 1)])
+        (void)mbar_wait(smem_u32(&full[u % kSlots]), (u / kSlots) & 1);
   } else if (warp == kTreeQ) {
     // =========================== q rows ===================================
     int piece = 0;
@@ -642,7 +650,8 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
           slot = 0;
           turn ^= 1u;
         }
-        return sleep_wait(smem_u32(&u_full[s]), ph, abort_s);
+        return sleep_wait(smem_u32(&u_full[s]), ph, abort_s,
+                          kQuant ? kWaitLimitNs : a.consumer_wait_ns);
       };
       while (ok && walk.next(q)) {
         const int nodes = min(IN, q.p.s.n - q.rt * IN);
@@ -736,7 +745,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
         for (int t = 0; t < 2 * T; ++t) {
           const bool is_v = next_k == T || (dual ? t & 1 : next_k - next_v == 2);  // as unit_at
           const int j = is_v ? next_v++ : next_k++;
-          if (!warp_sleep_wait(smem_u32(&r_full[rs]), r_turn, abort_s) ||
+          if (!warp_sleep_wait(smem_u32(&r_full[rs]), r_turn, abort_s, a.consumer_wait_ns) ||
               !warp_sleep_wait(smem_u32(&u_empty[us]), u_turn, abort_s)) {
             give_up(lane == 0);
             break;
