@@ -963,11 +963,11 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
               tmem_st16(o_tm + (kOneO ? 0 : X * D) + h * 16, v);
             }
           }
+          tmem_wait_st();  // (before a CTA that gives up frees the columns, too)
           if (lost) {
             give_up(lane == 0);
             break;
           }
-          tmem_wait_st();
         }
         tc_fence_before();
         __syncwarp();
