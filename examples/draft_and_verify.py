@@ -43,6 +43,7 @@ class Model:
 
         E, qkv = self.hidden, (self.hq + 2 * self.hkv) * self.d
         self.kv_dtype, self.num_blocks, self.block_size = kv_dtype, num_blocks, block_size
+        self.max_position = max_position
         self.kv_scale = 6.0 / 448 if kv_dtype == pd.PD_KV_FP8_E4M3 else 1.0
         self.embed = weight(E, self.vocab, gain=E ** 0.5).t().contiguous()
         self.wqkv = [weight(E, qkv) for _ in range(self.layers)]
@@ -101,14 +102,37 @@ def slots_of(tables, rows, seq, block_size):
     return (page * block_size + rows % block_size).int()
 
 
+def rows_needed(longest, steps, depth):
+    """Cached rows of a sequence that starts with `longest` and takes `steps` steps:
+    each adds depth + 1 at most, and the last needs its whole tree's."""
+    return longest + max(steps - 1, 0) * (depth + 1) + (1 + 2 * depth if steps > 0 else 0)
+
+
+def steps_that_fit(longest, rows, depth):
+    return max((rows - longest - (1 + 2 * depth)) // (depth + 1) + 1, 0)
+
+
 class DraftAndVerify:
     """Sequences being decoded: `tokens` accepted last, `lens` cached rows.
 
     A tree is the last accepted token, then `depth` levels of the bigram's first
-    choice (which goes on) and its second (which does not)."""
+    choice (which goes on) and its second (which does not).
+
+    Lengths are on the device, where a row past the block table is found by a fault
+    only: so `steps_left` counts on the host what fits whatever is accepted, and a
+    step beyond it is refused."""
 
     def __init__(self, model, prompts, tables, depth=4):
         dev = tables.device
+        rows = min(tables.shape[1] * model.block_size, model.max_position)
+        longest = max(len(p) for p in prompts)
+        if len(prompts) != tables.shape[0] or min(len(p) for p in prompts) < 1:
+            raise ValueError("one prompt of one token at least for each row of the block table")
+        if longest > rows:
+            raise ValueError(f"a prompt of {longest} tokens does not fit {rows} rows")
+        if any(int(p.min()) < 0 or int(p.max()) >= model.vocab for p in prompts):
+            raise ValueError(f"a token outside the vocabulary of {model.vocab}")
+        self.steps_left = steps_that_fit(longest, rows, depth)
         self.model, self.tables, self.depth = model, tables, depth
         B, n = tables.shape[0], 1 + 2 * depth
         self.B, self.n = B, n
@@ -144,6 +168,15 @@ class DraftAndVerify:
 
     def step(self):
         """One step; nothing here waits for the device or asks it for a length."""
+        self._take()
+        self._step()
+
+    def _take(self):
+        if self.steps_left < 1:
+            raise ValueError("no room for another step in the block table or the rotation table")
+        self.steps_left -= 1
+
+    def _step(self):
         m, B, n, depth = self.model, self.B, self.n, self.depth
         # ---- draft ----
         level = [self.tokens[:, None]]
@@ -183,16 +216,29 @@ class DraftAndVerify:
         self.lens.copy_(new_lens)
 
     def capture(self):
-        """The step as a CUDA graph; the state is as before the call."""
+        """The step as a CUDA graph, to replay(); the state is as before the call."""
+        if self.steps_left < 1:
+            raise ValueError("no room for a step in the block table or the rotation table")
         keep = [x.clone() for x in (self.lens, self.tokens)]
-        self.step()                                               # per-device set-up
+        self._step()                                              # per-device set-up
         graph = torch.cuda.CUDAGraph()
         torch.cuda.synchronize()
         with torch.cuda.graph(graph):
-            self.step()
+            self._step()
         for x, was in zip((self.lens, self.tokens), keep):
             x.copy_(was)
-        return graph
+        return Captured(self, graph)
+
+
+class Captured:
+    """A captured step: replay() is step() without the host's work."""
+
+    def __init__(self, run, graph):
+        self.run, self.graph = run, graph
+
+    def replay(self):
+        self.run._take()
+        self.graph.replay()
 
 
 def block_tables(num_seqs, blocks_per_seq, seed=0, device="cuda"):
@@ -201,17 +247,31 @@ def block_tables(num_seqs, blocks_per_seq, seed=0, device="cuda"):
     return torch.randperm(num_seqs * blocks_per_seq, generator=g).view(num_seqs, -1).int().to(device)
 
 
-def main():
+def sizes(prompt_lens, steps, depth, block_size=16):
+    """(pages of a sequence, positions) for `steps` steps of these prompts."""
+    rows = rows_needed(max(prompt_lens), steps, depth)
+    pages = (rows + block_size - 1) // block_size
+    return pages, pages * block_size
+
+
+def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     ap.add_argument("--kv", choices=sorted(KV), default="bf16")
     ap.add_argument("--steps", type=int, default=32)
     ap.add_argument("--seqs", type=int, default=8)
-    args = ap.parse_args()
-    tables = block_tables(args.seqs, 64)
-    model = Model(tables.numel(), kv_dtype=KV[args.kv])
+    args = ap.parse_args(argv)
+    if args.steps < 1 or args.seqs < 1:
+        ap.error("--steps and --seqs are 1 at least")
+    depth = 4
+    prompt_lens = [20 + 7 * b for b in range(args.seqs)]
+    pages, positions = sizes(prompt_lens, args.steps, depth)
+    if args.seqs * pages * 16 > 2 ** 31 - 1:
+        ap.error("more rows than a cache numbers")
+    tables = block_tables(args.seqs, pages)
+    model = Model(tables.numel(), kv_dtype=KV[args.kv], max_position=positions)
     g = torch.Generator().manual_seed(1)
-    prompts = [torch.randint(0, model.vocab, (20 + 7 * b,), generator=g) for b in range(args.seqs)]
-    run = DraftAndVerify(model, prompts, tables)
+    prompts = [torch.randint(0, model.vocab, (n,), generator=g) for n in prompt_lens]
+    run = DraftAndVerify(model, prompts, tables, depth)
     graph = run.capture()
     total = 0
     start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
