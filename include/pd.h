@@ -606,8 +606,9 @@ int pd_decode_tree_crosscheck(const void* q, int64_t q_stride, const int32_t* cu
 int pd_test_encode(int32_t format, uint32_t first_bits, int64_t count, uint8_t* codes,
                    void* stream);
 
-/* Set the limit (ns) of the decode partial kernels' and the tree attention
- * kernels' consumer-side waits for copies, for calls made after it; 0xFFFFFFFF restores the default
+/* Set the limit (ns) of the decode partial kernels' consumer-side waits for a
+ * stage of keys, and of the tree attention kernels' for the first copies of
+ * each piece of work, for calls made after it; 0xFFFFFFFF restores the default
  * (2 s). Returns the previous limit. A test sets it to 0 so that those waits
  * run out at once, to see the bounded-wait path report PD_DEV_TIMEOUT and the
  * kernel end normally: a consumer warp that gives up stops handing stages

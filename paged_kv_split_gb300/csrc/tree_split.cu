@@ -10,7 +10,7 @@
 // Keys are dealt by the device plan of tree_plan.cuh in 16-key tiles; a warp
 // produces (TMA copies for BF16 and FP8, bulk copies for NVFP4, one page a tile)
 // and four consume. All warps walk the plan themselves. Waits are bounded as in
-// decode_balanced.cu, the consumers' by consumer_wait_ns.
+// decode_balanced.cu, the consumers' for a piece's first copies by consumer_wait_ns.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -268,7 +268,12 @@ __global__ void __launch_bounds__(kMmaThreads, (SplitCfg<FMT, D, NT>::kPerSm))
       }
     mask.open_lo = __reduce_max_sync(0xFFFFFFFFu, open_lo);
     // ---- q fragments ----
-    if (!agree(warp_wait(smem_u32(q_full), piece & 1, abort_s, a.consumer_wait_ns))) return;
+    // (the first keys are waited for here, too: these two waits take the test's limit,
+    // which in the loop over the tiles cost 2% in 32 rows)
+    if (!agree(warp_wait(smem_u32(q_full), piece & 1, abort_s, a.consumer_wait_ns) &&
+               warp_wait(smem_u32(&full_bar[i % C::kStages]), (i / C::kStages) & 1, abort_s,
+                         a.consumer_wait_ns)))
+      return;
     TileState<C, NT> ts;
     load_q_fragments<FMT, D, NT>(ts, reinterpret_cast<const uint16_t*>(q_s), rows, a.scale_log2,
                                  a.k_scale, tp, qmax_s);
@@ -277,9 +282,7 @@ __global__ void __launch_bounds__(kMmaThreads, (SplitCfg<FMT, D, NT>::kPerSm))
     reset_state(ts);
     for (int j = q.j0; j < q.j1; ++j, ++i) {
       const int st = i % C::kStages;
-      if (!agree(warp_wait(smem_u32(&full_bar[st]), (i / C::kStages) & 1, abort_s,
-                           a.consumer_wait_ns)))
-        return;
+      if (!agree(warp_wait(smem_u32(&full_bar[st]), (i / C::kStages) & 1, abort_s))) return;
       const uint32_t kst = smem_u32(smem + st * C::kStageBytes);
       const int t0 = tile_key(q.p, j, C::kKT);
       consume_tile<FMT, D, NT>(

@@ -33,8 +33,9 @@
 //    same chain with the widening in it. Without the softmax these take 94, 65, 73
 //    and 141 us, with an eighth of the products 95, 66, 71 and 165. head_dim 512, 64
 //    nodes of 8 heads over 28000 keys: 179 us (mma.sync 690).
-//  * Every wait is bounded (2 s, those for copies by consumer_wait_ns): on time-out the CTA raises PD_DEV_TIMEOUT,
-//    waits for its copies and MMAs in flight, frees its TMEM and ends.
+//  * Every wait is bounded (2 s, that for a piece's first keys by consumer_wait_ns):
+//    on time-out the CTA raises PD_DEV_TIMEOUT, waits for its copies and MMAs in
+//    flight, frees its TMEM and ends.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -650,8 +651,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
           slot = 0;
           turn ^= 1u;
         }
-        return sleep_wait(smem_u32(&u_full[s]), ph, abort_s,
-                          kQuant ? kWaitLimitNs : a.consumer_wait_ns);
+        return sleep_wait(smem_u32(&u_full[s]), ph, abort_s);
       };
       while (ok && walk.next(q)) {
         const int nodes = min(IN, q.p.s.n - q.rt * IN);
@@ -659,9 +659,13 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
         const int T = q.j1 - q.j0;
         const int n0 = dual ? T : (T + 1) / 2, n1 = dual ? T : T / 2;
         const int buf = piece % nbuf;
-        // q has landed; the products that read the last P are done
+        // q has landed; the products that read the last P are done; the first keys are there
+        // (the one wait for copies that takes the test's limit: in the loop over the tiles
+        // it cost 3 to 7% above 128 rows)
         if (!(ok = wait(&q_full[buf], piece / nbuf) && (c0 == 0 || wait(&o_done[0], c0 - 1)) &&
-                   (c1 == 0 || wait(&o_done[1], c1 - 1))))
+                   (c1 == 0 || wait(&o_done[1], c1 - 1)) &&
+                   (kQuant ||
+                    sleep_wait(smem_u32(&u_full[slot]), turn, abort_s, a.consumer_wait_ns))))
           break;
         tc_fence_after();
         int ks = 0, vs = 0;  // the last K and V unit; dual pieces use each twice
@@ -731,7 +735,8 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
         const RowView any = any_view(a, q.p.s, lane);
         const int buf = piece % nbuf;
         if (!warp_sleep_wait(smem_u32(&q_raw[buf]), (piece / nbuf) & 1, abort_s) ||
-            (piece > 0 && !warp_sleep_wait(smem_u32(v_empty), (piece - 1) & 1, abort_s))) {
+            (piece > 0 && !warp_sleep_wait(smem_u32(v_empty), (piece - 1) & 1, abort_s)) ||
+            !warp_sleep_wait(smem_u32(&r_full[rs]), r_turn, abort_s, a.consumer_wait_ns)) {
           give_up(lane == 0);
           break;
         }
@@ -745,7 +750,7 @@ __global__ void __launch_bounds__(TreeCfg<FMT, D, BS>::kThreads, 1)
         for (int t = 0; t < 2 * T; ++t) {
           const bool is_v = next_k == T || (dual ? t & 1 : next_k - next_v == 2);  // as unit_at
           const int j = is_v ? next_v++ : next_k++;
-          if (!warp_sleep_wait(smem_u32(&r_full[rs]), r_turn, abort_s, a.consumer_wait_ns) ||
+          if (!warp_sleep_wait(smem_u32(&r_full[rs]), r_turn, abort_s) ||
               !warp_sleep_wait(smem_u32(&u_empty[us]), u_turn, abort_s)) {
             give_up(lane == 0);
             break;

@@ -1,8 +1,8 @@
 """Tree attention's bounded waits, made to run out on purpose: with a limit of 0
-a wait for copies is a single probe, so a kernel gives up on the first keys (or q
-rows) that have not landed. The call ends, reports PD_DEV_TIMEOUT and leaves the
+the wait for a piece's first copies is a single probe, so a kernel gives up at the
+first piece whose keys (or q rows) have not landed. The call ends, reports PD_DEV_TIMEOUT and leaves the
 device usable; the next ordinary call gives the bits of the one before. A call
-that reports nothing has found everything landed (most forms are slower than their
+that reports nothing has found everything landed (some forms are slower than their
 copies) and gives the same bits too. Nothing here faults the GPU or waits
 without a limit."""
 import time
@@ -60,16 +60,18 @@ def run_out(seqs, length, nodes, hq, hkv, d, bs, kv_dtype):
     assert B.pd_device_status(reset=True) == 0
     prev = B.pd_test_set_consumer_wait_ns(0)
     try:
-        for _ in range(3):
+        seen = 0
+        for _ in range(8):
             start = time.monotonic()
             out = B.pd_decode_tree(q, *args, torch.full_like(q, float("nan")), **kw)
             flags = B.pd_device_status(reset=True)
             # (whatever a CTA still waits for at its end comes; a wait alone would take 2 s)
             assert time.monotonic() - start < 1
-            # BF16 keys of these widths come no faster than they are used: some have not landed
-            late = kv_dtype == 0 and d in (128, 256)
-            assert flags == PD_DEV_TIMEOUT or (flags == 0 and not late)
+            assert flags in (0, PD_DEV_TIMEOUT)
             assert flags or torch.equal(out, want)
+            seen |= flags
+        # BF16 keys of these widths come no faster than they are used: some have not landed
+        assert seen or kv_dtype > 0 or d not in (128, 256)
     finally:
         B.pd_test_set_consumer_wait_ns(0xFFFFFFFF)
     assert prev == 2_000_000_000
