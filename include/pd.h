@@ -516,14 +516,17 @@ size_t pd_decode_tree_workspace_bytes(int32_t max_q_len, int32_t num_q_heads,
  *               the first tokens that stay visible. W = 0: everything stays.
  * Lengths are read on the device only: a captured graph follows cu_q, seq_lens
  * and the masks as they are at each replay (max_q_len is the one host bound).
- * out = softmax(scale q k) v over what the node sees, fp32 softmax; a node
- * that sees nothing gets a zero row. Cache rows that no node of the sequence
+ * out = softmax(scale q k) v over what the node sees: scores, exponentials
+ * and sums in fp32, the weights rounded to bf16 (BF16 cache) or f16 (FP8,
+ * NVFP4) for their product with v, summed in fp32; a node that sees nothing
+ * gets a zero row. Cache rows that no node of the sequence
  * sees may hold anything; rows that one does see are taken to be finite.
  * A sequence whose counts do not fit (n_b > max_q_len, L_b < n_b, L_b beyond
  * the block table, rows beyond total_q) raises PD_DEV_BAD_SEQ_LEN and its
- * rows are not written. workspace: pd_decode_tree_workspace_bytes, not shared
+ * rows are not written; keys on a page outside the pool drop out of the
+ * softmax (PD_DEV_BAD_PAGE). workspace: pd_decode_tree_workspace_bytes, not shared
  * by calls that overlap. head_dim in {64, 128, 256, 512}; block_size 16 or
- * 32; num_q_heads / num_kv_heads <= 16. */
+ * 32; num_q_heads / num_kv_heads <= 16; num_kv_heads <= 4095. */
 int pd_decode_tree(const void* q, int64_t q_stride, const int32_t* cu_q,
                    const uint64_t* tree_mask, const void* k_cache, const void* v_cache,
                    const int32_t* block_tables, const int32_t* seq_lens, void* out,
@@ -545,7 +548,8 @@ int pd_decode_tree(const void* q, int64_t q_stride, const int32_t* cu_q,
  *               that is not so raises PD_DEV_BAD_TREE and moves nothing
  *               (new_seq_lens[b] = p_b).
  *   seq_lens, cu_q, block_tables   as pd_decode_tree; new_seq_lens is another
- *               array. */
+ *               array. A row from or to a page outside the pool stays
+ *               where it is (PD_DEV_BAD_PAGE). */
 int pd_compact_tree(void* k_caches, void* v_caches, int64_t layer_bytes, int32_t num_layers,
                     const int32_t* block_tables, const int32_t* seq_lens, const int32_t* cu_q,
                     const int32_t* accepted, const int32_t* num_accepted, int32_t max_accepted,

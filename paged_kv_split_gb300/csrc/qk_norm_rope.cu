@@ -11,14 +11,16 @@
 // codes that K is quantised to afterwards are reproducible bit for bit.
 //
 // The pass reads each fused row once and writes each q row and cache row once;
-// memory bounds it as long as instructions do not, which is near: so a lane
+// instructions weigh as much as memory in it: so a lane
 // holds two 8-element chunks of a head half a head apart, where a full rotation
 // finds its partners without shuffles; the weights lie in shared memory; and
 // CTAs stay, each with a run of (token, head group) items, the next item's rows
 // on their way while one is computed. Measured: 8192 rows of 32 + 2 x 8 heads of
-// 128 in 41.4 us, 74% of the copy rate, 65% of the issue slots taken (one chunk a
-// lane, partners by shuffle: 77 us; 4 or 8 resident CTAs: 49 and 51); 832 rows
-// into FP8 9.5 us, 8 rows 2.4 us, both a chain of latencies.
+// 128 in 41.7 us, 74% of the copy rate, with 72% of the issue slots and 45% of the
+// DRAM rate taken (writes stay in L2): neither is full, one item ahead is 24 KB an SM
+// in flight (one chunk a lane, partners by shuffle: 77 us; 4 or 8 resident CTAs: 49 and
+// 51). Into FP8 49.4 us, into NVFP4 71.0. 832 rows of 64 + 2 x 8 heads into FP8 10.0
+// us, four or five items a CTA one after another; 8 rows 2.3 us, a chain of latencies.
 #include "pd_common.cuh"
 
 namespace pd {

@@ -286,12 +286,14 @@ cudaError_t launch_tree_join(const TreeArgs& a, const TreeWork& w, int head_dim,
 // On tcgen05 or, where it says so, on mma.sync. The workspace functions return
 // its size and, with w, lay it out.
 // head_dim 512 in up to 32 rows (nodes times q heads of a kv head) runs on mma.sync,
-// 16 rows a pass over the keys; on tcgen05 128 rows take two passes. 8 sequences
-// over 8192 keys, mma.sync against tcgen05 in us, BF16 / FP8 / NVFP4: 32 rows 113 /
-// 120 / 113 against 109 / 123 / 139, 64 rows 213 / 220 / 200 against 112 / 128 / 145.
-// head_dim 256 in up to 8 rows does too: 16 sequences over 4096 keys 52 / 39 / 41
-// against 58 / 59 / 58; 16 rows 97 / 70 / 69 against 60 / 61 / 60. At 128 the two
-// are equal in 8 rows.
+// 16 rows a pass over the keys; on tcgen05 128 rows take two passes. 16 / 2 heads, 8
+// sequences over 8192 keys, mma.sync against tcgen05 in us, BF16 / FP8 / NVFP4: 32
+// rows 112 / 119 / 114 against 109 / 123 / 139, 64 rows 213 / 220 / 200 against 114 /
+// 129 / 141. head_dim 256 in up to 8 rows does too: 8 / 4 heads, 16 sequences over
+// 4096 keys 53 / 41 / 44 against 58 / 59 / 58; 16 rows 97 / 70 / 69 against 59 / 60 /
+// 60. At 128 in 8 rows a batch takes as long on either (93.5 / 91 against 93.5 / 89.5),
+// one short sequence would take 12.3 against 14.2; but the FP8 form of mma.sync tiles
+// at that width gave wrong outputs, from a cause not found, and there is none.
 inline bool tree_on_umma(int max_q_len, int group, int head_dim) {
   return head_dim <= 128 || max_q_len * group > (head_dim == 256 ? 8 : 32);
 }

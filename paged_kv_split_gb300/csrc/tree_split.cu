@@ -4,7 +4,7 @@
 // heads) on N, head_dim split over four consumer warps, as decode_balanced.cu
 // has them (mma_tile.cuh). More rows than that are further node tiles, which
 // run side by side and find the keys in L2. Single tokens of 8 sequences over 8192
-// keys, 8 heads a kv head: 55 us in BF16 (floor 40), 42 in FP8 (20), 44 in NVFP4
+// keys, 16 / 2 heads of 512: 54 us in BF16 (floor 40), 41 in FP8 (20), 44 in NVFP4
 // (11), the quantised forms bound by widening in registers.
 //
 // Keys are dealt by the device plan of tree_plan.cuh in 16-key tiles; a warp

@@ -18,21 +18,24 @@
 //  * The producer warp copies K and V units (128 keys of one head) by TMA into
 //    a ring, in the order in which they are used. FP8 and NVFP4 units land raw
 //    and four more warps widen them to f16 (exact: every E4M3 value and every
-//    E2M1 x E4M3 product is an f16); q is then scaled by a power of two a row.
+//    E2M1 x E4M3 product is an f16); q is then scaled by a power of two a row
+//    (widen_q).
 //  * A row's P is taken against a running reference: the largest of the first
 //    scores it sees. Floating-point P need no exact maximum, so a tile is read
 //    once: the reference moves, and what was computed is rescaled, only where 32
-//    keys' P add up to 2^15. Sums and O are fp32; P is rounded to bf16 (BF16
-//    caches) or f16. The loops over a tile stay rolled: with one or two warps a
-//    scheduler, straight-line code for 128 keys runs at the rate of fetches.
+//    keys' P add up to 2^15. Sums, of the unrounded P, and O are fp32. P is rounded
+//    to bf16 with BF16 caches, since both operands of a product have one type, else to
+//    f16: outputs are 0.0023 of their size from 64 bits with the one (0.0017 with P in
+//    fp32) and 0.0017 with the other. The loops over a tile stay rolled: with one or
+//    two warps a scheduler, straight-line code for 128 keys runs at the rate of fetches.
 //  * V rows that no node sees are zeroed, so stale bytes never meet a weight.
-//  * Measured (GB300): single tokens of 32 sequences over 4096 keys 97 us, 6.5 TB/s
+//  * Measured (GB300): single tokens of 32 sequences over 4096 keys 98 us, 6.5 TB/s
 //    between a start and a join of 12 us together; 32 trees of 4 to 16 nodes 70 us;
 //    2 trees of 64 nodes over 32K keys 85 us (808 TFLOP/s), bound by each group's
-//    chain of scores, softmax and weighted values; 64 trees in FP8 181 us, by the
-//    same chain with the widening in it. Without the softmax these take 94, 65, 73
-//    and 141 us, with an eighth of the products 95, 66, 71 and 165. head_dim 512, 64
-//    nodes of 8 heads over 28000 keys: 179 us (mma.sync 690).
+//    chain of scores, softmax and weighted values; 64 trees in FP8 180 us, in NVFP4
+//    217, by the same chain with the widening in it. Without the softmax the four
+//    took 94, 65, 73 and 141 us (FP8), with an eighth of the products 95, 66, 71 and
+//    165. head_dim 512, 64 nodes of 8 heads over 28000 keys: 184 us (mma.sync 690).
 //  * Every wait is bounded (2 s, that for a piece's first keys by consumer_wait_ns):
 //    on time-out the CTA raises PD_DEV_TIMEOUT, waits for its copies and MMAs in
 //    flight, frees its TMEM and ends.
@@ -253,8 +256,9 @@ __device__ __forceinline__ void widen_unit(uint32_t raw, uint32_t op, int chunk0
 }
 
 // A piece's bf16 q rows to f16 times a power of two, in place, by four warps: a
-// row's largest |q| into [2^14, 2^15) (exact: f16 holds bf16's 8 bits). mul_s[r]
-// becomes row r's score multiplier. Rows from `second` on are the second tile's.
+// row's largest |q| into [2^14, 2^15). f16 holds bf16's 8 bits down to 2^-17, 2^-31 of
+// the largest; smaller elements are off by at most 2^-39 of it. mul_s[r] becomes row r's
+// score multiplier. Rows from `second` on are the second tile's.
 template <int D>
 __device__ __forceinline__ void widen_q(uint32_t tile, int tile_bytes, int rows, int second,
                                         float mul, float* mul_s, int warp, int lane) {
