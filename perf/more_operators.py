@@ -24,7 +24,7 @@ own = False
 
 DEV = "cuda"
 NEG = float("-inf")
-SMALLEST = 2.0 ** -60  # the smallest scale of a page
+SMALLEST, LARGEST = 2.0 ** -60, 2.0 ** 60  # a page's scale
 
 
 # ---------------------------------------------------------------------------
@@ -322,7 +322,7 @@ def _append_cache(cache, x, s, units):
     is_new = new_row[:, :, None, :, None]
     top = torch.where(is_new, vals.abs(), torch.zeros_like(vals)).amax((3, 4))
     full = torch.full((1,), 127.0, device=x.device)
-    want = (top / full).clamp(min=SMALLEST)
+    want = (top / full).clamp(min=SMALLEST, max=LARGEST)
     codes, scales = _codes(cache, c), _scales(cache, c)
     have = scales[page]
     on = new_row.any(-1)[..., None]
@@ -331,7 +331,7 @@ def _append_cache(cache, x, s, units):
     ratio = (have / scale)[..., None, None]
     grown = (scale > have)[..., None, None] & old_row[:, :, None, :, None]
     kept = torch.where(grown, torch.round(old.float() * ratio), old.float())
-    got = torch.round(vals / scale[..., None, None]).clamp(-127, 127)
+    got = torch.round(vals * (torch.ones_like(scale) / scale)[..., None, None]).clamp(-127, 127)
     codes[page] = torch.where(is_new, got, kept).to(torch.int8)
     scales[page] = scale
 
@@ -481,7 +481,7 @@ def _exact_append(s):
             p0 = lens[b] - (cu[b + 1] - cu[b])
             for i in range(p0 // bs, (lens[b] + bs - 1) // bs):
                 lo, hi = max(p0, i * bs), min(lens[b], (i + 1) * bs)
-                t = top[cu[b] + lo - p0:cu[b] + hi - p0].amax(0).clamp(min=SMALLEST)
+                t = top[cu[b] + lo - p0:cu[b] + hi - p0].amax(0).clamp(SMALLEST, LARGEST)
                 at = tables[b][i]
                 scale[at] = t if lo == i * bs else torch.maximum(t, scale[at])
         out[name] = scale
