@@ -43,6 +43,14 @@
  *                   one E4M3 scale per 16", block_stride_bytes,
  *                   data_section_bytes). The order inside each section is
  *                   this library's choice; the pages leave it open.
+ *   PD_KV_INT8      page = data section int8 [num_kv_heads][block_size]
+ *                   [head_dim] followed by one fp32 scale per kv head
+ *                   [num_kv_heads]; value = code * scale. The page stride is
+ *                   rounded up to a multiple of 128 bytes. Codes lie in
+ *                   [-127, 127], scales in [2^-60, 2^60]. Written by
+ *                   pd_rope_append_int8, read by every pd_decode* call; the
+ *                   other calls refuse it (PD_ERR_UNSUPPORTED): a row is only
+ *                   worth something beside its page's scale.
  *   Slot s of the pool is page s / block_size, row s % block_size.
  */
 #ifndef PD_H_
@@ -65,7 +73,7 @@ enum pd_status {
 };
 
 /* KV cache forms. */
-enum pd_kv_dtype { PD_KV_BF16 = 0, PD_KV_FP8_E4M3 = 1, PD_KV_NVFP4 = 2 };
+enum pd_kv_dtype { PD_KV_BF16 = 0, PD_KV_FP8_E4M3 = 1, PD_KV_NVFP4 = 2, PD_KV_INT8 = 3 };
 
 /* Device-side status bits, accumulated by the kernels (see pd_device_status). */
 enum pd_device_flag {
@@ -557,6 +565,77 @@ int pd_compact_tree(void* k_caches, void* v_caches, int64_t layer_bytes, int32_t
                     int32_t head_dim, int32_t block_size, int32_t max_blocks_per_seq,
                     int64_t num_blocks, int32_t kv_dtype, void* stream);
 
+/* ---- Serving from an INT8 cache ----
+ * A cache form with one scale per page and kv head (PD_KV_INT8 above): new
+ * tokens' rows go in with pd_rope_append_int8, every pd_decode* call reads it,
+ * and pd_prefill_packed attends whole prompts over their own rows, unquantised. */
+
+/* Rotate the q and k heads of each sequence's new tokens and append their K and
+ * V to the sequence's INT8 pages.
+ *   qkv         device bf16; row t at element t * qkv_stride (0 = packed):
+ *               num_q_heads q heads, num_kv_heads k heads, num_kv_heads v heads
+ *               of head_dim values.
+ *   cu_q        device int32 [num_seqs + 1]: sequence b's new tokens are rows
+ *               [cu_q[b], cu_q[b+1]), n_b of them, 0 <= n_b <= max_q_len.
+ *   seq_lens    device int32 [num_seqs]: L_b cached rows, the new ones included;
+ *               token i becomes row L_b - n_b + i of the sequence.
+ *   positions   device int32 [total_q], or NULL: the token's row in its sequence.
+ *               One outside [0, max_position) is clamped and flagged
+ *               PD_DEV_BAD_POSITION.
+ *   cos_sin, rot_dim, interleaved   as pd_qk_norm_rope_cache (without norm).
+ *   q_out       device bf16, token t's rotated q heads at t * q_out_stride
+ *               (0 = packed). May be qkv (with its stride): in place.
+ *   k_out       the same for the k heads, or NULL. May be the k heads of qkv
+ *               (qkv + num_q_heads * head_dim, with its stride).
+ * All arithmetic in fp32, each operation rounded once: the two products of a
+ * rotated element and their sum (q_out and k_out round that to bf16; the cache
+ * takes it as it is). For each page that gets rows, each kv head, and K and V
+ * apart: want = clamp(amax / 127, 2^-60, 2^60), amax the largest finite |x| of
+ * the rows the page gets. A page whose row 0 is among them takes want as its
+ * scale. Another keeps its scale unless want is larger: then it takes want, and
+ * the codes of its earlier rows become rint(code * (old scale / want)). New
+ * codes are rint(x * (1 / scale)) clamped to +-127 (NaN: 0). rint rounds to
+ * nearest even. So codes are reproducible bit for bit, and a value appended
+ * with scale s is off by s / 2 at most, plus half of each scale its page grows
+ * to later. Rows of the page behind the new ones keep their bytes.
+ * A page that gets rows belongs to one sequence (shared prefixes: whole pages).
+ * A sequence whose counts do not fit (n_b > max_q_len, L_b < n_b, L_b beyond
+ * the block table, rows beyond total_q) raises PD_DEV_BAD_SEQ_LEN and nothing of
+ * it is written; rows of a page outside the pool are not appended
+ * (PD_DEV_BAD_PAGE), their q_out and k_out are written. head_dim in {64, 128,
+ * 256, 512}; block_size in {16, 32}; rot_dim a multiple of 16 in [16,
+ * head_dim]; strides multiples of 8. */
+int pd_rope_append_int8(const void* qkv, int64_t qkv_stride, const int32_t* cu_q,
+                        const int32_t* seq_lens, const int32_t* positions, const float* cos_sin,
+                        int32_t max_position, int32_t rot_dim, int32_t interleaved, void* q_out,
+                        int64_t q_out_stride, void* k_out, int64_t k_out_stride, void* k_cache,
+                        void* v_cache, const int32_t* block_tables, int32_t num_seqs,
+                        int32_t total_q, int32_t max_q_len, int32_t num_q_heads,
+                        int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                        int32_t max_blocks_per_seq, int64_t num_blocks, void* stream);
+
+/* Attention of whole prompts over their own rows, packed one behind the other:
+ * no cache and no block table.
+ *   q, k, v     device bf16; row t (t < total_q) holds num_q_heads (num_kv_heads
+ *               for k and v) x head_dim values at element t * q_stride /
+ *               k_stride / v_stride (0 = packed): parts of fused rows, say.
+ *   cu_q        device int32 [num_seqs + 1]: sequence b owns rows [cu_q[b],
+ *               cu_q[b+1]), its n_b tokens, n_b <= max_q_len.
+ *   out         device bf16, total_q rows at t * out_stride (0 = packed).
+ *   causal      != 0: token i sees tokens j <= i of its sequence; 0: all n_b.
+ *   sliding_window  W > 0: token i sees j with i - j < W (causal; without: the
+ *               last W tokens, as pd_prefill); 0 = off.
+ * out = softmax(scale q k) v with scores, exponentials and sums in fp32 and the
+ * weights rounded to bf16 for their product with v. A sequence whose counts do
+ * not fit (n_b > max_q_len, rows beyond total_q) raises PD_DEV_BAD_SEQ_LEN and
+ * its rows are not written; nor are rows of no sequence. head_dim in {64, 128,
+ * 256}; num_q_heads / num_kv_heads <= 16; strides multiples of 8. */
+int pd_prefill_packed(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                      const void* v, int64_t v_stride, const int32_t* cu_q, void* out,
+                      int64_t out_stride, int32_t num_seqs, int32_t total_q, int32_t max_q_len,
+                      int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, float scale,
+                      int32_t causal, int32_t sliding_window, void* stream);
+
 /* ---- Cross-check kernels ----
  * Independent second implementations of two steps, kept to test the fast
  * kernels against: same arguments, same results up to fp32 summation order.
@@ -597,6 +676,14 @@ int pd_decode_tree_crosscheck(const void* q, int64_t q_stride, const int32_t* cu
                               int64_t num_blocks, float scale, int32_t sliding_window,
                               int32_t num_sinks, int32_t kv_dtype, float k_scale, float v_scale,
                               void* workspace, size_t workspace_bytes, void* stream);
+
+/* pd_prefill_packed on CUDA cores, one warp per (token, q head). */
+int pd_prefill_packed_crosscheck(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                 const void* v, int64_t v_stride, const int32_t* cu_q, void* out,
+                                 int64_t out_stride, int32_t num_seqs, int32_t total_q,
+                                 int32_t max_q_len, int32_t num_q_heads, int32_t num_kv_heads,
+                                 int32_t head_dim, float scale, int32_t causal,
+                                 int32_t sliding_window, void* stream);
 
 /* ---- Test hooks ----
  * For the library's own tests; a serving process has no reason to call them. */

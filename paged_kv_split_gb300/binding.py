@@ -44,8 +44,8 @@ def _load_marshal():
 _marshal = _load_marshal()
 
 PD_OK = 0
-PD_KV_BF16, PD_KV_FP8_E4M3, PD_KV_NVFP4 = 0, 1, 2
-KV_DTYPES = {"bf16": PD_KV_BF16, "fp8": PD_KV_FP8_E4M3, "nvfp4": PD_KV_NVFP4}
+PD_KV_BF16, PD_KV_FP8_E4M3, PD_KV_NVFP4, PD_KV_INT8 = 0, 1, 2, 3
+KV_DTYPES = {"bf16": PD_KV_BF16, "fp8": PD_KV_FP8_E4M3, "nvfp4": PD_KV_NVFP4, "int8": PD_KV_INT8}
 
 _P = ctypes.c_void_p
 _i32, _i64, _f32, _sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
@@ -124,6 +124,15 @@ _lib.pd_decode_tree_crosscheck.restype = ctypes.c_int
 _lib.pd_compact_tree.argtypes = [_P, _P, _i64, _i32, _P, _P, _P, _P, _P, _i32, _P, _i32, _i32, _i32,
                                  _i32, _i32, _i64, _i32, _P]
 _lib.pd_compact_tree.restype = ctypes.c_int
+_lib.pd_rope_append_int8.argtypes = [_P, _i64, _P, _P, _P, _P, _i32, _i32, _i32, _P, _i64, _P, _i64,
+                                     _P, _P, _P, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
+                                     _i64, _P]
+_lib.pd_rope_append_int8.restype = ctypes.c_int
+_lib.pd_prefill_packed.argtypes = [_P, _i64, _P, _i64, _P, _i64, _P, _P, _i64, _i32, _i32, _i32,
+                                   _i32, _i32, _i32, _f32, _i32, _i32, _P]
+_lib.pd_prefill_packed.restype = ctypes.c_int
+_lib.pd_prefill_packed_crosscheck.argtypes = _lib.pd_prefill_packed.argtypes
+_lib.pd_prefill_packed_crosscheck.restype = ctypes.c_int
 for _fn in ("pd_decode_balanced_partial", "pd_decode_balanced_combine"):
     getattr(_lib, _fn).argtypes = _lib.pd_decode_balanced.argtypes
     getattr(_lib, _fn).restype = ctypes.c_int
@@ -919,3 +928,125 @@ def pd_compact_tree(k_caches, v_caches, block_tables, seq_lens, cu_q, accepted, 
         block_size, mbs, num_blocks, _dtype_code(kv_dtype), _stream(stream))
     _check("pd_compact_tree", rc)
     return new_seq_lens
+
+
+# ---- serving from an INT8 cache ----------------------------------------------
+def _heads_rows(t, name, index):
+    """(address, row stride) of a CUDA bf16 [rows, heads, head_dim] tensor whose heads lie side
+    by side: contiguous, or a part of wider rows."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be bf16 [rows, heads, head_dim]")
+    if t.get_device() != index or index < 0:
+        raise ValueError(f"{name} must be a CUDA tensor on the call's device")
+    if t.dtype is not torch.bfloat16:
+        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    rows, heads, d = t.shape
+    s0, s1, s2 = t.stride()
+    if (d > 1 and s2 != 1) or (heads > 1 and s1 != d):
+        raise ValueError(f"{name}'s heads must lie side by side in each row")
+    if rows > 1 and s0 < heads * d:
+        raise ValueError(f"{name}'s rows overlap")
+    return t.data_ptr(), (s0 if rows > 1 else 0)
+
+
+def _rope_append(qkv, q_ptr, q_stride, k_ptr, k_stride, hq, d, k_cache, v_cache, block_tables,
+                 seq_lens, cu_q, cos_sin, max_q_len, num_kv_heads, block_size, num_blocks, positions,
+                 interleaved, stream):
+    T, row = qkv.shape
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq]")
+    B, mbs = block_tables.shape
+    if seq_lens.shape != (B,) or cu_q.shape != (B + 1,):
+        raise ValueError("seq_lens must be [num_seqs] and cu_q [num_seqs + 1]")
+    if cos_sin.dim() != 2:
+        raise ValueError("cos_sin must be float32 [max_position, rot_dim]")
+    if positions is not None and positions.shape != (T,):
+        raise ValueError("positions must be [num_tokens]")
+    dev = qkv.get_device()
+    if min(k_cache.numel() * k_cache.element_size(), v_cache.numel() * v_cache.element_size()) < \
+            pd_cache_bytes(PD_KV_INT8, num_blocks, block_size, num_kv_heads, d):
+        raise ValueError("k_cache and v_cache must hold pd_cache_bytes bytes each")
+    rc = _lib.pd_rope_append_int8(
+        _ptr(qkv, "qkv", torch.bfloat16, dev), row, _ptr(cu_q, "cu_q", torch.int32, dev),
+        _ptr(seq_lens, "seq_lens", torch.int32, dev),
+        None if positions is None else _ptr(positions, "positions", torch.int32, dev),
+        _ptr(cos_sin, "cos_sin", torch.float32, dev), cos_sin.shape[0], cos_sin.shape[1],
+        int(bool(interleaved)), q_ptr, q_stride, k_ptr, k_stride,
+        _cache_ptr(k_cache, "k_cache", dev), _cache_ptr(v_cache, "v_cache", dev),
+        _ptr(block_tables, "block_tables", torch.int32, dev), B, T, max_q_len, hq, num_kv_heads, d,
+        block_size, mbs, num_blocks, _stream(stream))
+    _check("pd_rope_append_int8", rc)
+
+
+def pd_rope_append_int8(qkv, q_out, k_cache, v_cache, block_tables, seq_lens, cu_q, cos_sin, *,
+                        max_q_len, num_kv_heads, block_size, num_blocks, positions=None, k_out=None,
+                        interleaved=False, stream=None):
+    """Rotate the new tokens' q and k heads and append K and V to INT8 pages.
+
+    qkv: contiguous bf16 [T, row], a row = q heads, k heads, v heads (and possibly
+    more), sequence b's new tokens rows cu_q[b] .. cu_q[b + 1] - 1. q_out: bf16
+    [T, Hq, D], k_out: bf16 [T, Hkv, D] or None, each contiguous or a part of
+    wider rows. seq_lens: int32 [B] cached rows, the new ones included; max_q_len:
+    host int, the most new tokens of a sequence. positions: int32 [T], or None for
+    the rows in the cache. cos_sin: float32 [max_position, rot_dim]."""
+    if q_out.dim() != 3 or qkv.dim() != 2 or q_out.shape[0] != qkv.shape[0]:
+        raise ValueError("qkv must be bf16 [num_tokens, row], q_out [num_tokens, num_q_heads, "
+                         "head_dim]")
+    T, hq, d = q_out.shape
+    if qkv.shape[1] < (hq + 2 * num_kv_heads) * d:
+        raise ValueError("a qkv row is shorter than its q, k and v heads")
+    dev = qkv.get_device()
+    q_ptr, q_stride = _heads_rows(q_out, "q_out", dev)
+    k_ptr, k_stride = None, 0
+    if k_out is not None:
+        if k_out.shape != (T, num_kv_heads, d):
+            raise ValueError("k_out must be [num_tokens, num_kv_heads, head_dim]")
+        k_ptr, k_stride = _heads_rows(k_out, "k_out", dev)
+    _rope_append(qkv, q_ptr, q_stride, k_ptr, k_stride, hq, d, k_cache, v_cache, block_tables,
+                 seq_lens, cu_q, cos_sin, max_q_len, num_kv_heads, block_size, num_blocks, positions,
+                 interleaved, stream)
+    return q_out
+
+
+def pd_rope_append_int8_(qkv, k_cache, v_cache, block_tables, seq_lens, cu_q, cos_sin, *, max_q_len,
+                         num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
+                         positions=None, interleaved=False, stream=None):
+    """pd_rope_append_int8 in place: the q and k heads of the fused rows are
+    replaced by their rotated form, ready for pd_prefill_packed."""
+    if qkv.dim() != 2 or qkv.shape[1] < (num_q_heads + 2 * num_kv_heads) * head_dim:
+        raise ValueError("qkv must be bf16 [num_tokens, row], a row its q, k and v heads")
+    row = qkv.shape[1]
+    at = _ptr(qkv, "qkv", torch.bfloat16, qkv.get_device())
+    _rope_append(qkv, at, row, at + 2 * num_q_heads * head_dim, row, num_q_heads, head_dim, k_cache,
+                 v_cache, block_tables, seq_lens, cu_q, cos_sin, max_q_len, num_kv_heads, block_size,
+                 num_blocks, positions, interleaved, stream)
+    return qkv
+
+
+def pd_prefill_packed(q, k, v, cu_q, out, *, max_q_len, scale, causal=True, sliding_window=0,
+                      stream=None, crosscheck=False):
+    """Attention of whole prompts over their own rows, packed one behind the other.
+
+    q, out: bf16 [total_q, Hq, D]; k, v: bf16 [total_q, Hkv, D]; each contiguous or
+    a part of wider rows (views of fused QKV rows). cu_q: int32 [B + 1] row
+    offsets; max_q_len: host int, the longest prompt.
+    crosscheck: call pd_prefill_packed_crosscheck (CUDA cores)."""
+    if q.dim() != 3 or k.dim() != 3 or out.shape != q.shape or v.shape != k.shape:
+        raise ValueError("q and out must be bf16 [total_q, num_q_heads, head_dim], k and v "
+                         "[total_q, num_kv_heads, head_dim]")
+    T, hq, d = q.shape
+    if k.shape[0] != T or k.shape[2] != d:
+        raise ValueError("q and k have different rows or head sizes")
+    if cu_q.dim() != 1 or cu_q.shape[0] < 1:
+        raise ValueError("cu_q must be int32 [num_seqs + 1]")
+    dev = q.get_device()
+    qp, qs = _heads_rows(q, "q", dev)
+    kp, ks = _heads_rows(k, "k", dev)
+    vp, vs = _heads_rows(v, "v", dev)
+    op, os_ = _heads_rows(out, "out", dev)
+    fn = _lib.pd_prefill_packed_crosscheck if crosscheck else _lib.pd_prefill_packed
+    rc = fn(qp, qs, kp, ks, vp, vs, _ptr(cu_q, "cu_q", torch.int32, dev), op, os_,
+            cu_q.shape[0] - 1, T, max_q_len, hq, k.shape[1], d, scale, int(bool(causal)),
+            int(sliding_window), _stream(stream))
+    _check(fn.__name__, rc)
+    return out

@@ -33,6 +33,10 @@ __device__ __forceinline__ float load_kv(const uint8_t* __restrict__ cache, int6
   } else if (FMT == PD_KV_FP8_E4M3) {
     const uint8_t* p = base + (static_cast<int64_t>(row) * a.num_kv_heads + head) * D + d;
     return e4m3_decode(*p) * sc;
+  } else if (FMT == PD_KV_INT8) {
+    const int64_t line = static_cast<int64_t>(head) * a.block_size + row;
+    const float s = reinterpret_cast<const float*>(base + a.data_bytes)[head];
+    return static_cast<float>(reinterpret_cast<const int8_t*>(base)[line * D + d]) * s;
   } else {
     const int64_t line = static_cast<int64_t>(head) * a.block_size + row;
     const uint8_t byte = base[line * (D / 2) + d / 2];
@@ -365,6 +369,7 @@ cudaError_t launch_decode_partial(const DecodeArgs& a, int head_dim, int kv_dtyp
   switch (kv_dtype) {
     case PD_KV_BF16: return launch_simple_fmt<PD_KV_BF16>(a, head_dim, st);
     case PD_KV_FP8_E4M3: return launch_simple_fmt<PD_KV_FP8_E4M3>(a, head_dim, st);
+    case PD_KV_INT8: return launch_simple_fmt<PD_KV_INT8>(a, head_dim, st);
     default: return launch_simple_fmt<PD_KV_NVFP4>(a, head_dim, st);
   }
 }

@@ -11,7 +11,7 @@
 #include <mutex>
 #include <vector>
 
-#include "pd_common.cuh"
+#include "serve_common.cuh"
 #include "tree_plan.cuh"
 
 namespace pd {
@@ -56,7 +56,9 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 bool dev_ptr_ok(const void* p) { return p != nullptr && aligned16(p); }
 bool head_dim_ok(int d) { return d == 64 || d == 128 || d == 256 || d == 512; }
 bool block_size_ok(int bs) { return bs == 16 || bs == 32; }
-bool dtype_ok(int t) { return t == PD_KV_BF16 || t == PD_KV_FP8_E4M3 || t == PD_KV_NVFP4; }
+// forms whose rows carry all that their values need
+bool row_dtype_ok(int t) { return t == PD_KV_BF16 || t == PD_KV_FP8_E4M3 || t == PD_KV_NVFP4; }
+bool dtype_ok(int t) { return row_dtype_ok(t) || t == PD_KV_INT8; }
 bool scale_ok(float s) { return isfinite(s) && s > 0.0f; }
 
 struct DecodeShape {
@@ -112,8 +114,9 @@ DecodeArgs make_decode_args(const DecodeShape& s, const void* q, const void* kc,
   a.out_stride = static_cast<int64_t>(s.Hq) * s.D;
   a.direct = 0;
   a.num_blocks = s.nb;
-  a.page_bytes = page_bytes_of(s.kv_dtype, s.bs, s.Hkv, s.D);
-  a.data_bytes = nvfp4_data_bytes(s.bs, s.Hkv, s.D);
+  a.page_bytes = any_page_bytes(s.kv_dtype, s.bs, s.Hkv, s.D);
+  a.data_bytes = s.kv_dtype == PD_KV_INT8 ? int8_data_bytes(s.bs, s.Hkv, s.D)
+                                          : nvfp4_data_bytes(s.bs, s.Hkv, s.D);
   a.num_seqs = s.B;
   a.num_q_heads = s.Hq;
   a.num_kv_heads = s.Hkv;
@@ -157,9 +160,25 @@ CombineArgs make_combine_args(int B, int Hq, int D, int bs, int mbs, int S, int 
   return c;
 }
 
+// Resident CTAs per SM and launches of the partial kernels, by cache form.
+int split_ctas_per_sm(int kv_dtype, int D) {
+  return kv_dtype == PD_KV_INT8 ? int8_ctas_per_sm(D, 8) : mma_ctas_per_sm_estimate(kv_dtype, D);
+}
+int plan_ctas_per_sm(int kv_dtype, int D, int G) {
+  return kv_dtype == PD_KV_INT8 ? int8_ctas_per_sm(D, G) : balanced_ctas_per_sm(kv_dtype, D, G);
+}
+cudaError_t launch_split_partial(const DecodeArgs& a, int D, int kv_dtype, cudaStream_t st) {
+  return kv_dtype == PD_KV_INT8 ? launch_decode_int8(a, D, st)
+                                : launch_decode_partial_mma(a, D, kv_dtype, st);
+}
+cudaError_t launch_plan_partial(const DecodeArgs& a, int D, int kv_dtype, cudaStream_t st) {
+  return kv_dtype == PD_KV_INT8 ? launch_decode_int8(a, D, st)
+                                : launch_decode_partial_balanced(a, D, kv_dtype, st);
+}
+
 // Bytes of K + V one (page, kv head) holds.
 double page_head_bytes(int bs, int D, int kv_dtype) {
-  const double elem = kv_dtype == PD_KV_BF16 ? 2.0 : (kv_dtype == PD_KV_FP8_E4M3 ? 1.0 : 0.5625);
+  const double elem = kv_dtype == PD_KV_BF16 ? 2.0 : (kv_dtype == PD_KV_NVFP4 ? 0.5625 : 1.0);
   return static_cast<double>(bs) * 2.0 * D * elem;
 }
 
@@ -297,7 +316,7 @@ int build_balanced_plan(const int32_t* lens, int B, int Hq, int Hkv, int D, int 
     P[b] = num_key_pages(L[b], W, bs);
     T += static_cast<int64_t>(P[b]) * Hkv;
   }
-  int64_t NC = static_cast<int64_t>(num_sms) * balanced_ctas_per_sm(kv_dtype, D, G);
+  int64_t NC = static_cast<int64_t>(num_sms) * plan_ctas_per_sm(kv_dtype, D, G);
   if (NC > kMaxBalancedCtas) NC = kMaxBalancedCtas;
   if (NC > T) NC = T;
   const int64_t segs = static_cast<int64_t>(B) * Hkv;
@@ -384,7 +403,7 @@ int prefer_balanced(const int32_t* lens, int B, int Hq, int Hkv, int mbs, int bs
                     int kv_dtype, int num_sms) {
   double split_t = 0.0;
   plan_splits_lengths(lens, B, Hkv, Hq, mbs, bs, W, D, kv_dtype, num_sms,
-                      mma_ctas_per_sm_estimate(kv_dtype, D), &split_t);
+                      split_ctas_per_sm(kv_dtype, D), &split_t);
   const int cap = mbs * bs;
   int64_t T = 0;
   for (int b = 0; b < B; ++b) {
@@ -392,7 +411,7 @@ int prefer_balanced(const int32_t* lens, int B, int Hq, int Hkv, int mbs, int bs
     T += static_cast<int64_t>(num_key_pages(L, W, bs)) * Hkv;
   }
   if (T == 0) return 0;
-  int64_t NC = static_cast<int64_t>(num_sms) * balanced_ctas_per_sm(kv_dtype, D, Hq / Hkv);
+  int64_t NC = static_cast<int64_t>(num_sms) * plan_ctas_per_sm(kv_dtype, D, Hq / Hkv);
   if (NC > kMaxBalancedCtas) NC = kMaxBalancedCtas;
   if (NC > T) NC = T;
   const double pieces_per_cta = static_cast<double>(static_cast<int64_t>(B) * Hkv + NC) / NC;
@@ -436,7 +455,7 @@ int decode_checks(const void* q, const void* k_cache, const void* v_cache,
     DeviceInfo* dev = nullptr;
     if (current_device(&dev) != cudaSuccess) return PD_ERR_CUDA;
     S = plan_splits(num_seqs, num_kv_heads, max_blocks_per_seq, block_size, sliding_window,
-                    dev->num_sms, mma_ctas_per_sm_estimate(kv_dtype, head_dim));
+                    dev->num_sms, split_ctas_per_sm(kv_dtype, head_dim));
   }
   *num_splits_out = S;
   return PD_OK;
@@ -463,7 +482,7 @@ size_t pd_page_bytes(int32_t kv_dtype, int32_t block_size, int32_t num_kv_heads,
                      int32_t head_dim) {
   if (!dtype_ok(kv_dtype) || block_size <= 0 || num_kv_heads <= 0 || head_dim <= 0) return 0;
   if (kv_dtype == PD_KV_NVFP4 && head_dim % 16 != 0) return 0;
-  return static_cast<size_t>(page_bytes_of(kv_dtype, block_size, num_kv_heads, head_dim));
+  return static_cast<size_t>(any_page_bytes(kv_dtype, block_size, num_kv_heads, head_dim));
 }
 
 size_t pd_cache_bytes(int32_t kv_dtype, int64_t num_blocks, int32_t block_size,
@@ -486,7 +505,7 @@ int pd_plan_num_splits(int32_t num_seqs, int32_t num_kv_heads, int32_t max_block
       sliding_window < 0 || num_sms <= 0 || !head_dim_ok(head_dim) || !dtype_ok(kv_dtype))
     return -PD_ERR_INVALID_ARG;
   return plan_splits(num_seqs, num_kv_heads, max_blocks_per_seq, block_size, sliding_window,
-                     num_sms, mma_ctas_per_sm_estimate(kv_dtype, head_dim));
+                     num_sms, split_ctas_per_sm(kv_dtype, head_dim));
 }
 
 int pd_plan_num_splits_for_lengths(const int32_t* seq_lens, int32_t num_seqs,
@@ -502,7 +521,7 @@ int pd_plan_num_splits_for_lengths(const int32_t* seq_lens, int32_t num_seqs,
   if (num_seqs == 0) return 1;
   return plan_splits_lengths(seq_lens, num_seqs, num_kv_heads, num_q_heads, max_blocks_per_seq,
                              block_size, sliding_window, head_dim, kv_dtype, num_sms,
-                             mma_ctas_per_sm_estimate(kv_dtype, head_dim));
+                             split_ctas_per_sm(kv_dtype, head_dim));
 }
 
 int pd_choose_num_splits(int32_t num_seqs, int32_t num_kv_heads, int32_t max_blocks_per_seq,
@@ -520,7 +539,7 @@ int pd_reshape_and_cache(const void* key, const void* value, void* k_cache, void
                          int32_t head_dim, int32_t block_size, int64_t num_blocks,
                          int32_t kv_dtype, float k_scale, float v_scale, void* stream) {
   if (num_tokens < 0 || num_kv_heads <= 0 || num_blocks <= 0) return PD_ERR_INVALID_ARG;
-  if (!head_dim_ok(head_dim) || !block_size_ok(block_size) || !dtype_ok(kv_dtype))
+  if (!head_dim_ok(head_dim) || !block_size_ok(block_size) || !row_dtype_ok(kv_dtype))
     return PD_ERR_UNSUPPORTED;
   if (kv_dtype == PD_KV_FP8_E4M3 && !(scale_ok(k_scale) && scale_ok(v_scale)))
     return PD_ERR_INVALID_ARG;
@@ -572,7 +591,7 @@ int partial_impl(const void* q, const void* k_cache, const void* v_cache,
   if (q_stride) a.q_stride = q_stride;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   return cuda_status(cuda_core ? launch_decode_partial(a, head_dim, kv_dtype, st)
-                               : launch_decode_partial_mma(a, head_dim, kv_dtype, st));
+                               : launch_split_partial(a, head_dim, kv_dtype, st));
 }
 }  // namespace
 
@@ -651,7 +670,7 @@ int decode_split(const void* q, const void* k_cache, const void* v_cache,
     c.out8 = static_cast<uint8_t*>(out);
     c.out_scale = e4m3_out_scale;
     const cudaError_t e = cuda_core ? launch_decode_partial(a, head_dim, kv_dtype, st)
-                                    : launch_decode_partial_mma(a, head_dim, kv_dtype, st);
+                                    : launch_split_partial(a, head_dim, kv_dtype, st);
     if (e != cudaSuccess) return PD_ERR_CUDA;
     return cuda_status(launch_decode_combine(c, head_dim, S, st));
   }
@@ -664,7 +683,7 @@ int decode_split(const void* q, const void* k_cache, const void* v_cache,
   // (and zero rows for empty ones); the combine merges the rest
   a.out = static_cast<uint16_t*>(out);
   a.direct = 1;
-  if (launch_decode_partial_mma(a, head_dim, kv_dtype, st) != cudaSuccess) return PD_ERR_CUDA;
+  if (launch_split_partial(a, head_dim, kv_dtype, st) != cudaSuccess) return PD_ERR_CUDA;
   c.skip_direct = 1;
   return cuda_status(launch_decode_combine(c, head_dim, S, st));
 }
@@ -792,7 +811,7 @@ int decode_balanced(const void* q, const void* k_cache, const void* v_cache,
   if (q_stride) a.q_stride = q_stride;
   if (out_stride) a.out_stride = out_stride;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (partial && launch_decode_partial_balanced(a, head_dim, kv_dtype, st) != cudaSuccess)
+  if (partial && launch_plan_partial(a, head_dim, kv_dtype, st) != cudaSuccess)
     return PD_ERR_CUDA;
   if (!combine) return PD_OK;
   CombineArgs c = make_combine_args(num_seqs, num_q_heads, head_dim, block_size,
@@ -887,7 +906,7 @@ int prefill_impl(const void* q, int64_t q_stride, const int32_t* cu_q, const voi
     return PD_ERR_INVALID_ARG;
   const int G = num_q_heads / num_kv_heads;
   if (G > kMaxGroup || num_kv_heads > 65535) return PD_ERR_UNSUPPORTED;
-  if (!dtype_ok(kv_dtype) || !head_dim_ok(head_dim) || !block_size_ok(block_size))
+  if (!row_dtype_ok(kv_dtype) || !head_dim_ok(head_dim) || !block_size_ok(block_size))
     return PD_ERR_UNSUPPORTED;
   if (head_dim > 256) return PD_ERR_UNSUPPORTED;
   if (kv_dtype == PD_KV_FP8_E4M3 && !(scale_ok(k_scale) && scale_ok(v_scale)))
@@ -1020,7 +1039,7 @@ int pd_qk_norm_rope_cache(const void* qkv, int64_t qkv_stride, const void* q_wei
                           void* stream) {
   if (num_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0) return PD_ERR_INVALID_ARG;
   if (num_q_heads > 65535 || num_kv_heads > 65535) return PD_ERR_UNSUPPORTED;
-  if (!head_dim_ok(head_dim) || !block_size_ok(block_size) || !dtype_ok(kv_dtype))
+  if (!head_dim_ok(head_dim) || !block_size_ok(block_size) || !row_dtype_ok(kv_dtype))
     return PD_ERR_UNSUPPORTED;
   if (rot_dim < 16 || rot_dim > head_dim || rot_dim % 16 != 0) return PD_ERR_UNSUPPORTED;
   if (num_blocks <= 0 || num_blocks * block_size > INT32_MAX || max_position <= 0)
@@ -1077,7 +1096,7 @@ size_t pd_decode_tree_workspace_bytes(int32_t max_q_len, int32_t num_q_heads,
                                       int32_t num_sms) {
   if (max_q_len < 0 || max_q_len > kMaxTreeNodes || num_sms < 1) return 0;
   if (num_kv_heads <= 0 || num_q_heads <= 0 || num_q_heads % num_kv_heads != 0 ||
-      num_q_heads / num_kv_heads > kMaxGroup || !head_dim_ok(head_dim) || !dtype_ok(kv_dtype))
+      num_q_heads / num_kv_heads > kMaxGroup || !head_dim_ok(head_dim) || !row_dtype_ok(kv_dtype))
     return 0;
   if (!tree_on_umma(max_q_len, num_q_heads / num_kv_heads, head_dim))
     return tree_split_workspace(max_q_len, num_q_heads / num_kv_heads, head_dim, kv_dtype, num_sms,
@@ -1102,7 +1121,7 @@ int decode_tree_impl(const void* q, int64_t q_stride, const int32_t* cu_q,
                        max_blocks_per_seq, 1, sliding_window, kv_dtype, num_blocks};
   const int rc = check_decode_shape(sh, k_scale, v_scale);
   if (rc != PD_OK) return rc;
-  if (num_kv_heads > 65535 / kMaxGroup) return PD_ERR_UNSUPPORTED;
+  if (num_kv_heads > 65535 / kMaxGroup || !row_dtype_ok(kv_dtype)) return PD_ERR_UNSUPPORTED;
   if (total_q < 0 || max_q_len < 0 || num_sinks < 0 || !isfinite(scale)) return PD_ERR_INVALID_ARG;
   if (max_q_len > kMaxTreeNodes) return PD_ERR_UNSUPPORTED;
   if (!q_stride_ok(q_stride, num_q_heads, head_dim) ||
@@ -1205,7 +1224,7 @@ int pd_compact_tree(void* k_caches, void* v_caches, int64_t layer_bytes, int32_t
     return PD_ERR_INVALID_ARG;
   if (num_kv_heads <= 0 || max_blocks_per_seq <= 0 || num_blocks <= 0 || max_accepted < 0)
     return PD_ERR_INVALID_ARG;
-  if (!head_dim_ok(head_dim) || !block_size_ok(block_size) || !dtype_ok(kv_dtype) ||
+  if (!head_dim_ok(head_dim) || !block_size_ok(block_size) || !row_dtype_ok(kv_dtype) ||
       max_accepted > kMaxTreeNodes)
     return PD_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(max_blocks_per_seq) * block_size > (int64_t{1} << 30) ||
@@ -1246,6 +1265,147 @@ int pd_compact_tree(void* k_caches, void* v_caches, int64_t layer_bytes, int32_t
   a.kv_dtype = kv_dtype;
   return cuda_status(launch_compact_tree(a, static_cast<cudaStream_t>(stream)));
 }
+
+int pd_rope_append_int8(const void* qkv, int64_t qkv_stride, const int32_t* cu_q,
+                        const int32_t* seq_lens, const int32_t* positions, const float* cos_sin,
+                        int32_t max_position, int32_t rot_dim, int32_t interleaved, void* q_out,
+                        int64_t q_out_stride, void* k_out, int64_t k_out_stride, void* k_cache,
+                        void* v_cache, const int32_t* block_tables, int32_t num_seqs,
+                        int32_t total_q, int32_t max_q_len, int32_t num_q_heads,
+                        int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                        int32_t max_blocks_per_seq, int64_t num_blocks, void* stream) {
+  if (num_seqs < 0 || num_seqs > 65535 || total_q < 0 || max_q_len < 0 || num_q_heads <= 0 ||
+      num_kv_heads <= 0)
+    return PD_ERR_INVALID_ARG;
+  if (num_q_heads > 32767 || num_kv_heads > 4095) return PD_ERR_UNSUPPORTED;
+  if (!head_dim_ok(head_dim) || !block_size_ok(block_size)) return PD_ERR_UNSUPPORTED;
+  if (rot_dim < 16 || rot_dim > head_dim || rot_dim % 16 != 0) return PD_ERR_UNSUPPORTED;
+  if (num_blocks <= 0 || num_blocks * block_size > INT32_MAX || max_position <= 0 ||
+      max_blocks_per_seq <= 0 ||
+      static_cast<int64_t>(max_blocks_per_seq) * block_size > (int64_t{1} << 30))
+    return PD_ERR_INVALID_ARG;
+  if (!q_stride_ok(qkv_stride, num_q_heads + 2 * num_kv_heads, head_dim) ||
+      !q_stride_ok(q_out_stride, num_q_heads, head_dim) ||
+      !q_stride_ok(k_out_stride, num_kv_heads, head_dim))
+    return PD_ERR_INVALID_ARG;
+  if (num_seqs == 0 || total_q == 0 || max_q_len == 0) return PD_OK;
+  if (!dev_ptr_ok(qkv) || !dev_ptr_ok(cu_q) || !dev_ptr_ok(seq_lens) || !aligned16(positions) ||
+      !dev_ptr_ok(cos_sin) || !dev_ptr_ok(q_out) || !aligned16(k_out) || !dev_ptr_ok(k_cache) ||
+      !dev_ptr_ok(v_cache) || !dev_ptr_ok(block_tables))
+    return PD_ERR_INVALID_ARG;
+  DeviceInfo* dev = nullptr;
+  if (current_device(&dev) != cudaSuccess) return PD_ERR_CUDA;
+  AppendArgs a;
+  a.qkv = static_cast<const uint16_t*>(qkv);
+  a.qkv_stride =
+      qkv_stride ? qkv_stride : static_cast<int64_t>(num_q_heads + 2 * num_kv_heads) * head_dim;
+  a.cu_q = cu_q;
+  a.seq_lens = seq_lens;
+  a.positions = positions;
+  a.cos_sin = cos_sin;
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.q_out_stride = q_out_stride ? q_out_stride : static_cast<int64_t>(num_q_heads) * head_dim;
+  a.k_out = static_cast<uint16_t*>(k_out);
+  a.k_out_stride = k_out_stride ? k_out_stride : static_cast<int64_t>(num_kv_heads) * head_dim;
+  a.k_cache = static_cast<uint8_t*>(k_cache);
+  a.v_cache = static_cast<uint8_t*>(v_cache);
+  a.block_tables = block_tables;
+  a.flags = dev->flags;
+  a.num_blocks = num_blocks;
+  a.page_bytes = any_page_bytes(PD_KV_INT8, block_size, num_kv_heads, head_dim);
+  a.data_bytes = int8_data_bytes(block_size, num_kv_heads, head_dim);
+  a.num_seqs = num_seqs;
+  a.total_q = total_q;
+  // no sequence has more tokens than there are rows
+  a.max_q_len = max_q_len < total_q ? max_q_len : total_q;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.block_size = block_size;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.max_position = max_position;
+  a.rot_dim = rot_dim;
+  a.interleaved = interleaved != 0;
+  a.heads_per_cta = 0;
+  return cuda_status(launch_rope_append_int8(a, head_dim, dev->num_sms,
+                                             static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+int prefill_packed(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                   int64_t v_stride, const int32_t* cu_q, void* out, int64_t out_stride,
+                   int32_t num_seqs, int32_t total_q, int32_t max_q_len, int32_t num_q_heads,
+                   int32_t num_kv_heads, int32_t head_dim, float scale, int32_t causal,
+                   int32_t sliding_window, void* stream, bool simple) {
+  if (num_seqs < 0 || num_seqs > 65535 || total_q < 0 || max_q_len < 0) return PD_ERR_INVALID_ARG;
+  if (num_kv_heads <= 0 || num_q_heads <= 0 || num_q_heads % num_kv_heads != 0)
+    return PD_ERR_INVALID_ARG;
+  const int G = num_q_heads / num_kv_heads;
+  if (G > kMaxGroup || num_kv_heads > 4095) return PD_ERR_UNSUPPORTED;
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return PD_ERR_UNSUPPORTED;
+  if (sliding_window < 0 || !isfinite(scale)) return PD_ERR_INVALID_ARG;
+  if (!q_stride_ok(q_stride, num_q_heads, head_dim) ||
+      !q_stride_ok(k_stride, num_kv_heads, head_dim) ||
+      !q_stride_ok(v_stride, num_kv_heads, head_dim) ||
+      !q_stride_ok(out_stride, num_q_heads, head_dim))
+    return PD_ERR_INVALID_ARG;
+  if (num_seqs == 0 || total_q == 0 || max_q_len == 0) return PD_OK;
+  if (!dev_ptr_ok(q) || !dev_ptr_ok(k) || !dev_ptr_ok(v) || !dev_ptr_ok(cu_q) || !dev_ptr_ok(out))
+    return PD_ERR_INVALID_ARG;
+  DeviceInfo* dev = nullptr;
+  if (current_device(&dev) != cudaSuccess) return PD_ERR_CUDA;
+  const int64_t q_row = static_cast<int64_t>(num_q_heads) * head_dim;
+  const int64_t kv_row = static_cast<int64_t>(num_kv_heads) * head_dim;
+  PackedArgs a;
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.out = static_cast<uint16_t*>(out);
+  a.q_stride = q_stride ? q_stride : q_row;
+  a.k_stride = k_stride ? k_stride : kv_row;
+  a.v_stride = v_stride ? v_stride : kv_row;
+  a.out_stride = out_stride ? out_stride : q_row;
+  a.cu_q = cu_q;
+  a.flags = dev->flags;
+  a.num_seqs = num_seqs;
+  a.total_q = total_q;
+  a.max_q_len = max_q_len < total_q ? max_q_len : total_q;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.group = G;
+  a.causal = causal != 0;
+  a.sliding_window = sliding_window;
+  a.scale_log2 = scale * kLog2e;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  (void)simple;
+  return cuda_status(launch_prefill_packed_simple(a, head_dim, st));
+}
+}  // namespace
+
+extern "C" {
+
+#define PD_PACKED_ARGS                                                                          \
+  q, q_stride, k, k_stride, v, v_stride, cu_q, out, out_stride, num_seqs, total_q, max_q_len,   \
+      num_q_heads, num_kv_heads, head_dim, scale, causal, sliding_window, stream
+
+int pd_prefill_packed(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                      const void* v, int64_t v_stride, const int32_t* cu_q, void* out,
+                      int64_t out_stride, int32_t num_seqs, int32_t total_q, int32_t max_q_len,
+                      int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, float scale,
+                      int32_t causal, int32_t sliding_window, void* stream) {
+  return prefill_packed(PD_PACKED_ARGS, false);
+}
+
+int pd_prefill_packed_crosscheck(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                 const void* v, int64_t v_stride, const int32_t* cu_q, void* out,
+                                 int64_t out_stride, int32_t num_seqs, int32_t total_q,
+                                 int32_t max_q_len, int32_t num_q_heads, int32_t num_kv_heads,
+                                 int32_t head_dim, float scale, int32_t causal,
+                                 int32_t sliding_window, void* stream) {
+  return prefill_packed(PD_PACKED_ARGS, true);
+}
+#undef PD_PACKED_ARGS
 
 float pd_fp8_scale(float absmax) { return absmax > 0.0f ? absmax / 448.0f : 1.0f; }
 
