@@ -628,7 +628,8 @@ int pd_rope_append_int8(const void* qkv, int64_t qkv_stride, const int32_t* cu_q
  * out = softmax(scale q k) v with scores, exponentials and sums in fp32 and the
  * weights rounded to bf16 for their product with v. A sequence whose counts do
  * not fit (n_b > max_q_len, rows beyond total_q) raises PD_DEV_BAD_SEQ_LEN and
- * its rows are not written; nor are rows of no sequence. head_dim in {64, 128,
+ * its rows are not written; nor are rows of no sequence. A sequence's own rows
+ * are taken to be finite; other rows may hold anything. head_dim in {64, 128,
  * 256}; num_q_heads / num_kv_heads <= 16; strides multiples of 8. */
 int pd_prefill_packed(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                       const void* v, int64_t v_stride, const int32_t* cu_q, void* out,

@@ -1378,8 +1378,8 @@ int prefill_packed(const void* q, int64_t q_stride, const void* k, int64_t k_str
   a.sliding_window = sliding_window;
   a.scale_log2 = scale * kLog2e;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  (void)simple;
-  return cuda_status(launch_prefill_packed_simple(a, head_dim, st));
+  return cuda_status(simple ? launch_prefill_packed_simple(a, head_dim, st)
+                            : launch_prefill_packed(a, head_dim, dev->num_sms, st));
 }
 }  // namespace
 

@@ -1,0 +1,707 @@
+// Attention of packed prompts over their own rows (pd_prefill_packed) on
+// tcgen05. out = softmax(scale Q K^T) V per (token, q head), fp32 scores and
+// sums, bf16 weights.
+//
+// The tensor core is what should bound it: per 128 x 128 tile and head_dim 128
+// the two products take 2 x 512 cycles of it, 16384 exponentials about as many
+// of the special-function units. So:
+//
+//  * A query tile is 128 (token, q head) rows of one GQA group (128 / G tokens):
+//    fewer tokens than rows, so the causal edge wastes little, and K and V are
+//    read once a group. At head_dim 64 / 128 a CTA works on two of them in turn:
+//    while one tile's softmax runs the tensor core has the other's products.
+//  * Scores of a 128-key tile lie in TMEM (128 columns a query tile), the weights
+//    go back over them as bf16 and are the A operand of the second product from
+//    there. The next scores of the same tile are issued behind that product:
+//    the tensor core takes the instructions of one thread in order.
+//  * One thread a row: maximum, exponentials and sum need no exchange. Weights
+//    are 2^(s - m) against a reference m that moves only when a tile passes it by
+//    2^8; O is rescaled in TMEM then.
+//  * CTAs stay. All (sequence, pair of tiles, kv head) items are ranked by the
+//    pair's place in its sequence, last first: with a causal mask that is
+//    costliest first, whatever the lengths. CTA c takes ranks c, 2 N - 1 - c,
+//    2 N + c ... of N CTAs. The copying warp finds the items (lengths are on the
+//    device only) and loads the next item's Q, K and V while the last one's
+//    softmax and output are under way.
+//  * Copies are TMA boxes (tokens x heads x 64 of head_dim, 128-byte swizzle), K
+//    and V in a ring of their own slots. Rows past a sequence's end come along in
+//    its last tile: as keys they are masked, as V rows zeroed in shared memory.
+//
+// head_dim 256: one query tile a CTA (O alone takes half of TMEM), 64-key tiles,
+// the scores in two buffers one tile ahead.
+//
+// Every wait is bounded (2 s); a role that gives up says so, and the copying warp
+// and the MMA thread wait for what they issued before the CTA ends.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cudaTypedefs.h>
+
+#include <cstring>
+
+#include "mma_common.cuh"
+#include "serve_common.cuh"
+#include "umma_common.cuh"
+
+namespace pd {
+namespace {
+
+using namespace ::pd::mma;
+using namespace ::pd::umma;
+
+constexpr float kMoveLog2 = 8.0f;  // weights stay below 2^8
+
+template <int D>
+struct PkCfg {
+  static constexpr int kTiles = D <= 128 ? 2 : 1;      // query tiles of a CTA
+  static constexpr int kKT = D <= 128 ? 128 : 64;      // keys of a tile
+  static constexpr int kBufs = kTiles == 2 ? 1 : 2;    // score buffers of a query tile
+  static constexpr int kDCH = D / 64;                  // 128-byte chunks of a row
+  static constexpr int kQBytes = 128 * 2 * D;          // one query tile
+  static constexpr int kSlotBytes = kKT * 2 * D;       // one tile of K or of V
+  static constexpr int kSlots = (224 * 1024 - kTiles * kQBytes) / kSlotBytes;
+  static constexpr int kRingOff = kTiles * kQBytes;
+  static constexpr int kBarOff = kRingOff + kSlots * kSlotBytes;
+  // kv_full, kv_empty [slots]; q_full, q_empty; item_full, item_empty [2]; per tile
+  // s_full[bufs], p_full, o_done; fin
+  static constexpr int kTileBars = kBufs + 2;
+  static constexpr int kNumBars = 2 * kSlots + 2 + 4 + kTiles * kTileBars + 1;
+  static constexpr int kItemOff = kBarOff + kNumBars * 8;
+  static constexpr int kHolderOff = kItemOff + 2 * 32;
+  static constexpr int kSmemBytes = kHolderOff + 16;
+  static constexpr int kSoftWarps = 4 * kTiles;
+  static constexpr int kProdWarp = kSoftWarps;
+  static constexpr int kMmaWarp = kSoftWarps + 1;
+  static constexpr int kThreads = (kSoftWarps + 2) * 32;
+  // TMEM: scores of (tile, buffer) at 128 * tile + kKT * buffer, O of tile X behind
+  static constexpr int kOCol = kTiles * kBufs * kKT;
+  static constexpr int kTmemCols = 512;
+  static_assert(kOCol + kTiles * D <= kTmemCols, "TMEM columns");
+  static_assert(kSmemBytes <= 227 * 1024, "one CTA's shared memory");
+  static_assert(kSlots >= 3, "K and V in use and one on its way");
+};
+
+// The wait for a load into v that other work stood between: v is read behind it.
+__device__ __forceinline__ void tmem_wait_ld32(uint32_t (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]),
+                 "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]),
+                 "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]),
+                 "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
+                 "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]),
+                 "+r"(v[30]), "+r"(v[31])
+               :
+               : "memory");
+}
+
+// An item, as the copying warp leaves it for the others.
+struct Item {
+  int q0, n;    // the sequence's first row and its tokens
+  int tok0;     // the pair's first token
+  int g;        // kv head; -1: no more items
+  int pad[4];
+};
+
+// What an item's tiles see. Tokens [t0(X), t1(X)) of query tile X, keys
+// [k_lo, k_hi), tiles from k_lo on; tile X works on tiles [j0, j1).
+struct Geometry {
+  int k_lo, ntiles;
+  int jA0, jA1, jB0, jB1;
+};
+template <int KT, int TILES>
+__device__ __forceinline__ Geometry geometry(const Item& it, int tpc, int causal, int W) {
+  Geometry r;
+  auto pos = [&](int t) { return causal ? t : it.n - 1; };
+  auto lo = [&](int t) { return (W > 0 && pos(t) >= W) ? pos(t) + 1 - W : 0; };
+  const int a0 = it.tok0, a1 = min(a0 + tpc, it.n);
+  const int b0 = a0 + tpc, b1 = min(b0 + tpc, it.n);
+  const bool has_b = TILES == 2 && b1 > b0;
+  r.k_lo = lo(a0);
+  const int hi_a = pos(a1 - 1) + 1, hi_b = has_b ? pos(b1 - 1) + 1 : 0;
+  r.ntiles = ((has_b ? hi_b : hi_a) - r.k_lo + KT - 1) / KT;
+  r.jA0 = 0;
+  r.jA1 = (hi_a - r.k_lo + KT - 1) / KT;
+  r.jB0 = has_b ? (lo(b0) - r.k_lo) / KT : 0;
+  r.jB1 = has_b ? (hi_b - r.k_lo + KT - 1) / KT : 0;
+  return r;
+}
+
+// Tokens of sequence b, or 0 where its counts do not fit the batch.
+__device__ __forceinline__ int prompt_len(const PackedArgs& a, int b, bool tell) {
+  const int q0 = __ldg(a.cu_q + b), q1 = __ldg(a.cu_q + b + 1);
+  const int n = q1 - q0;
+  if (q0 < 0 || n < 0 || q1 > a.total_q || n > a.max_q_len) {
+    if (tell) atomicOr(a.flags, PD_DEV_BAD_SEQ_LEN);
+    return 0;
+  }
+  return n;
+}
+
+template <int D>
+__global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
+    prefill_packed_kernel(const __grid_constant__ CUtensorMap tm_q,
+                          const __grid_constant__ CUtensorMap tm_k,
+                          const __grid_constant__ CUtensorMap tm_v, const PackedArgs a) {
+  using C = PkCfg<D>;
+  constexpr int KT = C::kKT;
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int G = a.group;
+  const int tpc = 128 / G;  // tokens of a query tile
+  const int tid = threadIdx.x;
+  const int warp = tid >> 5, lane = tid & 31;
+
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem = smem_raw;
+  const uint32_t s0 = smem_u32(smem);
+  if (s0 & 1023u) {  // the swizzled tiles need 1024-byte alignment
+    if (tid == 0) atomicOr(a.flags, PD_DEV_BAD_SMEM);
+    return;
+  }
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
+  uint64_t* kv_full = bars;
+  uint64_t* kv_empty = bars + C::kSlots;
+  uint64_t* q_full = bars + 2 * C::kSlots;
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* item_full = q_full + 2;
+  uint64_t* item_empty = q_full + 4;
+  uint64_t* tile_bars = q_full + 6;
+  uint64_t* fin_bar = tile_bars + C::kTiles * C::kTileBars;
+  auto s_full = [&](int X, int i) { return smem_u32(tile_bars + X * C::kTileBars + i); };
+  auto p_full = [&](int X) { return smem_u32(tile_bars + X * C::kTileBars + C::kBufs); };
+  auto o_done = [&](int X) { return smem_u32(tile_bars + X * C::kTileBars + C::kBufs + 1); };
+  Item* items = reinterpret_cast<Item*>(smem + C::kItemOff);
+  uint32_t* holder = reinterpret_cast<uint32_t*>(smem + C::kHolderOff);
+  volatile int* abort_s = reinterpret_cast<volatile int*>(holder + 1);
+
+  if (tid == 0) {
+    for (int i = 0; i < C::kNumBars; ++i) {
+      const uint32_t bar = smem_u32(bars + i);
+      uint32_t count = 1;
+      for (int X = 0; X < C::kTiles; ++X)
+        if (bar == p_full(X)) count = 4;
+      // an item's readers: the softmax warps and the MMA thread
+      if (bars + i == item_empty || bars + i == item_empty + 1) count = C::kSoftWarps + 1;
+      mbar_init(bar, count);
+    }
+    *abort_s = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == C::kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(holder)),
+                 "n"(C::kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (warp == C::kProdWarp && lane == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_q)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_v)) : "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *holder;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int W = a.sliding_window;
+  bool failed = false;
+
+  if (warp == C::kProdWarp) {
+    // ============================ copying warp ============================
+    const int span = C::kTiles * tpc;                        // tokens of an item
+    const int levels = (a.max_q_len + span - 1) / span;      // most items of a sequence
+    const bool first_cta = blockIdx.x == 0;
+    // items of sequences at levels >= p
+    auto above = [&](int p, bool tell) {
+      int c = 0;
+      for (int b = lane; b < a.num_seqs; b += 32)
+        c += max(0, (prompt_len(a, b, tell) + span - 1) / span - p);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xFFFFFFFFu, c, o);
+      return c;
+    };
+    const int hkv = a.num_kv_heads;
+    const int64_t total = static_cast<int64_t>(above(0, first_cta)) * hkv;
+    int slot = 0;      // ring slots filled so far
+    int k = 0;         // items so far
+    int top = levels;  // the level of the last item: ranks go up, levels down
+    for (int64_t round = 0;; ++round) {
+      const int64_t rank = round * gridDim.x +
+                           ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      const bool end = round * static_cast<int64_t>(gridDim.x) >= total;
+      if (!end && rank >= total) continue;  // a round that does not reach this CTA
+      Item it;
+      it.g = -1;
+      if (!end) {
+        const int pr = static_cast<int>(rank / hkv);
+        // the highest level p with above(p) > pr, searched below the last one
+        int lo = 0, hi = top;  // above(lo) > pr, above(hi) <= pr or unknown at top
+        int over = 0;          // above(lo + 1)
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          const int c = above(mid, false);
+          if (c > pr) {
+            lo = mid;
+          } else {
+            hi = mid;
+            over = c;
+          }
+        }
+        if (hi == top) over = above(hi, false);
+        if (over > pr) {  // still on the last item's level
+          lo = hi;
+          over = above(lo + 1, false);
+        }
+        top = lo;
+        int idx = pr - over;  // among the sequences that have level lo, in order
+        it.g = static_cast<int>(rank % hkv);
+        it.q0 = it.n = it.tok0 = 0;
+        for (int base = 0; base < a.num_seqs; base += 32) {
+          const int b = base + lane;
+          const int n = b < a.num_seqs ? prompt_len(a, b, false) : 0;
+          const uint32_t m = __ballot_sync(0xFFFFFFFFu, (n + span - 1) / span > lo);
+          const int c = __popc(m);
+          if (idx < c) {
+            uint32_t left = m;
+            for (int i = 0; i < idx; ++i) left &= left - 1;
+            const int src = __ffs(left) - 1;
+            it.n = __shfl_sync(0xFFFFFFFFu, n, src);
+            it.q0 = __ldg(a.cu_q + base + src);
+            it.tok0 = lo * span;
+            break;
+          }
+          idx -= c;
+        }
+      }
+      const int is = k & 1;
+      if (k >= 2 && !warp_wait(smem_u32(item_empty + is), ((k >> 1) - 1) & 1, abort_s)) {
+        failed = true;
+        break;
+      }
+      if (lane == 0) {
+        items[is] = it;
+        mbar_arrive(smem_u32(item_full + is));
+      }
+      __syncwarp();
+      if (end) break;
+      const Geometry ge = geometry<KT, C::kTiles>(it, tpc, a.causal, W);
+      // ---- Q: tokens x G heads x 64 of head_dim ----
+      if (k >= 1 && !warp_wait(smem_u32(q_empty), (k - 1) & 1, abort_s)) {
+        failed = true;
+        break;
+      }
+      if (lane == 0) {
+        const bool has_b = C::kTiles == 2 && it.tok0 + tpc < it.n;
+        const uint32_t box = static_cast<uint32_t>(tpc) * G * 128;
+        mbar_arrive_expect_tx(smem_u32(q_full), box * C::kDCH * (has_b ? 2 : 1));
+        for (int X = 0; X < (has_b ? 2 : 1); ++X)
+#pragma unroll
+          for (int ch = 0; ch < C::kDCH; ++ch)
+            tma_load_3d(s0 + X * C::kQBytes + ch * (128 * 128), &tm_q, ch * 64, it.g * G,
+                        it.q0 + it.tok0 + X * tpc, smem_u32(q_full));
+      }
+      ++k;
+      // ---- K and V tiles, in the order the MMA thread takes them ----
+      for (int j = 0; j < 2 * ge.ntiles; ++j, ++slot) {
+        const int st = slot % C::kSlots;
+        if (slot >= C::kSlots &&
+            !warp_wait(smem_u32(kv_empty + st), ((slot / C::kSlots) - 1) & 1, abort_s)) {
+          failed = true;
+          break;
+        }
+        if (lane == 0) {
+          const uint32_t fb = smem_u32(kv_full + st);
+          mbar_arrive_expect_tx(fb, C::kSlotBytes);
+          const uint32_t dst = s0 + C::kRingOff + st * C::kSlotBytes;
+#pragma unroll
+          for (int ch = 0; ch < C::kDCH; ++ch)
+            tma_load_3d(dst + ch * (KT * 128), (j & 1) ? &tm_v : &tm_k, ch * 64, it.g,
+                        it.q0 + ge.k_lo + (j >> 1) * KT, fb);
+        }
+        __syncwarp();
+      }
+      if (failed) break;
+    }
+    if (failed) {
+      if (lane == 0) atomicOr(a.flags, PD_DEV_TIMEOUT);
+      *abort_s = 1;
+    }
+    // the copies already issued land before the block can exit
+    for (int t = max(0, slot - C::kSlots); t < slot; ++t)
+      (void)mbar_wait(smem_u32(kv_full + t % C::kSlots), (t / C::kSlots) & 1);
+    if (k > 0) (void)mbar_wait(smem_u32(q_full), (k - 1) & 1);
+  } else if (warp == C::kMmaWarp) {
+    // ============================ MMA thread ==============================
+    if (lane == 0) {
+      constexpr uint32_t idS = umma_idesc(128, KT, 0);
+      constexpr uint32_t idO = umma_idesc(128, D, 1);
+      const uint64_t dq[2] = {umma_desc(s0, 16, 1024), umma_desc(s0 + C::kQBytes, 16, 1024)};
+      const uint64_t dk0 = umma_desc(s0 + C::kRingOff, 16, 1024);
+      const uint64_t dv0 = umma_desc(s0 + C::kRingOff, KT * 128, 1024);
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        return mbar_wait_or_abort(bar, parity, abort_s);
+      };
+      int slot = 0;             // K of the item's tile j is ring slot slot + 2 j, V the next
+      int done[2] = {0, 0};     // tiles of each query tile before this item
+      bool ok = true;
+      for (int k = 0; ok; ++k) {
+        if (!(ok = wait(smem_u32(item_full + (k & 1)), (k >> 1) & 1))) break;
+        const Item it = items[k & 1];
+        mbar_arrive(smem_u32(item_empty + (k & 1)));
+        if (it.g < 0) break;
+        const Geometry ge = geometry<KT, C::kTiles>(it, tpc, a.causal, W);
+        if (!(ok = wait(smem_u32(q_full), k & 1))) break;
+        auto in = [&](int X, int j) {
+          return X ? (j >= ge.jB0 && j < ge.jB1) : (j >= ge.jA0 && j < ge.jA1);
+        };
+        auto full = [&](int s) { return wait(smem_u32(kv_full + s % C::kSlots), (s / C::kSlots) & 1); };
+        // scores of tile j into X's next buffer
+        auto scores = [&](int X, int j) {
+          const int c = done[X] + j - (X ? ge.jB0 : ge.jA0);
+          const int buf = c % C::kBufs;
+          const uint64_t b0 =
+              dk0 + static_cast<uint64_t>((((slot + 2 * j) % C::kSlots) * C::kSlotBytes) >> 4);
+          const uint32_t d = tmem + X * 128 + buf * KT;
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks)
+            umma_f16(d, dq[X] + (((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4),
+                     b0 + (((ks >> 2) * (KT * 128) + (ks & 3) * 32) >> 4), idS, ks > 0 ? 1u : 0u);
+          umma_commit(s_full(X, buf));
+        };
+        auto product = [&](int X, int j) {  // O_X += P_X(j) V(j)
+          const int i = j - (X ? ge.jB0 : ge.jA0), c = done[X] + i;
+          if (!wait(p_full(X), c & 1)) return false;
+          tc_fence_after();
+          const uint64_t bv =
+              dv0 + static_cast<uint64_t>((((slot + 2 * j + 1) % C::kSlots) * C::kSlotBytes) >> 4);
+          const uint32_t p = tmem + X * 128 + (c % C::kBufs) * KT;
+#pragma unroll
+          for (int kk = 0; kk < KT / 16; ++kk)
+            umma_f16_ts(tmem + C::kOCol + X * D, p + kk * 8, bv + ((kk * 2048) >> 4), idO,
+                        (i > 0 || kk > 0) ? 1u : 0u);
+          umma_commit(o_done(X));
+          return true;
+        };
+        const int nt = ge.ntiles;
+        // scores of tile j of both query tiles, and K's slot handed back
+        auto all_scores = [&](int j) {
+          if (!full(slot + 2 * j)) return false;
+          tc_fence_after();
+          for (int X = 0; X < C::kTiles; ++X)
+            if (in(X, j)) scores(X, j);
+          umma_commit(smem_u32(kv_empty + (slot + 2 * j) % C::kSlots));
+          if (j == nt - 1) umma_commit(smem_u32(q_empty));
+          return true;
+        };
+        ok = all_scores(0);
+        for (int j = 0; j < nt && ok; ++j) {
+          if constexpr (C::kTiles == 1) {  // the next scores go ahead of this product
+            if (j + 1 < nt && !(ok = all_scores(j + 1))) break;
+          }
+          if (!(ok = full(slot + 2 * j + 1))) break;
+          tc_fence_after();
+          if constexpr (C::kTiles == 2) {
+            const bool more = j + 1 < nt;
+            for (int X = 0; X < 2 && ok; ++X) {
+              if (in(X, j)) ok = product(X, j);
+              // the next scores go over these weights, behind the product that reads them
+              if (ok && more) {
+                if (X == 0) ok = full(slot + 2 * j + 2);
+                if (ok && in(X, j + 1)) {
+                  tc_fence_after();
+                  scores(X, j + 1);
+                }
+              }
+            }
+            if (!ok) break;
+            umma_commit(smem_u32(kv_empty + (slot + 2 * j + 1) % C::kSlots));
+            if (more) {
+              umma_commit(smem_u32(kv_empty + (slot + 2 * j + 2) % C::kSlots));
+              if (j + 1 == nt - 1) umma_commit(smem_u32(q_empty));
+            }
+          } else {
+            if (!(ok = product(0, j))) break;
+            umma_commit(smem_u32(kv_empty + (slot + 2 * j + 1) % C::kSlots));
+          }
+        }
+        slot += 2 * nt;
+        done[0] += ge.jA1 - ge.jA0;
+        done[1] += ge.jB1 - ge.jB0;
+      }
+      if (!ok) {
+        atomicOr(a.flags, PD_DEV_TIMEOUT);
+        *abort_s = 1;
+      }
+      // every MMA issued has completed before TMEM is freed
+      umma_commit(smem_u32(fin_bar));
+      (void)mbar_wait(smem_u32(fin_bar), 0);
+    }
+    __syncwarp();
+  } else {
+    // =========================== softmax warps ============================
+    const int X = warp >> 2;
+    const int m = (warp & 3) * 32 + lane;  // row of the query tile: token m / G, head m % G
+    const int mt = m / G, mh = m % G;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t o_tm = tmem + lane_base + C::kOCol + X * D;
+    const float sl2 = a.scale_log2;
+    int slot = 0, done = 0;
+    for (int k = 0; !failed; ++k) {
+      if (!warp_wait(smem_u32(item_full + (k & 1)), (k >> 1) & 1, abort_s)) {
+        failed = true;
+        break;
+      }
+      const Item it = items[k & 1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(item_empty + (k & 1)));
+      if (it.g < 0) break;
+      const Geometry ge = geometry<KT, C::kTiles>(it, tpc, a.causal, W);
+      const int t = it.tok0 + X * tpc + mt;
+      const bool rvalid = mt < tpc && t < it.n;
+      // keys this row sees: [rlo, rhi); rows of no token count as seeing all
+      const int rpos = a.causal ? t : it.n - 1;
+      const int rhi = rvalid ? rpos + 1 : INT32_MAX;
+      const int rlo = (rvalid && W > 0 && rpos >= W) ? rpos + 1 - W : 0;
+      const int j0 = X ? ge.jB0 : ge.jA0, j1 = X ? ge.jB1 : ge.jA1;
+      float m_run = -INFINITY, l_run = 0.0f;
+      for (int j = j0; j < j1; ++j) {
+        const int c = done + j - j0;
+        const uint32_t s_tm = tmem + lane_base + X * 128 + (c % C::kBufs) * KT;
+        const int key0 = ge.k_lo + j * KT;
+        if (!warp_wait(s_full(X, c % C::kBufs), (c / C::kBufs) & 1, abort_s)) {
+          failed = true;
+          break;
+        }
+        tc_fence_after();
+        const int lo = rlo - key0, hi = rhi - key0;  // this tile's keys [lo, hi)
+        // all keys seen and a reference there: weights in one pass
+        const bool fast = __all_sync(0xFFFFFFFFu, !rvalid || (lo <= 0 && hi >= KT &&
+                                                              m_run != -INFINITY));
+        uint32_t p[KT / 2];
+        float sum[4];
+        float mn = m_run;
+        // weights of all keys against mn; returns the largest s - mn (fast tiles)
+        auto weights = [&](auto masked) {
+          constexpr bool kMasked = decltype(masked)::value;
+          const float ref = -mn;
+          float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sum[i] = 0.0f;
+          uint32_t v[2][32];
+          tmem_ld32(s_tm, v[0]);
+#pragma unroll
+          for (int ch = 0; ch < KT / 32; ++ch) {
+            tmem_wait_ld32(v[ch & 1]);
+            if (ch + 1 < KT / 32) tmem_ld32(s_tm + (ch + 1) * 32, v[(ch + 1) & 1]);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              float x0 = fmaf(__uint_as_float(v[ch & 1][i]), sl2, ref);
+              float x1 = fmaf(__uint_as_float(v[ch & 1][i + 1]), sl2, ref);
+              if constexpr (kMasked) {
+                const int kk = ch * 32 + i;
+                x0 = (kk >= lo && kk < hi) ? x0 : -INFINITY;
+                x1 = (kk + 1 >= lo && kk + 1 < hi) ? x1 : -INFINITY;
+              } else {
+                mx[0] = fmaxf(mx[0], x0);
+                mx[1] = fmaxf(mx[1], x1);
+              }
+              const float e0 = ex2(x0), e1 = ex2(x1);
+              sum[i & 2] += e0;
+              sum[(i & 2) + 1] += e1;
+              p[ch * 16 + i / 2] = pack_bf16x2(e0, e1);
+            }
+          }
+          return fmaxf(mx[0], mx[1]);
+        };
+        if (fast) {
+          const float mx = weights(std::false_type{});
+          const bool moves = rvalid && mx > kMoveLog2;
+          if (__any_sync(0xFFFFFFFFu, moves)) {  // the reference moves: again
+            mn = moves ? m_run + mx : m_run;
+            (void)weights(std::false_type{});
+          }
+        } else {
+          float mx = -INFINITY;
+#pragma unroll 1
+          for (int ch = 0; ch < KT / 32; ++ch) {
+            uint32_t v[32];
+            tmem_ld32(s_tm + ch * 32, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const int kk = ch * 32 + i;
+              if (kk >= lo && kk < hi) mx = fmaxf(mx, __uint_as_float(v[i]) * sl2);
+            }
+          }
+          if (mx > m_run + kMoveLog2 || m_run == -INFINITY) mn = fmaxf(mx, m_run);
+          if (mn == -INFINITY) mn = 0.0f;  // nothing seen yet: all weights 0
+          (void)weights(std::true_type{});
+          if (mx == -INFINITY && m_run == -INFINITY) mn = -INFINITY;
+        }
+        const float alpha = (mn == m_run || m_run == -INFINITY) ? 1.0f : ex2(m_run - mn);
+        l_run = l_run * alpha + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+        m_run = mn;
+
+        // V rows past the sequence's end belong to others: zeroed before the
+        // weights are released, by the first query tile that uses the tile
+        const bool zeroer = X == 0 || j >= ge.jA1;
+        const bool ragged = key0 + KT > it.n;
+        const int vs = slot + 2 * j + 1;
+        if (zeroer && ragged) {
+          if (!warp_wait(smem_u32(kv_full + vs % C::kSlots), (vs / C::kSlots) & 1, abort_s)) {
+            failed = true;
+            break;
+          }
+          const uint32_t vst = s0 + C::kRingOff + (vs % C::kSlots) * C::kSlotBytes;
+          const int first = it.n - key0;  // >= 1
+          for (int pc = first * 8 + m; pc < KT * 8; pc += 128)
+#pragma unroll
+            for (int ch = 0; ch < C::kDCH; ++ch)
+              sts128(vst + ch * (KT * 128) + swz128(pc * 16), 0u, 0u, 0u, 0u);
+          fence_async_smem();
+        }
+        // O may be rescaled once the product before has been added
+        if (j > j0 && __any_sync(0xFFFFFFFFu, alpha != 1.0f)) {
+          if (!warp_wait(o_done(X), (c - 1) & 1, abort_s)) {
+            failed = true;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll 1
+          for (int h = 0; h < D / 16; ++h) {
+            uint32_t v[16];
+            tmem_ld16(o_tm + h * 16, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
+            tmem_st16(o_tm + h * 16, v);
+          }
+        }
+        // weights over this row's scores
+#pragma unroll
+        for (int q = 0; q < KT / 32; ++q) {
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) w[i] = p[q * 16 + i];
+          tmem_st16(s_tm + q * 16, w);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(X));
+      }
+      if (failed) break;
+      slot += 2 * ge.ntiles;
+      if (j1 > j0) {
+        done += j1 - j0;
+        if (!warp_wait(o_done(X), (done - 1) & 1, abort_s)) {
+          failed = true;
+          break;
+        }
+        tc_fence_after();
+        uint16_t* orow = a.out + static_cast<int64_t>(it.q0 + t) * a.out_stride +
+                         static_cast<int64_t>(it.g * G + mh) * D;
+        const float inv = 1.0f / fmaxf(l_run, 1e-20f);
+#pragma unroll
+        for (int h = 0; h < D / 32; ++h) {
+          uint32_t v[32];
+          tmem_ld32(o_tm + h * 32, v);
+          tmem_wait_ld();
+          if (rvalid) {
+            uint4* dst = reinterpret_cast<uint4*>(orow + h * 32);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t w[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                w[i] = pack_bf16x2(__uint_as_float(v[q * 8 + 2 * i]) * inv,
+                                   __uint_as_float(v[q * 8 + 2 * i + 1]) * inv);
+              dst[q] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+        tc_fence_before();
+      }
+    }
+    if (failed) {
+      if (lane == 0) atomicOr(a.flags, PD_DEV_TIMEOUT);
+      *abort_s = 1;
+    }
+  }
+
+  // ---- free the TMEM columns once every warp is done with them ----
+  tc_fence_before();
+  __syncthreads();
+  if (warp == C::kMmaWarp) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "n"(C::kTmemCols)
+                 : "memory");
+  }
+}
+
+// 3-D map over rows of heads: (head_dim, head, row), box (64, heads, rows).
+bool encode_rows_map(CUtensorMap* m, const void* base, int D, int heads, int64_t rows,
+                     int64_t row_stride, int box_heads, int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2,
+                                 static_cast<cuuint64_t>(row_stride) * 2};
+  const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(box_heads),
+                             static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[3] = {1u, 1u, 1u};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t launch_packed(const PackedArgs& a, int num_sms, cudaStream_t st) {
+  using C = PkCfg<D>;
+  CUtensorMap tq, tk, tv;
+  const int tpc = 128 / a.group;
+  if (!encode_rows_map(&tq, a.q, D, a.num_q_heads, a.total_q, a.q_stride, a.group, tpc) ||
+      !encode_rows_map(&tk, a.k, D, a.num_kv_heads, a.total_q, a.k_stride, 1, C::kKT) ||
+      !encode_rows_map(&tv, a.v, D, a.num_kv_heads, a.total_q, a.v_stride, 1, C::kKT))
+    return cudaErrorInvalidValue;
+  auto kern = prefill_packed_kernel<D>;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  static bool attr_set[64] = {};  // per device; setting it twice is harmless
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!attr_set[dev]) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
+  }
+  // no more CTAs than there can be items: whole spans, and a last part a sequence
+  const int span = C::kTiles * tpc;
+  const int64_t most = (static_cast<int64_t>(a.total_q) / span + a.num_seqs) * a.num_kv_heads;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(most < num_sms ? most : num_sms));
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, a);
+}
+
+}  // namespace
+
+cudaError_t launch_prefill_packed(const PackedArgs& a, int head_dim, int num_sms,
+                                  cudaStream_t st) {
+  switch (head_dim) {
+    case 64: return launch_packed<64>(a, num_sms, st);
+    case 128: return launch_packed<128>(a, num_sms, st);
+    case 256: return launch_packed<256>(a, num_sms, st);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace pd
