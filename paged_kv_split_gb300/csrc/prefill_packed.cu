@@ -93,6 +93,67 @@ __device__ __forceinline__ void tmem_wait_ld32(uint32_t (&v)[32]) {
                : "memory");
 }
 
+// The one lane of a warp that issues for it.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
+}
+// Matrix descriptors (K-major or MN-major, 128-byte swizzle, 8-row groups 1024
+// bytes apart) as two words: the upper one is the same for all.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) {
+  return ((addr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                       bool accumulate, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\tmov.b64 da, {%1, %6};\n\tmov.b64 db, {%2, %6};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)), "r"(lead),
+      "r"(kDescHi)
+      : "memory");
+}
+// A in TMEM.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc,
+                                       bool accumulate, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\tmov.b64 db, {%2, %6};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)), "r"(lead),
+      "r"(kDescHi)
+      : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t lead, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t@q "
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void arrive_if(uint32_t lead, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t.reg .b64 st;\n\tsetp.ne.b32 q, %1, 0;\n\t@q "
+      "mbarrier.arrive.shared::cta.b64 st, [%0];\n\t}" ::"r"(bar),
+      "r"(lead)
+      : "memory");
+}
+// A place in a ring of N slots and the parity of its fill.
+template <int N>
+struct Ring {
+  int at = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == N) {
+      at = 0;
+      parity ^= 1u;
+    }
+  }
+};
+
 // An item, as the copying warp leaves it for the others.
 struct Item {
   int q0, n;    // the sequence's first row and its tokens
@@ -183,6 +244,7 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
       mbar_init(bar, count);
     }
     *abort_s = 0;
+    holder[2] = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == C::kMmaWarp) {
@@ -204,6 +266,7 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int W = a.sliding_window;
   bool failed = false;
+  const volatile int* no_abort = reinterpret_cast<const volatile int*>(holder + 2);  // stays 0
 
   if (warp == C::kProdWarp) {
     // ============================ copying warp ============================
@@ -330,112 +393,110 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
       (void)mbar_wait(smem_u32(kv_full + t % C::kSlots), (t / C::kSlots) & 1);
     if (k > 0) (void)mbar_wait(smem_u32(q_full), (k - 1) & 1);
   } else if (warp == C::kMmaWarp) {
-    // ============================ MMA thread ==============================
-    if (lane == 0) {
-      constexpr uint32_t idS = umma_idesc(128, KT, 0);
-      constexpr uint32_t idO = umma_idesc(128, D, 1);
-      const uint64_t dq[2] = {umma_desc(s0, 16, 1024), umma_desc(s0 + C::kQBytes, 16, 1024)};
-      const uint64_t dk0 = umma_desc(s0 + C::kRingOff, 16, 1024);
-      const uint64_t dv0 = umma_desc(s0 + C::kRingOff, KT * 128, 1024);
-      auto wait = [&](uint32_t bar, uint32_t parity) {
-        return mbar_wait_or_abort(bar, parity, abort_s);
+    // ============================= MMA warp ================================
+    // One lane issues; the whole warp runs the loop, so that descriptors stay in
+    // uniform registers and nothing is computed between two instructions
+    const uint32_t lead = elect_one();
+    constexpr uint32_t idS = umma_idesc(128, KT, 0);
+    constexpr uint32_t idO = umma_idesc(128, D, 1);
+    const uint32_t q_lo = desc_lo(s0, 16), k_lo = desc_lo(s0 + C::kRingOff, 16);
+    const uint32_t v_lo = desc_lo(s0 + C::kRingOff, KT * 128);
+    Ring<C::kSlots> kr, vr;  // the next tile of K, and of V
+    vr.next();
+    int buf = 0;                        // one query tile: the next scores' buffer
+    uint32_t p_par[2] = {0u, 0u};       // of the next weights
+    int pbuf = 0;
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      if (!(ok = warp_wait(smem_u32(item_full + (k & 1)), (k >> 1) & 1, abort_s))) break;
+      const Item it = items[k & 1];
+      __syncwarp();
+      arrive_if(lead, smem_u32(item_empty + (k & 1)));
+      const int g = __shfl_sync(0xFFFFFFFFu, it.g, 0);
+      if (g < 0) break;
+      const Geometry ge = geometry<KT, C::kTiles>(it, tpc, a.causal, W);
+      const int nt = __shfl_sync(0xFFFFFFFFu, ge.ntiles, 0);
+      const int jA1 = __shfl_sync(0xFFFFFFFFu, ge.jA1, 0);
+      const int jB0 = __shfl_sync(0xFFFFFFFFu, ge.jB0, 0);
+      const int jB1 = __shfl_sync(0xFFFFFFFFu, ge.jB1, 0);
+      if (!(ok = warp_wait(smem_u32(q_full), k & 1, abort_s))) break;
+      auto in = [&](int X, int j) { return X ? (j >= jB0 && j < jB1) : j < jA1; };
+      auto last = [&](int X, int j) { return j == (X ? jB1 : jA1) - 1; };
+      // scores of K's next tile for query tile X
+      auto scores = [&](int X) {
+        const uint32_t b = k_lo + kr.at * (C::kSlotBytes >> 4);
+        const uint32_t d = tmem + X * 128 + (C::kBufs == 2 ? buf * KT : 0);
+        const uint32_t q = q_lo + X * (C::kQBytes >> 4);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+          mma_ss(d, q + (((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4),
+                 b + (((ks >> 2) * (KT * 128) + (ks & 3) * 32) >> 4), idS, ks > 0, lead);
+        commit_if(lead, s_full(X, C::kBufs == 2 ? buf : 0));
       };
-      int slot = 0;             // K of the item's tile j is ring slot slot + 2 j, V the next
-      int done[2] = {0, 0};     // tiles of each query tile before this item
-      bool ok = true;
-      for (int k = 0; ok; ++k) {
-        if (!(ok = wait(smem_u32(item_full + (k & 1)), (k >> 1) & 1))) break;
-        const Item it = items[k & 1];
-        mbar_arrive(smem_u32(item_empty + (k & 1)));
-        if (it.g < 0) break;
-        const Geometry ge = geometry<KT, C::kTiles>(it, tpc, a.causal, W);
-        if (!(ok = wait(smem_u32(q_full), k & 1))) break;
-        auto in = [&](int X, int j) {
-          return X ? (j >= ge.jB0 && j < ge.jB1) : (j >= ge.jA0 && j < ge.jA1);
-        };
-        auto full = [&](int s) { return wait(smem_u32(kv_full + s % C::kSlots), (s / C::kSlots) & 1); };
-        // scores of tile j into X's next buffer
-        auto scores = [&](int X, int j) {
-          const int c = done[X] + j - (X ? ge.jB0 : ge.jA0);
-          const int buf = c % C::kBufs;
-          const uint64_t b0 =
-              dk0 + static_cast<uint64_t>((((slot + 2 * j) % C::kSlots) * C::kSlotBytes) >> 4);
-          const uint32_t d = tmem + X * 128 + buf * KT;
+      // O_X += weights V's next tile
+      auto product = [&](int X, bool first) {
+        const uint32_t b = v_lo + vr.at * (C::kSlotBytes >> 4);
+        const uint32_t p = tmem + X * 128 + (C::kBufs == 2 ? pbuf * KT : 0);
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks)
-            umma_f16(d, dq[X] + (((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4),
-                     b0 + (((ks >> 2) * (KT * 128) + (ks & 3) * 32) >> 4), idS, ks > 0 ? 1u : 0u);
-          umma_commit(s_full(X, buf));
-        };
-        auto product = [&](int X, int j) {  // O_X += P_X(j) V(j)
-          const int i = j - (X ? ge.jB0 : ge.jA0), c = done[X] + i;
-          if (!wait(p_full(X), c & 1)) return false;
-          tc_fence_after();
-          const uint64_t bv =
-              dv0 + static_cast<uint64_t>((((slot + 2 * j + 1) % C::kSlots) * C::kSlotBytes) >> 4);
-          const uint32_t p = tmem + X * 128 + (c % C::kBufs) * KT;
+        for (int kk = 0; kk < KT / 16; ++kk)
+          mma_ts(tmem + C::kOCol + X * D, p + kk * 8, b + ((kk * 2048) >> 4), idO,
+                 !first || kk > 0, lead);
+      };
+      auto wait_k = [&]() { return warp_wait(smem_u32(kv_full + kr.at), kr.parity, abort_s); };
+      auto wait_v = [&]() { return warp_wait(smem_u32(kv_full + vr.at), vr.parity, abort_s); };
+      auto pass_k = [&](int j) {  // K's tile j handed back behind its scores
+        commit_if(lead, smem_u32(kv_empty + kr.at));
+        if (j == nt - 1) commit_if(lead, smem_u32(q_empty));
+        kr.next();
+        kr.next();
+        if constexpr (C::kBufs == 2) buf ^= 1;
+      };
+      if (!(ok = wait_k())) break;
+      tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < KT / 16; ++kk)
-            umma_f16_ts(tmem + C::kOCol + X * D, p + kk * 8, bv + ((kk * 2048) >> 4), idO,
-                        (i > 0 || kk > 0) ? 1u : 0u);
-          umma_commit(o_done(X));
-          return true;
-        };
-        const int nt = ge.ntiles;
-        // scores of tile j of both query tiles, and K's slot handed back
-        auto all_scores = [&](int j) {
-          if (!full(slot + 2 * j)) return false;
+      for (int X = 0; X < C::kTiles; ++X)
+        if (in(X, 0)) scores(X);
+      pass_k(0);
+      for (int j = 0; j < nt; ++j) {
+        const bool more = j + 1 < nt;
+        if (C::kTiles == 1 && more) {  // two score buffers: the next scores go ahead
+          if (!(ok = wait_k())) break;
           tc_fence_after();
-          for (int X = 0; X < C::kTiles; ++X)
-            if (in(X, j)) scores(X, j);
-          umma_commit(smem_u32(kv_empty + (slot + 2 * j) % C::kSlots));
-          if (j == nt - 1) umma_commit(smem_u32(q_empty));
-          return true;
-        };
-        ok = all_scores(0);
-        for (int j = 0; j < nt && ok; ++j) {
-          if constexpr (C::kTiles == 1) {  // the next scores go ahead of this product
-            if (j + 1 < nt && !(ok = all_scores(j + 1))) break;
-          }
-          if (!(ok = full(slot + 2 * j + 1))) break;
-          tc_fence_after();
-          if constexpr (C::kTiles == 2) {
-            const bool more = j + 1 < nt;
-            for (int X = 0; X < 2 && ok; ++X) {
-              if (in(X, j)) ok = product(X, j);
-              // the next scores go over these weights, behind the product that reads them
-              if (ok && more) {
-                if (X == 0) ok = full(slot + 2 * j + 2);
-                if (ok && in(X, j + 1)) {
-                  tc_fence_after();
-                  scores(X, j + 1);
-                }
-              }
-            }
-            if (!ok) break;
-            umma_commit(smem_u32(kv_empty + (slot + 2 * j + 1) % C::kSlots));
-            if (more) {
-              umma_commit(smem_u32(kv_empty + (slot + 2 * j + 2) % C::kSlots));
-              if (j + 1 == nt - 1) umma_commit(smem_u32(q_empty));
-            }
-          } else {
-            if (!(ok = product(0, j))) break;
-            umma_commit(smem_u32(kv_empty + (slot + 2 * j + 1) % C::kSlots));
-          }
+          scores(0);
+          pass_k(j + 1);
         }
-        slot += 2 * nt;
-        done[0] += ge.jA1 - ge.jA0;
-        done[1] += ge.jB1 - ge.jB0;
+        if (!(ok = wait_v())) break;
+        if (C::kTiles == 2 && more && !(ok = wait_k())) break;
+#pragma unroll
+        for (int X = 0; X < C::kTiles; ++X) {
+          if (in(X, j)) {
+            if (!(ok = warp_wait(p_full(X), p_par[X], abort_s))) break;
+            p_par[X] ^= 1u;
+            tc_fence_after();
+            product(X, X == 1 ? j == jB0 : j == 0);
+            // two score buffers: each tile's weights wait for it; one: the scores
+            // that follow tell of it, but behind the last
+            if (C::kBufs == 2 || last(X, j)) commit_if(lead, o_done(X));
+          }
+          // one buffer: the next scores go over these weights, behind the product
+          // that reads them in the tensor core's order
+          if (C::kTiles == 2 && more && in(X, j + 1)) scores(X);
+        }
+        if (!ok) break;
+        commit_if(lead, smem_u32(kv_empty + vr.at));
+        vr.next();
+        vr.next();
+        if constexpr (C::kBufs == 2) pbuf ^= 1;
+        if (C::kTiles == 2 && more) pass_k(j + 1);
       }
-      if (!ok) {
-        atomicOr(a.flags, PD_DEV_TIMEOUT);
-        *abort_s = 1;
-      }
-      // every MMA issued has completed before TMEM is freed
-      umma_commit(smem_u32(fin_bar));
-      (void)mbar_wait(smem_u32(fin_bar), 0);
     }
-    __syncwarp();
+    if (!ok) {
+      if (lane == 0) atomicOr(a.flags, PD_DEV_TIMEOUT);
+      *abort_s = 1;
+    }
+    // every MMA issued has completed before TMEM is freed
+    commit_if(lead, smem_u32(fin_bar));
+    (void)warp_wait(smem_u32(fin_bar), 0, no_abort);
   } else {
     // =========================== softmax warps ============================
     const int X = warp >> 2;
@@ -444,7 +505,8 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t o_tm = tmem + lane_base + C::kOCol + X * D;
     const float sl2 = a.scale_log2;
-    int slot = 0, done = 0;
+    int slot = 0, done = 0;  // ring slots and key tiles before the item
+    int runs = 0;            // items this query tile had part in
     for (int k = 0; !failed; ++k) {
       if (!warp_wait(smem_u32(item_full + (k & 1)), (k >> 1) & 1, abort_s)) {
         failed = true;
@@ -559,13 +621,19 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
               sts128(vst + ch * (KT * 128) + swz128(pc * 16), 0u, 0u, 0u, 0u);
           fence_async_smem();
         }
-        // O may be rescaled once the product before has been added
-        if (j > j0 && __any_sync(0xFFFFFFFFu, alpha != 1.0f)) {
+        // O may be rescaled once the product before has been added: with one score
+        // buffer these scores came behind it. With two its barrier says so, and
+        // these weights wait for it in any case, so that no barrier here runs a
+        // phase ahead of its readers
+        const bool rescale = j > j0 && __any_sync(0xFFFFFFFFu, alpha != 1.0f);
+        if (C::kBufs == 2 && j > j0) {
           if (!warp_wait(o_done(X), (c - 1) & 1, abort_s)) {
             failed = true;
             break;
           }
           tc_fence_after();
+        }
+        if (rescale) {
 #pragma unroll 1
           for (int h = 0; h < D / 16; ++h) {
             uint32_t v[16];
@@ -593,7 +661,8 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
       slot += 2 * ge.ntiles;
       if (j1 > j0) {
         done += j1 - j0;
-        if (!warp_wait(o_done(X), (done - 1) & 1, abort_s)) {
+        ++runs;
+        if (!warp_wait(o_done(X), ((C::kBufs == 2 ? done : runs) - 1) & 1, abort_s)) {
           failed = true;
           break;
         }
