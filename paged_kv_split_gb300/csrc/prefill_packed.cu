@@ -141,6 +141,17 @@ __device__ __forceinline__ void arrive_if(uint32_t lead, uint32_t bar) {
       "r"(lead)
       : "memory");
 }
+// 16 bf16 to p, in one 32-byte store where p is so aligned.
+__device__ __forceinline__ void store16(uint16_t* p, const uint32_t (&w)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
 // A place in a ring of N slots and the parity of its fill.
 template <int N>
 struct Ring {
@@ -535,25 +546,38 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
         }
         tc_fence_after();
         const int lo = rlo - key0, hi = rhi - key0;  // this tile's keys [lo, hi)
-        // all keys seen and a reference there: weights in one pass
-        const bool fast = __all_sync(0xFFFFFFFFu, !rvalid || (lo <= 0 && hi >= KT &&
-                                                              m_run != -INFINITY));
+        // weights in one pass against the reference as it is; the first 32 keys'
+        // maximum where there is none yet
+        const bool open = __all_sync(0xFFFFFFFFu, !rvalid || (lo <= 0 && hi >= KT));
         uint32_t p[KT / 2];
         float sum[4];
         float mn = m_run;
-        // weights of all keys against mn; returns the largest s - mn (fast tiles)
-        auto weights = [&](auto masked) {
-          constexpr bool kMasked = decltype(masked)::value;
-          const float ref = -mn;
+        // weights of the tile against mn; returns the largest s - mn. FIRST: mn is
+        // the largest product of the first chunk (times the scale), if that has a
+        // key that the row sees
+        auto weights = [&](auto masked, auto first) {
+          constexpr bool kMasked = decltype(masked)::value, kFirst = decltype(first)::value;
           float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
           for (int i = 0; i < 4; ++i) sum[i] = 0.0f;
           uint32_t v[2][32];
           tmem_ld32(s_tm, v[0]);
+          float ref = -mn;
 #pragma unroll
           for (int ch = 0; ch < KT / 32; ++ch) {
             tmem_wait_ld32(v[ch & 1]);
             if (ch + 1 < KT / 32) tmem_ld32(s_tm + (ch + 1) * 32, v[(ch + 1) & 1]);
+            if (kFirst && ch == 0) {
+              float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const float x = __uint_as_float(v[0][i]);
+                if (!kMasked || (i >= lo && i < hi)) top[i & 3] = fmaxf(top[i & 3], x);
+              }
+              const float t = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+              mn = t == -INFINITY ? t : t * sl2;
+              ref = mn == -INFINITY ? 0.0f : -mn;
+            }
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
               float x0 = fmaf(__uint_as_float(v[ch & 1][i]), sl2, ref);
@@ -562,10 +586,9 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
                 const int kk = ch * 32 + i;
                 x0 = (kk >= lo && kk < hi) ? x0 : -INFINITY;
                 x1 = (kk + 1 >= lo && kk + 1 < hi) ? x1 : -INFINITY;
-              } else {
-                mx[0] = fmaxf(mx[0], x0);
-                mx[1] = fmaxf(mx[1], x1);
               }
+              mx[0] = fmaxf(mx[0], x0);
+              mx[1] = fmaxf(mx[1], x1);
               const float e0 = ex2(x0), e1 = ex2(x1);
               sum[i & 2] += e0;
               sum[(i & 2) + 1] += e1;
@@ -574,14 +597,26 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
           }
           return fmaxf(mx[0], mx[1]);
         };
-        if (fast) {
-          const float mx = weights(std::false_type{});
-          const bool moves = rvalid && mx > kMoveLog2;
-          if (__any_sync(0xFFFFFFFFu, moves)) {  // the reference moves: again
-            mn = moves ? m_run + mx : m_run;
-            (void)weights(std::false_type{});
-          }
+        // rows without a reference: in an item's first tile, or where a window
+        // hid all keys so far
+        const bool fresh = __any_sync(0xFFFFFFFFu, rvalid && m_run == -INFINITY);
+        bool again = false;  // the weights want another reference
+        if (!fresh) {
+          const float mx = open ? weights(std::false_type{}, std::false_type{})
+                                : weights(std::true_type{}, std::false_type{});
+          again = rvalid && mx > kMoveLog2;
+          if (again) mn = m_run + mx;
+        } else if (open && j == j0) {
+          const float mx = weights(std::false_type{}, std::true_type{});
+          again = rvalid && mx > kMoveLog2;
+          if (again) mn = mn + mx;
+        } else if (j == j0) {
+          const float mx = weights(std::true_type{}, std::true_type{});
+          // a key seen behind the first chunk alone: it has no reference yet
+          again = rvalid && (mn == -INFINITY ? mx != -INFINITY : mx > kMoveLog2);
+          if (again) mn = mn == -INFINITY ? mx : mn + mx;
         } else {
+          // a later tile in which some rows see their first key: the maximum first
           float mx = -INFINITY;
 #pragma unroll 1
           for (int ch = 0; ch < KT / 32; ++ch) {
@@ -594,10 +629,14 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
               if (kk >= lo && kk < hi) mx = fmaxf(mx, __uint_as_float(v[i]) * sl2);
             }
           }
-          if (mx > m_run + kMoveLog2 || m_run == -INFINITY) mn = fmaxf(mx, m_run);
-          if (mn == -INFINITY) mn = 0.0f;  // nothing seen yet: all weights 0
-          (void)weights(std::true_type{});
-          if (mx == -INFINITY && m_run == -INFINITY) mn = -INFINITY;
+          if (mx > m_run + kMoveLog2 || m_run == -INFINITY) mn = mx;
+          again = true;
+        }
+        if (__any_sync(0xFFFFFFFFu, again)) {
+          const bool none = mn == -INFINITY;  // nothing seen yet: all weights 0
+          if (none) mn = 0.0f;
+          (void)weights(std::true_type{}, std::false_type{});
+          if (none) mn = -INFINITY;
         }
         const float alpha = (mn == m_run || m_run == -INFINITY) ? 1.0f : ex2(m_run - mn);
         l_run = l_run * alpha + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
@@ -670,21 +709,22 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
         uint16_t* orow = a.out + static_cast<int64_t>(it.q0 + t) * a.out_stride +
                          static_cast<int64_t>(it.g * G + mh) * D;
         const float inv = 1.0f / fmaxf(l_run, 1e-20f);
+        // whole 32-byte sectors a store, where the rows start on them
+        const bool wide = ((reinterpret_cast<uintptr_t>(a.out) | (a.out_stride * 2)) & 31) == 0;
 #pragma unroll
         for (int h = 0; h < D / 32; ++h) {
           uint32_t v[32];
           tmem_ld32(o_tm + h * 32, v);
           tmem_wait_ld();
           if (rvalid) {
-            uint4* dst = reinterpret_cast<uint4*>(orow + h * 32);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint32_t w[4];
+            for (int q = 0; q < 2; ++q) {
+              uint32_t w[8];
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                w[i] = pack_bf16x2(__uint_as_float(v[q * 8 + 2 * i]) * inv,
-                                   __uint_as_float(v[q * 8 + 2 * i + 1]) * inv);
-              dst[q] = make_uint4(w[0], w[1], w[2], w[3]);
+              for (int i = 0; i < 8; ++i)
+                w[i] = pack_bf16x2(__uint_as_float(v[q * 16 + 2 * i]) * inv,
+                                   __uint_as_float(v[q * 16 + 2 * i + 1]) * inv);
+              store16(orow + h * 32 + q * 16, w, wide);
             }
           }
         }
