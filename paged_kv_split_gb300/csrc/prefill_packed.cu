@@ -62,8 +62,8 @@ struct PkCfg {
   static constexpr int kRingOff = kTiles * kQBytes;
   static constexpr int kBarOff = kRingOff + kSlots * kSlotBytes;
   // kv_full, kv_empty [slots]; q_full, q_empty; item_full, item_empty [2]; per tile
-  // s_full[bufs], p_full, o_done; fin
-  static constexpr int kTileBars = kBufs + 2;
+  // s_full[bufs], p_full, o_done, p_half; fin
+  static constexpr int kTileBars = kBufs + 3;
   static constexpr int kNumBars = 2 * kSlots + 2 + 4 + kTiles * kTileBars + 1;
   static constexpr int kItemOff = kBarOff + kNumBars * 8;
   static constexpr int kHolderOff = kItemOff + 2 * 32;
@@ -93,6 +93,40 @@ __device__ __forceinline__ void tmem_wait_ld32(uint32_t (&v)[32]) {
                : "memory");
 }
 
+// The same for another load that the wait covered.
+__device__ __forceinline__ void after_wait32(uint32_t (&v)[32]) {
+  asm volatile(""
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]),
+                 "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]),
+                 "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]),
+                 "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
+                 "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]),
+                 "+r"(v[30]), "+r"(v[31])
+               :
+               : "memory");
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// (x, y) times f plus g, and sums of pairs: two lanes of one instruction.
+__device__ __forceinline__ float2 fma2(uint32_t x, uint32_t y, float f, float g) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\t"
+      "mov.b64 c, {%5, %5};\n\tfma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "r"(x), "r"(y), "f"(f), "f"(g));
+  return r;
+}
+__device__ __forceinline__ float2 add2(const float2& x, const float2& y) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+  return r;
+}
 // The one lane of a warp that issues for it.
 __device__ __forceinline__ uint32_t elect_one() {
   uint32_t r;
@@ -240,6 +274,7 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
   auto s_full = [&](int X, int i) { return smem_u32(tile_bars + X * C::kTileBars + i); };
   auto p_full = [&](int X) { return smem_u32(tile_bars + X * C::kTileBars + C::kBufs); };
   auto o_done = [&](int X) { return smem_u32(tile_bars + X * C::kTileBars + C::kBufs + 1); };
+  auto p_half = [&](int X) { return smem_u32(tile_bars + X * C::kTileBars + C::kBufs + 2); };
   Item* items = reinterpret_cast<Item*>(smem + C::kItemOff);
   uint32_t* holder = reinterpret_cast<uint32_t*>(smem + C::kHolderOff);
   volatile int* abort_s = reinterpret_cast<volatile int*>(holder + 1);
@@ -249,7 +284,7 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
       const uint32_t bar = smem_u32(bars + i);
       uint32_t count = 1;
       for (int X = 0; X < C::kTiles; ++X)
-        if (bar == p_full(X)) count = 4;
+        if (bar == p_full(X) || bar == p_half(X)) count = 4;
       // an item's readers: the softmax warps and the MMA thread
       if (bars + i == item_empty || bars + i == item_empty + 1) count = C::kSoftWarps + 1;
       mbar_init(bar, count);
@@ -449,9 +484,16 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
         const uint32_t b = v_lo + vr.at * (C::kSlotBytes >> 4);
         const uint32_t p = tmem + X * 128 + (C::kBufs == 2 ? pbuf * KT : 0);
 #pragma unroll
-        for (int kk = 0; kk < KT / 16; ++kk)
-          mma_ts(tmem + C::kOCol + X * D, p + kk * 8, b + ((kk * 2048) >> 4), idO,
-                 !first || kk > 0, lead);
+        for (int half = 0; half < 2; ++half) {
+          if (!warp_wait(half ? p_full(X) : p_half(X), p_par[X], abort_s)) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = half * (KT / 32); kk < (half + 1) * (KT / 32); ++kk)
+            mma_ts(tmem + C::kOCol + X * D, p + kk * 8, b + ((kk * 2048) >> 4), idO,
+                   !first || kk > 0, lead);
+        }
+        p_par[X] ^= 1u;
+        return true;
       };
       auto wait_k = [&]() { return warp_wait(smem_u32(kv_full + kr.at), kr.parity, abort_s); };
       auto wait_v = [&]() { return warp_wait(smem_u32(kv_full + vr.at), vr.parity, abort_s); };
@@ -481,10 +523,7 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
 #pragma unroll
         for (int X = 0; X < C::kTiles; ++X) {
           if (in(X, j)) {
-            if (!(ok = warp_wait(p_full(X), p_par[X], abort_s))) break;
-            p_par[X] ^= 1u;
-            tc_fence_after();
-            product(X, X == 1 ? j == jB0 : j == 0);
+            if (!(ok = product(X, X == 1 ? j == jB0 : j == 0))) break;
             // two score buffers: each tile's weights wait for it; one: the scores
             // that follow tell of it, but behind the last
             if (C::kBufs == 2 || last(X, j)) commit_if(lead, o_done(X));
@@ -515,7 +554,8 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
     const int mt = m / G, mh = m % G;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t o_tm = tmem + lane_base + C::kOCol + X * D;
-    const float sl2 = a.scale_log2;
+    // a masked score is -inf before it is multiplied: never by zero
+    const float sl2 = fmaxf(fabsf(a.scale_log2), 1.17549435e-38f);
     int slot = 0, done = 0;  // ring slots and key tiles before the item
     int runs = 0;            // items this query tile had part in
     for (int k = 0; !failed; ++k) {
@@ -546,100 +586,43 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
         }
         tc_fence_after();
         const int lo = rlo - key0, hi = rhi - key0;  // this tile's keys [lo, hi)
-        // weights in one pass against the reference as it is; the first 32 keys'
-        // maximum where there is none yet
         const bool open = __all_sync(0xFFFFFFFFu, !rvalid || (lo <= 0 && hi >= KT));
-        uint32_t p[KT / 2];
-        float sum[4];
-        float mn = m_run;
-        // weights of the tile against mn; returns the largest s - mn. FIRST: mn is
-        // the largest product of the first chunk (times the scale), if that has a
-        // key that the row sees
-        auto weights = [&](auto masked, auto first) {
-          constexpr bool kMasked = decltype(masked)::value, kFirst = decltype(first)::value;
-          float mx[2] = {-INFINITY, -INFINITY};
+        // ---- the row's scores, their maximum, the reference ----
+        uint32_t v[KT / 32][32];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sum[i] = 0.0f;
-          uint32_t v[2][32];
-          tmem_ld32(s_tm, v[0]);
-          float ref = -mn;
+        for (int ch = 0; ch < KT / 32; ++ch) tmem_ld32(s_tm + ch * 32, v[ch]);
+        tmem_wait_ld32(v[0]);
 #pragma unroll
-          for (int ch = 0; ch < KT / 32; ++ch) {
-            tmem_wait_ld32(v[ch & 1]);
-            if (ch + 1 < KT / 32) tmem_ld32(s_tm + (ch + 1) * 32, v[(ch + 1) & 1]);
-            if (kFirst && ch == 0) {
-              float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        for (int ch = 1; ch < KT / 32; ++ch) after_wait32(v[ch]);
+        if (a.scale_log2 < 0.0f) {  // the largest product is the smallest score's
 #pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const float x = __uint_as_float(v[0][i]);
-                if (!kMasked || (i >= lo && i < hi)) top[i & 3] = fmaxf(top[i & 3], x);
-              }
-              const float t = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-              mn = t == -INFINITY ? t : t * sl2;
-              ref = mn == -INFINITY ? 0.0f : -mn;
-            }
+          for (int ch = 0; ch < KT / 32; ++ch)
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              float x0 = fmaf(__uint_as_float(v[ch & 1][i]), sl2, ref);
-              float x1 = fmaf(__uint_as_float(v[ch & 1][i + 1]), sl2, ref);
-              if constexpr (kMasked) {
-                const int kk = ch * 32 + i;
-                x0 = (kk >= lo && kk < hi) ? x0 : -INFINITY;
-                x1 = (kk + 1 >= lo && kk + 1 < hi) ? x1 : -INFINITY;
-              }
-              mx[0] = fmaxf(mx[0], x0);
-              mx[1] = fmaxf(mx[1], x1);
-              const float e0 = ex2(x0), e1 = ex2(x1);
-              sum[i & 2] += e0;
-              sum[(i & 2) + 1] += e1;
-              p[ch * 16 + i / 2] = pack_bf16x2(e0, e1);
-            }
-          }
-          return fmaxf(mx[0], mx[1]);
-        };
-        // rows without a reference: in an item's first tile, or where a window
-        // hid all keys so far
-        const bool fresh = __any_sync(0xFFFFFFFFu, rvalid && m_run == -INFINITY);
-        bool again = false;  // the weights want another reference
-        if (!fresh) {
-          const float mx = open ? weights(std::false_type{}, std::false_type{})
-                                : weights(std::true_type{}, std::false_type{});
-          again = rvalid && mx > kMoveLog2;
-          if (again) mn = m_run + mx;
-        } else if (open && j == j0) {
-          const float mx = weights(std::false_type{}, std::true_type{});
-          again = rvalid && mx > kMoveLog2;
-          if (again) mn = mn + mx;
-        } else if (j == j0) {
-          const float mx = weights(std::true_type{}, std::true_type{});
-          // a key seen behind the first chunk alone: it has no reference yet
-          again = rvalid && (mn == -INFINITY ? mx != -INFINITY : mx > kMoveLog2);
-          if (again) mn = mn == -INFINITY ? mx : mn + mx;
-        } else {
-          // a later tile in which some rows see their first key: the maximum first
-          float mx = -INFINITY;
-#pragma unroll 1
-          for (int ch = 0; ch < KT / 32; ++ch) {
-            uint32_t v[32];
-            tmem_ld32(s_tm + ch * 32, v);
-            tmem_wait_ld();
+            for (int i = 0; i < 32; ++i) v[ch][i] ^= 0x80000000u;
+        }
+        if (!open) {
+#pragma unroll
+          for (int ch = 0; ch < KT / 32; ++ch)
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
               const int kk = ch * 32 + i;
-              if (kk >= lo && kk < hi) mx = fmaxf(mx, __uint_as_float(v[i]) * sl2);
+              v[ch][i] = (kk >= lo && kk < hi) ? v[ch][i] : 0xFF800000u;  // -inf
             }
-          }
-          if (mx > m_run + kMoveLog2 || m_run == -INFINITY) mn = mx;
-          again = true;
         }
-        if (__any_sync(0xFFFFFFFFu, again)) {
-          const bool none = mn == -INFINITY;  // nothing seen yet: all weights 0
-          if (none) mn = 0.0f;
-          (void)weights(std::true_type{}, std::false_type{});
-          if (none) mn = -INFINITY;
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int ch = 0; ch < KT / 32; ++ch)
+#pragma unroll
+          for (int i = 0; i < 32; i += 2)
+            top[(i >> 1) & 3] = max3(top[(i >> 1) & 3], __uint_as_float(v[ch][i]),
+                                     __uint_as_float(v[ch][i + 1]));
+        const float mx = fmaxf(max3(top[0], top[1], top[2]), top[3]);
+        float mn = m_run;
+        if (mx != -INFINITY) {  // some key seen
+          const float ms = mx * sl2;
+          if (ms > m_run + kMoveLog2 || m_run == -INFINITY) mn = ms;
         }
         const float alpha = (mn == m_run || m_run == -INFINITY) ? 1.0f : ex2(m_run - mn);
-        l_run = l_run * alpha + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
         m_run = mn;
 
         // V rows past the sequence's end belong to others: zeroed before the
@@ -683,18 +666,28 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
             tmem_st16(o_tm + h * 16, v);
           }
         }
-        // weights over this row's scores
+        // ---- weights over this row's scores, each half told of when it is there ----
+        const float ref = mn == -INFINITY ? 0.0f : -mn;
+        float2 sum[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
 #pragma unroll
-        for (int q = 0; q < KT / 32; ++q) {
+        for (int ch = 0; ch < KT / 32; ++ch) {
           uint32_t w[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) w[i] = p[q * 16 + i];
-          tmem_st16(s_tm + q * 16, w);
+          for (int i = 0; i < 16; ++i) {
+            const float2 x = fma2(v[ch][2 * i], v[ch][2 * i + 1], sl2, ref);
+            const float2 e = {ex2(x.x), ex2(x.y)};
+            sum[i & 1] = add2(sum[i & 1], e);
+            w[i] = pack_bf16x2(e.x, e.y);
+          }
+          tmem_st16(s_tm + ch * 16, w);
+          if ((ch + 1) % (KT / 64) == 0) {
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(ch + 1 == KT / 32 ? p_full(X) : p_half(X));
+          }
         }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full(X));
+        l_run = l_run * alpha + ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
       }
       if (failed) break;
       slot += 2 * ge.ntiles;

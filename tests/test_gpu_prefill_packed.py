@@ -108,6 +108,15 @@ def test_far_scores(std, d):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("scale", [0.0, -0.09, 1.5])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_any_scale(scale, d):
+    c = Case([150, 300], 4, 2, d, seed=5)
+    c.scale = scale
+    c.check(c.run())
+    c.check(c.run(window=40), window=40)
+
+
 @pytest.mark.parametrize("d", [64, 128, 256])
 def test_rising_scores(d):
     """Each key's score passes the one before: the reference moves in every tile."""
