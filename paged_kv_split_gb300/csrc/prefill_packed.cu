@@ -58,9 +58,11 @@ struct PkCfg {
   static constexpr int kDCH = D / 64;                  // 128-byte chunks of a row
   static constexpr int kQBytes = 128 * 2 * D;          // one query tile
   static constexpr int kSlotBytes = kKT * 2 * D;       // one tile of K or of V
-  static constexpr int kSlots = (224 * 1024 - kTiles * kQBytes) / kSlotBytes;
+  static constexpr int kOutBytes = kTiles * 4 * 4096;  // a warp's 32 rows x 64 outputs
+  static constexpr int kSlots = (224 * 1024 - kTiles * kQBytes - kOutBytes) / kSlotBytes;
   static constexpr int kRingOff = kTiles * kQBytes;
-  static constexpr int kBarOff = kRingOff + kSlots * kSlotBytes;
+  static constexpr int kOutOff = kRingOff + kSlots * kSlotBytes;
+  static constexpr int kBarOff = kOutOff + kOutBytes;
   // kv_full, kv_empty [slots]; q_full, q_empty; item_full, item_empty [2]; per tile
   // s_full[bufs], p_full, o_done, p_half; fin
   static constexpr int kTileBars = kBufs + 3;
@@ -104,6 +106,10 @@ __device__ __forceinline__ void after_wait32(uint32_t (&v)[32]) {
                  "+r"(v[30]), "+r"(v[31])
                :
                : "memory");
+}
+// The lowest n bits, n clamped to [0, 32].
+__device__ __forceinline__ uint32_t bits_below(int n) {
+  return n <= 0 ? 0u : (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u);
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
@@ -174,17 +180,6 @@ __device__ __forceinline__ void arrive_if(uint32_t lead, uint32_t bar) {
       "mbarrier.arrive.shared::cta.b64 st, [%0];\n\t}" ::"r"(bar),
       "r"(lead)
       : "memory");
-}
-// 16 bf16 to p, in one 32-byte store where p is so aligned.
-__device__ __forceinline__ void store16(uint16_t* p, const uint32_t (&w)[8], bool wide) {
-  if (wide) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
-                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
-  } else {
-    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-  }
 }
 // A place in a ring of N slots and the parity of its fill.
 template <int N>
@@ -602,12 +597,12 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
         }
         if (!open) {
 #pragma unroll
-          for (int ch = 0; ch < KT / 32; ++ch)
+          for (int ch = 0; ch < KT / 32; ++ch) {
+            const uint32_t keep = bits_below(hi - ch * 32) & ~bits_below(lo - ch * 32);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int kk = ch * 32 + i;
-              v[ch][i] = (kk >= lo && kk < hi) ? v[ch][i] : 0xFF800000u;  // -inf
-            }
+            for (int i = 0; i < 32; ++i)
+              v[ch][i] = (keep & (1u << i)) ? v[ch][i] : 0xFF800000u;  // -inf
+          }
         }
         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -699,27 +694,41 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
           break;
         }
         tc_fence_after();
+        // Out by way of shared memory: a lane holds a whole row, but stores that
+        // touch a line a lane take a cycle a line. 64 outputs of the warp's 32 rows
+        // at a time, 16-byte pieces swizzled; four rows a store
         uint16_t* orow = a.out + static_cast<int64_t>(it.q0 + t) * a.out_stride +
                          static_cast<int64_t>(it.g * G + mh) * D;
+        const uint32_t valid = __ballot_sync(0xFFFFFFFFu, rvalid);
         const float inv = 1.0f / fmaxf(l_run, 1e-20f);
-        // whole 32-byte sectors a store, where the rows start on them
-        const bool wide = ((reinterpret_cast<uintptr_t>(a.out) | (a.out_stride * 2)) & 31) == 0;
+        const uint32_t stage = s0 + C::kOutOff + warp * 4096;
+#pragma unroll 1
+        for (int h = 0; h < D / 64; ++h) {
+          uint32_t v[2][32];
+          tmem_ld32(o_tm + h * 64, v[0]);
+          tmem_ld32(o_tm + h * 64 + 32, v[1]);
+          tmem_wait_ld32(v[0]);
+          after_wait32(v[1]);
 #pragma unroll
-        for (int h = 0; h < D / 32; ++h) {
-          uint32_t v[32];
-          tmem_ld32(o_tm + h * 32, v);
-          tmem_wait_ld();
-          if (rvalid) {
+          for (int q = 0; q < 8; ++q) {
+            uint32_t w[4];
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              uint32_t w[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                w[i] = pack_bf16x2(__uint_as_float(v[q * 16 + 2 * i]) * inv,
-                                   __uint_as_float(v[q * 16 + 2 * i + 1]) * inv);
-              store16(orow + h * 32 + q * 16, w, wide);
-            }
+            for (int i = 0; i < 4; ++i)
+              w[i] = pack_bf16x2(__uint_as_float(v[q >> 2][(q & 3) * 8 + 2 * i]) * inv,
+                                 __uint_as_float(v[q >> 2][(q & 3) * 8 + 2 * i + 1]) * inv);
+            sts128(stage + swz128(lane * 128 + q * 16), w[0], w[1], w[2], w[3]);
           }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int row = 4 * i + (lane >> 3);
+            const uint4 w = lds128(stage + swz128(row * 128 + (lane & 7) * 16));
+            const uint64_t at = __shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(orow), row);
+            if ((valid >> row) & 1u)
+              *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(at) + h * 64 + (lane & 7) * 8) =
+                  w;
+          }
+          __syncwarp();
         }
         tc_fence_before();
       }
