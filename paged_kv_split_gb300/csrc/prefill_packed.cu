@@ -73,7 +73,7 @@ struct PkCfg {
   static constexpr int kSoftWarps = 4 * kTiles;
   static constexpr int kProdWarp = kSoftWarps;
   static constexpr int kMmaWarp = kSoftWarps + 1;
-  static constexpr int kThreads = (kSoftWarps + 2) * 32;
+  static constexpr int kThreads = (kSoftWarps + 4) * 32;  // two warps of the last four idle
   // TMEM: scores of (tile, buffer) at 128 * tile + kKT * buffer, O of tile X behind
   static constexpr int kOCol = kTiles * kBufs * kKT;
   static constexpr int kTmemCols = 512;
@@ -309,240 +309,245 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
   bool failed = false;
   const volatile int* no_abort = reinterpret_cast<const volatile int*>(holder + 2);  // stays 0
 
-  if (warp == C::kProdWarp) {
-    // ============================ copying warp ============================
-    const int span = C::kTiles * tpc;                        // tokens of an item
-    const int levels = (a.max_q_len + span - 1) / span;      // most items of a sequence
-    const bool first_cta = blockIdx.x == 0;
-    // items of sequences at levels >= p
-    auto above = [&](int p, bool tell) {
-      int c = 0;
-      for (int b = lane; b < a.num_seqs; b += 32)
-        c += max(0, (prompt_len(a, b, tell) + span - 1) / span - p);
+  // registers dealt by warpgroup (two tiles: 3 x 168 at launch, then 64 and 2 x 216)
+  if (warp >= C::kSoftWarps) {
+    if constexpr (C::kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp == C::kProdWarp) {
+      // ============================ copying warp ============================
+      const int span = C::kTiles * tpc;                        // tokens of an item
+      const int levels = (a.max_q_len + span - 1) / span;      // most items of a sequence
+      const bool first_cta = blockIdx.x == 0;
+      // items of sequences at levels >= p
+      auto above = [&](int p, bool tell) {
+        int c = 0;
+        for (int b = lane; b < a.num_seqs; b += 32)
+          c += max(0, (prompt_len(a, b, tell) + span - 1) / span - p);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xFFFFFFFFu, c, o);
-      return c;
-    };
-    const int hkv = a.num_kv_heads;
-    const int64_t total = static_cast<int64_t>(above(0, first_cta)) * hkv;
-    int slot = 0;      // ring slots filled so far
-    int k = 0;         // items so far
-    int top = levels;  // the level of the last item: ranks go up, levels down
-    for (int64_t round = 0;; ++round) {
-      const int64_t rank = round * gridDim.x +
-                           ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-      const bool end = round * static_cast<int64_t>(gridDim.x) >= total;
-      if (!end && rank >= total) continue;  // a round that does not reach this CTA
-      Item it;
-      it.g = -1;
-      if (!end) {
-        const int pr = static_cast<int>(rank / hkv);
-        // the highest level p with above(p) > pr, searched below the last one
-        int lo = 0, hi = top;  // above(lo) > pr, above(hi) <= pr or unknown at top
-        int over = 0;          // above(lo + 1)
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          const int c = above(mid, false);
-          if (c > pr) {
-            lo = mid;
-          } else {
-            hi = mid;
-            over = c;
+        for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xFFFFFFFFu, c, o);
+        return c;
+      };
+      const int hkv = a.num_kv_heads;
+      const int64_t total = static_cast<int64_t>(above(0, first_cta)) * hkv;
+      int slot = 0;      // ring slots filled so far
+      int k = 0;         // items so far
+      int top = levels;  // the level of the last item: ranks go up, levels down
+      for (int64_t round = 0;; ++round) {
+        const int64_t rank = round * gridDim.x +
+                             ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        const bool end = round * static_cast<int64_t>(gridDim.x) >= total;
+        if (!end && rank >= total) continue;  // a round that does not reach this CTA
+        Item it;
+        it.g = -1;
+        if (!end) {
+          const int pr = static_cast<int>(rank / hkv);
+          // the highest level p with above(p) > pr, searched below the last one
+          int lo = 0, hi = top;  // above(lo) > pr, above(hi) <= pr or unknown at top
+          int over = 0;          // above(lo + 1)
+          while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            const int c = above(mid, false);
+            if (c > pr) {
+              lo = mid;
+            } else {
+              hi = mid;
+              over = c;
+            }
+          }
+          if (hi == top) over = above(hi, false);
+          if (over > pr) {  // still on the last item's level
+            lo = hi;
+            over = above(lo + 1, false);
+          }
+          top = lo;
+          int idx = pr - over;  // among the sequences that have level lo, in order
+          it.g = static_cast<int>(rank % hkv);
+          it.q0 = it.n = it.tok0 = 0;
+          for (int base = 0; base < a.num_seqs; base += 32) {
+            const int b = base + lane;
+            const int n = b < a.num_seqs ? prompt_len(a, b, false) : 0;
+            const uint32_t m = __ballot_sync(0xFFFFFFFFu, (n + span - 1) / span > lo);
+            const int c = __popc(m);
+            if (idx < c) {
+              uint32_t left = m;
+              for (int i = 0; i < idx; ++i) left &= left - 1;
+              const int src = __ffs(left) - 1;
+              it.n = __shfl_sync(0xFFFFFFFFu, n, src);
+              it.q0 = __ldg(a.cu_q + base + src);
+              it.tok0 = lo * span;
+              break;
+            }
+            idx -= c;
           }
         }
-        if (hi == top) over = above(hi, false);
-        if (over > pr) {  // still on the last item's level
-          lo = hi;
-          over = above(lo + 1, false);
-        }
-        top = lo;
-        int idx = pr - over;  // among the sequences that have level lo, in order
-        it.g = static_cast<int>(rank % hkv);
-        it.q0 = it.n = it.tok0 = 0;
-        for (int base = 0; base < a.num_seqs; base += 32) {
-          const int b = base + lane;
-          const int n = b < a.num_seqs ? prompt_len(a, b, false) : 0;
-          const uint32_t m = __ballot_sync(0xFFFFFFFFu, (n + span - 1) / span > lo);
-          const int c = __popc(m);
-          if (idx < c) {
-            uint32_t left = m;
-            for (int i = 0; i < idx; ++i) left &= left - 1;
-            const int src = __ffs(left) - 1;
-            it.n = __shfl_sync(0xFFFFFFFFu, n, src);
-            it.q0 = __ldg(a.cu_q + base + src);
-            it.tok0 = lo * span;
-            break;
-          }
-          idx -= c;
-        }
-      }
-      const int is = k & 1;
-      if (k >= 2 && !warp_wait(smem_u32(item_empty + is), ((k >> 1) - 1) & 1, abort_s)) {
-        failed = true;
-        break;
-      }
-      if (lane == 0) {
-        items[is] = it;
-        mbar_arrive(smem_u32(item_full + is));
-      }
-      __syncwarp();
-      if (end) break;
-      const Geometry ge = geometry<KT, C::kTiles>(it, tpc, a.causal, W);
-      // ---- Q: tokens x G heads x 64 of head_dim ----
-      if (k >= 1 && !warp_wait(smem_u32(q_empty), (k - 1) & 1, abort_s)) {
-        failed = true;
-        break;
-      }
-      if (lane == 0) {
-        const bool has_b = C::kTiles == 2 && it.tok0 + tpc < it.n;
-        const uint32_t box = static_cast<uint32_t>(tpc) * G * 128;
-        mbar_arrive_expect_tx(smem_u32(q_full), box * C::kDCH * (has_b ? 2 : 1));
-        for (int X = 0; X < (has_b ? 2 : 1); ++X)
-#pragma unroll
-          for (int ch = 0; ch < C::kDCH; ++ch)
-            tma_load_3d(s0 + X * C::kQBytes + ch * (128 * 128), &tm_q, ch * 64, it.g * G,
-                        it.q0 + it.tok0 + X * tpc, smem_u32(q_full));
-      }
-      ++k;
-      // ---- K and V tiles, in the order the MMA thread takes them ----
-      for (int j = 0; j < 2 * ge.ntiles; ++j, ++slot) {
-        const int st = slot % C::kSlots;
-        if (slot >= C::kSlots &&
-            !warp_wait(smem_u32(kv_empty + st), ((slot / C::kSlots) - 1) & 1, abort_s)) {
+        const int is = k & 1;
+        if (k >= 2 && !warp_wait(smem_u32(item_empty + is), ((k >> 1) - 1) & 1, abort_s)) {
           failed = true;
           break;
         }
         if (lane == 0) {
-          const uint32_t fb = smem_u32(kv_full + st);
-          mbar_arrive_expect_tx(fb, C::kSlotBytes);
-          const uint32_t dst = s0 + C::kRingOff + st * C::kSlotBytes;
-#pragma unroll
-          for (int ch = 0; ch < C::kDCH; ++ch)
-            tma_load_3d(dst + ch * (KT * 128), (j & 1) ? &tm_v : &tm_k, ch * 64, it.g,
-                        it.q0 + ge.k_lo + (j >> 1) * KT, fb);
+          items[is] = it;
+          mbar_arrive(smem_u32(item_full + is));
         }
         __syncwarp();
-      }
-      if (failed) break;
-    }
-    if (failed) {
-      if (lane == 0) atomicOr(a.flags, PD_DEV_TIMEOUT);
-      *abort_s = 1;
-    }
-    // the copies already issued land before the block can exit
-    for (int t = max(0, slot - C::kSlots); t < slot; ++t)
-      (void)mbar_wait(smem_u32(kv_full + t % C::kSlots), (t / C::kSlots) & 1);
-    if (k > 0) (void)mbar_wait(smem_u32(q_full), (k - 1) & 1);
-  } else if (warp == C::kMmaWarp) {
-    // ============================= MMA warp ================================
-    // One lane issues; the whole warp runs the loop, so that descriptors stay in
-    // uniform registers and nothing is computed between two instructions
-    const uint32_t lead = elect_one();
-    constexpr uint32_t idS = umma_idesc(128, KT, 0);
-    constexpr uint32_t idO = umma_idesc(128, D, 1);
-    const uint32_t q_lo = desc_lo(s0, 16), k_lo = desc_lo(s0 + C::kRingOff, 16);
-    const uint32_t v_lo = desc_lo(s0 + C::kRingOff, KT * 128);
-    Ring<C::kSlots> kr, vr;  // the next tile of K, and of V
-    vr.next();
-    int buf = 0;                        // one query tile: the next scores' buffer
-    uint32_t p_par[2] = {0u, 0u};       // of the next weights
-    int pbuf = 0;
-    bool ok = true;
-    for (int k = 0; ok; ++k) {
-      if (!(ok = warp_wait(smem_u32(item_full + (k & 1)), (k >> 1) & 1, abort_s))) break;
-      const Item it = items[k & 1];
-      __syncwarp();
-      arrive_if(lead, smem_u32(item_empty + (k & 1)));
-      const int g = __shfl_sync(0xFFFFFFFFu, it.g, 0);
-      if (g < 0) break;
-      const Geometry ge = geometry<KT, C::kTiles>(it, tpc, a.causal, W);
-      const int nt = __shfl_sync(0xFFFFFFFFu, ge.ntiles, 0);
-      const int jA1 = __shfl_sync(0xFFFFFFFFu, ge.jA1, 0);
-      const int jB0 = __shfl_sync(0xFFFFFFFFu, ge.jB0, 0);
-      const int jB1 = __shfl_sync(0xFFFFFFFFu, ge.jB1, 0);
-      if (!(ok = warp_wait(smem_u32(q_full), k & 1, abort_s))) break;
-      auto in = [&](int X, int j) { return X ? (j >= jB0 && j < jB1) : j < jA1; };
-      auto last = [&](int X, int j) { return j == (X ? jB1 : jA1) - 1; };
-      // scores of K's next tile for query tile X
-      auto scores = [&](int X) {
-        const uint32_t b = k_lo + kr.at * (C::kSlotBytes >> 4);
-        const uint32_t d = tmem + X * 128 + (C::kBufs == 2 ? buf * KT : 0);
-        const uint32_t q = q_lo + X * (C::kQBytes >> 4);
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          mma_ss(d, q + (((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4),
-                 b + (((ks >> 2) * (KT * 128) + (ks & 3) * 32) >> 4), idS, ks > 0, lead);
-        commit_if(lead, s_full(X, C::kBufs == 2 ? buf : 0));
-      };
-      // O_X += weights V's next tile
-      auto product = [&](int X, bool first) {
-        const uint32_t b = v_lo + vr.at * (C::kSlotBytes >> 4);
-        const uint32_t p = tmem + X * 128 + (C::kBufs == 2 ? pbuf * KT : 0);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (!warp_wait(half ? p_full(X) : p_half(X), p_par[X], abort_s)) return false;
-          tc_fence_after();
-#pragma unroll
-          for (int kk = half * (KT / 32); kk < (half + 1) * (KT / 32); ++kk)
-            mma_ts(tmem + C::kOCol + X * D, p + kk * 8, b + ((kk * 2048) >> 4), idO,
-                   !first || kk > 0, lead);
+        if (end) break;
+        const Geometry ge = geometry<KT, C::kTiles>(it, tpc, a.causal, W);
+        // ---- Q: tokens x G heads x 64 of head_dim ----
+        if (k >= 1 && !warp_wait(smem_u32(q_empty), (k - 1) & 1, abort_s)) {
+          failed = true;
+          break;
         }
-        p_par[X] ^= 1u;
-        return true;
-      };
-      auto wait_k = [&]() { return warp_wait(smem_u32(kv_full + kr.at), kr.parity, abort_s); };
-      auto wait_v = [&]() { return warp_wait(smem_u32(kv_full + vr.at), vr.parity, abort_s); };
-      auto pass_k = [&](int j) {  // K's tile j handed back behind its scores
-        commit_if(lead, smem_u32(kv_empty + kr.at));
-        if (j == nt - 1) commit_if(lead, smem_u32(q_empty));
-        kr.next();
-        kr.next();
-        if constexpr (C::kBufs == 2) buf ^= 1;
-      };
-      if (!(ok = wait_k())) break;
-      tc_fence_after();
+        if (lane == 0) {
+          const bool has_b = C::kTiles == 2 && it.tok0 + tpc < it.n;
+          const uint32_t box = static_cast<uint32_t>(tpc) * G * 128;
+          mbar_arrive_expect_tx(smem_u32(q_full), box * C::kDCH * (has_b ? 2 : 1));
+          for (int X = 0; X < (has_b ? 2 : 1); ++X)
 #pragma unroll
-      for (int X = 0; X < C::kTiles; ++X)
-        if (in(X, 0)) scores(X);
-      pass_k(0);
-      for (int j = 0; j < nt; ++j) {
-        const bool more = j + 1 < nt;
-        if (C::kTiles == 1 && more) {  // two score buffers: the next scores go ahead
-          if (!(ok = wait_k())) break;
-          tc_fence_after();
-          scores(0);
-          pass_k(j + 1);
+            for (int ch = 0; ch < C::kDCH; ++ch)
+              tma_load_3d(s0 + X * C::kQBytes + ch * (128 * 128), &tm_q, ch * 64, it.g * G,
+                          it.q0 + it.tok0 + X * tpc, smem_u32(q_full));
         }
-        if (!(ok = wait_v())) break;
-        if (C::kTiles == 2 && more && !(ok = wait_k())) break;
-#pragma unroll
-        for (int X = 0; X < C::kTiles; ++X) {
-          if (in(X, j)) {
-            if (!(ok = product(X, X == 1 ? j == jB0 : j == 0))) break;
-            // two score buffers: each tile's weights wait for it; one: the scores
-            // that follow tell of it, but behind the last
-            if (C::kBufs == 2 || last(X, j)) commit_if(lead, o_done(X));
+        ++k;
+        // ---- K and V tiles, in the order the MMA thread takes them ----
+        for (int j = 0; j < 2 * ge.ntiles; ++j, ++slot) {
+          const int st = slot % C::kSlots;
+          if (slot >= C::kSlots &&
+              !warp_wait(smem_u32(kv_empty + st), ((slot / C::kSlots) - 1) & 1, abort_s)) {
+            failed = true;
+            break;
           }
-          // one buffer: the next scores go over these weights, behind the product
-          // that reads them in the tensor core's order
-          if (C::kTiles == 2 && more && in(X, j + 1)) scores(X);
+          if (lane == 0) {
+            const uint32_t fb = smem_u32(kv_full + st);
+            mbar_arrive_expect_tx(fb, C::kSlotBytes);
+            const uint32_t dst = s0 + C::kRingOff + st * C::kSlotBytes;
+#pragma unroll
+            for (int ch = 0; ch < C::kDCH; ++ch)
+              tma_load_3d(dst + ch * (KT * 128), (j & 1) ? &tm_v : &tm_k, ch * 64, it.g,
+                          it.q0 + ge.k_lo + (j >> 1) * KT, fb);
+          }
+          __syncwarp();
         }
-        if (!ok) break;
-        commit_if(lead, smem_u32(kv_empty + vr.at));
-        vr.next();
-        vr.next();
-        if constexpr (C::kBufs == 2) pbuf ^= 1;
-        if (C::kTiles == 2 && more) pass_k(j + 1);
+        if (failed) break;
       }
+      if (failed) {
+        if (lane == 0) atomicOr(a.flags, PD_DEV_TIMEOUT);
+        *abort_s = 1;
+      }
+      // the copies already issued land before the block can exit
+      for (int t = max(0, slot - C::kSlots); t < slot; ++t)
+        (void)mbar_wait(smem_u32(kv_full + t % C::kSlots), (t / C::kSlots) & 1);
+      if (k > 0) (void)mbar_wait(smem_u32(q_full), (k - 1) & 1);
+    } else if (warp == C::kMmaWarp) {
+      // ============================= MMA warp ================================
+      // One lane issues; the whole warp runs the loop, so that descriptors stay in
+      // uniform registers and nothing is computed between two instructions
+      const uint32_t lead = elect_one();
+      constexpr uint32_t idS = umma_idesc(128, KT, 0);
+      constexpr uint32_t idO = umma_idesc(128, D, 1);
+      const uint32_t q_lo = desc_lo(s0, 16), k_lo = desc_lo(s0 + C::kRingOff, 16);
+      const uint32_t v_lo = desc_lo(s0 + C::kRingOff, KT * 128);
+      Ring<C::kSlots> kr, vr;  // the next tile of K, and of V
+      vr.next();
+      int buf = 0;                        // one query tile: the next scores' buffer
+      uint32_t p_par[2] = {0u, 0u};       // of the next weights
+      int pbuf = 0;
+      bool ok = true;
+      for (int k = 0; ok; ++k) {
+        if (!(ok = warp_wait(smem_u32(item_full + (k & 1)), (k >> 1) & 1, abort_s))) break;
+        const Item it = items[k & 1];
+        __syncwarp();
+        arrive_if(lead, smem_u32(item_empty + (k & 1)));
+        const int g = __shfl_sync(0xFFFFFFFFu, it.g, 0);
+        if (g < 0) break;
+        const Geometry ge = geometry<KT, C::kTiles>(it, tpc, a.causal, W);
+        const int nt = __shfl_sync(0xFFFFFFFFu, ge.ntiles, 0);
+        const int jA1 = __shfl_sync(0xFFFFFFFFu, ge.jA1, 0);
+        const int jB0 = __shfl_sync(0xFFFFFFFFu, ge.jB0, 0);
+        const int jB1 = __shfl_sync(0xFFFFFFFFu, ge.jB1, 0);
+        if (!(ok = warp_wait(smem_u32(q_full), k & 1, abort_s))) break;
+        auto in = [&](int X, int j) { return X ? (j >= jB0 && j < jB1) : j < jA1; };
+        auto last = [&](int X, int j) { return j == (X ? jB1 : jA1) - 1; };
+        // scores of K's next tile for query tile X
+        auto scores = [&](int X) {
+          const uint32_t b = k_lo + kr.at * (C::kSlotBytes >> 4);
+          const uint32_t d = tmem + X * 128 + (C::kBufs == 2 ? buf * KT : 0);
+          const uint32_t q = q_lo + X * (C::kQBytes >> 4);
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks)
+            mma_ss(d, q + (((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4),
+                   b + (((ks >> 2) * (KT * 128) + (ks & 3) * 32) >> 4), idS, ks > 0, lead);
+          commit_if(lead, s_full(X, C::kBufs == 2 ? buf : 0));
+        };
+        // O_X += weights V's next tile
+        auto product = [&](int X, bool first) {
+          const uint32_t b = v_lo + vr.at * (C::kSlotBytes >> 4);
+          const uint32_t p = tmem + X * 128 + (C::kBufs == 2 ? pbuf * KT : 0);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            if (!warp_wait(half ? p_full(X) : p_half(X), p_par[X], abort_s)) return false;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = half * (KT / 32); kk < (half + 1) * (KT / 32); ++kk)
+              mma_ts(tmem + C::kOCol + X * D, p + kk * 8, b + ((kk * 2048) >> 4), idO,
+                     !first || kk > 0, lead);
+          }
+          p_par[X] ^= 1u;
+          return true;
+        };
+        auto wait_k = [&]() { return warp_wait(smem_u32(kv_full + kr.at), kr.parity, abort_s); };
+        auto wait_v = [&]() { return warp_wait(smem_u32(kv_full + vr.at), vr.parity, abort_s); };
+        auto pass_k = [&](int j) {  // K's tile j handed back behind its scores
+          commit_if(lead, smem_u32(kv_empty + kr.at));
+          if (j == nt - 1) commit_if(lead, smem_u32(q_empty));
+          kr.next();
+          kr.next();
+          if constexpr (C::kBufs == 2) buf ^= 1;
+        };
+        if (!(ok = wait_k())) break;
+        tc_fence_after();
+#pragma unroll
+        for (int X = 0; X < C::kTiles; ++X)
+          if (in(X, 0)) scores(X);
+        pass_k(0);
+        for (int j = 0; j < nt; ++j) {
+          const bool more = j + 1 < nt;
+          if (C::kTiles == 1 && more) {  // two score buffers: the next scores go ahead
+            if (!(ok = wait_k())) break;
+            tc_fence_after();
+            scores(0);
+            pass_k(j + 1);
+          }
+          if (!(ok = wait_v())) break;
+          if (C::kTiles == 2 && more && !(ok = wait_k())) break;
+#pragma unroll
+          for (int X = 0; X < C::kTiles; ++X) {
+            if (in(X, j)) {
+              if (!(ok = product(X, X == 1 ? j == jB0 : j == 0))) break;
+              // two score buffers: each tile's weights wait for it; one: the scores
+              // that follow tell of it, but behind the last
+              if (C::kBufs == 2 || last(X, j)) commit_if(lead, o_done(X));
+            }
+            // one buffer: the next scores go over these weights, behind the product
+            // that reads them in the tensor core's order
+            if (C::kTiles == 2 && more && in(X, j + 1)) scores(X);
+          }
+          if (!ok) break;
+          commit_if(lead, smem_u32(kv_empty + vr.at));
+          vr.next();
+          vr.next();
+          if constexpr (C::kBufs == 2) pbuf ^= 1;
+          if (C::kTiles == 2 && more) pass_k(j + 1);
+        }
+      }
+      if (!ok) {
+        if (lane == 0) atomicOr(a.flags, PD_DEV_TIMEOUT);
+        *abort_s = 1;
+      }
+      // every MMA issued has completed before TMEM is freed
+      commit_if(lead, smem_u32(fin_bar));
+      (void)warp_wait(smem_u32(fin_bar), 0, no_abort);
     }
-    if (!ok) {
-      if (lane == 0) atomicOr(a.flags, PD_DEV_TIMEOUT);
-      *abort_s = 1;
-    }
-    // every MMA issued has completed before TMEM is freed
-    commit_if(lead, smem_u32(fin_bar));
-    (void)warp_wait(smem_u32(fin_bar), 0, no_abort);
   } else {
+    if constexpr (C::kTiles == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     // =========================== softmax warps ============================
     const int X = warp >> 2;
     const int m = (warp & 3) * 32 + lane;  // row of the query tile: token m / G, head m % G
