@@ -11,12 +11,14 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib
 import os
 import warnings
 
 import torch
 
-from .build import LIB as _LIB_PATH, MARSHAL as _MARSHAL_PATH, marshal_fits
+from .build import (LIB as _LIB_PATH, MARSHAL as _MARSHAL_PATH, SERVE as _SERVE_PATH,
+                    marshal_fits, serve_fits)
 
 if not os.path.exists(_LIB_PATH):
     raise ImportError(f"{_LIB_PATH} is not built; run `python -m paged_kv_split_gb300.build` "
@@ -25,23 +27,23 @@ if not os.path.exists(_LIB_PATH):
 _lib = ctypes.CDLL(_LIB_PATH)
 
 
-def _load_marshal():
-    """The draft-and-verify calls without ctypes, for the arguments they usually
+def _load_marshal(name, path, fits):
+    """A module that makes calls without ctypes, for the arguments they usually
     get: a status, or None for others, which the Python below then takes or
     refuses. None where it was not built for this Python and torch: then the
     Python below takes all calls, some 10 us slower each."""
     why = "it was not built for this Python and torch"
-    if marshal_fits():
+    if fits():
         try:
-            from . import _marshal
-            return _marshal
+            return importlib.import_module("." + name, __package__)
         except ImportError as e:
             why = str(e)
-    warnings.warn(f"{_MARSHAL_PATH} is not used, calls take longer without it: {why}")
+    warnings.warn(f"{path} is not used, calls take longer without it: {why}")
     return None
 
 
-_marshal = _load_marshal()
+_marshal = _load_marshal("_marshal", _MARSHAL_PATH, marshal_fits)  # draft and verify
+_serve = _load_marshal("_marshal_serve", _SERVE_PATH, serve_fits)  # decode, append, packed prompts
 
 PD_OK = 0
 PD_KV_BF16, PD_KV_FP8_E4M3, PD_KV_NVFP4, PD_KV_INT8 = 0, 1, 2, 3
@@ -374,6 +376,13 @@ def pd_decode(q, k_cache, v_cache, block_tables, seq_lens, out, *, num_kv_heads,
             S = pd_choose_num_splits(B, num_kv_heads, mbs, block_size, sliding_window, d, code,
                                      q.device.index)
         workspace = _scratch(pd_decode_workspace_bytes(B, hq, d, S), q.device, stream)
+    if not crosscheck and _serve is not None and q.is_cuda:
+        rc = _serve.decode(q, k_cache, v_cache, block_tables, seq_lens, out, num_kv_heads,
+                           block_size, num_blocks, scale, S, sliding_window, code, k_scale,
+                           v_scale, workspace, _stream(stream))
+        if rc is not None:
+            _check("pd_decode", rc)
+            return out
     dev = q.device
     fn = "pd_decode_crosscheck" if crosscheck else "pd_decode"
     rc = getattr(_lib, fn)(
@@ -512,6 +521,14 @@ def pd_decode_balanced(q, k_cache, v_cache, block_tables, plan_dev, plan, out, *
     dev = q.device
     if workspace is None:
         workspace = _scratch(plan.workspace_bytes, dev, stream)
+    if _fn == "pd_decode_balanced" and _serve is not None and q.is_cuda:
+        rc = _serve.decode_balanced(q, k_cache, v_cache, block_tables, plan_dev, out, num_kv_heads,
+                                    block_size, num_blocks, scale, sliding_window,
+                                    _dtype_code(kv_dtype), k_scale, v_scale, plan.num_ctas,
+                                    plan.num_pieces, workspace, _stream(stream))
+        if rc is not None:
+            _check(_fn, rc)
+            return out
     rc = getattr(_lib, _fn)(
         _dev(q, "q", torch.bfloat16, dev), _dev(k_cache, "k_cache", None, dev),
         _dev(v_cache, "v_cache", None, dev), _dev(block_tables, "block_tables", torch.int32, dev),
@@ -989,6 +1006,13 @@ def pd_rope_append_int8(qkv, q_out, k_cache, v_cache, block_tables, seq_lens, cu
     wider rows. seq_lens: int32 [B] cached rows, the new ones included; max_q_len:
     host int, the most new tokens of a sequence. positions: int32 [T], or None for
     the rows in the cache. cos_sin: float32 [max_position, rot_dim]."""
+    if _serve is not None and qkv.is_cuda:
+        rc = _serve.rope_append(qkv, q_out, 0, 0, k_cache, v_cache, block_tables, seq_lens, cu_q,
+                                cos_sin, max_q_len, num_kv_heads, block_size, num_blocks, positions,
+                                k_out, interleaved, _stream(stream))
+        if rc is not None:
+            _check("pd_rope_append_int8", rc)
+            return q_out
     if q_out.dim() != 3 or qkv.dim() != 2 or q_out.shape[0] != qkv.shape[0]:
         raise ValueError("qkv must be bf16 [num_tokens, row], q_out [num_tokens, num_q_heads, "
                          "head_dim]")
@@ -1013,6 +1037,13 @@ def pd_rope_append_int8_(qkv, k_cache, v_cache, block_tables, seq_lens, cu_q, co
                          positions=None, interleaved=False, stream=None):
     """pd_rope_append_int8 in place: the q and k heads of the fused rows are
     replaced by their rotated form, ready for pd_prefill_packed."""
+    if _serve is not None and qkv.is_cuda:
+        rc = _serve.rope_append(qkv, None, num_q_heads, head_dim, k_cache, v_cache, block_tables,
+                                seq_lens, cu_q, cos_sin, max_q_len, num_kv_heads, block_size,
+                                num_blocks, positions, None, interleaved, _stream(stream))
+        if rc is not None:
+            _check("pd_rope_append_int8", rc)
+            return qkv
     if qkv.dim() != 2 or qkv.shape[1] < (num_q_heads + 2 * num_kv_heads) * head_dim:
         raise ValueError("qkv must be bf16 [num_tokens, row], a row its q, k and v heads")
     row = qkv.shape[1]
@@ -1031,6 +1062,12 @@ def pd_prefill_packed(q, k, v, cu_q, out, *, max_q_len, scale, causal=True, slid
     a part of wider rows (views of fused QKV rows). cu_q: int32 [B + 1] row
     offsets; max_q_len: host int, the longest prompt.
     crosscheck: call pd_prefill_packed_crosscheck (CUDA cores)."""
+    if not crosscheck and _serve is not None and q.is_cuda:
+        rc = _serve.prefill_packed(q, k, v, cu_q, out, max_q_len, scale, causal, sliding_window,
+                                   _stream(stream))
+        if rc is not None:
+            _check("pd_prefill_packed", rc)
+            return out
     if q.dim() != 3 or k.dim() != 3 or out.shape != q.shape or v.shape != k.shape:
         raise ValueError("q and out must be bf16 [total_q, num_q_heads, head_dim], k and v "
                          "[total_q, num_kv_heads, head_dim]")

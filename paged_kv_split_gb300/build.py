@@ -4,10 +4,11 @@ Each .cu under csrc/ compiles to an object in parallel; the objects link into
 paged_kv_split_gb300/libpd.so against the shared CUDA runtime. A rebuild
 happens only when a source or header is newer than the library.
 
-csrc/marshal.cpp becomes the Python module _marshal.so beside it, against the
-headers of torch and Python. The binding works without it, its calls take some
-10 us longer: where it cannot be built there is a warning, and one built for
-another Python or torch is rebuilt, and not loaded before that.
+csrc/marshal.cpp and csrc/marshal_serve.cpp become the Python modules _marshal.so
+and _marshal_serve.so beside it, against the headers of torch and Python. The
+binding works without them, its calls take some 10 us longer: where one cannot be
+built there is a warning, and one built for another Python or torch is rebuilt,
+and not loaded before that.
 
     python -m paged_kv_split_gb300.build [--force] [--verbose-ptxas]
 """
@@ -22,6 +23,7 @@ import subprocess
 import sys
 import sysconfig
 import warnings
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -32,6 +34,9 @@ LIB = os.path.join(PKG, "libpd.so")
 MARSHAL_SRC = os.path.join(CSRC, "marshal.cpp")
 MARSHAL = os.path.join(PKG, "_marshal.so")
 MARSHAL_ABI = os.path.join(BUILD_DIR, "marshal.abi")  # what _marshal.so was built for
+SERVE_SRC = os.path.join(CSRC, "marshal_serve.cpp")
+SERVE = os.path.join(PKG, "_marshal_serve.so")
+SERVE_ABI = os.path.join(BUILD_DIR, "marshal_serve.abi")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = [
@@ -82,13 +87,22 @@ def marshal_abi() -> str:
     return f"{sysconfig.get_config_var('SOABI')} torch {torch}"
 
 
-def marshal_fits() -> bool:
-    """_marshal.so is there, for this Python and this torch."""
+def _fits(lib, mark) -> bool:
     try:
-        with open(MARSHAL_ABI) as f:
-            return os.path.exists(MARSHAL) and f.read() == marshal_abi()
+        with open(mark) as f:
+            return os.path.exists(lib) and f.read() == marshal_abi()
     except (OSError, AttributeError):
         return False
+
+
+def marshal_fits() -> bool:
+    """_marshal.so is there, for this Python and this torch."""
+    return _fits(MARSHAL, MARSHAL_ABI)
+
+
+def serve_fits() -> bool:
+    """The same of _marshal_serve.so."""
+    return _fits(SERVE, SERVE_ABI)
 
 
 def _older(path, inputs) -> bool:
@@ -100,16 +114,24 @@ def is_stale() -> bool:
     return _older(LIB, _inputs())
 
 
+def _module_inputs(src):
+    return [src, os.path.abspath(__file__)] + glob.glob(os.path.join(INCLUDE, "*.h")) + \
+        glob.glob(os.path.join(CSRC, "*.h"))
+
+
 def marshal_is_stale() -> bool:
-    return not marshal_fits() or _older(MARSHAL, [MARSHAL_SRC, os.path.abspath(__file__)] +
-                                        glob.glob(os.path.join(INCLUDE, "*.h")))
+    return not marshal_fits() or _older(MARSHAL, _module_inputs(MARSHAL_SRC))
 
 
-def _build_marshal() -> bool:
-    """Build _marshal.so; without it, a warning and False."""
-    tmp = MARSHAL + f".tmp{os.getpid()}"
+def serve_is_stale() -> bool:
+    return not serve_fits() or _older(SERVE, _module_inputs(SERVE_SRC))
+
+
+def _build_module(src, lib, mark) -> bool:
+    """Build one module; without it, a warning and False."""
+    tmp = lib + f".tmp{os.getpid()}"
     try:
-        cmd = ["g++", *marshal_cflags(), "-shared", "-o", tmp, MARSHAL_SRC, "-L", PKG,
+        cmd = ["g++", *marshal_cflags(), "-shared", "-o", tmp, src, "-L", PKG,
                "-l:libpd.so", *marshal_ldflags(), "-Wl,-rpath,$ORIGIN"]
         r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
         why = r.stdout.decode(errors="replace") if r.returncode else None
@@ -119,14 +141,22 @@ def _build_marshal() -> bool:
     if why is not None:
         if os.path.exists(tmp):
             os.remove(tmp)
-        warnings.warn(f"{MARSHAL} was not built; calls take longer without it:\n{why}")
+        warnings.warn(f"{lib} was not built; calls take longer without it:\n{why}")
         return False
-    if os.path.exists(MARSHAL_ABI):
-        os.remove(MARSHAL_ABI)  # never a module beside another one's mark
-    os.replace(tmp, MARSHAL)
-    with open(MARSHAL_ABI, "w") as f:
+    if os.path.exists(mark):
+        os.remove(mark)  # never a module beside another one's mark
+    os.replace(tmp, lib)
+    with open(mark, "w") as f:
         f.write(abi)
     return True
+
+
+def _build_modules(force: bool) -> None:
+    """Build the stale ones, side by side."""
+    stale = [m for m, old in (((MARSHAL_SRC, MARSHAL, MARSHAL_ABI), marshal_is_stale()),
+                              ((SERVE_SRC, SERVE, SERVE_ABI), serve_is_stale())) if force or old]
+    with ThreadPoolExecutor(2) as pool:
+        list(pool.map(lambda m: _build_module(*m), stale))
 
 
 def _build_lib(verbose_ptxas: bool, quiet: bool) -> None:
@@ -161,9 +191,8 @@ def _build_lib(verbose_ptxas: bool, quiet: bool) -> None:
 def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = True) -> str:
     if force or is_stale():
         _build_lib(verbose_ptxas, quiet)
-    if force or marshal_is_stale():
-        os.makedirs(BUILD_DIR, exist_ok=True)
-        _build_marshal()
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    _build_modules(force)
     return LIB
 
 
