@@ -19,10 +19,13 @@
 // table entries at a time, and leave them in the stage's record. The CTA's work
 // is one (sequence, kv head, split), or the pieces of a balanced plan.
 //
-// head_dim 64 / 128: each warp has 16 of the stage's 64 keys and its own softmax
-// state, merged at the end of a piece through the stage of its last tile.
-// head_dim 256 / 512: the warps share head_dim and sum their scores through
-// shared memory per 16-key tile.
+// head_dim 64 / 128: warps 0 and 1 take 32 keys each of the even 64-key stages, 2
+// and 3 of the odd ones, each with its own softmax state, merged at the end of a
+// piece through the stage of its last tile. head_dim 256 / 512: the warps share
+// head_dim and sum their scores through shared memory per 32-key stage. Integer
+// operations bound it (their pipe takes half an instruction a cycle), so whatever
+// is not widening is kept small: 32 keys an update, ring places counted up, a
+// maximum sought over the lanes only when one moves.
 //
 // Waits are bounded (2 s): a warp that gives up raises the CTA's abort word and
 // PD_DEV_TIMEOUT; the copying warp then issues nothing more and waits for what
@@ -45,21 +48,20 @@ namespace {
 
 using namespace ::pd::mma;
 
-constexpr uint32_t kMetaLast = 1u;    // last tile of a piece
-constexpr uint32_t kMetaDirect = 2u;  // the piece is all of its (sequence, head): write out
-constexpr uint32_t kMetaEnd = 4u;     // no more pieces
-constexpr int kMaxCopies = 4;         // copies of a stage: 64 keys of 16-row pages
+constexpr int kMaxCopies = 4;  // copies of a stage and cache: 64 keys of 16-row pages
 
-// What the copying warp says of a stage, before it arms the stage's barrier.
-struct StageMeta {
-  int b, g;             // sequence and kv head
-  int t0;               // key index of the tile's first row
-  int t_begin, t_end;   // the piece's key range
-  uint32_t bad;         // bit j: copy j's page was outside the pool
-  uint32_t flags;       // kMeta* bits; bits 8..: the piece's q slot
+// A piece of work, as the copying warp leaves it with the piece's q rows.
+struct Piece {
+  int b, g;              // sequence and kv head
+  int t_base;            // key index of the first tile's first row
+  int t_begin, t_end;    // the keys that count
+  int ntiles;            // 0: no more pieces
+  int direct;            // all of its (sequence, head): write the output
   int pad;
-  int64_t ws_row;       // the piece's first row in the workspace
-  float scales[3 * kMaxCopies];
+  int64_t ws_row;        // its first row in the workspace
+};
+struct StageScales {
+  I8Scales copy[kMaxCopies];
 };
 
 template <int D, int NT, int BS>
@@ -68,9 +70,11 @@ struct I8Cfg {
   static constexpr int kDSplit = D <= 128 ? 1 : 4;       // warps sharing head_dim
   static constexpr int kDS = D / kDSplit;                // head_dim of a warp
   static constexpr int kKSteps = kDS / 16;
-  static constexpr int kWM = 1;
-  static constexpr int kKT = kDSplit == 1 ? 64 : 16;     // keys per stage
-  static constexpr int kMT = kKT / 16;
+  static constexpr int kU = 2;                           // 16-key m-tiles of a warp per stage
+  // head_dim <= 128: 64-key stages, warps 0 / 1 take the even ones' halves, 2 / 3 the
+  // odd ones'. Else all warps take all of a 32-key stage
+  static constexpr int kKT = kDSplit == 1 ? 64 : 32;
+  static constexpr int kOwners = kDSplit == 1 ? 2 : 4;   // warps that work on a stage
   static constexpr int kBR = kKT < BS ? kKT : BS;        // rows per copy
   static constexpr int kNCopy = kKT / kBR;
   static constexpr int kCRB = D < 128 ? D : 128;         // bytes of a row chunk
@@ -78,25 +82,27 @@ struct I8Cfg {
   static constexpr bool kSwizzle = kCRB == 128;
   static constexpr int kCacheStageBytes = kKT * D;
   static constexpr int kStageBytes = 2 * kCacheStageBytes;
-  // as the FP8 form: three 16 KB stages and four CTAs an SM at head_dim 128
-  static constexpr int kRing = kDSplit == 1 ? 48 * 1024 : (D == 256 ? 64 * 1024 : 96 * 1024);
+  static constexpr int kRing = D == 64 ? 48 * 1024 : (D <= 256 ? 64 * 1024 : 96 * 1024);
   static constexpr int kStages = kRing / kStageBytes > 8 ? 8 : kRing / kStageBytes;
   static constexpr int kRingBytes = kStages * kStageBytes;
-  static constexpr int kRedBytes = kDSplit == 4 ? 2 * 4 * kMT * 32 * 4 * NT * 4 : 0;
+  static constexpr int kRedBytes = kDSplit == 4 ? 2 * 4 * kU * 32 * 4 * NT * 4 : 0;
   static constexpr int kQMaxBytes = kDSplit == 4 ? NT * 4 * 8 * 4 : 0;
   static constexpr int kHW = 8 * NT;
   static constexpr int kMergeBytes = kDSplit == 1 ? 2 * 2 * 4 * kHW * 4 : 0;  // m, l by parity
   static constexpr int kQSlots = kDSplit == 1 ? 2 : 1;
   static constexpr int kMergeOffset = kRingBytes + kRedBytes + kQMaxBytes;
-  static constexpr int kMetaOffset = (kMergeOffset + kMergeBytes + 15) / 16 * 16;
-  static constexpr int kBarOffset = kMetaOffset + kStages * static_cast<int>(sizeof(StageMeta));
-  static constexpr int kNumBars = 2 * kStages + kQSlots + 1;
+  static constexpr int kScaleOffset = (kMergeOffset + kMergeBytes + 15) / 16 * 16;
+  static constexpr int kPieceOffset = kScaleOffset + kStages * static_cast<int>(sizeof(StageScales));
+  static constexpr int kBarOffset = kPieceOffset + kQSlots * static_cast<int>(sizeof(Piece));
+  static constexpr int kNumBars = 2 * kStages + 2 * kQSlots + 1;
   static constexpr int kAbortOffset = kBarOffset + kNumBars * 8;
   static constexpr int kQOffset = (kAbortOffset + 16 + 127) / 128 * 128;
   static constexpr uint32_t kCopyBytes = kBR * D;
-  static_assert(kNCopy <= kMaxCopies, "the record holds the scales of four copies");
+  static_assert(kNCopy <= kMaxCopies, "a stage's record holds the scales of four copies");
   static_assert(kDSplit == 4 || 4 * 8 * D * 4 <= kStageBytes, "eight heads' merge fits a stage");
-  static_assert(sizeof(StageMeta) % 8 == 0, "the barriers behind the records are 8-byte aligned");
+  // a stage always belongs to the same warps: they see every phase of its barriers
+  static_assert(kDSplit == 4 || kStages % 2 == 0, "even and odd tiles keep to their stages");
+  static_assert(sizeof(Piece) % 8 == 0, "the barriers behind the records are 8-byte aligned");
   static constexpr int smem_bytes(int G) { return kQOffset + kQSlots * G * D * 2 + 1024; }
 };
 
@@ -135,10 +141,12 @@ __global__ void __launch_bounds__(kMmaThreads,
   float* qmax_s = reinterpret_cast<float*>(smem + C::kRingBytes + C::kRedBytes);
   float* mrec = reinterpret_cast<float*>(smem + C::kMergeOffset);  // [2][4][kHW]
   float* lrec = mrec + 2 * 4 * C::kHW;
-  StageMeta* meta = reinterpret_cast<StageMeta*>(smem + C::kMetaOffset);
+  StageScales* scales = reinterpret_cast<StageScales*>(smem + C::kScaleOffset);
+  Piece* pieces = reinterpret_cast<Piece*>(smem + C::kPieceOffset);
   uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + C::kBarOffset);
   uint64_t* empty_bar = full_bar + C::kStages;
-  uint64_t* qempty_bar = empty_bar + C::kStages;
+  uint64_t* qfull_bar = empty_bar + C::kStages;
+  uint64_t* qempty_bar = qfull_bar + C::kQSlots;
   uint64_t* cons_bar = qempty_bar + C::kQSlots;
   volatile int* abort_s = reinterpret_cast<volatile int*>(smem + C::kAbortOffset);
   unsigned char* qslots = smem + C::kQOffset;
@@ -146,9 +154,12 @@ __global__ void __launch_bounds__(kMmaThreads,
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(smem_u32(&full_bar[i]), 1);
-      mbar_init(smem_u32(&empty_bar[i]), kConsumerWarps);
+      mbar_init(smem_u32(&empty_bar[i]), C::kOwners);
     }
-    for (int i = 0; i < C::kQSlots; ++i) mbar_init(smem_u32(&qempty_bar[i]), kConsumerWarps);
+    for (int i = 0; i < C::kQSlots; ++i) {
+      mbar_init(smem_u32(&qfull_bar[i]), 1);
+      mbar_init(smem_u32(&qempty_bar[i]), kConsumerWarps);
+    }
     mbar_init(smem_u32(cons_bar), kConsumerWarps);
     *abort_s = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -205,9 +216,28 @@ __global__ void __launch_bounds__(kMmaThreads,
     if constexpr (PLAN) {
       if (p_begin + lane < p_end) my_desc = a.plan_pieces[p_begin + lane];
     }
-    int i = 0;  // tiles issued
-    int k = 0;  // pieces started
+    int i = 0;   // tiles issued
+    int st = 0;  // the next one's stage, and the parity of its fill
+    uint32_t parity = 0;
+    int k = 0;   // pieces started
     bool ok = true;
+    // piece k's record and q rows into its slot
+    auto start = [&](int kk, const Piece& pc) {
+      const int slot = kk % C::kQSlots;
+      if (kk >= C::kQSlots &&
+          !warp_wait(smem_u32(&qempty_bar[slot]), ((kk / C::kQSlots) - 1) & 1, abort_s))
+        return false;
+      if (lane == 0) {
+        const uint32_t qb = smem_u32(&qfull_bar[slot]);
+        pieces[slot] = pc;
+        mbar_arrive_expect_tx(qb, pc.ntiles ? q_bytes : 0u);
+        if (pc.ntiles)
+          bulk_load(smem_u32(qslots + slot * q_bytes),
+                    a.q + static_cast<int64_t>(pc.b) * a.q_stride + pc.g * G * D, q_bytes, qb);
+      }
+      __syncwarp();
+      return true;
+    };
     for (int piece = p_begin; piece < p_end && ok; ++piece) {
       int4 d = split;
       if constexpr (PLAN) {
@@ -248,100 +278,57 @@ __global__ void __launch_bounds__(kMmaThreads,
       refill(first_page);
       const int t_base = first_page * BS;
       const int ntiles = (t_end - t_base + C::kKT - 1) / C::kKT;
-      const int qslot = k % C::kQSlots;
-      if (k >= C::kQSlots &&
-          !warp_wait(smem_u32(&qempty_bar[qslot]), ((k / C::kQSlots) - 1) & 1, abort_s)) {
+      if (!start(k, Piece{b, g, t_base, t_begin, t_end, ntiles, d.w & 1, 0, ws_row})) {
         ok = false;
         break;
       }
-      const uint32_t piece_flags =
-          ((d.w & 1) ? kMetaDirect : 0u) | (static_cast<uint32_t>(qslot) << 8);
-      for (int j = 0; j < ntiles; ++j, ++i) {
-        const int st = i % C::kStages;
-        if (i >= C::kStages &&
-            !warp_wait(smem_u32(&empty_bar[st]), ((i / C::kStages) - 1) & 1, abort_s)) {
+      ++k;
+      for (int j = 0; j < ntiles; ++j) {
+        if (i >= C::kStages && !warp_wait(smem_u32(&empty_bar[st]), parity ^ 1u, abort_s)) {
           ok = false;
           break;
         }
+        // lane jj < kNCopy makes copy jj of K and of V
         const int t0 = t_base + j * C::kKT;
-        uint32_t bad = 0, bytes = 0;
-        int my_page = -1;                 // lane jj < kNCopy: copy jj's page and scales
-        float ks = 0.0f, vs = 1.0f;
-#pragma unroll
-        for (int jj = 0; jj < C::kNCopy; ++jj) {
-          const int tt = t0 + jj * C::kBR;
-          if (tt < t_end) {
-            const int pidx = tt / BS;
-            if (pidx - cached_base >= 32) refill(pidx);  // warp-uniform
-            const int src = pidx - cached_base;
-            const int pg = __shfl_sync(0xFFFFFFFFu, my_entry, src);
-            const float kk = __shfl_sync(0xFFFFFFFFu, my_ks, src);
-            const float vv = __shfl_sync(0xFFFFFFFFu, my_vs, src);
-            if (pg >= 0 && pg < a.num_blocks) {
-              bytes += 2u * C::kCopyBytes;
-              if (lane == jj) {
-                my_page = pg;
-                ks = kk;
-                vs = vv;
-              }
-            } else {
-              bad |= 1u << jj;
-            }
-          }
-        }
-        if (j == 0) bytes += q_bytes;
+        const int last_page = (min(t0 + C::kKT, t_end) - 1) / BS;
+        if (last_page - cached_base >= 32) refill(t0 / BS);  // warp-uniform
+        const int tt = t0 + lane * C::kBR;
+        const bool mine = lane < C::kNCopy && tt < t_end;
+        const int src = mine ? tt / BS - cached_base : 0;
+        const int page = __shfl_sync(0xFFFFFFFFu, my_entry, src);
+        const float ks = __shfl_sync(0xFFFFFFFFu, my_ks, src);
+        const float vs = __shfl_sync(0xFFFFFFFFu, my_vs, src);
+        const bool copies = mine && page >= 0 && page < a.num_blocks;
         const uint32_t fb = smem_u32(&full_bar[st]);
-        StageMeta& m = meta[st];
-        if (lane < C::kNCopy) {
-          m.scales[lane] = ks;
-          m.scales[C::kNCopy + lane] = __log2f(vs);
-          m.scales[2 * C::kNCopy + lane] = __fdividef(1.0f, vs);
-        }
+        const uint32_t n = __popc(__ballot_sync(0xFFFFFFFFu, copies));
+        if (lane < C::kNCopy)
+          scales[st].copy[lane] = copies ? I8Scales{ks, __log2f(vs), __fdividef(1.0f, vs), 0.0f}
+                                         : I8Scales{0.0f, -INFINITY, 0.0f, 0.0f};
+        if (mine && !copies) atomicOr(a.flags, PD_DEV_BAD_PAGE);
         __syncwarp();
-        if (lane == 0) {
-          if (bad) atomicOr(a.flags, PD_DEV_BAD_PAGE);
-          m.b = b;
-          m.g = g;
-          m.t0 = t0;
-          m.t_begin = t_begin;
-          m.t_end = t_end;
-          m.bad = bad;
-          m.flags = piece_flags | (j == ntiles - 1 ? kMetaLast : 0u);
-          m.ws_row = ws_row;
-          mbar_arrive_expect_tx(fb, bytes);
-        }
+        if (lane == 0) mbar_arrive_expect_tx(fb, 2u * C::kCopyBytes * n);
         __syncwarp();
-        if (j == 0 && lane == 31)  // the group's q rows ride with the piece's first tile
-          bulk_load(smem_u32(qslots + qslot * q_bytes),
-                    a.q + static_cast<int64_t>(b) * a.q_stride + g * G * D, q_bytes, fb);
-        if (lane < C::kNCopy && my_page >= 0) {
+        if (copies) {
           const uint32_t kst = smem_u32(ring + st * C::kStageBytes);
-          const int line = g * BS + (t0 + lane * C::kBR) % BS;
+          const int line = g * BS + tt % BS;
 #pragma unroll
           for (int ch = 0; ch < C::kDCH; ++ch) {
             const uint32_t off = ch * (C::kKT * C::kCRB) + lane * (C::kBR * C::kCRB);
-            tma_load_3d(kst + off, &tm_k, ch * C::kCRB, line, my_page, fb);
-            tma_load_3d(kst + C::kCacheStageBytes + off, &tm_v, ch * C::kCRB, line, my_page, fb);
+            tma_load_3d(kst + off, &tm_k, ch * C::kCRB, line, page, fb);
+            tma_load_3d(kst + C::kCacheStageBytes + off, &tm_v, ch * C::kCRB, line, page, fb);
           }
         }
         __syncwarp();
-      }
-      ++k;
-    }
-    if (ok) {
-      // end marker: a stage with no copies whose record tells the consumers to leave
-      const int st = i % C::kStages;
-      if (i >= C::kStages &&
-          !warp_wait(smem_u32(&empty_bar[st]), ((i / C::kStages) - 1) & 1, abort_s)) {
-        ok = false;
-      } else {
-        if (lane == 0) {
-          meta[st].flags = kMetaEnd;
-          mbar_arrive(smem_u32(&full_bar[st]));
-        }
         ++i;
+        if (++st == C::kStages) {
+          st = 0;
+          parity ^= 1u;
+        }
       }
     }
+    // the end: a piece of no tiles
+    if (ok) ok = start(k, Piece{0, 0, 0, 0, 0, 0, 0, 0, 0});
+    if (ok) ++k;
     if (!ok) {
       if (lane == 0) atomicOr(a.flags, PD_DEV_TIMEOUT);
       *abort_s = 1;
@@ -349,6 +336,8 @@ __global__ void __launch_bounds__(kMmaThreads,
     // every copy issued lands before the block can exit
     for (int t = max(0, i - C::kStages); t < i; ++t)
       (void)mbar_wait(smem_u32(&full_bar[t % C::kStages]), (t / C::kStages) & 1);
+    for (int t = max(0, k - C::kQSlots); t < k; ++t)
+      (void)mbar_wait(smem_u32(&qfull_bar[t % C::kQSlots]), (t / C::kQSlots) & 1);
     return;
   }
 
@@ -358,12 +347,12 @@ __global__ void __launch_bounds__(kMmaThreads,
   // head_dim index of accumulator element (m-tile md, row half hh)
   auto drow = [&](int md, int hh) { return d0 + r * (C::kDS / 8) + hh * C::kKSteps + md; };
   const ThreadPlace tp{warp, lane, r, c, d0};
-  int i = 0, red_buf = 0, ip = 0;
-  // waits for stage i of the ring; false (for all warps alike where they share
+  const int first = C::kDSplit == 1 ? (warp & 1) * 32 : 0;  // the warp's first key of a stage
+  const I8Place<C> at(first, d0, r, c);
+  // waits for a barrier's phase; false (for all warps alike where they share
   // barriers) if the wait ran out
-  auto stage_wait = [&]() {
-    bool ok = warp_wait(smem_u32(&full_bar[i % C::kStages]), (i / C::kStages) & 1, abort_s,
-                        a.consumer_wait_ns);
+  auto await = [&](uint64_t* bar, uint32_t par) {
+    bool ok = warp_wait(smem_u32(bar), par, abort_s, a.consumer_wait_ns);
     if constexpr (C::kDSplit == 4) ok = consumers_vote(ok);
     if (!ok) {
       if (lane == 0) atomicOr(a.flags, PD_DEV_TIMEOUT);
@@ -371,16 +360,17 @@ __global__ void __launch_bounds__(kMmaThreads,
     }
     return ok;
   };
-  while (stage_wait()) {
-    int st = i % C::kStages;
-    uint32_t flags = meta[st].flags;
-    if (flags & kMetaEnd) break;
-    const int b = meta[st].b, g = meta[st].g;
-    const int t_begin = meta[st].t_begin, t_end = meta[st].t_end;
-    const int64_t ws_row = meta[st].ws_row;
-    const bool direct = (flags & kMetaDirect) != 0;
-    const int qslot = static_cast<int>(flags >> 8);
-
+  int st = 0, red_buf = 0, ip = 0;
+  uint32_t parity = 0;   // of stage st's fill
+  uint32_t turn = 0;     // the tile's number, even or odd
+  for (int k = 0;; ++k) {
+    const int qslot = k % C::kQSlots;
+    if (!await(&qfull_bar[qslot], (k / C::kQSlots) & 1)) break;
+    const Piece pc = pieces[qslot];
+    if (pc.ntiles == 0) break;
+    const int b = pc.b, g = pc.g, t_begin = pc.t_begin, t_end = pc.t_end;
+    const int64_t ws_row = pc.ws_row;
+    const bool direct = pc.direct != 0;
     TileState<C, NT> ts;
     load_q_fragments<PD_KV_INT8, D, NT>(
         ts, reinterpret_cast<const uint16_t*>(qslots + qslot * q_bytes), G, a.scale_log2, 1.0f, tp,
@@ -392,26 +382,32 @@ __global__ void __launch_bounds__(kMmaThreads,
     auto& m_run = ts.m_run;
     auto& l_run = ts.l_run;
     bool gave_up = false;
-    while (true) {
-      const uint32_t kst = smem_u32(ring + st * C::kStageBytes);
-      consume_int8_tile<D, NT>(
-          ts,
-          I8Stage{kst, kst + C::kCacheStageBytes, meta[st].t0, t_begin, t_end, meta[st].bad,
-                  meta[st].scales},
-          tp, red, red_buf);
-      if constexpr (C::kDSplit == 4) red_buf ^= 1;
-      const bool last = (flags & kMetaLast) != 0;
-      __syncwarp();
-      // head_dim <= 128: the piece's last stage is handed back after the merge
-      if (lane == 0 && !(C::kDSplit == 1 && last)) mbar_arrive(smem_u32(&empty_bar[st]));
-      ++i;
-      if (last) break;
-      if (!stage_wait()) {
-        gave_up = true;
-        break;
+    int held = 0;  // the last tile's stage, and whether this warp worked on it
+    bool held_own = false;
+    int key0 = pc.t_base + first;
+    for (int j = 0; j < pc.ntiles; ++j, key0 += C::kKT) {
+      const bool own = C::kDSplit == 4 || turn == static_cast<uint32_t>(warp >> 1);
+      const bool last = j == pc.ntiles - 1;
+      if (own) {
+        if (!await(&full_bar[st], parity)) {
+          gave_up = true;
+          break;
+        }
+        const uint32_t kst = smem_u32(ring + st * C::kStageBytes);
+        consume_int8_tile<D, NT>(ts, at, kst, kst + C::kCacheStageBytes, key0, t_begin, t_end,
+                                 scales[st].copy + first / C::kBR, tp, red, red_buf);
+        if constexpr (C::kDSplit == 4) red_buf ^= 1;
+        __syncwarp();
+        // head_dim <= 128: the piece's last stage is handed back after the merge
+        if (lane == 0 && !(C::kDSplit == 1 && last)) mbar_arrive(smem_u32(&empty_bar[st]));
       }
-      st = i % C::kStages;
-      flags = meta[st].flags;
+      held = st;
+      held_own = own;
+      turn ^= 1u;
+      if (++st == C::kStages) {
+        st = 0;
+        parity ^= 1u;
+      }
     }
     if (gave_up) break;
 
@@ -459,7 +455,7 @@ __global__ void __launch_bounds__(kMmaThreads,
             mr[warp * C::kHW + nt * 8 + 2 * c + j] = m_run[nt][j];
             lr[warp * C::kHW + nt * 8 + 2 * c + j] = l_run[nt][j];
           }
-      float* orec = reinterpret_cast<float*>(ring + st * C::kStageBytes);
+      float* orec = reinterpret_cast<float*>(ring + held * C::kStageBytes);
       constexpr int kE = D / 8;  // elements of d per fragment row group
       bool ok = true;
 #pragma unroll
@@ -502,10 +498,11 @@ __global__ void __launch_bounds__(kMmaThreads,
         }
       }
       if (!ok) break;
-      // the merge's stores come before the copies into this stage that follow
+      // all warps are done with the stage, and their stores come before the copies
+      // into it that follow
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&empty_bar[st]));
+      if (!csync(lane)) break;
+      if (lane == 0 && held_own) mbar_arrive(smem_u32(&empty_bar[held]));
       ip ^= 1;
     }
   }
