@@ -296,18 +296,10 @@ __global__ void __launch_bounds__(kMmaThreads,
         const bool mine = lane < C::kNCopy && tt < t_end;
         const int src = mine ? tt / BS - cached_base : 0;
         const int page = __shfl_sync(0xFFFFFFFFu, my_entry, src);
-        const float ks = __shfl_sync(0xFFFFFFFFu, my_ks, src);
-        const float vs = __shfl_sync(0xFFFFFFFFu, my_vs, src);
         const bool copies = mine && page >= 0 && page < a.num_blocks;
         const uint32_t fb = smem_u32(&full_bar[st]);
-        const uint32_t n = __popc(__ballot_sync(0xFFFFFFFFu, copies));
-        if (lane < C::kNCopy)
-          scales[st].copy[lane] = copies ? I8Scales{ks, __log2f(vs), __fdividef(1.0f, vs), 0.0f}
-                                         : I8Scales{0.0f, -INFINITY, 0.0f, 0.0f};
-        if (mine && !copies) atomicOr(a.flags, PD_DEV_BAD_PAGE);
-        __syncwarp();
-        if (lane == 0) mbar_arrive_expect_tx(fb, 2u * C::kCopyBytes * n);
-        __syncwarp();
+        // the copies first: the scales may still be on their way (the barrier's phase
+        // ends with the arrival below at the earliest)
         if (copies) {
           const uint32_t kst = smem_u32(ring + st * C::kStageBytes);
           const int line = g * BS + tt % BS;
@@ -318,6 +310,15 @@ __global__ void __launch_bounds__(kMmaThreads,
             tma_load_3d(kst + C::kCacheStageBytes + off, &tm_v, ch * C::kCRB, line, page, fb);
           }
         }
+        const float ks = __shfl_sync(0xFFFFFFFFu, my_ks, src);
+        const float vs = __shfl_sync(0xFFFFFFFFu, my_vs, src);
+        const uint32_t n = __popc(__ballot_sync(0xFFFFFFFFu, copies));
+        if (lane < C::kNCopy)
+          scales[st].copy[lane] = copies ? I8Scales{ks, __log2f(vs), __fdividef(1.0f, vs), 0.0f}
+                                         : I8Scales{0.0f, -INFINITY, 0.0f, 0.0f};
+        if (mine && !copies) atomicOr(a.flags, PD_DEV_BAD_PAGE);
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(fb, 2u * C::kCopyBytes * n);
         __syncwarp();
         ++i;
         if (++st == C::kStages) {
