@@ -368,6 +368,14 @@ def pd_decode(q, k_cache, v_cache, block_tables, seq_lens, out, *, num_kv_heads,
     workspace: a CUDA uint8 tensor of at least pd_decode_workspace_bytes for
     the split count used; when None, one is allocated here with torch.
     crosscheck: call pd_decode_crosscheck (the CUDA-core partial kernel)."""
+    if (not crosscheck and _serve is not None and q.is_cuda and
+            (workspace is not None or stream is None)):
+        rc = _serve.decode(q, k_cache, v_cache, block_tables, seq_lens, out, num_kv_heads,
+                           block_size, num_blocks, scale, num_splits, sliding_window,
+                           _dtype_code(kv_dtype), k_scale, v_scale, workspace, _stream(stream))
+        if rc is not None:
+            _check("pd_decode", rc)
+            return out
     B, hq, d, mbs = _decode_shape(q, block_tables, seq_lens, out)
     code = _dtype_code(kv_dtype)
     S = num_splits
@@ -376,13 +384,6 @@ def pd_decode(q, k_cache, v_cache, block_tables, seq_lens, out, *, num_kv_heads,
             S = pd_choose_num_splits(B, num_kv_heads, mbs, block_size, sliding_window, d, code,
                                      q.device.index)
         workspace = _scratch(pd_decode_workspace_bytes(B, hq, d, S), q.device, stream)
-    if not crosscheck and _serve is not None and q.is_cuda:
-        rc = _serve.decode(q, k_cache, v_cache, block_tables, seq_lens, out, num_kv_heads,
-                           block_size, num_blocks, scale, S, sliding_window, code, k_scale,
-                           v_scale, workspace, _stream(stream))
-        if rc is not None:
-            _check("pd_decode", rc)
-            return out
     dev = q.device
     fn = "pd_decode_crosscheck" if crosscheck else "pd_decode"
     rc = getattr(_lib, fn)(
@@ -512,6 +513,16 @@ def pd_decode_balanced(q, k_cache, v_cache, block_tables, plan_dev, plan, out, *
                        block_size, num_blocks, scale, sliding_window=0, kv_dtype=PD_KV_BF16,
                        k_scale=1.0, v_scale=1.0, workspace=None, stream=None, _fn="pd_decode_balanced"):
     """One balanced decode step into out; plan_dev is plan.to(device)."""
+    if (_fn == "pd_decode_balanced" and _serve is not None and q.is_cuda and
+            (workspace is not None or stream is None)):
+        rc = _serve.decode_balanced(q, k_cache, v_cache, block_tables, plan_dev, out, num_kv_heads,
+                                    block_size, num_blocks, scale, sliding_window,
+                                    _dtype_code(kv_dtype), k_scale, v_scale, plan.num_ctas,
+                                    plan.num_pieces, workspace, plan.workspace_bytes,
+                                    _stream(stream))
+        if rc is not None:
+            _check(_fn, rc)
+            return out
     B, hq, d = q.shape
     if block_tables.dim() != 2 or block_tables.shape[0] != B:
         raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq]")
@@ -521,14 +532,6 @@ def pd_decode_balanced(q, k_cache, v_cache, block_tables, plan_dev, plan, out, *
     dev = q.device
     if workspace is None:
         workspace = _scratch(plan.workspace_bytes, dev, stream)
-    if _fn == "pd_decode_balanced" and _serve is not None and q.is_cuda:
-        rc = _serve.decode_balanced(q, k_cache, v_cache, block_tables, plan_dev, out, num_kv_heads,
-                                    block_size, num_blocks, scale, sliding_window,
-                                    _dtype_code(kv_dtype), k_scale, v_scale, plan.num_ctas,
-                                    plan.num_pieces, workspace, _stream(stream))
-        if rc is not None:
-            _check(_fn, rc)
-            return out
     rc = getattr(_lib, _fn)(
         _dev(q, "q", torch.bfloat16, dev), _dev(k_cache, "k_cache", None, dev),
         _dev(v_cache, "v_cache", None, dev), _dev(block_tables, "block_tables", torch.int32, dev),

@@ -4,6 +4,8 @@
 // does, checks included, and returns its status, or None, having done nothing, for
 // arguments that binding.py has to refuse. Through ctypes these calls took 12 to 30
 // us of a Grace core, the calls themselves 4 to 6.
+#include <ATen/ops/empty.h>
+
 #include "marshal_args.h"
 
 namespace {
@@ -39,6 +41,30 @@ Heads heads_rows(Args& g, int i) {
   return h;
 }
 int32_t i32_of(int64_t v) { return static_cast<int32_t>(v); }
+
+// The workspace of a call: the caller's (argument i), or for None one of `bytes`
+// bytes from the current stream's memory (the call runs on that stream then).
+struct Work {
+  at::Tensor own;
+  void* p = nullptr;
+  size_t bytes = 0;
+};
+Work workspace(Args& g, int i, const at::Tensor& like, size_t bytes) {
+  Work w;
+  if (g.a[i] != Py_None) {
+    const at::Tensor* t = g.tensor(i);
+    if (t) {
+      w.p = t->data_ptr();
+      w.bytes = t->nbytes();
+    }
+    return w;
+  }
+  if (!g.ok) return w;
+  w.bytes = bytes < 16 ? 16 : bytes;
+  w.own = at::empty({static_cast<int64_t>(w.bytes)}, like.options().dtype(at::kByte));
+  w.p = w.own.data_ptr();
+  return w;
+}
 
 // (qkv, q_out or None: in place, num_q_heads, head_dim (read in place only), k_cache, v_cache,
 //  block_tables, seq_lens, cu_q, cos_sin, max_q_len, num_kv_heads, block_size, num_blocks,
@@ -151,21 +177,31 @@ bool decode_tensors(Args& g, int out_at, DecodeTensors& t) {
 }
 
 // (q, k_cache, v_cache, block_tables, seq_lens, out, num_kv_heads, block_size, num_blocks, scale,
-//  num_splits, sliding_window, kv_dtype, k_scale, v_scale, workspace, stream)
+//  num_splits, sliding_window, kv_dtype, k_scale, v_scale, workspace or None: from the current
+//  stream's memory, stream)
 PyObject* decode(PyObject* const* args) {
   Args g{args};
   DecodeTensors t;
   if (!decode_tensors(g, 5, t)) Py_RETURN_NONE;
   const void* lens = g.ptr(4, kI32, t.B);
-  const int32_t hkv = g.i32(6), bs = g.i32(7), splits = g.i32(10), window = g.i32(11);
+  const int32_t hkv = g.i32(6), bs = g.i32(7), window = g.i32(11);
+  int32_t splits = g.i32(10);
   const int64_t nb = g.i64(8);
   const float scale = g.f32(9), ks = g.f32(13), vs = g.f32(14);
   const int32_t code = g.i32(12);
-  const at::Tensor* ws = g.tensor(15);
   void* st = g.stream(16);
+  size_t need = 0;
+  if (g.ok && args[15] == Py_None) {
+    if (splits == 0)
+      splits = pd_choose_num_splits(i32_of(t.B), hkv, i32_of(t.mbs), bs, window, i32_of(t.d), code,
+                                    g.dev);
+    if (splits < 1) Py_RETURN_NONE;  // a shape that binding.py says what is wrong with
+    need = pd_decode_workspace_bytes(i32_of(t.B), i32_of(t.hq), i32_of(t.d), splits);
+  }
+  const Work ws = workspace(g, 15, THPVariable_Unpack(args[0]), need);
   if (!g.ok) Py_RETURN_NONE;
-  void* work = ws->data_ptr();
-  const size_t work_bytes = ws->nbytes();
+  void* work = ws.p;
+  const size_t work_bytes = ws.bytes;
   return status([&] {
     return pd_decode(t.q, t.kc, t.vc, static_cast<const int32_t*>(t.tables),
                      static_cast<const int32_t*>(lens), t.out, i32_of(t.B), i32_of(t.hq), hkv,
@@ -175,7 +211,8 @@ PyObject* decode(PyObject* const* args) {
 }
 
 // (q, k_cache, v_cache, block_tables, plan, out, num_kv_heads, block_size, num_blocks, scale,
-//  sliding_window, kv_dtype, k_scale, v_scale, num_ctas, num_pieces, workspace, stream)
+//  sliding_window, kv_dtype, k_scale, v_scale, num_ctas, num_pieces, workspace or None, the plan's
+//  workspace_bytes, stream)
 PyObject* decode_balanced(PyObject* const* args) {
   Args g{args};
   DecodeTensors t;
@@ -185,13 +222,15 @@ PyObject* decode_balanced(PyObject* const* args) {
   const int64_t nb = g.i64(8);
   const float scale = g.f32(9), ks = g.f32(12), vs = g.f32(13);
   const int32_t ctas = g.i32(14), pieces = g.i32(15);
-  const at::Tensor* ws = g.tensor(16);
-  void* st = g.stream(17);
-  if (!g.ok || plan->scalar_type() != kI32) Py_RETURN_NONE;
+  const int64_t need = g.i64(17);
+  void* st = g.stream(18);
+  if (!g.ok || plan->scalar_type() != kI32 || need < 0) Py_RETURN_NONE;
+  const Work ws = workspace(g, 16, THPVariable_Unpack(args[0]), static_cast<size_t>(need));
+  if (!g.ok) Py_RETURN_NONE;
   const void* words = plan->data_ptr();
   const size_t plan_bytes = plan->nbytes();
-  void* work = ws->data_ptr();
-  const size_t work_bytes = ws->nbytes();
+  void* work = ws.p;
+  const size_t work_bytes = ws.bytes;
   return status([&] {
     return pd_decode_balanced(t.q, t.kc, t.vc, static_cast<const int32_t*>(t.tables), words,
                               plan_bytes, t.out, i32_of(t.B), i32_of(t.hq), hkv, i32_of(t.d), bs,
@@ -203,7 +242,7 @@ PyObject* decode_balanced(PyObject* const* args) {
 PyMethodDef kMethods[] = {method<rope_append, 18>("rope_append"),
                           method<prefill_packed, 10>("prefill_packed"),
                           method<decode, 17>("decode"),
-                          method<decode_balanced, 18>("decode_balanced"),
+                          method<decode_balanced, 19>("decode_balanced"),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_marshal_serve", nullptr, -1, kMethods};
 

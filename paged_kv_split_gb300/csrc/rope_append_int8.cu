@@ -15,10 +15,13 @@
 // lane), finds the maximum over the block, and writes the codes: one pass over
 // memory. A decode step (max_q_len 1) has one row a page: there a lane group
 // takes a (token, head) by itself, without a block barrier.
+#include "mma_common.cuh"
 #include "serve_common.cuh"
 
 namespace pd {
 namespace {
+
+using ::pd::mma::pack_bf16x2;
 
 constexpr int kAppendThreads = 128;
 constexpr float kScaleMin = 8.673617379884035e-19f;  // 2^-60
@@ -52,8 +55,7 @@ __device__ __forceinline__ void pack16(const float (&x)[16], uint4 (&w)[2]) {
   uint32_t u[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    u[i] = static_cast<uint32_t>(f32_to_bf16(x[2 * i])) |
-           (static_cast<uint32_t>(f32_to_bf16(x[2 * i + 1])) << 16);
+    u[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
   w[0] = make_uint4(u[0], u[1], u[2], u[3]);
   w[1] = make_uint4(u[4], u[5], u[6], u[7]);
 }
@@ -381,8 +383,9 @@ cudaError_t launch_append(AppendArgs a, int num_sms, cudaStream_t st) {
   const int bs = a.block_size;
   const int pages = (a.max_q_len + bs - 2) / bs + 1;
   // runs of heads long enough to reuse the cosines, short enough to fill the SMs
+  // (8945 rows of 48 heads of 128: 32 CTAs an SM 49.5 us, 8 58, 16 51, 64 51.5)
   const int64_t units = (static_cast<int64_t>(a.total_q) + bs - 1) / bs + a.num_seqs;
-  int64_t groups = (static_cast<int64_t>(num_sms) * 16 + units - 1) / units;
+  int64_t groups = (static_cast<int64_t>(num_sms) * 32 + units - 1) / units;
   if (groups > heads) groups = heads;
   a.heads_per_cta = static_cast<int>((heads + groups - 1) / groups);
   const dim3 grid(pages, a.num_seqs, (heads + a.heads_per_cta - 1) / a.heads_per_cta);

@@ -10,14 +10,20 @@ import torch
 
 from paged_kv_split_gb300 import binding as B, build
 
-COUNTS = {"rope_append": 18, "prefill_packed": 10, "decode": 17, "decode_balanced": 18}
+COUNTS = {"rope_append": 18, "prefill_packed": 10, "decode": 17, "decode_balanced": 19}
 X = torch.zeros(4, 4)
 
 STUBS = """
 #define PD_MARSHAL_DEVICE at::kCPU
 #include "%s"
-static int g_qs, g_ks;
 extern "C" {
+size_t pd_decode_workspace_bytes(int32_t B, int32_t hq, int32_t d, int32_t s) {
+  return B == 2 && hq == 4 && d == 64 ? 256 : 0;
+}
+int pd_choose_num_splits(int32_t B, int32_t hkv, int32_t mbs, int32_t bs, int32_t w, int32_t d,
+                         int32_t f, int) {
+  return B == 2 && hkv == 2 && mbs == 4 && bs == 16 && w == 7 && d == 64 ? (f == 3 ? 1 : -2) : -1;
+}
 size_t pd_cache_bytes(int32_t f, int64_t n, int32_t bs, int32_t h, int32_t d) {
   return f == 3 ? n * bs * h * d : 0;
 }
@@ -69,7 +75,7 @@ GOOD = {
     "decode": [q, cache, cache, z(2, 4, dtype=i32), z(2, dtype=i32), z(2, 4, 64, dtype=bf), 2, 16,
                4, 1.0, 1, 7, 3, 1.0, 1.0, ws, 0],
     "decode_balanced": [q, cache, cache, z(2, 4, dtype=i32), z(8, dtype=i32),
-                        z(2, 4, 64, dtype=bf), 2, 16, 4, 1.0, 7, 3, 1.0, 1.0, 5, 6, ws, 0],
+                        z(2, 4, 64, dtype=bf), 2, 16, 4, 1.0, 7, 3, 1.0, 1.0, 5, 6, ws, 0, 0],
 }
 def call(name, **at):
     a = list(GOOD[name])
@@ -81,6 +87,9 @@ def call(name, **at):
 CASES = {
     "taken": """
 assert call("decode") == 53 and call("decode_balanced") == 54
+assert call("decode", _15=None) == 53 and call("decode", _10=0, _15=None) == 53
+assert call("decode", _10=0, _12=9, _15=None) is None       # no split count for the form
+assert call("decode_balanced", _16=None, _17=256) == 54
 assert call("prefill_packed") == 3 * 512 + 256
 assert call("rope_append") == 100 + 256
 assert call("rope_append", _1=None, _2=4, _3=64) == 51
@@ -106,7 +115,8 @@ assert call("decode", _5=z(2, 4, 32, dtype=bf)) is None
 assert call("decode", _3=z(3, 4, dtype=i32)) is None
 assert call("decode", _4=z(3, dtype=i32)) is None
 assert call("decode", _10=1 << 40) is None
-assert call("decode_balanced", _4=z(8)) is None""",
+assert call("decode_balanced", _4=z(8)) is None
+assert call("decode_balanced", _16=None, _17=-1) is None""",
     "0-dim": """
 for name, args in GOOD.items():
     for i, x in enumerate(args):
