@@ -48,9 +48,10 @@
  *                   [num_kv_heads]; value = code * scale. The page stride is
  *                   rounded up to a multiple of 128 bytes. Codes lie in
  *                   [-127, 127], scales in [2^-60, 2^60]. Written by
- *                   pd_rope_append_int8, read by every pd_decode* call; the
- *                   other calls refuse it (PD_ERR_UNSUPPORTED): a row is only
- *                   worth something beside its page's scale.
+ *                   pd_rope_append_int8, read by pd_prefill and the pd_decode*
+ *                   calls but pd_decode_tree; the other calls refuse it
+ *                   (PD_ERR_UNSUPPORTED): a row is only worth something beside
+ *                   its page's scale.
  *   Slot s of the pool is page s / block_size, row s % block_size.
  */
 #ifndef PD_H_
@@ -425,15 +426,15 @@ int pd_decode_static_ws(const void* q, const void* k_cache, const void* v_cache,
  *               keys j <= its position; 0: every query sees all L_b keys.
  *   sliding_window  W > 0 keeps keys j with position - j < W; 0 = off.
  * Scores, softmax and the bf16 output follow pd_decode (scale after the dot
- * product, 1e-20 guard). Cache (all three forms, with k_scale / v_scale for
+ * product, 1e-20 guard). Cache (all forms, with k_scale / v_scale for
  * FP8), block tables, scale, status codes and device flags as in pd_decode
  * ([AstrAI]: prefill kernels templated on the paged KV source). Supported:
  * head_dim 64, 128 or 256, block_size 16 or 32, G = num_q_heads /
  * num_kv_heads <= 16; anything else returns PD_ERR_UNSUPPORTED. No
  * workspace: each query tile writes its rows. BF16 caches run on the tcgen05
  * tensor cores (accumulators in TMEM; at head_dim 64 and 128 two 128-row
- * query tiles share each CTA's K/V stages); FP8 and NVFP4 caches on mma.sync
- * tiles, each stage widened once to f16 (exact) before its MMAs.
+ * query tiles share each CTA's K/V stages); FP8, NVFP4 and INT8 caches on
+ * mma.sync tiles, each stage widened once to f16 (exact) before its MMAs.
  * Device pointers owned by the caller, 16-byte aligned; enqueued on `stream`,
  * never synchronises. */
 int pd_prefill(const void* q, int64_t q_stride, const int32_t* cu_q, const void* k_cache,
@@ -567,8 +568,9 @@ int pd_compact_tree(void* k_caches, void* v_caches, int64_t layer_bytes, int32_t
 
 /* ---- Serving from an INT8 cache ----
  * A cache form with one scale per page and kv head (PD_KV_INT8 above): new
- * tokens' rows go in with pd_rope_append_int8, every pd_decode* call reads it,
- * and pd_prefill_packed attends whole prompts over their own rows, unquantised. */
+ * tokens' rows go in with pd_rope_append_int8, pd_decode* and pd_prefill (a later
+ * chunk of a prompt) read it, and pd_prefill_packed attends whole prompts over
+ * their own rows, unquantised. */
 
 /* Rotate the q and k heads of each sequence's new tokens and append their K and
  * V to the sequence's INT8 pages.

@@ -906,7 +906,7 @@ int prefill_impl(const void* q, int64_t q_stride, const int32_t* cu_q, const voi
     return PD_ERR_INVALID_ARG;
   const int G = num_q_heads / num_kv_heads;
   if (G > kMaxGroup || num_kv_heads > 65535) return PD_ERR_UNSUPPORTED;
-  if (!row_dtype_ok(kv_dtype) || !head_dim_ok(head_dim) || !block_size_ok(block_size))
+  if (!dtype_ok(kv_dtype) || !head_dim_ok(head_dim) || !block_size_ok(block_size))
     return PD_ERR_UNSUPPORTED;
   if (head_dim > 256) return PD_ERR_UNSUPPORTED;
   if (kv_dtype == PD_KV_FP8_E4M3 && !(scale_ok(k_scale) && scale_ok(v_scale)))

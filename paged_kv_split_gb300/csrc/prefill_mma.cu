@@ -35,7 +35,10 @@
 //    q enters the f16 MMAs multiplied by a power of two per row (its largest
 //    magnitude into [2^14, 2^15)) and the factor, with the FP8 k_scale, is
 //    folded into the row's score multiplier; the FP8 v_scale multiplies O at
-//    the end.
+//    the end. INT8 codes widen to f16 exactly too; the key scale of a page
+//    multiplies its scores, and the value scale rides in the exponent (log2 of it
+//    joins the score, the row sum divides it out again), so the weights stay in
+//    (0, 1].
 //  * Keys outside a row's range score -inf. V rows that no row of the CTA may
 //    read (before the CTA's first key, past its last, pages outside the pool)
 //    are zeroed in the fragments, so whatever bytes sit in those stage rows
@@ -46,8 +49,9 @@
 
 #include <cstring>
 
+#include "int8_tile.cuh"
 #include "mma_common.cuh"
-#include "pd_common.cuh"
+#include "serve_common.cuh"
 
 namespace pd {
 namespace {
@@ -70,7 +74,7 @@ struct PCfg {
   // one key row of one head as stored in the cache (bytes) and a 16-bit
   // operand tile of the stage's keys (BF16: the stage itself; else the f16 tile)
   static constexpr int kRowBytes =
-      FMT == PD_KV_BF16 ? 2 * D : (FMT == PD_KV_FP8_E4M3 ? D : D / 2);
+      FMT == PD_KV_BF16 ? 2 * D : (FMT == PD_KV_NVFP4 ? D / 2 : D);
   static constexpr int kOpCacheBytes = kKT * 2 * D;
   // NVFP4 stage: data [kKT][D/2] then scales [kKT][D/16]
   static constexpr int kDataBytes = kKT * kRowBytes;
@@ -85,7 +89,10 @@ struct PCfg {
   static constexpr int kOpOffset = kRingBytes;
   static constexpr int kBarOffset = kOpOffset + kOpBytes;
   // full[kStages], empty[kStages], the stages' bad-copy masks, the abort word
-  static constexpr int kSmemBytes = kBarOffset + 2 * kStages * 8 + kStages * 4 + 16 + 1024;
+  // and, for INT8, the scales of each stage's copies and of the widened tile's
+  static constexpr int kScaleOffset = (kBarOffset + 2 * kStages * 8 + kStages * 4 + 16 + 15) / 16 * 16;
+  static constexpr int kSmemBytes =
+      kScaleOffset + (FMT == PD_KV_INT8 ? (kStages + 1) * kNCopy * 16 : 0) + 1024;
   static constexpr uint32_t kCopyBytes =
       kBR * kRowBytes + (FMT == PD_KV_NVFP4 ? kBR * (D / 16) : 0);
   static constexpr int kKS = D / 16;  // k-steps of S = Q K^T
@@ -119,6 +126,12 @@ __device__ __forceinline__ void widen_stage(uint32_t raw, uint32_t op, int tid) 
       f[1] = e4m3x2_f16x2(w.x >> 16);
       f[2] = e4m3x2_f16x2(w.y & 0xFFFFu);
       f[3] = e4m3x2_f16x2(w.y >> 16);
+    } else if constexpr (FMT == PD_KV_INT8) {
+      const uint2 w = lds64(raw + key * D + e);
+      f[0] = i8x2_f16x2<0x4140>(w.x ^ 0x80808080u);
+      f[1] = i8x2_f16x2<0x4342>(w.x ^ 0x80808080u);
+      f[2] = i8x2_f16x2<0x4140>(w.y ^ 0x80808080u);
+      f[3] = i8x2_f16x2<0x4342>(w.y ^ 0x80808080u);
     } else {
       const uint32_t w = lds32(raw + key * (D / 2) + e / 2);
       const uint32_t sc = lds_u8(raw + kKT * (D / 2) + key * (D / 16) + e / 16);
@@ -197,6 +210,8 @@ __global__ void __launch_bounds__(kMmaThreads, D <= 128 ? 2 : 1)
   uint32_t* bad_copies = reinterpret_cast<uint32_t*>(empty_bar + C::kStages);
   // set by a warp that stops early: the others stop waiting on it
   volatile int* abort_s = reinterpret_cast<volatile int*>(bad_copies + C::kStages);
+  I8Scales* scales = reinterpret_cast<I8Scales*>(smem + C::kScaleOffset);  // INT8 only
+  I8Scales* op_scales = scales + C::kStages * C::kNCopy;
 
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) {
@@ -210,17 +225,18 @@ __global__ void __launch_bounds__(kMmaThreads, D <= 128 ? 2 : 1)
 
   // =========================== producer warp ===============================
   if (warp == kConsumerWarps) {
-    if constexpr (FMT != PD_KV_NVFP4) {
+    if constexpr (FMT == PD_KV_BF16 || FMT == PD_KV_FP8_E4M3) {
       if (lane == 0) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_k)) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_v)) : "memory");
       }
     }
     const int64_t data_bytes = static_cast<int64_t>(bs) * a.num_kv_heads * (D / 2);
-    const int64_t page_bytes = page_bytes_of(FMT, bs, a.num_kv_heads, D);
+    const int64_t page_bytes = any_page_bytes(FMT, bs, a.num_kv_heads, D);
     // entries [cached_base, cached_base + 32) of the block-table row, one per lane
     int cached_base = -(1 << 30);
     int my_entry = -1;
+    float my_ks = 0.0f, my_vs = 1.0f;  // INT8: the two scales of that page and kv head
     int i = 0;  // tiles issued
     for (; i < ntiles; ++i) {
       const int st = i % C::kStages;
@@ -246,8 +262,23 @@ __global__ void __launch_bounds__(kMmaThreads, D <= 128 ? 2 : 1)
             cached_base = pidx;
             const int e = cached_base + lane;
             my_entry = (e < a.max_blocks_per_seq) ? bt[e] : -1;
+            if constexpr (FMT == PD_KV_INT8) {
+              if (my_entry >= 0 && my_entry < a.num_blocks && e * bs < k_hi) {
+                const int64_t at =
+                    my_entry * page_bytes + int8_data_bytes(bs, a.num_kv_heads, D) + 4 * g;
+                my_ks = *reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.k_cache) + at);
+                my_vs = *reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.v_cache) + at);
+              }
+            }
           }
           const int pg = __shfl_sync(0xFFFFFFFFu, my_entry, pidx - cached_base);
+          if constexpr (FMT == PD_KV_INT8) {
+            const float ks = __shfl_sync(0xFFFFFFFFu, my_ks, pidx - cached_base);
+            const float vs = __shfl_sync(0xFFFFFFFFu, my_vs, pidx - cached_base);
+            if (lane == 0)
+              scales[st * C::kNCopy + j] =
+                  I8Scales{ks, __log2f(vs), __fdividef(1.0f, vs), 0.0f};
+          }
           if (pg >= 0 && pg < a.num_blocks) {
             pages[j] = pg;
             bytes += 2u * C::kCopyBytes;
@@ -286,6 +317,13 @@ __global__ void __launch_bounds__(kMmaThreads, D <= 128 ? 2 : 1)
             bulk_load(vst + doff, vp + line * (D / 2), db, fb);
             bulk_load(kst + soff, kp + data_bytes + line * (D / 16), sb, fb);
             bulk_load(vst + soff, vp + data_bytes + line * (D / 16), sb, fb);
+          } else if constexpr (FMT == PD_KV_INT8) {
+            // a head's rows of a page lie one behind the other: [key][D] in the stage
+            const int64_t at = my_page * page_bytes + (static_cast<int64_t>(g) * bs + row0) * D;
+            bulk_load(kst + j * (C::kBR * D), static_cast<const uint8_t*>(a.k_cache) + at,
+                      C::kCopyBytes, fb);
+            bulk_load(vst + j * (C::kBR * D), static_cast<const uint8_t*>(a.v_cache) + at,
+                      C::kCopyBytes, fb);
           } else if constexpr (FMT == PD_KV_FP8_E4M3) {
             // one unswizzled box of kBR rows x D bytes: [key][D] in the stage
             const int z = my_page * bs + row0;
@@ -396,6 +434,9 @@ __global__ void __launch_bounds__(kMmaThreads, D <= 128 ? 2 : 1)
       consumers_sync();  // every warp is done with the previous tile's f16 operands
       widen_stage<FMT, D>(kst, op_k, tid);
       widen_stage<FMT, D>(vst, op_v, tid);
+      if constexpr (FMT == PD_KV_INT8) {
+        if (tid < C::kNCopy) op_scales[tid] = scales[st * C::kNCopy + tid];
+      }
       consumers_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&empty_bar[st]));  // the raw stage is free
@@ -429,7 +470,13 @@ __global__ void __launch_bounds__(kMmaThreads, D <= 128 ? 2 : 1)
         const int kk = nt * 8 + 2 * c + (e & 1);
         const int key = t0 + kk;
         const bool okk = key >= rlo[hh] && key <= rpos[hh] && !((bad >> (kk / C::kBR)) & 1u);
-        s[nt][e] = okk ? s[nt][e] * sl2[hh] : -INFINITY;
+        if constexpr (FMT == PD_KV_INT8) {
+          // the weight times the value scale, whose logarithm joins the score
+          const I8Scales& f = op_scales[nt * 8 / C::kBR];
+          s[nt][e] = okk ? fmaf(s[nt][e], sl2[hh] * f.k, f.v_log2) : -INFINITY;
+        } else {
+          s[nt][e] = okk ? s[nt][e] * sl2[hh] : -INFINITY;
+        }
         mx[hh] = fmaxf(mx[hh], s[nt][e]);
       }
     float alpha[2];
@@ -448,7 +495,10 @@ __global__ void __launch_bounds__(kMmaThreads, D <= 128 ? 2 : 1)
       for (int e = 0; e < 4; ++e) {
         const int hh = e >> 1;
         s[nt][e] = (m_run[hh] == -INFINITY) ? 0.0f : ex2(s[nt][e] - m_run[hh]);
-        ls[hh] += s[nt][e];
+        if constexpr (FMT == PD_KV_INT8)  // the row sum is of the weights alone
+          ls[hh] = fmaf(s[nt][e], op_scales[nt * 8 / C::kBR].v_inv, ls[hh]);
+        else
+          ls[hh] += s[nt][e];
       }
 #pragma unroll
     for (int hh = 0; hh < 2; ++hh) l_run[hh] = l_run[hh] * alpha[hh] + ls[hh];
@@ -597,6 +647,8 @@ cudaError_t launch_prefill(const PrefillArgs& a, const void* k_cache, const void
       return launch_prefill_fmt<PD_KV_BF16>(a, k_cache, v_cache, head_dim, max_q_len, st);
     case PD_KV_FP8_E4M3:
       return launch_prefill_fmt<PD_KV_FP8_E4M3>(a, k_cache, v_cache, head_dim, max_q_len, st);
+    case PD_KV_INT8:
+      return launch_prefill_fmt<PD_KV_INT8>(a, k_cache, v_cache, head_dim, max_q_len, st);
     default:
       return launch_prefill_fmt<PD_KV_NVFP4>(a, k_cache, v_cache, head_dim, max_q_len, st);
   }

@@ -216,6 +216,39 @@ def test_bad_pages_and_lengths():
     assert B.pd_device_status(reset=True) == 2
 
 
+PREFILL = [  # lens, q lens, hq, hkv, d, bs, window
+    ([40, 17, 300, 5], [3, 17, 65, 0], 4, 2, 64, 16, 0),
+    ([130, 700, 64], [30, 100, 1], 32, 8, 128, 16, 0),
+    ([130, 700, 64], [30, 100, 64], 12, 1, 128, 32, 60),
+    ([200, 333], [77, 40], 8, 4, 256, 16, 0),
+    ([200, 333], [20, 333], 16, 2, 64, 32, 100),
+]
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lens,q_lens,hq,hkv,d,bs,window", PREFILL)
+def test_chunks_of_prompts(lens, q_lens, hq, hkv, d, bs, window, causal):
+    """pd_prefill over the cache: each query row is decode over the keys it sees."""
+    c = Case(lens, hq, hkv, d, bs, seed=21)
+    T = sum(q_lens)
+    qb = V.bf16_bits(c.rng.standard_normal((T, hq, d)).astype(np.float32))
+    cu = np.concatenate([[0], np.cumsum(q_lens)]).astype(np.int32)
+    q = U.bf16_dev(qb)
+    out = torch.full_like(q, 7.0)
+    U.pd().pd_prefill(q, U.to_dev(cu), U.to_dev(c.k), U.to_dev(c.v), U.to_dev(c.tables),
+                      U.to_dev(c.lens), out, max_q_len=max(q_lens), causal=causal,
+                      sliding_window=window, **c.args())
+    torch.cuda.synchronize()
+    got = V.f32(bits(out))
+    for b, n in enumerate(q_lens):
+        for i in range(0, n, 7):
+            pos = lens[b] - n + i if causal else lens[b] - 1
+            want, bound = R.decode_f64(qb[cu[b] + i][None], c.k, c.v, c.tables[b][None], [pos + 1],
+                                       hkv, bs, c.scale, window=window)
+            err = np.abs(got[cu[b] + i] - want[0])
+            assert (err <= bound[0]).all(), (b, i, float((err / bound[0]).max()))
+
+
 def test_graph_follows_lengths():
     c = Case([300, 500], 8, 2, 128, 16, seed=13)
     B = U.pd()
@@ -263,13 +296,14 @@ def test_other_calls_refuse_the_form():
     cu = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
     geom = dict(num_kv_heads=2, block_size=16, num_blocks=c.nb, kv_dtype="int8")
     calls = [
-        lambda: B.pd_prefill(q, cu, k, v, tables, lens, torch.empty_like(q), max_q_len=1, scale=1.0,
-                             **geom),
         lambda: B.pd_reshape_and_cache(q[:, :2].contiguous(), q[:, :2].contiguous(), k, v, lens,
                                        num_blocks=c.nb, block_size=16, kv_dtype="int8"),
         lambda: B.pd_decode_tree(q, cu, k, v, tables, lens, torch.empty_like(q), max_q_len=1,
                                  scale=1.0, workspace=torch.empty(1 << 20, dtype=torch.uint8,
                                                                   device="cuda"), **geom),
+        lambda: B.pd_compact_tree(k, v, tables, lens, cu, cu[None, :1].contiguous(), lens,
+                                  torch.empty_like(lens), num_kv_heads=2, head_dim=64, block_size=16,
+                                  num_blocks=c.nb, kv_dtype="int8"),
     ]
     for call in calls:
         with pytest.raises(B.PdError) as e:
