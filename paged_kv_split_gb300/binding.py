@@ -969,6 +969,13 @@ def _heads_rows(t, name, index):
     return t.data_ptr(), (s0 if rows > 1 else 0)
 
 
+def _on_current_device(t):
+    """The calls run on the current device: tensors of another are refused."""
+    if t.is_cuda and t.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"the tensors are on {t.device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
 def _rope_append(qkv, q_ptr, q_stride, k_ptr, k_stride, hq, d, k_cache, v_cache, block_tables,
                  seq_lens, cu_q, cos_sin, max_q_len, num_kv_heads, block_size, num_blocks, positions,
                  interleaved, stream):
@@ -1009,6 +1016,7 @@ def pd_rope_append_int8(qkv, q_out, k_cache, v_cache, block_tables, seq_lens, cu
     wider rows. seq_lens: int32 [B] cached rows, the new ones included; max_q_len:
     host int, the most new tokens of a sequence. positions: int32 [T], or None for
     the rows in the cache. cos_sin: float32 [max_position, rot_dim]."""
+    _on_current_device(qkv)
     if _serve is not None and qkv.is_cuda:
         rc = _serve.rope_append(qkv, q_out, 0, 0, k_cache, v_cache, block_tables, seq_lens, cu_q,
                                 cos_sin, max_q_len, num_kv_heads, block_size, num_blocks, positions,
@@ -1040,6 +1048,7 @@ def pd_rope_append_int8_(qkv, k_cache, v_cache, block_tables, seq_lens, cu_q, co
                          positions=None, interleaved=False, stream=None):
     """pd_rope_append_int8 in place: the q and k heads of the fused rows are
     replaced by their rotated form, ready for pd_prefill_packed."""
+    _on_current_device(qkv)
     if _serve is not None and qkv.is_cuda:
         rc = _serve.rope_append(qkv, None, num_q_heads, head_dim, k_cache, v_cache, block_tables,
                                 seq_lens, cu_q, cos_sin, max_q_len, num_kv_heads, block_size,
@@ -1065,6 +1074,7 @@ def pd_prefill_packed(q, k, v, cu_q, out, *, max_q_len, scale, causal=True, slid
     a part of wider rows (views of fused QKV rows). cu_q: int32 [B + 1] row
     offsets; max_q_len: host int, the longest prompt.
     crosscheck: call pd_prefill_packed_crosscheck (CUDA cores)."""
+    _on_current_device(q)
     if not crosscheck and _serve is not None and q.is_cuda:
         rc = _serve.prefill_packed(q, k, v, cu_q, out, max_q_len, scale, causal, sliding_window,
                                    _stream(stream))

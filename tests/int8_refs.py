@@ -101,6 +101,8 @@ def append_f32(qkv_bits, cu_q, seq_lens, cos_sin, k_cache, v_cache, tables, hq, 
         cc, ss = codes_view(cache, bs, hkv, d), scales(cache, bs, hkv, d)
         for b in range(len(seq_lens)):
             n = cu_q[b + 1] - cu_q[b]
+            if n == 0:
+                continue
             first = seq_lens[b] - n
             for p in range(first // bs, (seq_lens[b] + bs - 1) // bs):
                 lo, hi = max(first, p * bs), min(seq_lens[b], (p + 1) * bs)

@@ -94,8 +94,8 @@ SHAPES = [  # hq, hkv, d, bs, rot, interleaved
 @pytest.mark.parametrize("old,new", [
     ([0], [1]),
     ([5, 0, 15, 16, 31, 32, 100], [1] * 7),             # a decode step
-    ([5, 0, 33], [1, 0, 1]),                            # with an idle sequence
-    ([0, 3, 15, 0, 16], [7, 2, 1, 0, 40]),              # short chunks
+    ([5, 7, 33], [1, 0, 1]),                            # with an idle sequence
+    ([0, 3, 15, 9, 16], [7, 2, 1, 0, 40]),              # short chunks
     ([0, 11], [97, 64]),                                # prompts
 ])
 def test_bits(old, new, hq, hkv, d, bs, rot, inter):

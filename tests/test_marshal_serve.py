@@ -189,3 +189,19 @@ def test_without_the_module(monkeypatch):
     assert not build.serve_fits() and build.serve_is_stale()
     with pytest.warns(UserWarning, match="not used"):
         assert B._load_marshal("_marshal_serve", build.SERVE, build.serve_fits) is None
+
+
+def test_tensors_of_another_device(monkeypatch):
+    class T:
+        is_cuda, device = True, torch.device("cuda", 1)
+
+        def get_device(self):
+            return 1
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    with pytest.raises(ValueError, match="cuda:1, the current device is cuda:0"):
+        B.pd_prefill_packed(T(), T(), T(), T(), T(), max_q_len=1, scale=1.0)
+    with pytest.raises(ValueError, match="current device"):
+        B.pd_rope_append_int8(T(), T(), T(), T(), T(), T(), T(), T(), max_q_len=1, num_kv_heads=1,
+                              block_size=16, num_blocks=1)
