@@ -67,8 +67,8 @@ struct PkCfg {
   // s_full[bufs], p_full, o_done, p_half; fin
   static constexpr int kTileBars = kBufs + 3;
   static constexpr int kNumBars = 2 * kSlots + 2 + 4 + kTiles * kTileBars + 1;
-  static constexpr int kItemOff = kBarOff + kNumBars * 8;
-  static constexpr int kHolderOff = kItemOff + 2 * 32;
+  static constexpr int kItemOff = (kBarOff + kNumBars * 8 + 15) / 16 * 16;
+  static constexpr int kHolderOff = kItemOff + 2 * 48;
   static constexpr int kSmemBytes = kHolderOff + 16;
   static constexpr int kSoftWarps = 4 * kTiles;
   static constexpr int kProdWarp = kSoftWarps;
@@ -181,6 +181,13 @@ __device__ __forceinline__ void arrive_if(uint32_t lead, uint32_t bar) {
       "r"(lead)
       : "memory");
 }
+// A box of a tensor map into L2.
+__device__ __forceinline__ void prefetch_3d(const CUtensorMap* map, int x, int y, int z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
 // A place in a ring of N slots and the parity of its fill.
 template <int N>
 struct Ring {
@@ -194,36 +201,29 @@ struct Ring {
   }
 };
 
-// An item, as the copying warp leaves it for the others.
-struct Item {
+// An item, as the copying warp leaves it for the others: tokens tok0 .. of query
+// tile A, tok0 + 128 / G .. of B, key tiles from k_lo on; A works on tiles [0, jA1),
+// B on [jB0, jB1) (none: 0, 0).
+struct alignas(16) Item {
   int q0, n;    // the sequence's first row and its tokens
   int tok0;     // the pair's first token
   int g;        // kv head; -1: no more items
-  int pad[4];
-};
-
-// What an item's tiles see. Tokens [t0(X), t1(X)) of query tile X, keys
-// [k_lo, k_hi), tiles from k_lo on; tile X works on tiles [j0, j1).
-struct Geometry {
-  int k_lo, ntiles;
-  int jA0, jA1, jB0, jB1;
+  int k_lo, ntiles, jA1, jB0, jB1;
+  int pad[3];
 };
 template <int KT, int TILES>
-__device__ __forceinline__ Geometry geometry(const Item& it, int tpc, int causal, int W) {
-  Geometry r;
+__device__ __forceinline__ void set_tiles(Item& it, int tpc, int causal, int W) {
   auto pos = [&](int t) { return causal ? t : it.n - 1; };
   auto lo = [&](int t) { return (W > 0 && pos(t) >= W) ? pos(t) + 1 - W : 0; };
   const int a0 = it.tok0, a1 = min(a0 + tpc, it.n);
   const int b0 = a0 + tpc, b1 = min(b0 + tpc, it.n);
   const bool has_b = TILES == 2 && b1 > b0;
-  r.k_lo = lo(a0);
+  it.k_lo = lo(a0);
   const int hi_a = pos(a1 - 1) + 1, hi_b = has_b ? pos(b1 - 1) + 1 : 0;
-  r.ntiles = ((has_b ? hi_b : hi_a) - r.k_lo + KT - 1) / KT;
-  r.jA0 = 0;
-  r.jA1 = (hi_a - r.k_lo + KT - 1) / KT;
-  r.jB0 = has_b ? (lo(b0) - r.k_lo) / KT : 0;
-  r.jB1 = has_b ? (hi_b - r.k_lo + KT - 1) / KT : 0;
-  return r;
+  it.ntiles = ((has_b ? hi_b : hi_a) - it.k_lo + KT - 1) / KT;
+  it.jA1 = (hi_a - it.k_lo + KT - 1) / KT;
+  it.jB0 = has_b ? (lo(b0) - it.k_lo) / KT : 0;
+  it.jB1 = has_b ? (hi_b - it.k_lo + KT - 1) / KT : 0;
 }
 
 // Tokens of sequence b, or 0 where its counts do not fit the batch.
@@ -328,6 +328,25 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
       };
       const int hkv = a.num_kv_heads;
       const int64_t total = static_cast<int64_t>(above(0, first_cta)) * hkv;
+      // Q of item kk: tokens x G heads x 64 of head_dim a copy
+      int q_loads = 0;
+      auto load_q = [&](const Item& it, bool has_b, int kk) {
+        if (kk >= 1 && !warp_wait(smem_u32(q_empty), (kk - 1) & 1, abort_s)) {
+          failed = true;
+          return;
+        }
+        if (lane == 0) {
+          const uint32_t box = static_cast<uint32_t>(tpc) * G * 128;
+          mbar_arrive_expect_tx(smem_u32(q_full), box * C::kDCH * (has_b ? 2 : 1));
+          for (int X = 0; X < (has_b ? 2 : 1); ++X)
+#pragma unroll
+            for (int ch = 0; ch < C::kDCH; ++ch)
+              tma_load_3d(s0 + X * C::kQBytes + ch * (128 * 128), &tm_q, ch * 64, it.g * G,
+                          it.q0 + it.tok0 + X * tpc, smem_u32(q_full));
+        }
+        ++q_loads;
+        __syncwarp();
+      };
       int slot = 0;      // ring slots filled so far
       int k = 0;         // items so far
       int top = levels;  // the level of the last item: ranks go up, levels down
@@ -336,7 +355,7 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
                              ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
         const bool end = round * static_cast<int64_t>(gridDim.x) >= total;
         if (!end && rank >= total) continue;  // a round that does not reach this CTA
-        Item it;
+        Item it = {};
         it.g = -1;
         if (!end) {
           const int pr = static_cast<int>(rank / hkv);
@@ -361,7 +380,6 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
           top = lo;
           int idx = pr - over;  // among the sequences that have level lo, in order
           it.g = static_cast<int>(rank % hkv);
-          it.q0 = it.n = it.tok0 = 0;
           for (int base = 0; base < a.num_seqs; base += 32) {
             const int b = base + lane;
             const int n = b < a.num_seqs ? prompt_len(a, b, false) : 0;
@@ -379,6 +397,7 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
             idx -= c;
           }
         }
+        if (!end) set_tiles<KT, C::kTiles>(it, tpc, a.causal, W);
         const int is = k & 1;
         if (k >= 2 && !warp_wait(smem_u32(item_empty + is), ((k >> 1) - 1) & 1, abort_s)) {
           failed = true;
@@ -390,25 +409,16 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
         }
         __syncwarp();
         if (end) break;
-        const Geometry ge = geometry<KT, C::kTiles>(it, tpc, a.causal, W);
-        // ---- Q: tokens x G heads x 64 of head_dim ----
-        if (k >= 1 && !warp_wait(smem_u32(q_empty), (k - 1) & 1, abort_s)) {
-          failed = true;
-          break;
-        }
-        if (lane == 0) {
-          const bool has_b = C::kTiles == 2 && it.tok0 + tpc < it.n;
-          const uint32_t box = static_cast<uint32_t>(tpc) * G * 128;
-          mbar_arrive_expect_tx(smem_u32(q_full), box * C::kDCH * (has_b ? 2 : 1));
-          for (int X = 0; X < (has_b ? 2 : 1); ++X)
-#pragma unroll
-            for (int ch = 0; ch < C::kDCH; ++ch)
-              tma_load_3d(s0 + X * C::kQBytes + ch * (128 * 128), &tm_q, ch * 64, it.g * G,
-                          it.q0 + it.tok0 + X * tpc, smem_u32(q_full));
-        }
-        ++k;
-        // ---- K and V tiles, in the order the MMA thread takes them ----
-        for (int j = 0; j < 2 * ge.ntiles; ++j, ++slot) {
+        const bool has_b = it.jB1 > 0;
+        // Q's buffer is the last item's until its last scores are there: Q into L2
+        // meanwhile, and the first K and V tile, whose slots are free before that
+        if (lane < C::kDCH * (has_b ? 2 : 1))
+          prefetch_3d(&tm_q, lane % C::kDCH * 64, it.g * G,
+                      it.q0 + it.tok0 + lane / C::kDCH * tpc);
+        // K and V tiles go in the order the MMA warp takes them
+        for (int j = 0; j < 2 * it.ntiles; ++j, ++slot) {
+          if (j == 2) load_q(it, has_b, k);
+          if (failed) break;
           const int st = slot % C::kSlots;
           if (slot >= C::kSlots &&
               !warp_wait(smem_u32(kv_empty + st), ((slot / C::kSlots) - 1) & 1, abort_s)) {
@@ -422,10 +432,12 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
 #pragma unroll
             for (int ch = 0; ch < C::kDCH; ++ch)
               tma_load_3d(dst + ch * (KT * 128), (j & 1) ? &tm_v : &tm_k, ch * 64, it.g,
-                          it.q0 + ge.k_lo + (j >> 1) * KT, fb);
+                          it.q0 + it.k_lo + (j >> 1) * KT, fb);
           }
           __syncwarp();
         }
+        if (!failed && it.ntiles == 1) load_q(it, has_b, k);
+        if (!failed) ++k;
         if (failed) break;
       }
       if (failed) {
@@ -435,7 +447,7 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
       // the copies already issued land before the block can exit
       for (int t = max(0, slot - C::kSlots); t < slot; ++t)
         (void)mbar_wait(smem_u32(kv_full + t % C::kSlots), (t / C::kSlots) & 1);
-      if (k > 0) (void)mbar_wait(smem_u32(q_full), (k - 1) & 1);
+      if (q_loads > 0) (void)mbar_wait(smem_u32(q_full), (q_loads - 1) & 1);
     } else if (warp == C::kMmaWarp) {
       // ============================= MMA warp ================================
       // One lane issues; the whole warp runs the loop, so that descriptors stay in
@@ -451,18 +463,26 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
       uint32_t p_par[2] = {0u, 0u};       // of the next weights
       int pbuf = 0;
       bool ok = true;
-      for (int k = 0; ok; ++k) {
-        if (!(ok = warp_wait(smem_u32(item_full + (k & 1)), (k >> 1) & 1, abort_s))) break;
-        const Item it = items[k & 1];
+      int nt = 0, jA1 = 0, jB0 = 0, jB1 = 0;
+      // item kk's tiles, in uniform registers; false at the end (or a failed wait)
+      int nt1 = 0, jA1_1 = 0, jB0_1 = 0, jB1_1 = 0;
+      auto look = [&](int kk) {
+        nt1 = 0;
+        if (!(ok = warp_wait(smem_u32(item_full + (kk & 1)), (kk >> 1) & 1, abort_s))) return;
+        const Item it = items[kk & 1];
         __syncwarp();
-        arrive_if(lead, smem_u32(item_empty + (k & 1)));
-        const int g = __shfl_sync(0xFFFFFFFFu, it.g, 0);
-        if (g < 0) break;
-        const Geometry ge = geometry<KT, C::kTiles>(it, tpc, a.causal, W);
-        const int nt = __shfl_sync(0xFFFFFFFFu, ge.ntiles, 0);
-        const int jA1 = __shfl_sync(0xFFFFFFFFu, ge.jA1, 0);
-        const int jB0 = __shfl_sync(0xFFFFFFFFu, ge.jB0, 0);
-        const int jB1 = __shfl_sync(0xFFFFFFFFu, ge.jB1, 0);
+        arrive_if(lead, smem_u32(item_empty + (kk & 1)));
+        nt1 = __shfl_sync(0xFFFFFFFFu, it.ntiles, 0);
+        jA1_1 = __shfl_sync(0xFFFFFFFFu, it.jA1, 0);
+        jB0_1 = __shfl_sync(0xFFFFFFFFu, it.jB0, 0);
+        jB1_1 = __shfl_sync(0xFFFFFFFFu, it.jB1, 0);
+      };
+      look(0);
+      for (int k = 0; ok && nt1 > 0; ++k) {
+        nt = nt1;
+        jA1 = jA1_1;
+        jB0 = jB0_1;
+        jB1 = jB1_1;
         if (!(ok = warp_wait(smem_u32(q_full), k & 1, abort_s))) break;
         auto in = [&](int X, int j) { return X ? (j >= jB0 && j < jB1) : j < jA1; };
         auto last = [&](int X, int j) { return j == (X ? jB1 : jA1) - 1; };
@@ -493,6 +513,8 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
           p_par[X] ^= 1u;
           return true;
         };
+        // the next item is looked up behind this one's last scores, while their
+        // softmax is under way
         auto wait_k = [&]() { return warp_wait(smem_u32(kv_full + kr.at), kr.parity, abort_s); };
         auto wait_v = [&]() { return warp_wait(smem_u32(kv_full + vr.at), vr.parity, abort_s); };
         auto pass_k = [&](int j) {  // K's tile j handed back behind its scores
@@ -508,13 +530,16 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
         for (int X = 0; X < C::kTiles; ++X)
           if (in(X, 0)) scores(X);
         pass_k(0);
-        for (int j = 0; j < nt; ++j) {
+        if (nt == 1) look(k + 1);
+        for (int j = 0; ok && j < nt; ++j) {
           const bool more = j + 1 < nt;
           if (C::kTiles == 1 && more) {  // two score buffers: the next scores go ahead
             if (!(ok = wait_k())) break;
             tc_fence_after();
             scores(0);
             pass_k(j + 1);
+            if (j + 2 == nt) look(k + 1);
+            if (!ok) break;
           }
           if (!(ok = wait_v())) break;
           if (C::kTiles == 2 && more && !(ok = wait_k())) break;
@@ -535,7 +560,10 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
           vr.next();
           vr.next();
           if constexpr (C::kBufs == 2) pbuf ^= 1;
-          if (C::kTiles == 2 && more) pass_k(j + 1);
+          if (C::kTiles == 2 && more) {
+            pass_k(j + 1);
+            if (j + 2 == nt) look(k + 1);
+          }
         }
       }
       if (!ok) {
@@ -567,19 +595,18 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(item_empty + (k & 1)));
       if (it.g < 0) break;
-      const Geometry ge = geometry<KT, C::kTiles>(it, tpc, a.causal, W);
       const int t = it.tok0 + X * tpc + mt;
       const bool rvalid = mt < tpc && t < it.n;
       // keys this row sees: [rlo, rhi); rows of no token count as seeing all
       const int rpos = a.causal ? t : it.n - 1;
       const int rhi = rvalid ? rpos + 1 : INT32_MAX;
       const int rlo = (rvalid && W > 0 && rpos >= W) ? rpos + 1 - W : 0;
-      const int j0 = X ? ge.jB0 : ge.jA0, j1 = X ? ge.jB1 : ge.jA1;
+      const int j0 = X ? it.jB0 : 0, j1 = X ? it.jB1 : it.jA1;
       float m_run = -INFINITY, l_run = 0.0f;
       for (int j = j0; j < j1; ++j) {
         const int c = done + j - j0;
         const uint32_t s_tm = tmem + lane_base + X * 128 + (c % C::kBufs) * KT;
-        const int key0 = ge.k_lo + j * KT;
+        const int key0 = it.k_lo + j * KT;
         if (!warp_wait(s_full(X, c % C::kBufs), (c / C::kBufs) & 1, abort_s)) {
           failed = true;
           break;
@@ -627,7 +654,7 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
 
         // V rows past the sequence's end belong to others: zeroed before the
         // weights are released, by the first query tile that uses the tile
-        const bool zeroer = X == 0 || j >= ge.jA1;
+        const bool zeroer = X == 0 || j >= it.jA1;
         const bool ragged = key0 + KT > it.n;
         const int vs = slot + 2 * j + 1;
         if (zeroer && ragged) {
@@ -690,7 +717,7 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
         l_run = l_run * alpha + ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
       }
       if (failed) break;
-      slot += 2 * ge.ntiles;
+      slot += 2 * it.ntiles;
       if (j1 > j0) {
         done += j1 - j0;
         ++runs;
@@ -707,33 +734,44 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
         const uint32_t valid = __ballot_sync(0xFFFFFFFFu, rvalid);
         const float inv = 1.0f / fmaxf(l_run, 1e-20f);
         const uint32_t stage = s0 + C::kOutOff + warp * 4096;
+        // (head_dim 256 in two parts: a whole row takes too many registers)
+        constexpr int kCols = D <= 128 ? D : 128;
 #pragma unroll 1
-        for (int h = 0; h < D / 64; ++h) {
-          uint32_t v[2][32];
-          tmem_ld32(o_tm + h * 64, v[0]);
-          tmem_ld32(o_tm + h * 64 + 32, v[1]);
+        for (int part = 0; part < D / kCols; ++part) {
+          uint32_t v[kCols / 32][32];
+#pragma unroll
+          for (int ch = 0; ch < kCols / 32; ++ch) tmem_ld32(o_tm + part * kCols + ch * 32, v[ch]);
+          uint64_t at[8];  // the rows this lane stores a piece of
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            at[i] = __shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(orow), 4 * i + (lane >> 3));
           tmem_wait_ld32(v[0]);
-          after_wait32(v[1]);
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            uint32_t w[4];
+          for (int ch = 1; ch < kCols / 32; ++ch) after_wait32(v[ch]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              w[i] = pack_bf16x2(__uint_as_float(v[q >> 2][(q & 3) * 8 + 2 * i]) * inv,
-                                 __uint_as_float(v[q >> 2][(q & 3) * 8 + 2 * i + 1]) * inv);
-            sts128(stage + swz128(lane * 128 + q * 16), w[0], w[1], w[2], w[3]);
+          for (int h = 0; h < kCols / 64; ++h) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              uint32_t w[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                w[i] = pack_bf16x2(__uint_as_float(v[2 * h + (q >> 2)][(q & 3) * 8 + 2 * i]) * inv,
+                                   __uint_as_float(v[2 * h + (q >> 2)][(q & 3) * 8 + 2 * i + 1]) *
+                                       inv);
+              sts128(stage + swz128(lane * 128 + q * 16), w[0], w[1], w[2], w[3]);
+            }
+            __syncwarp();
+            uint4 w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              w[i] = lds128(stage + swz128((4 * i + (lane >> 3)) * 128 + (lane & 7) * 16));
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if ((valid >> (4 * i + (lane >> 3))) & 1u)
+                *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(at[i]) + part * kCols + h * 64 +
+                                          (lane & 7) * 8) = w[i];
+            __syncwarp();
           }
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int row = 4 * i + (lane >> 3);
-            const uint4 w = lds128(stage + swz128(row * 128 + (lane & 7) * 16));
-            const uint64_t at = __shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(orow), row);
-            if ((valid >> row) & 1u)
-              *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(at) + h * 64 + (lane & 7) * 8) =
-                  w;
-          }
-          __syncwarp();
         }
         tc_fence_before();
       }
