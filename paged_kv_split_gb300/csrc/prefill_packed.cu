@@ -309,36 +309,113 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
   bool failed = false;
   const volatile int* no_abort = reinterpret_cast<const volatile int*>(holder + 2);  // stays 0
 
-  // registers dealt by warpgroup (two tiles: 3 x 168 at launch, then 64 and 2 x 216)
+  // registers dealt by warpgroup (two tiles: 3 x 168 at launch, then 72 and 2 x 216)
   if (warp >= C::kSoftWarps) {
-    if constexpr (C::kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if constexpr (C::kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == C::kProdWarp) {
       // ============================ copying warp ============================
-      const int span = C::kTiles * tpc;                        // tokens of an item
-      const int levels = (a.max_q_len + span - 1) / span;      // most items of a sequence
-      const bool first_cta = blockIdx.x == 0;
-      // items of sequences at levels >= p
-      auto above = [&](int p, bool tell) {
-        int c = 0;
-        for (int b = lane; b < a.num_seqs; b += 32)
-          c += max(0, (prompt_len(a, b, tell) + span - 1) / span - p);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xFFFFFFFFu, c, o);
-        return c;
-      };
+      const int span = C::kTiles * tpc;                    // tokens of an item
+      const int levels = (a.max_q_len + span - 1) / span;  // most items of a sequence
       const int hkv = a.num_kv_heads;
-      const int64_t total = static_cast<int64_t>(above(0, first_cta)) * hkv;
+      auto levels_of = [&](int n) { return (n + span - 1) / span; };
+      // lane x keeps sequence x's tokens and levels: batches of up to 32 need no loads
+      const int my_n = lane < a.num_seqs ? prompt_len(a, lane, blockIdx.x == 0) : 0;
+      const int my_levels = levels_of(my_n);
+      // items a kv head has at levels >= p
+      auto above = [&](int p, bool tell) {
+        int c = max(0, my_levels - p);
+        for (int b = 32 + lane; b < a.num_seqs; b += 32)
+          c += max(0, levels_of(prompt_len(a, b, tell)) - p);
+        return static_cast<int>(__reduce_add_sync(0xFFFFFFFFu, c));
+      };
+      const int64_t total = static_cast<int64_t>(above(0, blockIdx.x == 0)) * hkv;
+      int64_t round = 0;
+      int top = levels;  // the level of the last item: ranks go up, levels down
+      // this CTA's next item; g = -1: none left
+      auto find = [&]() {
+        Item it = {};
+        it.g = -1;
+        int64_t rank;
+        do {  // at most one round does not reach this CTA
+          if (round * static_cast<int64_t>(gridDim.x) >= total) return it;
+          rank = round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+          ++round;
+        } while (rank >= total);
+        int pr;
+        if (total <= INT32_MAX) {
+          pr = static_cast<int>(static_cast<uint32_t>(rank) / static_cast<uint32_t>(hkv));
+        } else {
+          pr = static_cast<int>(rank / hkv);
+        }
+        it.g = static_cast<int>(rank - static_cast<int64_t>(pr) * hkv);
+        // the highest level p with above(p) > pr, searched below the last one
+        int lo = 0, hi = top;  // above(lo) > pr, above(hi) <= pr or unknown at top
+        int over = 0;          // above(lo + 1)
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          const int c = above(mid, false);
+          if (c > pr) {
+            lo = mid;
+          } else {
+            hi = mid;
+            over = c;
+          }
+        }
+        if (hi == top) over = above(hi, false);
+        if (over > pr) {  // still on the last item's level
+          lo = hi;
+          over = above(lo + 1, false);
+        }
+        top = lo;
+        int idx = pr - over;  // among the sequences that have level lo, in order
+        for (int base = 0; base < a.num_seqs; base += 32) {
+          const int b = base + lane;
+          const int n = base == 0 ? my_n : (b < a.num_seqs ? prompt_len(a, b, false) : 0);
+          const uint32_t m =
+              __ballot_sync(0xFFFFFFFFu, (base == 0 ? my_levels : levels_of(n)) > lo);
+          const int c = __popc(m);
+          if (idx < c) {
+            uint32_t left = m;
+            for (int i = 0; i < idx; ++i) left &= left - 1;
+            const int src = __ffs(left) - 1;
+            it.n = __shfl_sync(0xFFFFFFFFu, n, src);
+            it.q0 = __ldg(a.cu_q + base + src);
+            it.tok0 = lo * span;
+            break;
+          }
+          idx -= c;
+        }
+        set_tiles<KT, C::kTiles>(it, tpc, a.causal, W);
+        return it;
+      };
+      // item kk for the others to read; its Q into L2
+      auto publish = [&](const Item& it, int kk) {
+        const int is = kk & 1;
+        if (kk >= 2 && !warp_wait(smem_u32(item_empty + is), ((kk >> 1) - 1) & 1, abort_s)) {
+          failed = true;
+          return;
+        }
+        if (lane == 0) {
+          items[is] = it;
+          mbar_arrive(smem_u32(item_full + is));
+        }
+        __syncwarp();
+        if (it.g >= 0 && lane < C::kDCH * (it.jB1 > 0 ? 2 : 1))
+          prefetch_3d(&tm_q, lane % C::kDCH * 64, it.g * G,
+                      it.q0 + it.tok0 + lane / C::kDCH * tpc);
+      };
       // Q of item kk: tokens x G heads x 64 of head_dim a copy
       int q_loads = 0;
-      auto load_q = [&](const Item& it, bool has_b, int kk) {
+      auto load_q = [&](const Item& it, int kk) {
         if (kk >= 1 && !warp_wait(smem_u32(q_empty), (kk - 1) & 1, abort_s)) {
           failed = true;
           return;
         }
         if (lane == 0) {
           const uint32_t box = static_cast<uint32_t>(tpc) * G * 128;
-          mbar_arrive_expect_tx(smem_u32(q_full), box * C::kDCH * (has_b ? 2 : 1));
-          for (int X = 0; X < (has_b ? 2 : 1); ++X)
+          const int parts = it.jB1 > 0 ? 2 : 1;
+          mbar_arrive_expect_tx(smem_u32(q_full), box * C::kDCH * parts);
+          for (int X = 0; X < parts; ++X)
 #pragma unroll
             for (int ch = 0; ch < C::kDCH; ++ch)
               tma_load_3d(s0 + X * C::kQBytes + ch * (128 * 128), &tm_q, ch * 64, it.g * G,
@@ -347,77 +424,22 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
         ++q_loads;
         __syncwarp();
       };
-      int slot = 0;      // ring slots filled so far
-      int k = 0;         // items so far
-      int top = levels;  // the level of the last item: ranks go up, levels down
-      for (int64_t round = 0;; ++round) {
-        const int64_t rank = round * gridDim.x +
-                             ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-        const bool end = round * static_cast<int64_t>(gridDim.x) >= total;
-        if (!end && rank >= total) continue;  // a round that does not reach this CTA
-        Item it = {};
-        it.g = -1;
-        if (!end) {
-          const int pr = static_cast<int>(rank / hkv);
-          // the highest level p with above(p) > pr, searched below the last one
-          int lo = 0, hi = top;  // above(lo) > pr, above(hi) <= pr or unknown at top
-          int over = 0;          // above(lo + 1)
-          while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            const int c = above(mid, false);
-            if (c > pr) {
-              lo = mid;
-            } else {
-              hi = mid;
-              over = c;
-            }
+      int slot = 0;  // ring slots filled so far
+      Item it = find();
+      publish(it, 0);
+      for (int k = 0; it.g >= 0 && !failed; ++k) {
+        Item next;
+        // K and V tiles go in the order the MMA warp takes them. Q's buffer is the
+        // last item's until its last scores are there: the first K and V tile, whose
+        // slots are free before that, go ahead of it. The next item is sought while
+        // the ring is full
+        const int loads = 2 * it.ntiles;
+        for (int j = 0; j < loads; ++j, ++slot) {
+          if (j == (k == 0 ? 0 : 2)) load_q(it, k);
+          if (j == 4) {
+            next = find();
+            publish(next, k + 1);
           }
-          if (hi == top) over = above(hi, false);
-          if (over > pr) {  // still on the last item's level
-            lo = hi;
-            over = above(lo + 1, false);
-          }
-          top = lo;
-          int idx = pr - over;  // among the sequences that have level lo, in order
-          it.g = static_cast<int>(rank % hkv);
-          for (int base = 0; base < a.num_seqs; base += 32) {
-            const int b = base + lane;
-            const int n = b < a.num_seqs ? prompt_len(a, b, false) : 0;
-            const uint32_t m = __ballot_sync(0xFFFFFFFFu, (n + span - 1) / span > lo);
-            const int c = __popc(m);
-            if (idx < c) {
-              uint32_t left = m;
-              for (int i = 0; i < idx; ++i) left &= left - 1;
-              const int src = __ffs(left) - 1;
-              it.n = __shfl_sync(0xFFFFFFFFu, n, src);
-              it.q0 = __ldg(a.cu_q + base + src);
-              it.tok0 = lo * span;
-              break;
-            }
-            idx -= c;
-          }
-        }
-        if (!end) set_tiles<KT, C::kTiles>(it, tpc, a.causal, W);
-        const int is = k & 1;
-        if (k >= 2 && !warp_wait(smem_u32(item_empty + is), ((k >> 1) - 1) & 1, abort_s)) {
-          failed = true;
-          break;
-        }
-        if (lane == 0) {
-          items[is] = it;
-          mbar_arrive(smem_u32(item_full + is));
-        }
-        __syncwarp();
-        if (end) break;
-        const bool has_b = it.jB1 > 0;
-        // Q's buffer is the last item's until its last scores are there: Q into L2
-        // meanwhile, and the first K and V tile, whose slots are free before that
-        if (lane < C::kDCH * (has_b ? 2 : 1))
-          prefetch_3d(&tm_q, lane % C::kDCH * 64, it.g * G,
-                      it.q0 + it.tok0 + lane / C::kDCH * tpc);
-        // K and V tiles go in the order the MMA warp takes them
-        for (int j = 0; j < 2 * it.ntiles; ++j, ++slot) {
-          if (j == 2) load_q(it, has_b, k);
           if (failed) break;
           const int st = slot % C::kSlots;
           if (slot >= C::kSlots &&
@@ -436,9 +458,13 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
           }
           __syncwarp();
         }
-        if (!failed && it.ntiles == 1) load_q(it, has_b, k);
-        if (!failed) ++k;
         if (failed) break;
+        if (loads == 2 && k > 0) load_q(it, k);
+        if (loads <= 4 && !failed) {
+          next = find();
+          publish(next, k + 1);
+        }
+        it = next;
       }
       if (failed) {
         if (lane == 0) atomicOr(a.flags, PD_DEV_TIMEOUT);
