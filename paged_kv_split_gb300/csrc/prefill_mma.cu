@@ -256,6 +256,8 @@ __global__ void __launch_bounds__(kMmaThreads, D <= 128 ? 2 : 1)
       for (int j = 0; j < C::kNCopy; ++j) {
         const int tt = t0 + j * C::kBR;
         pages[j] = -1;
+        // a copy that is not made (past the keys, a page outside the pool) masks its keys
+        I8Scales sc = {0.0f, -INFINITY, 0.0f, 0.0f};
         if (tt < k_hi) {
           const int pidx = tt / bs;
           if (pidx - cached_base >= 32 || pidx < cached_base) {  // warp-uniform refill
@@ -272,19 +274,20 @@ __global__ void __launch_bounds__(kMmaThreads, D <= 128 ? 2 : 1)
             }
           }
           const int pg = __shfl_sync(0xFFFFFFFFu, my_entry, pidx - cached_base);
-          if constexpr (FMT == PD_KV_INT8) {
-            const float ks = __shfl_sync(0xFFFFFFFFu, my_ks, pidx - cached_base);
-            const float vs = __shfl_sync(0xFFFFFFFFu, my_vs, pidx - cached_base);
-            if (lane == 0)
-              scales[st * C::kNCopy + j] =
-                  I8Scales{ks, __log2f(vs), __fdividef(1.0f, vs), 0.0f};
-          }
           if (pg >= 0 && pg < a.num_blocks) {
             pages[j] = pg;
             bytes += 2u * C::kCopyBytes;
+            if constexpr (FMT == PD_KV_INT8) {
+              const float ks = __shfl_sync(0xFFFFFFFFu, my_ks, pidx - cached_base);
+              const float vs = __shfl_sync(0xFFFFFFFFu, my_vs, pidx - cached_base);
+              sc = I8Scales{ks, __log2f(vs), __fdividef(1.0f, vs), 0.0f};
+            }
           } else {
             bad |= 1u << j;
           }
+        }
+        if constexpr (FMT == PD_KV_INT8) {
+          if (lane == 0) scales[st * C::kNCopy + j] = sc;
         }
       }
       const uint32_t fb = smem_u32(&full_bar[st]);

@@ -309,3 +309,24 @@ def test_other_calls_refuse_the_form():
         with pytest.raises(B.PdError) as e:
             call()
         assert e.value.status == 2
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_chunk_ends_inside_a_stage(d):
+    """The places of a stage that no page is copied to hold what was there before,
+    here NaN from another kernel's rows: no part of the result."""
+    B = U.pd()
+    foul = torch.full((4096, 16, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+    B.pd_prefill_packed(foul, foul[:, :8], foul[:, :8], U.to_dev(np.array([0, 4096], np.int32)),
+                        torch.empty_like(foul), max_q_len=4096, scale=1.0)
+    lens = [5 + 16 * (i % 7) for i in range(64)]
+    c = Case(lens, 16, 8, d, 16, seed=22)
+    qb = V.bf16_bits(c.rng.standard_normal((len(lens), 16, d)).astype(np.float32))
+    cu = np.arange(len(lens) + 1, dtype=np.int32)
+    q = U.bf16_dev(qb)
+    out = torch.full_like(q, 7.0)
+    U.pd().pd_prefill(q, U.to_dev(cu), U.to_dev(c.k), U.to_dev(c.v), U.to_dev(c.tables),
+                      U.to_dev(c.lens), out, max_q_len=1, **c.args())
+    torch.cuda.synchronize()
+    want, bound = R.decode_f64(qb, c.k, c.v, c.tables, lens, 8, 16, c.scale)
+    assert (np.abs(V.f32(bits(out)) - want) <= bound).all()
