@@ -271,8 +271,8 @@ __global__ void __launch_bounds__(kMmaThreads,
         my_entry = base + lane < pages ? bt[base + lane] : -1;
         if (my_entry >= 0 && my_entry < a.num_blocks) {
           const int64_t at = my_entry * a.page_bytes + a.data_bytes + 4 * g;
-          my_ks = __ldg(reinterpret_cast<const float*>(a.k_cache + at));
-          my_vs = __ldg(reinterpret_cast<const float*>(a.v_cache + at));
+          my_ks = *reinterpret_cast<const float*>(a.k_cache + at);
+          my_vs = *reinterpret_cast<const float*>(a.v_cache + at);
         }
       };
       refill(first_page);
