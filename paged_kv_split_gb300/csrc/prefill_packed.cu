@@ -228,7 +228,7 @@ __device__ __forceinline__ void set_tiles(Item& it, int tpc, int causal, int W) 
 
 // Tokens of sequence b, or 0 where its counts do not fit the batch.
 __device__ __forceinline__ int prompt_len(const PackedArgs& a, int b, bool tell) {
-  const int q0 = __ldg(a.cu_q + b), q1 = __ldg(a.cu_q + b + 1);
+  const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1];
   const int n = q1 - q0;
   if (q0 < 0 || n < 0 || q1 > a.total_q || n > a.max_q_len) {
     if (tell) atomicOr(a.flags, PD_DEV_BAD_SEQ_LEN);
@@ -314,77 +314,75 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
     if constexpr (C::kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == C::kProdWarp) {
       // ============================ copying warp ============================
-      const int span = C::kTiles * tpc;                    // tokens of an item
-      const int levels = (a.max_q_len + span - 1) / span;  // most items of a sequence
+      const int span = C::kTiles * tpc;  // tokens of an item
       const int hkv = a.num_kv_heads;
-      auto levels_of = [&](int n) { return (n + span - 1) / span; };
-      // lane x keeps sequence x's tokens and levels: batches of up to 32 need no loads
-      const int my_n = lane < a.num_seqs ? prompt_len(a, lane, blockIdx.x == 0) : 0;
-      const int my_levels = levels_of(my_n);
-      // items a kv head has at levels >= p
-      auto above = [&](int p, bool tell) {
-        int c = max(0, my_levels - p);
-        for (int b = 32 + lane; b < a.num_seqs; b += 32)
-          c += max(0, levels_of(prompt_len(a, b, tell)) - p);
-        return static_cast<int>(__reduce_add_sync(0xFFFFFFFFu, c));
+      // Items in order: levels from the highest down, in a level the sequences that
+      // reach it, in order, and each one's kv heads. This CTA's ranks only go up, so
+      // a place in that order moves along: 32 sequences at a time (lane x has the
+      // batch's sequence x, and that of the batch to come), then the next level
+      struct Seq {
+        int n, levels;
       };
-      const int64_t total = static_cast<int64_t>(above(0, blockIdx.x == 0)) * hkv;
+      auto seq_at = [&](int b, bool tell) {
+        const int n = b < a.num_seqs ? prompt_len(a, b, tell) : 0;
+        return Seq{n, (n + span - 1) / span};
+      };
+      const int batches = (a.num_seqs + 31) / 32;
+      Seq now = seq_at(lane, blockIdx.x == 0);
+      int level = now.levels;
+      for (int i = 1; i < batches; ++i)
+        level = max(level, seq_at(i * 32 + lane, blockIdx.x == 0).levels);
+      level = __reduce_max_sync(0xFFFFFFFFu, level) - 1;
+      Seq ahead = batches > 1 ? seq_at(32 + lane, false) : now;
+      int batch = 0, before = 0;  // before: (sequence, level) pairs before the place
       int64_t round = 0;
-      int top = levels;  // the level of the last item: ranks go up, levels down
       // this CTA's next item; g = -1: none left
       auto find = [&]() {
         Item it = {};
         it.g = -1;
-        int64_t rank;
-        do {  // at most one round does not reach this CTA
-          if (round * static_cast<int64_t>(gridDim.x) >= total) return it;
-          rank = round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-          ++round;
-        } while (rank >= total);
-        int pr;
-        if (total <= INT32_MAX) {
-          pr = static_cast<int>(static_cast<uint32_t>(rank) / static_cast<uint32_t>(hkv));
-        } else {
-          pr = static_cast<int>(rank / hkv);
-        }
-        it.g = static_cast<int>(rank - static_cast<int64_t>(pr) * hkv);
-        // the highest level p with above(p) > pr, searched below the last one
-        int lo = 0, hi = top;  // above(lo) > pr, above(hi) <= pr or unknown at top
-        int over = 0;          // above(lo + 1)
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          const int c = above(mid, false);
-          if (c > pr) {
-            lo = mid;
-          } else {
-            hi = mid;
-            over = c;
-          }
-        }
-        if (hi == top) over = above(hi, false);
-        if (over > pr) {  // still on the last item's level
-          lo = hi;
-          over = above(lo + 1, false);
-        }
-        top = lo;
-        int idx = pr - over;  // among the sequences that have level lo, in order
-        for (int base = 0; base < a.num_seqs; base += 32) {
-          const int b = base + lane;
-          const int n = base == 0 ? my_n : (b < a.num_seqs ? prompt_len(a, b, false) : 0);
-          const uint32_t m =
-              __ballot_sync(0xFFFFFFFFu, (base == 0 ? my_levels : levels_of(n)) > lo);
+        const int64_t rank =
+            round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        ++round;
+        const int64_t pr64 = rank <= UINT32_MAX
+                                 ? static_cast<uint32_t>(rank) / static_cast<uint32_t>(hkv)
+                                 : rank / hkv;
+        if (pr64 > INT32_MAX) return it;
+        const int pr = static_cast<int>(pr64);
+        while (level >= 0) {
+          const uint32_t m = __ballot_sync(0xFFFFFFFFu, now.levels > level);
           const int c = __popc(m);
-          if (idx < c) {
+          if (batches == 1 && pr - before >= 8 * c) {
+            // far to go: levels from here down to the next shorter sequence's have as
+            // many, and are skipped at once, to the pair's own or past them all (one
+            // prompt of 4096 tokens, 64 levels: 57.7 us, level by level 60.6)
+            const int next = static_cast<int>(
+                __reduce_max_sync(0xFFFFFFFFu, now.levels > level ? 0 : now.levels));
+            const int skip = min((pr - before) / c, level + 1 - next);
+            before += skip * c;
+            level -= skip;
+            if (level < next) continue;
+          }
+          if (pr - before < c) {
             uint32_t left = m;
-            for (int i = 0; i < idx; ++i) left &= left - 1;
+            for (int i = before; i < pr; ++i) left &= left - 1;
             const int src = __ffs(left) - 1;
-            it.n = __shfl_sync(0xFFFFFFFFu, n, src);
-            it.q0 = __ldg(a.cu_q + base + src);
-            it.tok0 = lo * span;
+            it.g = static_cast<int>(rank - pr64 * hkv);
+            it.n = __shfl_sync(0xFFFFFFFFu, now.n, src);
+            it.q0 = a.cu_q[batch * 32 + src];
+            it.tok0 = level * span;
             break;
           }
-          idx -= c;
+          before += c;
+          if (++batch == batches) {
+            batch = 0;
+            --level;
+          }
+          if (batches > 1) {
+            now = ahead;
+            ahead = seq_at((batch + 1 == batches ? 0 : batch + 1) * 32 + lane, false);
+          }
         }
+        if (it.g < 0) return it;
         set_tiles<KT, C::kTiles>(it, tpc, a.causal, W);
         return it;
       };

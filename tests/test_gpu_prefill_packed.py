@@ -201,3 +201,20 @@ def test_long_prompt_against_crosscheck():
     a, b = c.run().float(), c.run(crosscheck=True).float()
     # two roundings of the output and the rounded weights: a few bf16 steps of V's size
     assert (a - b).abs().max() < 4 * 2.0 ** -8 * b.abs().max()
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(16, 1, 64), (8, 8, 128), (12, 2, 256)])
+@pytest.mark.parametrize("count,longest", [(1, 2500), (31, 500), (32, 700), (33, 700), (64, 300),
+                                           (65, 300), (200, 90)])
+def test_every_item_is_found(count, longest, hq, hkv, d):
+    """Many levels, lengths that repeat, sequences of none, more than a warp of them:
+    each row of each sequence is some CTA's, and no other row is touched."""
+    rng = np.random.default_rng(count)
+    lens = rng.integers(0, longest, count)
+    lens[rng.integers(0, count)] = longest
+    lens[::5] = lens[0]
+    c = Case(np.concatenate([lens, [9]]), hq, hkv, d, seed=count)
+    c.cu = c.cu[:-1]
+    a, b = c.run().float(), c.run(crosscheck=True).float()
+    assert (a[-9:] == 7.0).all() and (b[-9:] == 7.0).all()
+    assert (a - b).abs().max() < 4 * 2.0 ** -8 * b.abs().max()
