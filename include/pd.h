@@ -51,7 +51,10 @@
  *                   pd_rope_append_int8, read by pd_prefill and the pd_decode*
  *                   calls but pd_decode_tree; the other calls refuse it
  *                   (PD_ERR_UNSUPPORTED): a row is only worth something beside
- *                   its page's scale.
+ *                   its page's scale. Its readers weight a row by its value
+ *                   scale too: of one sequence and kv head, rows whose value
+ *                   scale is less than 2^-90 of the largest may drop out of the
+ *                   softmax's sum.
  *   Slot s of the pool is page s / block_size, row s % block_size.
  */
 #ifndef PD_H_
@@ -599,7 +602,8 @@ int pd_compact_tree(void* k_caches, void* v_caches, int64_t layer_bytes, int32_t
  * codes are rint(x * (1 / scale)) clamped to +-127 (NaN: 0). rint rounds to
  * nearest even. So codes are reproducible bit for bit, and a value appended
  * with scale s is off by s / 2 at most, plus half of each scale its page grows
- * to later. Rows of the page behind the new ones keep their bytes.
+ * to later (one past 127 * 2^60 is clamped there). Rows of the page behind the
+ * new ones keep their bytes.
  * A page that gets rows belongs to one sequence (shared prefixes: whole pages).
  * A sequence whose counts do not fit (n_b > max_q_len, L_b < n_b, L_b beyond
  * the block table, rows beyond total_q) raises PD_DEV_BAD_SEQ_LEN and nothing of

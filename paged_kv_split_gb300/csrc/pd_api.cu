@@ -1316,8 +1316,8 @@ int pd_rope_append_int8(const void* qkv, int64_t qkv_stride, const int32_t* cu_q
   a.data_bytes = int8_data_bytes(block_size, num_kv_heads, head_dim);
   a.num_seqs = num_seqs;
   a.total_q = total_q;
-  // no sequence has more tokens than there are rows
-  a.max_q_len = max_q_len < total_q ? max_q_len : total_q;
+  // no sequence has more tokens than there are rows, or places in its block table
+  a.max_q_len = std::min(std::min(max_q_len, total_q), max_blocks_per_seq * block_size);
   a.num_q_heads = num_q_heads;
   a.num_kv_heads = num_kv_heads;
   a.block_size = block_size;

@@ -10,11 +10,19 @@
 //           rint(code * (old scale / scale)) for the page's earlier rows
 // A (page, head) is one CTA's or one lane group's alone, so nothing is atomic.
 //
-// Two kernels. A prompt's page takes 16 or 32 rows: one CTA per page and run
-// of heads holds a head's rows in registers (kLanes lanes a row, 16 elements a
-// lane), finds the maximum over the block, and writes the codes: one pass over
-// memory. A decode step (max_q_len 1) has one row a page: there a lane group
-// takes a (token, head) by itself, without a block barrier.
+// Two kernels. A prompt's page takes 16 or 32 rows: one CTA per page and run of
+// heads holds a head's rows in registers (kLanes lanes a row, 16 elements a lane),
+// finds the maximum over the block, and writes the codes: one pass over memory,
+// which bounds it. 8945 rows of 32/8 heads of 128, 245 MB with the output rows: 49
+// us, 5.0 TB/s, of it 195 MB from and to DRAM (the rest stays in L2).
+//
+// A decode step (max_q_len 1) has one row a page. It is a chain of memory latencies
+// (counts, table, scale and rows) that no bandwidth shortens, and in most steps
+// some page's scale grows. There a warp takes a kv head: its lane groups all work
+// the new row out, without a block barrier, and hold the page's earlier rows, read
+// beside the scale, in case it grows. 64 sequences of 32/8 heads of 128, every page
+// a step fuller than in the call before: 3.8 us; one lane group a kv head, which
+// reads the rows once the scale is known, 13.0.
 #include "mma_common.cuh"
 #include "serve_common.cuh"
 
@@ -95,18 +103,45 @@ __device__ __forceinline__ uint2 codes8(const float* x, float inv) {
     w[i >> 2] |= (static_cast<uint32_t>(int8_code(x[i], inv)) & 0xFFu) << (8 * (i & 3));
   return make_uint2(w[0], w[1]);
 }
-// codes of 16 bytes brought to another scale
+// Codes of 16 bytes times a ratio <= 1: c + 128 as the low byte of 2^23 gives the
+// code as a float exactly, and adding 1.5 * 2^23 rounds the product to the nearest
+// even integer, whose low byte is the new code.
 __device__ __forceinline__ uint4 rescale16(const uint4& v, float ratio) {
   const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-  uint32_t o[4] = {0u, 0u, 0u, 0u};
+  uint32_t o[4];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int8_t c = static_cast<int8_t>((u[i >> 2] >> (8 * (i & 3))) & 0xFFu);
-    o[i >> 2] |= (static_cast<uint32_t>(int8_code(static_cast<float>(c), ratio)) & 0xFFu)
-                 << (8 * (i & 3));
+  for (int w = 0; w < 4; ++w) {
+    const uint32_t flipped = u[w] ^ 0x80808080u;
+    uint32_t n[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float c = __uint_as_float(__byte_perm(flipped, 0x4B000000u, 0x7440u + i)) - 8388736.0f;
+      n[i] = __float_as_uint(__fadd_rn(__fmul_rn(c, ratio), 12582912.0f));
+    }
+    o[w] = __byte_perm(__byte_perm(n[0], n[1], 0x0040), __byte_perm(n[2], n[3], 0x0040), 0x5410);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
+// A lane's part of rows first, first + step .. below n of a head, N of them at a
+// time: all of a batch is on its way before the first is needed.
+template <int N>
+struct OldRows {
+  uint4 v[N];
+  __device__ __forceinline__ void load(const uint8_t* at, int row_bytes, int first, int step,
+                                       int n) {
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (first + k * step < n)
+        v[k] = *reinterpret_cast<const uint4*>(at + (first + k * step) * row_bytes);
+  }
+  __device__ __forceinline__ void store(uint8_t* at, int row_bytes, int first, int step, int n,
+                                        float ratio) const {
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (first + k * step < n)
+        *reinterpret_cast<uint4*>(at + (first + k * step) * row_bytes) = rescale16(v[k], ratio);
+  }
+};
 
 // A sequence's rows in the batch and in its cache; n = 0 where its counts do
 // not fit.
@@ -277,35 +312,36 @@ __global__ void __launch_bounds__(kAppendThreads) append_pages_kernel(const Appe
 }
 
 // ---------------------------------------------------------------------------
-// One row a sequence: lane groups of kLanes take (sequence, head) items.
-template <int D, bool INTER>
+// One row a sequence. A kv head of K or V is a warp's, each of whose lane groups
+// of kLanes works the new row out; the page's earlier rows are dealt among them.
+// A q head is a lane group's.
+template <int D, int BS, bool INTER>
 __global__ void __launch_bounds__(kAppendThreads) append_step_kernel(const AppendArgs a) {
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int kLanes = D / 16;
-  constexpr int kSlots = kAppendThreads / kLanes;
-  const int l = threadIdx.x % kLanes, slot = threadIdx.x / kLanes;
+  constexpr int kWarps = kAppendThreads / 32, kSlots = 32 / kLanes;
+  // a lane's earlier rows, at most 16 (64 registers) at a time: BS / kSlots are all
+  constexpr int kAhead = BS / kSlots < 16 ? BS / kSlots : 16;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int l = lane % kLanes, slot = lane / kLanes;
   const int hq = a.num_q_heads, hkv = a.num_kv_heads;
-  const int heads = hq + 2 * hkv;
   const int b = blockIdx.y;
-  const int h = blockIdx.x * kSlots + slot;
-  if (h >= heads) return;  // whole groups leave: the shuffles below stay within one
-  const bool teller = l == 0 && h == 0;
+  const int kv_blocks = (2 * hkv + kWarps - 1) / kWarps;
+  const bool is_q = blockIdx.x >= kv_blocks;
+  // the head's place in the row
+  const int h = is_q ? ((blockIdx.x - kv_blocks) * kWarps + warp) * kSlots + slot
+                     : hq + blockIdx.x * kWarps + warp;
+  if (h >= (is_q ? hq : hq + 2 * hkv)) return;  // kv heads: a whole warp leaves
+  const bool is_v = h >= hq + hkv;
+  const bool teller = h == hq && lane == 0;
   const AppendSeq sq = append_seq(a, b, teller);
   if (sq.n <= 0) return;
-  const bool is_v = h >= hq + hkv, is_k = !is_v && h >= hq;
   const LaneChunks ch = lane_chunks(l, a.rot_dim, INTER);
   const int64_t row = sq.q0;
   const uint16_t* src = a.qkv + row * a.qkv_stride + static_cast<int64_t>(h) * D;
-  uint4 raw[2] = {*reinterpret_cast<const uint4*>(src + ch.c0),
-                  *reinterpret_cast<const uint4*>(src + ch.c1)};
-  const int bs = a.block_size;
-  const int page_index = sq.first / bs, r = sq.first % bs;
-  int64_t page = 0;
-  if (h >= hq || teller)
-    page = a.block_tables[static_cast<int64_t>(b) * a.max_blocks_per_seq + page_index];
-  const bool in_pool = page >= 0 && page < a.num_blocks;
-  if (!in_pool && teller) atomicOr(a.flags, PD_DEV_BAD_PAGE);
+  const uint4 raw[2] = {*reinterpret_cast<const uint4*>(src + ch.c0),
+                        *reinterpret_cast<const uint4*>(src + ch.c1)};
   float x[16];
   unpack16(raw, x);
   if (!is_v) {
@@ -315,41 +351,55 @@ __global__ void __launch_bounds__(kAppendThreads) append_step_kernel(const Appen
       load_turn(a, pos, l, c, s);
       rotate16(x, c, s, INTER);
     }
-    if (!is_k || a.k_out) {
-      uint16_t* dst = (is_k ? a.k_out + row * a.k_out_stride + static_cast<int64_t>(h - hq) * D
-                            : a.q_out + row * a.q_out_stride + static_cast<int64_t>(h) * D);
-      uint4 w[2];
-      pack16(x, w);
-      *reinterpret_cast<uint4*>(dst + ch.c0) = w[0];
-      *reinterpret_cast<uint4*>(dst + ch.c1) = w[1];
-    }
   }
-  if (h < hq || !in_pool) return;
-  const uint32_t mask =
-      kLanes == 32 ? 0xFFFFFFFFu
-                   : ((1u << (kLanes & 31)) - 1u) << (((threadIdx.x & 31) / kLanes) * kLanes);
+  auto put = [&](uint16_t* dst) {
+    uint4 w[2];
+    pack16(x, w);
+    *reinterpret_cast<uint4*>(dst + ch.c0) = w[0];
+    *reinterpret_cast<uint4*>(dst + ch.c1) = w[1];
+  };
+  if (is_q) {
+    put(a.q_out + row * a.q_out_stride + static_cast<int64_t>(h) * D);
+    return;
+  }
+  const int page_index = sq.first / BS, r = sq.first % BS;
+  const int64_t page =
+      a.block_tables[static_cast<int64_t>(b) * a.max_blocks_per_seq + page_index];
+  const bool in_pool = page >= 0 && page < a.num_blocks;
+  if (!in_pool && teller) atomicOr(a.flags, PD_DEV_BAD_PAGE);
   const int g = is_v ? h - hq - hkv : h - hq;
-  uint8_t* base = (is_v ? a.v_cache : a.k_cache) + page * a.page_bytes;
+  uint8_t* base = (is_v ? a.v_cache : a.k_cache) + (in_pool ? page * a.page_bytes : 0);
   float* scale_p = reinterpret_cast<float*>(base + a.data_bytes) + g;
-  const float have = r > 0 ? *scale_p : 0.0f;
+  uint8_t* lines = base + static_cast<int64_t>(g) * BS * D;
+  // the earlier rows come with the scale: a page that grows waits no second time
+  const int have_rows = in_pool ? r : 0;
+  const float have = have_rows > 0 ? *scale_p : 0.0f;
+  OldRows<kAhead> old;
+  old.load(lines + l * 16, D, slot, kSlots, have_rows);
   float m = finite_max(x, 0.0f);
 #pragma unroll
-  for (int o = kLanes / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(mask, m, o));
+  for (int o = kLanes / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  // every lane has read the row (k_out may be the row itself) and the old scale
+  __syncwarp();
+  if (!is_v && a.k_out && slot == 0)
+    put(a.k_out + row * a.k_out_stride + static_cast<int64_t>(g) * D);
+  if (!in_pool) return;
   const float want = wanted_scale(m);
   const bool grown = r > 0 && want > have;
   const float scale = (r == 0 || grown) ? want : have;
-  const float inv = __fdiv_rn(1.0f, scale);
-  uint8_t* lines = base + static_cast<int64_t>(g) * bs * D;
-  *reinterpret_cast<uint2*>(lines + r * D + ch.c0) = codes8(x, inv);
-  *reinterpret_cast<uint2*>(lines + r * D + ch.c1) = codes8(x + 8, inv);
+  if (slot == 0) {
+    const float inv = __fdiv_rn(1.0f, scale);
+    *reinterpret_cast<uint2*>(lines + r * D + ch.c0) = codes8(x, inv);
+    *reinterpret_cast<uint2*>(lines + r * D + ch.c1) = codes8(x + 8, inv);
+  }
   if (r == 0 || grown) {
-    __syncwarp(mask);  // every lane of the group has read the old scale
-    if (l == 0) *scale_p = scale;
+    if (lane == 0) *scale_p = scale;
     if (grown) {
       const float ratio = __fdiv_rn(have, scale);
-      for (int i = 0; i < r; ++i) {
-        uint4* p = reinterpret_cast<uint4*>(lines + i * D + l * 16);
-        *p = rescale16(*p, ratio);
+      old.store(lines + l * 16, D, slot, kSlots, r, ratio);
+      if constexpr (kAhead * kSlots < BS) {  // head_dim 512, 32 rows
+        old.load(lines + l * 16, D, slot + kAhead * kSlots, kSlots, r);
+        old.store(lines + l * 16, D, slot + kAhead * kSlots, kSlots, r, ratio);
       }
     }
   }
@@ -373,14 +423,23 @@ cudaError_t launch(K kern, dim3 grid, const AppendArgs& a, cudaStream_t st) {
 template <int D>
 cudaError_t launch_append(AppendArgs a, int num_sms, cudaStream_t st) {
   const int heads = a.num_q_heads + 2 * a.num_kv_heads;
+  const int bs = a.block_size;
+  const bool inter = a.interleaved != 0;
+  // One new row a sequence: the step kernel (64 sequences of 32/8 heads of 128 in
+  // pages that grow as they fill, 3.8 us; the pages kernel, a CTA a head and page,
+  // 10.0; 1024 sequences 13.9 and 72)
   if (a.max_q_len == 1) {
-    constexpr int kSlots = kAppendThreads / (D / 16);
-    const dim3 grid((heads + kSlots - 1) / kSlots, a.num_seqs);
-    return a.interleaved ? launch(append_step_kernel<D, true>, grid, a, st)
-                         : launch(append_step_kernel<D, false>, grid, a, st);
+    constexpr int kWarps = kAppendThreads / 32, kSlots = kAppendThreads / (D / 16);
+    const dim3 grid((2 * a.num_kv_heads + kWarps - 1) / kWarps +
+                        (a.num_q_heads + kSlots - 1) / kSlots,
+                    a.num_seqs);
+    if (bs == 16)
+      return inter ? launch(append_step_kernel<D, 16, true>, grid, a, st)
+                   : launch(append_step_kernel<D, 16, false>, grid, a, st);
+    return inter ? launch(append_step_kernel<D, 32, true>, grid, a, st)
+                 : launch(append_step_kernel<D, 32, false>, grid, a, st);
   }
   // the most pages a sequence's new rows touch
-  const int bs = a.block_size;
   const int pages = (a.max_q_len + bs - 2) / bs + 1;
   // runs of heads long enough to reuse the cosines, short enough to fill the SMs
   // (8945 rows of 48 heads of 128: 32 CTAs an SM 49.5 us, 8 58, 16 51, 64 51.5)
@@ -390,10 +449,10 @@ cudaError_t launch_append(AppendArgs a, int num_sms, cudaStream_t st) {
   a.heads_per_cta = static_cast<int>((heads + groups - 1) / groups);
   const dim3 grid(pages, a.num_seqs, (heads + a.heads_per_cta - 1) / a.heads_per_cta);
   if (bs == 16)
-    return a.interleaved ? launch(append_pages_kernel<D, 16, true>, grid, a, st)
-                         : launch(append_pages_kernel<D, 16, false>, grid, a, st);
-  return a.interleaved ? launch(append_pages_kernel<D, 32, true>, grid, a, st)
-                       : launch(append_pages_kernel<D, 32, false>, grid, a, st);
+    return inter ? launch(append_pages_kernel<D, 16, true>, grid, a, st)
+                 : launch(append_pages_kernel<D, 16, false>, grid, a, st);
+  return inter ? launch(append_pages_kernel<D, 32, true>, grid, a, st)
+               : launch(append_pages_kernel<D, 32, false>, grid, a, st);
 }
 
 }  // namespace
