@@ -82,7 +82,14 @@ struct I8Cfg {
   static constexpr bool kSwizzle = kCRB == 128;
   static constexpr int kCacheStageBytes = kKT * D;
   static constexpr int kStageBytes = 2 * kCacheStageBytes;
-  static constexpr int kRing = D == 64 ? 48 * 1024 : (D <= 256 ? 64 * 1024 : 96 * 1024);
+  // Stages in flight against CTAs (and registers) an SM. Up to eight heads a group, 32
+  // sequences of 4096 keys of 8 heads of 64 / 128 (64 sequences) / 4 of 256 / 2 of 512:
+  // 35.5 / 96.2 / 54.6 / 51.1 us; the rings a step smaller 35.2 / 108.7 / 54.8 / 53.5, a
+  // step larger 40.6 / 112.0 / 61.1 / 68.8. Sixteen heads a group hold twice the state:
+  // head_dim 128 at two CTAs of 96 KB 30.7, three of 64 KB 40.6; head_dim 512 at 64 KB
+  // 139 (8 kv heads, 2048 keys), 96 KB 169
+  static constexpr int kRing =
+      (D == 64 ? 48 : D == 128 ? (NT == 1 ? 64 : 96) : D == 256 ? 64 : (NT == 1 ? 96 : 64)) * 1024;
   static constexpr int kStages = kRing / kStageBytes > 8 ? 8 : kRing / kStageBytes;
   static constexpr int kRingBytes = kStages * kStageBytes;
   static constexpr int kRedBytes = kDSplit == 4 ? 2 * 4 * kU * 32 * 4 * NT * 4 : 0;

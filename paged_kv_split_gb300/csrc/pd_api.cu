@@ -161,8 +161,9 @@ CombineArgs make_combine_args(int B, int Hq, int D, int bs, int mbs, int S, int 
 }
 
 // Resident CTAs per SM and launches of the partial kernels, by cache form.
-int split_ctas_per_sm(int kv_dtype, int D) {
-  return kv_dtype == PD_KV_INT8 ? int8_ctas_per_sm(D, 8) : mma_ctas_per_sm_estimate(kv_dtype, D);
+// (INT8's depend on the group, which some calls do not get: taken as up to 8 heads.)
+int split_ctas_per_sm(int kv_dtype, int D, int G = 8) {
+  return kv_dtype == PD_KV_INT8 ? int8_ctas_per_sm(D, G) : mma_ctas_per_sm_estimate(kv_dtype, D);
 }
 int plan_ctas_per_sm(int kv_dtype, int D, int G) {
   return kv_dtype == PD_KV_INT8 ? int8_ctas_per_sm(D, G) : balanced_ctas_per_sm(kv_dtype, D, G);
@@ -403,7 +404,7 @@ int prefer_balanced(const int32_t* lens, int B, int Hq, int Hkv, int mbs, int bs
                     int kv_dtype, int num_sms) {
   double split_t = 0.0;
   plan_splits_lengths(lens, B, Hkv, Hq, mbs, bs, W, D, kv_dtype, num_sms,
-                      split_ctas_per_sm(kv_dtype, D), &split_t);
+                      split_ctas_per_sm(kv_dtype, D, Hq / Hkv), &split_t);
   const int cap = mbs * bs;
   int64_t T = 0;
   for (int b = 0; b < B; ++b) {
@@ -521,7 +522,7 @@ int pd_plan_num_splits_for_lengths(const int32_t* seq_lens, int32_t num_seqs,
   if (num_seqs == 0) return 1;
   return plan_splits_lengths(seq_lens, num_seqs, num_kv_heads, num_q_heads, max_blocks_per_seq,
                              block_size, sliding_window, head_dim, kv_dtype, num_sms,
-                             split_ctas_per_sm(kv_dtype, head_dim));
+                             split_ctas_per_sm(kv_dtype, head_dim, num_q_heads / num_kv_heads));
 }
 
 int pd_choose_num_splits(int32_t num_seqs, int32_t num_kv_heads, int32_t max_blocks_per_seq,
