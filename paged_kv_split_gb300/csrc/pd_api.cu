@@ -400,6 +400,16 @@ int build_balanced_plan(const int32_t* lens, int B, int Hq, int Hkv, int D, int 
 constexpr double kBalancedTilePremium = 1.08;
 constexpr double kBalancedTilePremiumSplitD = 1.12;
 constexpr double kPieceOverheadBytes = 8.0 * 1024.0;
+// INT8: one kernel for both, so up to eight heads a group no premium is seen; above,
+// its two column tiles make a change of pieces dear at head_dim 64 / 128. A plan of
+// little work makes many small pieces: below 64 KB a CTA (head_dim 64: 32 KB) the
+// splits. us, plan and splits: 32 sequences of 4096 keys, head_dim 64 / 256 / 512, 35 /
+// 55 / 51 and 40 / 58 / 66; 16 of 100 to 3000 keys, head_dim 64 / 128 / 256 (37 / 106 /
+// 89 KB a CTA), 14.2 / 18.2 / 16.4 and 18.1 / 21.2 / 20.7; 8 of 1500 (20 / 53 / 53 KB),
+// 11.2 / 14.6 / 13.9 and 9.8 / 13.3 / 13.1; 32 of 300, head_dim 128 (40 KB), 14.7 and
+// 10.5; 16 heads a group, 16 of 100 to 6000 keys, head_dim 128, 41.4 and 28.6.
+constexpr double kInt8TilePremiumWide = 1.4;
+double int8_plan_bytes(int D) { return 512.0 * (D < 128 ? D : 128); }
 int prefer_balanced(const int32_t* lens, int B, int Hq, int Hkv, int mbs, int bs, int W, int D,
                     int kv_dtype, int num_sms) {
   double split_t = 0.0;
@@ -416,9 +426,14 @@ int prefer_balanced(const int32_t* lens, int B, int Hq, int Hkv, int mbs, int bs
   if (NC > kMaxBalancedCtas) NC = kMaxBalancedCtas;
   if (NC > T) NC = T;
   const double pieces_per_cta = static_cast<double>(static_cast<int64_t>(B) * Hkv + NC) / NC;
-  const double premium = D <= 128 ? kBalancedTilePremium : kBalancedTilePremiumSplitD;
-  const double bal_t = premium * T * page_head_bytes(bs, D, kv_dtype) / NC +
-                       kCtaOverheadBytes + (pieces_per_cta - 1.0) * kPieceOverheadBytes;
+  const double cta_bytes = T * page_head_bytes(bs, D, kv_dtype) / NC;
+  double premium = D <= 128 ? kBalancedTilePremium : kBalancedTilePremiumSplitD;
+  if (kv_dtype == PD_KV_INT8) {
+    if (cta_bytes < int8_plan_bytes(D)) return 0;
+    premium = Hq / Hkv > 8 && D <= 128 ? kInt8TilePremiumWide : 1.0;
+  }
+  const double bal_t =
+      premium * cta_bytes + kCtaOverheadBytes + (pieces_per_cta - 1.0) * kPieceOverheadBytes;
   return bal_t < split_t ? 1 : 0;
 }
 
