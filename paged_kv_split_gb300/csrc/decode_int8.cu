@@ -27,6 +27,12 @@
 // is not widening is kept small: 32 keys an update, ring places counted up, a
 // maximum sought over the lanes only when one moves.
 //
+// Measured: 64 sequences of 512 to 16384 keys, 64/8 heads of 128, balanced: 79.5 us
+// with the merge of its partials, 390 MB (4.9 TB/s; floor 57.5); this kernel alone
+// 76 us, DRAM 67% of its rate, integer pipe 45%, issue slots 44%. Equal lengths, 64 x
+// 4096 keys, 32/8 heads: 96 us, 5.6 TB/s. 16 keys an update, all warps on each stage:
+// 90.8 us for the first; scales before the copies: 80.7.
+//
 // Waits are bounded (2 s): a warp that gives up raises the CTA's abort word and
 // PD_DEV_TIMEOUT; the copying warp then issues nothing more and waits for what
 // it issued.
