@@ -13,8 +13,8 @@
 // Two kernels. A prompt's page takes 16 or 32 rows: one CTA per page and run of
 // heads holds a head's rows in registers (kLanes lanes a row, 16 elements a lane),
 // finds the maximum over the block, and writes the codes: one pass over memory,
-// which bounds it. 8945 rows of 32/8 heads of 128, 245 MB with the output rows: 49
-// us, 5.0 TB/s, of it 195 MB from and to DRAM (the rest stays in L2).
+// which bounds it. 8945 rows of 32/8 heads of 128, 245 MB with the output rows: 47.7
+// us, 5.1 TB/s, of it 195 MB from and to DRAM (the rest stays in L2).
 //
 // A decode step (max_q_len 1) has one row a page. It is a chain of memory latencies
 // (counts, table, scale and rows) that no bandwidth shortens, and in most steps
@@ -185,8 +185,11 @@ __device__ __forceinline__ void load_turn(const AppendArgs& a, int pos, int l, f
 
 // ---------------------------------------------------------------------------
 // Pages of several rows: CTA (page u of sequence b's new rows, head group z).
+// Where a lane has one row, seven CTAs an SM (72 registers; 8945 rows: 47.7 us, six
+// CTAs 49.6, eight 48.7, ten, with spills, 56); with more rows what the compiler takes.
 template <int D, int BS, bool INTER>
-__global__ void __launch_bounds__(kAppendThreads) append_pages_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kAppendThreads, D * BS <= 2048 ? 7 : 0)
+    append_pages_kernel(const AppendArgs a) {
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int kLanes = D / 16;                        // lanes of a row
@@ -442,7 +445,8 @@ cudaError_t launch_append(AppendArgs a, int num_sms, cudaStream_t st) {
   // the most pages a sequence's new rows touch
   const int pages = (a.max_q_len + bs - 2) / bs + 1;
   // runs of heads long enough to reuse the cosines, short enough to fill the SMs
-  // (8945 rows of 48 heads of 128: 32 CTAs an SM 49.5 us, 8 58, 16 51, 64 51.5)
+  // (8945 rows of 48 heads of 128, six CTAs at a time: 32 an SM 49.5 us, 8 58, 16 51,
+  // 64 51.5)
   const int64_t units = (static_cast<int64_t>(a.total_q) + bs - 1) / bs + a.num_seqs;
   int64_t groups = (static_cast<int64_t>(num_sms) * 32 + units - 1) / units;
   if (groups > heads) groups = heads;
