@@ -964,8 +964,10 @@ int prefill_impl(const void* q, int64_t q_stride, const int32_t* cu_q, const voi
   a.k_scale = k_scale;
   a.v_scale = v_scale;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // the tcgen05 kernel reads BF16 caches; FP8 / NVFP4 caches (and the
-  // cross-check) run on the mma.sync kernel, which widens each stage to f16
+  if (!mma_sync && kv_dtype == PD_KV_INT8 && head_dim <= 128)
+    return cuda_status(launch_prefill_int8(a, head_dim, max_q_len, dev->num_sms, st));
+  // the tcgen05 kernel reads BF16 caches; FP8 / NVFP4 caches, INT8's at head_dim 256
+  // (and the cross-check) run on the mma.sync kernel, which widens each stage to f16
   if (mma_sync || kv_dtype != PD_KV_BF16) {
     a.tokens_per_cta = 64 / G;
     return cuda_status(launch_prefill(a, k_cache, v_cache, head_dim, kv_dtype, max_q_len, st));

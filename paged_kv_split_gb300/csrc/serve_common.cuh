@@ -61,6 +61,9 @@ cudaError_t launch_decode_int8(const DecodeArgs& a, int head_dim, cudaStream_t s
 cudaError_t launch_decode_int8_simple(const DecodeArgs& a, int head_dim, cudaStream_t st);
 // Resident CTAs per SM of launch_decode_int8's kernel (host only).
 int int8_ctas_per_sm(int head_dim, int group);
+// pd_prefill over INT8 pages on tcgen05, head_dim 64 and 128.
+cudaError_t launch_prefill_int8(const PrefillArgs& a, int head_dim, int max_q_len, int num_sms,
+                                cudaStream_t st);
 cudaError_t launch_prefill_packed(const PackedArgs& a, int head_dim, int num_sms,
                                   cudaStream_t st);
 cudaError_t launch_prefill_packed_simple(const PackedArgs& a, int head_dim, cudaStream_t st);

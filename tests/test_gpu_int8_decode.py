@@ -330,3 +330,20 @@ def test_chunk_ends_inside_a_stage(d):
     torch.cuda.synchronize()
     want, bound = R.decode_f64(qb, c.k, c.v, c.tables, lens, 8, 16, c.scale)
     assert (np.abs(V.f32(bits(out)) - want) <= bound).all()
+
+
+def test_the_call_s_scales_are_not_read():
+    """k_scale and v_scale are FP8's."""
+    c = Case([300, 41], 8, 2, 128, 16, seed=23)
+    B = U.pd()
+    for kw in (dict(), dict(crosscheck=True)):
+        assert np.array_equal(c.split(2, **kw), c.split(2, k_scale=3.0, v_scale=0.0, **kw))
+    q, k, v = U.bf16_dev(c.q), U.to_dev(c.k), U.to_dev(c.v)
+    cu = U.to_dev(np.arange(3, dtype=np.int32))
+    outs = []
+    for ks, vs in ((1.0, 1.0), (3.0, 0.0)):
+        out = torch.empty_like(q)
+        B.pd_prefill(q, cu, k, v, U.to_dev(c.tables), U.to_dev(c.lens), out, max_q_len=1,
+                     k_scale=ks, v_scale=vs, **c.args())
+        outs.append(out)
+    assert torch.equal(*outs)
