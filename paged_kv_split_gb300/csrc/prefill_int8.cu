@@ -112,6 +112,32 @@ __device__ __forceinline__ uint32_t i8x2_bf16x2(uint32_t w) {
   return o;
 }
 
+// A thread's part of a tile's codes at `from` as operand elements at `to` and, the
+// second eight of a piece, `odd` bytes behind.
+template <int D, bool V>
+__device__ __forceinline__ void widen_tile(uint32_t from, uint32_t to, uint32_t odd) {
+  constexpr int kRows = D == 128 ? 16 : 32;  // rows between a thread's pieces
+#pragma unroll
+  for (int i = 0; i < kKT / kRows; ++i) {
+    const uint4 w = lds128(from + i * kRows * D);
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    uint32_t o[8];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if constexpr (V) {
+        const uint32_t x = u[q] ^ 0x80808080u;
+        o[2 * q] = i8x2_f16x2<0x4140>(x);
+        o[2 * q + 1] = i8x2_f16x2<0x4342>(x);
+      } else {
+        o[2 * q] = i8x2_bf16x2<0x4140>(u[q]);
+        o[2 * q + 1] = i8x2_bf16x2<0x4342>(u[q]);
+      }
+    }
+    sts128(to + i * kRows * 128, o[0], o[1], o[2], o[3]);
+    sts128(to + odd + i * kRows * 128, o[4], o[5], o[6], o[7]);
+  }
+}
+
 template <int D, int BS>
 __global__ void __launch_bounds__(ChCfg<D>::kThreads, 1)
     prefill_int8_kernel(const PrefillArgs a, const int max_q_len, const int64_t page_bytes,
@@ -463,7 +489,14 @@ __global__ void __launch_bounds__(ChCfg<D>::kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
     // =========================== widening warps ===========================
     const int wt = tid - C::kWidenWarp * 32;  // 0 .. 127
-    constexpr int kPieces = D / 16;           // 16-code pieces of a row
+    // This thread's pieces of 16 codes: one of every 16th (head_dim 64: 32nd) row. Eight
+    // lanes of an access meet eight places of 128 bytes: four pieces of an even row and
+    // four of the next, at head_dim 128 of the other half of it
+    const int key = D == 128 ? 2 * (wt >> 4) + ((wt >> 2) & 1) : wt >> 2;
+    const int ch = D == 128 ? ((wt >> 2) ^ (wt >> 3)) & 1 : 0;
+    const uint32_t from = key * D + (ch * 4 + (wt & 3)) * 16;
+    const uint32_t to = ch * (kKT * 128) + swz128(key * 128 + (wt & 3) * 32);
+    const uint32_t odd = swz128(key * 128 + (wt & 3) * 32 + 16) - swz128(key * 128 + (wt & 3) * 32);
     int slot = 0;                             // slots filled so far, of both rings
     for (int k = 0; !failed; ++k) {
       if (!warp_wait(smem_u32(item_full + (k & 1)), (k >> 1) & 1, abort_s)) {
@@ -509,27 +542,8 @@ __global__ void __launch_bounds__(ChCfg<D>::kThreads, 1)
         const uint32_t src = s0 + C::kRawOff + rs * C::kRawBytes;
         const uint32_t dst = s0 + C::kRingOff + st * C::kSlotBytes;
         if ((j & 1) && wt < NG) scales[st * kMaxGroups + wt] = raw_scales[rs * kMaxGroups + wt];
-#pragma unroll 4
-        for (int i = 0; i < kPieces; ++i) {
-          const int e = i * 128 + wt, key = e / kPieces, pc = e % kPieces;
-          const uint4 w = lds128(src + e * 16);
-          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-          uint32_t o[8];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            o[2 * q] = j & 1 ? i8x2_f16x2<0x4140>(u[q] ^ 0x80808080u) : i8x2_bf16x2<0x4140>(u[q]);
-            o[2 * q + 1] =
-                j & 1 ? i8x2_f16x2<0x4342>(u[q] ^ 0x80808080u) : i8x2_bf16x2<0x4342>(u[q]);
-          }
-          // eight lanes of a store: eight places of a row's 128 bytes, so the second half
-          // of a wide row begins with its odd one
-          const uint32_t at = dst + (pc >> 2) * (kKT * 128);
-          const uint32_t c0 = key * 128 + (pc & 3) * 32, odd = (pc >> 2) & 1;
-          sts128(at + swz128(c0 + odd * 16), o[odd ? 4 : 0], o[odd ? 5 : 1], o[odd ? 6 : 2],
-                 o[odd ? 7 : 3]);
-          sts128(at + swz128(c0 + (odd ^ 1u) * 16), o[odd ? 0 : 4], o[odd ? 1 : 5], o[odd ? 2 : 6],
-                 o[odd ? 3 : 7]);
-        }
+        if (j & 1) widen_tile<D, true>(src + from, dst + to, odd);
+        else widen_tile<D, false>(src + from, dst + to, odd);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
