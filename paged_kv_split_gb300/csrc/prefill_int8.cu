@@ -1,6 +1,6 @@
 // Chunks of prompts over INT8 pages (pd_prefill) on tcgen05, head_dim 64 and 128:
-// the persistent kernel of prefill_packed.cu with a warpgroup more between the copies
-// and the tensor core.
+// the persistent kernel of prefill_packed.cu with widening warps between the copies and
+// the tensor core.
 //
 //   t_j = scale * kscale(j) * (q . kcode_j) + log2 vscale(j),  w_j = 2^(t_j - m)
 //   out = sum w_j vcode_j / sum (w_j / vscale(j))
@@ -10,9 +10,9 @@
 // page's two scales cost half a fused multiply-add a score. A masked key has weight
 // zero and any byte is a finite code: nothing is cleared.
 //
-// Warps: 8 for the softmax of two 128-row query tiles (one thread a row), 4 that
+// Warps: 8 for the softmax of two 128-row query tiles (one thread a row), 6 that
 // widen (and bring Q, row by row: its last row is known on the device only), one that
-// finds the items and copies, one that issues MMAs, two idle. K and V tiles of 128
+// finds the items and copies, one that issues MMAs. K and V tiles of 128
 // keys come as codes into a raw ring, one bulk copy a page, and go widened, swizzled,
 // into the operand ring. A pair of codes takes four instructions as bf16 (128 + (c mod
 // 128), less 128, or 256 for a negative code), two as f16 (int8_tile.cuh), all exact.
@@ -60,6 +60,7 @@ struct ChCfg {
   static constexpr int kHolderOff = kItemOff + 2 * 64;
   static constexpr int kSmemBytes = kHolderOff + 16;
   static constexpr int kWidenWarp = 8, kProdWarp = 12, kMmaWarp = 13;
+  static constexpr int kWideners = 6;  // warps 8 to 11, 14 and 15
   static constexpr int kThreads = 16 * 32;
   static constexpr int kOCol = 2 * kKT;  // scores of tile X at column 128 X, O behind
   static constexpr int kTmemCols = 512;
@@ -112,14 +113,14 @@ __device__ __forceinline__ uint32_t i8x2_bf16x2(uint32_t w) {
   return o;
 }
 
-// A thread's part of a tile's codes at `from` as operand elements at `to` and, the
-// second eight of a piece, `odd` bytes behind.
-template <int D, bool V>
-__device__ __forceinline__ void widen_tile(uint32_t from, uint32_t to, uint32_t odd) {
-  constexpr int kRows = D == 128 ? 16 : 32;  // rows between a thread's pieces
+// A lane's pieces of a tile, `n` of them STEP rows apart: codes at `from` as operand
+// elements at `to` and, the second eight of a piece, `odd` bytes behind.
+template <int D, int STEP, bool V>
+__device__ __forceinline__ void widen_tile(uint32_t from, uint32_t to, uint32_t odd, int n) {
 #pragma unroll
-  for (int i = 0; i < kKT / kRows; ++i) {
-    const uint4 w = lds128(from + i * kRows * D);
+  for (int i = 0; i < (kKT + STEP - 1) / STEP; ++i) {
+    if (i >= n) break;  // warp-uniform
+    const uint4 w = lds128(from + i * STEP * D);
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
     uint32_t o[8];
 #pragma unroll
@@ -133,8 +134,8 @@ __device__ __forceinline__ void widen_tile(uint32_t from, uint32_t to, uint32_t 
         o[2 * q + 1] = i8x2_bf16x2<0x4342>(u[q]);
       }
     }
-    sts128(to + i * kRows * 128, o[0], o[1], o[2], o[3]);
-    sts128(to + odd + i * kRows * 128, o[4], o[5], o[6], o[7]);
+    sts128(to + i * STEP * 128, o[0], o[1], o[2], o[3]);
+    sts128(to + odd + i * STEP * 128, o[4], o[5], o[6], o[7]);
   }
 }
 
@@ -184,10 +185,10 @@ __global__ void __launch_bounds__(ChCfg<D>::kThreads, 1)
       // item's readers
       const uint64_t* bar = bars + i;
       uint32_t count = 1;
-      if ((bar >= raw_empty && bar < kv_empty) || bar == q_full) count = 4;
+      if ((bar >= raw_empty && bar < kv_empty) || bar == q_full) count = C::kWideners;
       for (int X = 0; X < 2; ++X)
         if (smem_u32(bar) == p_full(X) || smem_u32(bar) == p_half(X)) count = 4;
-      if (bar == item_empty || bar == item_empty + 1) count = 8 + 4 + 1;
+      if (bar == item_empty || bar == item_empty + 1) count = 8 + C::kWideners + 1;
       mbar_init(smem_u32(bar), count);
     }
     *abort_s = 0;
@@ -210,9 +211,9 @@ __global__ void __launch_bounds__(ChCfg<D>::kThreads, 1)
   bool failed = false;
   const volatile int* no_abort = reinterpret_cast<const volatile int*>(holder + 2);  // stays 0
 
-  // registers dealt by warpgroup (4 x 128 at launch: 64, 96 and 2 x 176)
-  if (warp >= C::kProdWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+  // registers dealt by warpgroup (4 x 128 at launch: 2 x 80 and 2 x 176)
+  if (warp >= C::kWidenWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if (warp == C::kProdWarp) {
       // ============================ copying warp ============================
       const int span = 2 * tpc;  // tokens of an item
@@ -484,77 +485,83 @@ __global__ void __launch_bounds__(ChCfg<D>::kThreads, 1)
       // every MMA issued has completed before TMEM is freed
       commit_if(lead, smem_u32(fin_bar));
       (void)warp_wait(smem_u32(fin_bar), 0, no_abort);
-    }
-  } else if (warp >= C::kWidenWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-    // =========================== widening warps ===========================
-    const int wt = tid - C::kWidenWarp * 32;  // 0 .. 127
-    // This thread's pieces of 16 codes: one of every 16th (head_dim 64: 32nd) row. Eight
-    // lanes of an access meet eight places of 128 bytes: four pieces of an even row and
-    // four of the next, at head_dim 128 of the other half of it
-    const int key = D == 128 ? 2 * (wt >> 4) + ((wt >> 2) & 1) : wt >> 2;
-    const int ch = D == 128 ? ((wt >> 2) ^ (wt >> 3)) & 1 : 0;
-    const uint32_t from = key * D + (ch * 4 + (wt & 3)) * 16;
-    const uint32_t to = ch * (kKT * 128) + swz128(key * 128 + (wt & 3) * 32);
-    const uint32_t odd = swz128(key * 128 + (wt & 3) * 32 + 16) - swz128(key * 128 + (wt & 3) * 32);
-    int slot = 0;                             // slots filled so far, of both rings
-    for (int k = 0; !failed; ++k) {
-      if (!warp_wait(smem_u32(item_full + (k & 1)), (k >> 1) & 1, abort_s)) {
-        failed = true;
-        break;
-      }
-      const Item it = items[k & 1];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(item_empty + (k & 1)));
-      if (it.g < 0) break;
-      // ---- Q: rows (token, head) of the two tiles, swizzled; no token: zeros ----
-      if (k >= 1 && !warp_wait(smem_u32(q_empty), (k - 1) & 1, abort_s)) {
-        failed = true;
-        break;
-      }
-      const int parts = it.jB1 > 0 ? 2 : 1;
-      for (int X = 0; X < parts; ++X) {
-#pragma unroll 4
-        for (int i = 0; i < D / 8; ++i) {
-          const int e = i * 128 + wt, m = e / (D / 8), pc = e % (D / 8);
-          const int mt = m / G, mh = m - mt * G;
-          const int t = it.tok0 + X * tpc + mt;
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          if (mt < tpc && t < it.n)
-            v = *reinterpret_cast<const uint4*>(a.q + static_cast<int64_t>(it.q0 + t) * a.q_stride +
-                                                static_cast<int64_t>(it.g * G + mh) * D + pc * 8);
-          sts128(s0 + X * C::kQBytes + (pc >> 3) * (128 * 128) + swz128(m * 128 + (pc & 7) * 16),
-                 v.x, v.y, v.z, v.w);
-        }
-      }
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(q_full));
-      // ---- K and V tiles, in the order the MMA warp takes them ----
-      for (int j = 0; j < 2 * it.ntiles; ++j, ++slot) {
-        const int rs = slot % C::kRaw, st = slot % C::kSlots;
-        if (!warp_wait(smem_u32(raw_full + rs), (slot / C::kRaw) & 1, abort_s) ||
-            (slot >= C::kSlots &&
-             !warp_wait(smem_u32(kv_empty + st), ((slot / C::kSlots) - 1) & 1, abort_s))) {
+    } else {
+      // =========================== widening warps ===========================
+      const int ww = warp < C::kProdWarp ? warp - C::kWidenWarp : warp - C::kWidenWarp - 2;
+      const int wt = ww * 32 + lane;  // 0 .. 191
+      // A warp takes units of four rows (head_dim 64: eight), every sixth, a lane a piece
+      // of 16 codes. Eight lanes of an access meet eight places of 128 bytes: four pieces
+      // of an even row and four of the next, at head_dim 128 of the other half of it
+      constexpr int kUnit = D == 128 ? 4 : 8;
+      const int urow = D == 128 ? 2 * (lane >> 4) + ((lane >> 2) & 1) : lane >> 2;
+      const int ch = D == 128 ? ((lane >> 2) ^ (lane >> 3)) & 1 : 0;
+      int slot = 0;                             // slots filled so far, of both rings
+      for (int k = 0; !failed; ++k) {
+        if (!warp_wait(smem_u32(item_full + (k & 1)), (k >> 1) & 1, abort_s)) {
           failed = true;
           break;
         }
-        const uint32_t src = s0 + C::kRawOff + rs * C::kRawBytes;
-        const uint32_t dst = s0 + C::kRingOff + st * C::kSlotBytes;
-        if ((j & 1) && wt < NG) scales[st * kMaxGroups + wt] = raw_scales[rs * kMaxGroups + wt];
-        if (j & 1) widen_tile<D, true>(src + from, dst + to, odd);
-        else widen_tile<D, false>(src + from, dst + to, odd);
+        const Item it = items[k & 1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(item_empty + (k & 1)));
+        if (it.g < 0) break;
+        // ---- Q: rows (token, head) of the two tiles, swizzled; no token: zeros ----
+        if (k >= 1 && !warp_wait(smem_u32(q_empty), (k - 1) & 1, abort_s)) {
+          failed = true;
+          break;
+        }
+        const int parts = it.jB1 > 0 ? 2 : 1;
+        for (int X = 0; X < parts; ++X) {
+#pragma unroll 4
+          for (int e = wt; e < 128 * D / 8; e += C::kWideners * 32) {
+            const int m = e / (D / 8), pc = e % (D / 8);
+            const int mt = m / G, mh = m - mt * G;
+            const int t = it.tok0 + X * tpc + mt;
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (mt < tpc && t < it.n)
+              v = *reinterpret_cast<const uint4*>(a.q + static_cast<int64_t>(it.q0 + t) * a.q_stride +
+                                                  static_cast<int64_t>(it.g * G + mh) * D + pc * 8);
+            sts128(s0 + X * C::kQBytes + (pc >> 3) * (128 * 128) + swz128(m * 128 + (pc & 7) * 16),
+                   v.x, v.y, v.z, v.w);
+          }
+        }
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(smem_u32(raw_empty + rs));
-          mbar_arrive(smem_u32(kv_full + st));
+        if (lane == 0) mbar_arrive(smem_u32(q_full));
+        // ---- K and V tiles, in the order the MMA warp takes them ----
+        for (int j = 0; j < 2 * it.ntiles; ++j, ++slot) {
+          const int rs = slot % C::kRaw, st = slot % C::kSlots;
+          if (!warp_wait(smem_u32(raw_full + rs), (slot / C::kRaw) & 1, abort_s) ||
+              (slot >= C::kSlots &&
+               !warp_wait(smem_u32(kv_empty + st), ((slot / C::kSlots) - 1) & 1, abort_s))) {
+            failed = true;
+            break;
+          }
+          const uint32_t src = s0 + C::kRawOff + rs * C::kRawBytes;
+          const uint32_t dst = s0 + C::kRingOff + st * C::kSlotBytes;
+          if ((j & 1) && wt < NG) scales[st * kMaxGroups + wt] = raw_scales[rs * kMaxGroups + wt];
+          // two warps have a unit more: others at V than at K
+          const int first = (j & 1) ? (ww < 2 ? ww + 4 : ww - 2) : ww;
+          const int key = first * kUnit + urow;
+          const uint32_t from = src + key * D + (ch * 4 + (lane & 3)) * 16;
+          const uint32_t to0 = swz128(key * 128 + (lane & 3) * 32);
+          const uint32_t odd = swz128(key * 128 + (lane & 3) * 32 + 16) - to0;
+          const uint32_t to = dst + ch * (kKT * 128) + to0;
+          const int units = (kKT / kUnit - first + C::kWideners - 1) / C::kWideners;
+          if (j & 1) widen_tile<D, C::kWideners * kUnit, true>(from, to, odd, units);
+          else widen_tile<D, C::kWideners * kUnit, false>(from, to, odd, units);
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(smem_u32(raw_empty + rs));
+            mbar_arrive(smem_u32(kv_full + st));
+          }
         }
       }
-    }
-    if (failed) {
-      if (lane == 0) atomicOr(a.flags, PD_DEV_TIMEOUT);
-      *abort_s = 1;
+      if (failed) {
+        if (lane == 0) atomicOr(a.flags, PD_DEV_TIMEOUT);
+        *abort_s = 1;
+      }
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
