@@ -347,3 +347,116 @@ def test_the_call_s_scales_are_not_read():
                      k_scale=ks, v_scale=vs, **c.args())
         outs.append(out)
     assert torch.equal(*outs)
+
+
+def chunk(c, q_lens, out=7.0, flags=0, scale=None, seed=0, most=None, **kw):
+    """pd_prefill of the case's newest q_lens tokens: (q bits, first rows, outputs)."""
+    B = U.pd()
+    rng = np.random.default_rng(seed)
+    qb = V.bf16_bits(rng.standard_normal((sum(q_lens) + 3, c.hq, c.d)).astype(np.float32))
+    cu = np.concatenate([[0], np.cumsum(q_lens)]).astype(np.int32)
+    q = U.bf16_dev(qb)
+    out = torch.full_like(q, 7.0)
+    args = c.args()
+    args["scale"] = c.scale if scale is None else scale
+    B.pd_prefill(q, U.to_dev(cu), U.to_dev(c.k), U.to_dev(c.v), U.to_dev(c.tables),
+                 U.to_dev(c.lens), out, max_q_len=max(q_lens) if most is None else most, **args, **kw)
+    torch.cuda.synchronize()
+    assert B.pd_device_status(reset=True) == flags
+    return qb, cu, V.f32(bits(out))
+
+
+@pytest.mark.parametrize("hq,hkv,d,bs", [(16, 2, 128, 16), (4, 4, 64, 32), (16, 1, 64, 16)])
+@pytest.mark.parametrize("count", [31, 33, 70])
+def test_chunks_of_many_prompts(count, hq, hkv, d, bs):
+    rng = np.random.default_rng(count)
+    q_lens = rng.integers(0, 90, count)
+    q_lens[::4] = q_lens[0]
+    lens = q_lens + rng.integers(0, 300, count)
+    c = Case(lens, hq, hkv, d, bs, seed=count)
+    qb, cu, got = chunk(c, q_lens.tolist(), most=130)
+    assert (got[cu[-1]:] == 7.0).all()       # rows of no sequence
+    assert not (got[:cu[-1]] == 7.0).all(axis=(1, 2)).any()
+    for b in range(count):
+        for i in {0, int(q_lens[b]) // 2, int(q_lens[b]) - 1}:
+            if 0 <= i < q_lens[b]:
+                want, bound = R.decode_f64(qb[cu[b] + i][None], c.k, c.v, c.tables[b][None],
+                                           [lens[b] - q_lens[b] + i + 1], hkv, bs, c.scale)
+                assert (np.abs(got[cu[b] + i] - want[0]) <= bound[0]).all(), (b, i)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("scale", [0.0, -0.1, 2.0])
+def test_chunks_at_any_scale(scale, d):
+    c = Case([300, 41], 8, 2, d, 16, seed=31)
+    q_lens = [100, 41]
+    qb, cu, got = chunk(c, q_lens, scale=scale)
+    for b in range(2):
+        for i in range(0, q_lens[b], 9):
+            want, bound = R.decode_f64(qb[cu[b] + i][None], c.k, c.v, c.tables[b][None],
+                                       [int(c.lens[b]) - q_lens[b] + i + 1], 2, 16, scale)
+            assert (np.abs(got[cu[b] + i] - want[0]) <= bound[0]).all(), (b, i)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_chunks_with_bad_pages_and_counts(d):
+    """A page outside the pool: its keys are left out, as if the sequence had not had
+    them. Counts that do not fit: nothing is written, the others are right."""
+    c = Case([160, 90, 50], 4, 2, d, 16, seed=32)
+    keep = c.tables.copy()
+    c.tables[0][2] = c.nb + 7
+    c.tables[0][9] = -1                     # the last page: a row's own keys
+    qb, cu, got = chunk(c, [20, 30, 50], flags=1)
+    order = [0, 1, 3, 4, 5, 6, 7, 8]
+    few = keep.copy()
+    few[0][:8] = keep[0][order]
+    for b, n in ((0, 20), (1, 30), (2, 50)):
+        for i in range(0, n, 3):
+            pos = int(c.lens[b]) - n + i
+            keys = min(pos, 143) + 1 - 16 if b == 0 else pos + 1
+            want, bound = R.decode_f64(qb[cu[b] + i][None], c.k, c.v, few[b][None], [keys], 2, 16,
+                                       c.scale)
+            assert (np.abs(got[cu[b] + i] - want[0]) <= bound[0]).all(), (b, i)
+    c.tables = keep
+    lens = c.lens.copy()
+    for bad, q_lens, most in (([160, 20, 50], [20, 30, 50], None),          # fewer keys than rows
+                              ([160, keep.shape[1] * 16 + 1, 50], [20, 30, 50], None),
+                              ([160, 90, 50], [20, 30, 25], 25)):           # more than max_q_len
+        c.lens = np.array(bad, np.int32)
+        qb, cu, got = chunk(c, q_lens, flags=2, most=most)
+        assert (got[cu[1]:cu[2]] == 7.0).all()
+        for b in (0, 2):
+            want, bound = R.decode_f64(qb[cu[b]][None], c.k, c.v, keep[b][None],
+                                       [int(lens[b]) - q_lens[b] + 1], 2, 16, c.scale)
+            assert (np.abs(got[cu[b]] - want[0]) <= bound[0]).all()
+
+
+def test_chunk_graph_follows_lengths():
+    c = Case([300, 500, 64], 8, 2, 128, 16, seed=33)
+    B = U.pd()
+    T = 200
+    qb = V.bf16_bits(c.rng.standard_normal((T, 8, 128)).astype(np.float32))
+    q, k, v = U.bf16_dev(qb), U.to_dev(c.k), U.to_dev(c.v)
+    tables, lens = U.to_dev(c.tables), U.to_dev(c.lens)
+    cu = U.to_dev(np.array([0, 60, 136, 200], np.int32))
+    out = torch.empty_like(q)
+
+    def call():
+        B.pd_prefill(q, cu, k, v, tables, lens, out, max_q_len=200, **c.args())
+    call()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for ls, qs in (([300, 500, 64], [60, 76, 64]), ([5, 320, 0], [0, 200, 0]),
+                   ([290, 77, 1], [199, 0, 1])):
+        lens.copy_(U.to_dev(np.array(ls, np.int32)))
+        cq = np.concatenate([[0], np.cumsum(qs)]).astype(np.int32)
+        cu.copy_(U.to_dev(cq))
+        g.replay()
+        torch.cuda.synchronize()
+        got = V.f32(bits(out))
+        for b in range(3):
+            for i in range(0, qs[b], 11):
+                want, bound = R.decode_f64(qb[cq[b] + i][None], c.k, c.v, c.tables[b][None],
+                                           [ls[b] - qs[b] + i + 1], 2, 16, c.scale)
+                assert (np.abs(got[cq[b] + i] - want[0]) <= bound[0]).all(), (b, i)
