@@ -457,13 +457,13 @@ __global__ void __launch_bounds__(ChCfg<D>::kThreads, 1)
         for (int j = 0; ok && j < nt; ++j) {
           const bool more = j + 1 < nt;
           if (!(ok = wait_v())) break;
-          if (more && !(ok = wait_k())) break;
 #pragma unroll
           for (int X = 0; X < 2; ++X) {
             if (in(X, j)) {
               if (!(ok = product(X, X == 1 ? j == jB0 : j == 0))) break;
               if (last(X, j)) commit_if(lead, o_done(X));
             }
+            if (X == 0 && more && !(ok = wait_k())) break;
             // the next scores go over these weights, behind the product that reads them
             // in the tensor core's order
             if (more && in(X, j + 1)) scores(X);
