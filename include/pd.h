@@ -436,8 +436,9 @@ int pd_decode_static_ws(const void* q, const void* k_cache, const void* v_cache,
  * num_kv_heads <= 16; anything else returns PD_ERR_UNSUPPORTED. No
  * workspace: each query tile writes its rows. BF16 caches run on the tcgen05
  * tensor cores (accumulators in TMEM; at head_dim 64 and 128 two 128-row
- * query tiles share each CTA's K/V stages); FP8, NVFP4 and INT8 caches on
- * mma.sync tiles, each stage widened once to f16 (exact) before its MMAs.
+ * query tiles share each CTA's K/V stages), INT8 caches of head_dim 64 and 128
+ * too, widened (exact) by warps of their own; FP8 and NVFP4 caches, and INT8
+ * ones of head_dim 256, on mma.sync tiles, each stage widened once to f16.
  * Device pointers owned by the caller, 16-byte aligned; enqueued on `stream`,
  * never synchronises. */
 int pd_prefill(const void* q, int64_t q_stride, const int32_t* cu_q, const void* k_cache,

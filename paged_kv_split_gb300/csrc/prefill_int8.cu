@@ -6,9 +6,9 @@
 //   out = sum w_j vcode_j / sum (w_j / vscale(j))
 //
 // Codes of 8 bits are exact in bf16 and in f16: K goes in as bf16, beside q as it is,
-// V as f16, beside weights rounded to f16. Value scales ride in the exponent as in the decode kernel; a
-// page's two scales cost half a fused multiply-add a score. A masked key has weight
-// zero and any byte is a finite code: nothing is cleared.
+// V as f16, beside weights rounded to f16. Value scales ride in the exponent as in the
+// decode kernel; a page's two scales cost half a fused multiply-add a score. A masked
+// key has weight zero and any byte is a finite code: nothing is cleared.
 //
 // Warps: 8 for the softmax of two 128-row query tiles (one thread a row), 6 that
 // widen (and bring Q, row by row: its last row is known on the device only), one that
@@ -16,6 +16,14 @@
 // keys come as codes into a raw ring, one bulk copy a page, and go widened, swizzled,
 // into the operand ring. A pair of codes takes four instructions as bf16 (128 + (c mod
 // 128), less 128, or 256 for a negative code), two as f16 (int8_tile.cuh), all exact.
+//
+// Measured: 8 chunks of 512 tokens over 4096 keys, 32/8 heads of 128, 274 us (940
+// TFLOP/s; a BF16 cache's kernel 420, mma.sync tiles 1930), head_dim 64 195; 16 tokens
+// over 8000 keys 107 us, mma.sync 415; there is no size from 1 token on at which those
+// were faster. Issue slots 40%, tensor pipe 35%: the chain of a tile bounds it, copy,
+// widen, scores, softmax, product (with four widening warps 315 us where six took 297;
+// seven eighths of it left out 226). Three operand slots are what fits at head_dim
+// 128; four with a raw ring of two, or a raw ring of four, change nothing.
 //
 // Every wait is bounded (2 s); a role that gives up says so, and the copying warp
 // and the MMA warp wait for what they issued before the CTA ends.

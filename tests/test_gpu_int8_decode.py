@@ -460,3 +460,14 @@ def test_chunk_graph_follows_lengths():
                 want, bound = R.decode_f64(qb[cq[b] + i][None], c.k, c.v, c.tables[b][None],
                                            [ls[b] - qs[b] + i + 1], 2, 16, c.scale)
                 assert (np.abs(got[cq[b] + i] - want[0]) <= bound[0]).all(), (b, i)
+
+
+@pytest.mark.parametrize("hq,hkv,d,bs,window", [(8, 2, 128, 16, 0), (12, 1, 64, 32, 50)])
+def test_chunks_on_the_crosscheck(hq, hkv, d, bs, window):
+    c = Case([200, 77], hq, hkv, d, bs, seed=41)
+    qb, cu, got = chunk(c, [90, 77], crosscheck=True, sliding_window=window)
+    for b, n in ((0, 90), (1, 77)):
+        for i in range(0, n, 7):
+            want, bound = R.decode_f64(qb[cu[b] + i][None], c.k, c.v, c.tables[b][None],
+                                       [int(c.lens[b]) - n + i + 1], hkv, bs, c.scale, window=window)
+            assert (np.abs(got[cu[b] + i] - want[0]) <= bound[0]).all(), (b, i)
