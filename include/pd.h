@@ -52,7 +52,11 @@
  *                   calls but pd_decode_tree; the other calls refuse it
  *                   (PD_ERR_UNSUPPORTED): a row is only worth something beside
  *                   its page's scale. Its readers weight a row by its value
- *                   scale too: of one sequence and kv head, rows whose value
+ *                   scale too, and round that weight to f16 for the product with
+ *                   the codes: it is off by 2^-11 of itself and, of one sequence
+ *                   and kv head, by up to 2^-40 of the largest (pd_prefill at
+ *                   head_dim 64 and 128: 2^-32), so that what rows of a far
+ *                   smaller value scale add to an output is lost. Rows whose value
  *                   scale is less than 2^-90 of the largest may drop out of the
  *                   softmax's sum.
  *   Slot s of the pool is page s / block_size, row s % block_size.

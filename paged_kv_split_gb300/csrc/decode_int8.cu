@@ -1,11 +1,11 @@
 // Decode attention over INT8 pages (one scale per page and kv head): the
 // split-KV partial kernel of every pd_decode* call for this form.
 //
-//   s_j = scale * kscale(j) * (q . kcode_j),  w_j = 2^(s_j + log2 vscale(j) - m)
+//   s_j = scale * kscale(j) * (q . kcode_j),  w_j = 2^(s_j + log2 vscale(j) - m + 15)
 //   O = sum w_j vcode_j,  l = sum w_j / vscale(j),  out = O / l
 //
 // with s in log2 units and m the running maximum of s_j + log2 vscale(j): the
-// value scale rides in the exponent, so the weights stay in (0, 1] for f16, the
+// value scale rides in the exponent, so the weights stay in (0, 2^15] for f16, the
 // codes enter the tensor cores as they are, and a page's two scales cost two
 // fused multiply-adds a score. Codes are widened to f16 exactly by integer
 // operations (c + 128 as mantissa bits of 1024, less 1152): 1.25 (K) and 1.5 (V)
@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(kMmaThreads,
               if (direct) a.out[orow0 + static_cast<int64_t>(h) * D + drow(md, hh)] = f32_to_bf16(v);
               else a.ws_o[row * D + drow(md, hh)] = v;
             }
-          if (!direct && warp == 0 && r == 0) a.ws_ml[row] = make_float2(m_run[nt][j], l_run[nt][j]);
+          if (!direct && warp == 0 && r == 0) a.ws_ml[row] = make_float2(m_run[nt][j] - kWeightLog2, l_run[nt][j]);
         }
     } else {
       // the four warps' m and l by piece parity (a warp can reach the next
@@ -507,7 +507,7 @@ __global__ void __launch_bounds__(kMmaThreads,
           } else {
             const int64_t row = ws_row + h * head_rows;
             a.ws_o[row * D + d] = v;
-            if (d == 0) a.ws_ml[row] = make_float2(M, lsum);
+            if (d == 0) a.ws_ml[row] = make_float2(M - kWeightLog2, lsum);
           }
         }
       }

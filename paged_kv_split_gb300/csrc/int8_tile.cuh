@@ -35,6 +35,12 @@ __device__ __forceinline__ uint32_t i8_pair_f16x2(uint32_t x, uint32_t y) {
   return hsub2_u32((__byte_perm(x, y, kSel) & 0x00FF00FFu) ^ 0x64806480u, 0x64806480u);
 }
 
+// Weights are 2^(t - m + kWeightLog2) for scores t (the value scale's logarithm in
+// them) with maximum m. f16 holds 2^-14 to 65504 in full and loses what is below
+// 2^-25: with the largest weight at 2^15 that is 2^-40 of it, with the largest at 1
+// pages whose value scales lie 2^25 apart would lose the smaller one's values.
+constexpr float kWeightLog2 = 15.0f;
+
 // What a copy (a page, or half of one) brings beside its codes: the key scale,
 // log2 of the value scale and its reciprocal. A copy that was not made (past the
 // keys, a page outside the pool) has log2 = -inf, which masks its keys.
@@ -180,8 +186,8 @@ __device__ __forceinline__ void consume_int8_tile(TileState<C, NT>& s, const I8P
       s.m_run[nt][0] = mn0;
       s.m_run[nt][1] = mn1;
     }
-    const float r0 = s.m_run[nt][0] == -INFINITY ? 0.0f : s.m_run[nt][0];
-    const float r1 = s.m_run[nt][1] == -INFINITY ? 0.0f : s.m_run[nt][1];
+    const float r0 = s.m_run[nt][0] == -INFINITY ? 0.0f : s.m_run[nt][0] - kWeightLog2;
+    const float r1 = s.m_run[nt][1] == -INFINITY ? 0.0f : s.m_run[nt][1] - kWeightLog2;
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       const float p0 = ex2(p[u][nt][0] - r0), p1 = ex2(p[u][nt][1] - r1);

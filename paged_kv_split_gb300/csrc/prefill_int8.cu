@@ -2,7 +2,7 @@
 // the persistent kernel of prefill_packed.cu with widening warps between the copies and
 // the tensor core.
 //
-//   t_j = scale * kscale(j) * (q . kcode_j) + log2 vscale(j),  w_j = 2^(t_j - m)
+//   t_j = scale * kscale(j) * (q . kcode_j) + log2 vscale(j),  w_j = 2^(t_j - m + 7)
 //   out = sum w_j vcode_j / sum (w_j / vscale(j))
 //
 // Codes of 8 bits are exact in bf16 and in f16: K goes in as bf16, beside q as it is,
@@ -42,7 +42,10 @@ namespace {
 using namespace ::pd::mma;
 using namespace ::pd::umma;
 
-constexpr float kMoveLog2 = 8.0f;  // weights stay below 2^8
+// Weights 2^(t - m + kLift) against a reference m that the maximum passes by 2^8 at
+// most: they stay below 2^15, and the largest is 2^7 or more, so that what f16 loses
+// (below 2^-25) is below 2^-32 of it.
+constexpr float kMoveLog2 = 8.0f, kLift = kWeightLog2 - kMoveLog2;
 constexpr int kKT = 128;           // keys of a tile
 constexpr int kMaxGroups = kKT / 16;
 
@@ -667,7 +670,7 @@ __global__ void __launch_bounds__(ChCfg<D>::kThreads, 1)
           }
         }
         // ---- weights over this row's scores, each half told of when it is there ----
-        const float ref = mn == -INFINITY ? 0.0f : -mn;
+        const float ref = mn == -INFINITY ? 0.0f : kLift - mn;
         l_run *= alpha;
 #pragma unroll
         for (int ch = 0; ch < kKT / 32; ++ch) {

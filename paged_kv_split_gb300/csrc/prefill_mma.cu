@@ -38,7 +38,7 @@
 //    the end. INT8 codes widen to f16 exactly too; the key scale of a page
 //    multiplies its scores, and the value scale rides in the exponent (log2 of it
 //    joins the score, the row sum divides it out again), so the weights stay in
-//    (0, 1]. INT8 runs here at head_dim 256 (4 chunks of 256 tokens, 4096 keys, 8/4
+//    (0, 2^15]. INT8 runs here at head_dim 256 (4 chunks of 256 tokens, 4096 keys, 8/4
 //    heads: 401 us, FP8 389) and for the cross-check.
 //  * Keys outside a row's range score -inf. V rows that no row of the CTA may
 //    read (before the CTA's first key, past its last, pages outside the pool)
@@ -498,7 +498,8 @@ __global__ void __launch_bounds__(kMmaThreads, D <= 128 ? 2 : 1)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int hh = e >> 1;
-        s[nt][e] = (m_run[hh] == -INFINITY) ? 0.0f : ex2(s[nt][e] - m_run[hh]);
+        const float m = FMT == PD_KV_INT8 ? m_run[hh] - kWeightLog2 : m_run[hh];
+        s[nt][e] = (m_run[hh] == -INFINITY) ? 0.0f : ex2(s[nt][e] - m);
         if constexpr (FMT == PD_KV_INT8)  // the row sum is of the weights alone
           ls[hh] = fmaf(s[nt][e], op_scales[nt * 8 / C::kBR].v_inv, ls[hh]);
         else

@@ -121,9 +121,10 @@ def append_f32(qkv_bits, cu_q, seq_lens, cos_sin, k_cache, v_cache, tables, hq, 
 
 
 # ---- attention ----------------------------------------------------------------
-def decode_f64(q_bits, k_cache, v_cache, tables, seq_lens, hkv, bs, scale, *, window=0):
+def decode_f64(q_bits, k_cache, v_cache, tables, seq_lens, hkv, bs, scale, *, window=0,
+               lost=-25):
     """(out, bound) [B, Hq, D]. The bound: weights times value scales rounded to
-    f16, small ones off by up to 2^-25 of the largest; scores with D fp32
+    f16, small ones off by up to 2^lost of the largest; scores with D fp32
     additions, each off by at most a full fp32 step of the terms' magnitude, four
     roundings of the score and its factors, log2 of a value scale off by 2^-22 of
     itself, the exponential within 2^-20, one rounding of the output."""
@@ -150,7 +151,7 @@ def decode_f64(q_bits, k_cache, v_cache, tables, seq_lens, hkv, bs, scale, *, wi
             dt = 2 * d * V.HALF_F32 * terms + 4 * V.HALF_F32 * np.abs(s).max() * 1.5 + \
                 np.abs(np.log2(sv)).max() * 2.0 ** -22 + \
                 V.HALF_F32 * np.abs(s * 1.4427 + np.log2(sv)).max()
-            small = 2.0 ** -25 * (p * sv).max() * (np.abs(v) / sv[:, None]).sum(0) / l
+            small = 2.0 ** lost * (p * sv).max() * (np.abs(v) / sv[:, None]).sum(0) / l
             out[b, h] = o
             bound[b, h] = (V.HALF_F16 + 2 * dt + 2.0 ** -20) * (p @ np.abs(v) / l) + small + \
                 V.HALF_BF16 * np.abs(o)
