@@ -33,6 +33,7 @@
 #include <cstring>
 
 #include "int8_tile.cuh"
+#include "prompt_items.cuh"
 #include "prompt_roles.cuh"
 #include "serve_common.cuh"
 
@@ -69,7 +70,8 @@ struct ChCfg {
   static constexpr int kNumBars = 2 * kRaw + 2 * kSlots + 2 + 4 + 2 * 4 + 1;
   static constexpr int kItemOff = (kBarOff + kNumBars * 8 + 15) / 16 * 16;
   static constexpr int kHolderOff = kItemOff + 2 * 64;
-  static constexpr int kSmemBytes = kHolderOff + 16;
+  static constexpr int kSearchOff = kHolderOff + 16;  // words of the item search
+  static constexpr int kSmemBytes = kSearchOff + 2 * 32 * 4;
   static constexpr int kWidenWarp = 8, kProdWarp = 12, kMmaWarp = 13;
   static constexpr int kWideners = 6;  // warps 8 to 11, 14 and 15
   static constexpr int kThreads = 16 * 32;
@@ -109,6 +111,28 @@ __device__ __forceinline__ void set_tiles(Item& it, int tpc, int causal, int W, 
   it.jB0 = has_b ? (lo(b0) - it.k_lo) / kKT : 0;
   it.jB1 = has_b ? (hi_b - it.k_lo + kKT - 1) / kKT : 0;
 }
+
+// New tokens of a sequence, none where its counts do not fit.
+struct ChunkCounts {
+  struct Raw {
+    int q0, q1, L;
+  };
+  const int32_t* cu_q;
+  const int32_t* seq_lens;
+  int* flags;
+  int max_q_len, max_keys;
+  __device__ __forceinline__ Raw load(int b) const {
+    return Raw{cu_q[b], cu_q[b + 1], seq_lens[b]};
+  }
+  __device__ __forceinline__ int tokens(const Raw& r, bool tell) const {
+    const int n = r.q1 - r.q0;
+    if (n > max_q_len || (n > 0 && (r.L < n || r.L > max_keys))) {
+      if (tell) atomicOr(flags, PD_DEV_BAD_SEQ_LEN);
+      return 0;
+    }
+    return max(n, 0);
+  }
+};
 
 // Codes 2 i, 2 i + 1 (SEL 0x4140) or 2 i + 2, 2 i + 3 (0x4342) of a word as bf16.
 template <uint32_t SEL>
@@ -228,71 +252,21 @@ __global__ void __launch_bounds__(ChCfg<D>::kThreads, 1)
     if (warp == C::kProdWarp) {
       // ============================ copying warp ============================
       const int span = 2 * tpc;  // tokens of an item
-      const int hkv = a.num_kv_heads;
-      struct Seq {
-        int n, levels;
-      };
-      // new tokens of sequence b, or 0 where its counts do not fit
-      auto seq_at = [&](int b, bool tell) {
-        int n = 0;
-        if (b < a.num_seqs) {
-          n = a.cu_q[b + 1] - a.cu_q[b];
-          const int L = a.seq_lens[b];
-          if (n > max_q_len || (n > 0 && (L < n || L > a.max_blocks_per_seq * BS))) {
-            if (tell) atomicOr(a.flags, PD_DEV_BAD_SEQ_LEN);
-            n = 0;
-          }
-          n = max(n, 0);
-        }
-        return Seq{n, (n + span - 1) / span};
-      };
-      const int batches = (a.num_seqs + 31) / 32;
-      Seq now = seq_at(lane, blockIdx.x == 0);
-      int level = now.levels;
-      for (int i = 1; i < batches; ++i)
-        level = max(level, seq_at(i * 32 + lane, blockIdx.x == 0).levels);
-      level = __reduce_max_sync(0xFFFFFFFFu, level) - 1;
-      Seq ahead = batches > 1 ? seq_at(32 + lane, false) : now;
-      int batch = 0, before = 0;  // before: (sequence, level) pairs before the place
-      int64_t round = 0;
-      // this CTA's next item; g = -1: none left (as prefill_packed.cu's)
-      auto find = [&]() {
+      const ChunkCounts counts{a.cu_q, a.seq_lens, a.flags, max_q_len, a.max_blocks_per_seq * BS};
+      ItemSearch<ChunkCounts> search(counts, lane, a.num_seqs, span, a.num_kv_heads,
+                                     blockIdx.x == 0,
+                                     reinterpret_cast<int(*)[32]>(smem + C::kSearchOff));
+      auto find = [&]() {  // this CTA's next item; g = -1: none left
+        const auto at = search.next();
         Item it = {};
-        it.g = -1;
-        const int64_t rank =
-            round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-        ++round;
-        const int64_t pr64 = rank <= UINT32_MAX
-                                 ? static_cast<uint32_t>(rank) / static_cast<uint32_t>(hkv)
-                                 : rank / hkv;
-        if (pr64 > INT32_MAX) return it;
-        const int pr = static_cast<int>(pr64);
-        while (level >= 0) {
-          const uint32_t m = __ballot_sync(0xFFFFFFFFu, now.levels > level);
-          const int c = __popc(m);
-          if (pr - before < c) {
-            uint32_t left = m;
-            for (int i = before; i < pr; ++i) left &= left - 1;
-            const int src = __ffs(left) - 1;
-            it.g = static_cast<int>(rank - pr64 * hkv);
-            it.n = __shfl_sync(0xFFFFFFFFu, now.n, src);
-            it.b = batch * 32 + src;
-            it.q0 = a.cu_q[it.b];
-            it.L = a.seq_lens[it.b];
-            it.tok0 = level * span;
-            break;
-          }
-          before += c;
-          if (++batch == batches) {
-            batch = 0;
-            --level;
-          }
-          if (batches > 1) {
-            now = ahead;
-            ahead = seq_at((batch + 1 == batches ? 0 : batch + 1) * 32 + lane, false);
-          }
-        }
-        if (it.g >= 0) set_tiles(it, tpc, a.causal, W, BS);
+        it.g = at.g;
+        if (at.g < 0) return it;
+        it.n = at.n;
+        it.b = at.b;
+        it.q0 = a.cu_q[at.b];
+        it.L = a.seq_lens[at.b];
+        it.tok0 = at.tok0;
+        set_tiles(it, tpc, a.causal, W, BS);
         return it;
       };
       // item kk for the others to read
@@ -314,7 +288,6 @@ __global__ void __launch_bounds__(ChCfg<D>::kThreads, 1)
       Item it = find();
       publish(it, 0);
       for (int k = 0; it.g >= 0 && !failed; ++k) {
-        Item next;
         const int32_t* bt = a.block_tables + static_cast<int64_t>(it.b) * a.max_blocks_per_seq;
         const int pages = (it.k_hi + BS - 1) / BS;
         // lane x: entry base + x of the table and its page's two scales, and the same
@@ -339,7 +312,9 @@ __global__ void __launch_bounds__(ChCfg<D>::kThreads, 1)
         };
         int base = it.k_lo / BS;
         Entry cur = entry_at(base + lane), nxt = entry_at(base + 32 + lane);
-        for (int j = 0; j < it.ntiles && !failed; ++j) {
+        for (int j = 0; j < max(it.ntiles, 3) && !failed; ++j) {
+          if (j == 2) publish(find(), k + 1);
+          if (failed || j >= it.ntiles) continue;
           const int first = it.k_lo / BS + j * NG;  // a tile's pages: NG divides 32
           if (first - base >= 32) {
             base += 32;
@@ -357,13 +332,9 @@ __global__ void __launch_bounds__(ChCfg<D>::kThreads, 1)
           const int64_t at = page * page_bytes + static_cast<int64_t>(it.g) * (BS * D);
 #pragma unroll
           for (int part = 0; part < 2; ++part, ++raw) {
-            if (part == 0 && j == 2) {
-              next = find();
-              publish(next, k + 1);
-            }
             const int rs = raw % C::kRaw;
-            if (failed || (raw >= C::kRaw && !warp_wait(smem_u32(raw_empty + rs),
-                                                        ((raw / C::kRaw) - 1) & 1, abort_s))) {
+            if (raw >= C::kRaw &&
+                !warp_wait(smem_u32(raw_empty + rs), ((raw / C::kRaw) - 1) & 1, abort_s)) {
               failed = true;
               break;
             }
@@ -381,11 +352,7 @@ __global__ void __launch_bounds__(ChCfg<D>::kThreads, 1)
           }
         }
         if (failed) break;
-        if (it.ntiles <= 2) {
-          next = find();
-          publish(next, k + 1);
-        }
-        it = next;
+        it = items[(k + 1) & 1];
       }
       if (failed) {
         if (lane == 0) atomicOr(a.flags, PD_DEV_TIMEOUT);

@@ -20,10 +20,10 @@
 //  * CTAs stay. All (sequence, pair of tiles, kv head) items are ranked by the
 //    pair's place in its sequence, last first: with a causal mask that is
 //    costliest first, whatever the lengths. CTA c takes ranks c, 2 N - 1 - c,
-//    2 N + c ... of N CTAs. The copying warp finds the items (lengths are on the
-//    device only) and loads the next item's Q, K and V while the last one's
-//    softmax and output are under way. It seeks an item while the ring is full:
-//    sought before the loads, 16 ragged prompts took 185 us instead of 167.
+//    2 N + c ... of N CTAs. The copying warp finds the items (prompt_items.cuh) and
+//    loads the next item's Q, K and V while the last one's softmax and output are
+//    under way. It seeks an item while the ring is full: sought before the loads, 16
+//    ragged prompts took 185 us instead of 167.
 //  * Copies are TMA boxes (tokens x heads x 64 of head_dim, 128-byte swizzle), K
 //    and V in a ring of their own slots. Rows past a sequence's end come along in
 //    its last tile: as keys they are masked, as V rows zeroed in shared memory.
@@ -50,6 +50,7 @@
 
 #include <cstring>
 
+#include "prompt_items.cuh"
 #include "prompt_roles.cuh"
 #include "serve_common.cuh"
 
@@ -80,7 +81,8 @@ struct PkCfg {
   static constexpr int kNumBars = 2 * kSlots + 2 + 4 + kTiles * kTileBars + 1;
   static constexpr int kItemOff = (kBarOff + kNumBars * 8 + 15) / 16 * 16;
   static constexpr int kHolderOff = kItemOff + 2 * 48;
-  static constexpr int kSmemBytes = kHolderOff + 16;
+  static constexpr int kSearchOff = kHolderOff + 16;  // words of the item search
+  static constexpr int kSmemBytes = kSearchOff + 2 * 32 * 4;
   static constexpr int kSoftWarps = 4 * kTiles;
   static constexpr int kProdWarp = kSoftWarps;
   static constexpr int kMmaWarp = kSoftWarps + 1;
@@ -125,16 +127,24 @@ __device__ __forceinline__ void set_tiles(Item& it, int tpc, int causal, int W) 
   it.jB1 = has_b ? (hi_b - it.k_lo + KT - 1) / KT : 0;
 }
 
-// Tokens of sequence b, or 0 where its counts do not fit the batch.
-__device__ __forceinline__ int prompt_len(const PackedArgs& a, int b, bool tell) {
-  const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1];
-  const int n = q1 - q0;
-  if (q0 < 0 || n < 0 || q1 > a.total_q || n > a.max_q_len) {
-    if (tell) atomicOr(a.flags, PD_DEV_BAD_SEQ_LEN);
-    return 0;
+// Tokens of a sequence, none where its counts do not fit the batch.
+struct PromptCounts {
+  struct Raw {
+    int q0, q1;
+  };
+  const int32_t* cu_q;
+  int* flags;
+  int total_q, max_q_len;
+  __device__ __forceinline__ Raw load(int b) const { return Raw{cu_q[b], cu_q[b + 1]}; }
+  __device__ __forceinline__ int tokens(const Raw& r, bool tell) const {
+    const int n = r.q1 - r.q0;
+    if (r.q0 < 0 || n < 0 || r.q1 > total_q || n > max_q_len) {
+      if (tell) atomicOr(flags, PD_DEV_BAD_SEQ_LEN);
+      return 0;
+    }
+    return n;
   }
-  return n;
-}
+};
 
 template <int D>
 __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
@@ -214,74 +224,17 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
     if (warp == C::kProdWarp) {
       // ============================ copying warp ============================
       const int span = C::kTiles * tpc;  // tokens of an item
-      const int hkv = a.num_kv_heads;
-      // Items in order: levels from the highest down, in a level the sequences that
-      // reach it, in order, and each one's kv heads. This CTA's ranks only go up, so
-      // a place in that order moves along: 32 sequences at a time (lane x has the
-      // batch's sequence x, and that of the batch to come), then the next level
-      struct Seq {
-        int n, levels;
-      };
-      auto seq_at = [&](int b, bool tell) {
-        const int n = b < a.num_seqs ? prompt_len(a, b, tell) : 0;
-        return Seq{n, (n + span - 1) / span};
-      };
-      const int batches = (a.num_seqs + 31) / 32;
-      Seq now = seq_at(lane, blockIdx.x == 0);
-      int level = now.levels;
-      for (int i = 1; i < batches; ++i)
-        level = max(level, seq_at(i * 32 + lane, blockIdx.x == 0).levels);
-      level = __reduce_max_sync(0xFFFFFFFFu, level) - 1;
-      Seq ahead = batches > 1 ? seq_at(32 + lane, false) : now;
-      int batch = 0, before = 0;  // before: (sequence, level) pairs before the place
-      int64_t round = 0;
-      // this CTA's next item; g = -1: none left
-      auto find = [&]() {
+      ItemSearch<PromptCounts> search(PromptCounts{a.cu_q, a.flags, a.total_q, a.max_q_len}, lane,
+                                      a.num_seqs, span, a.num_kv_heads, blockIdx.x == 0,
+                                      reinterpret_cast<int(*)[32]>(smem + C::kSearchOff));
+      auto find = [&]() {  // this CTA's next item; g = -1: none left
+        const auto at = search.next();
         Item it = {};
-        it.g = -1;
-        const int64_t rank =
-            round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-        ++round;
-        const int64_t pr64 = rank <= UINT32_MAX
-                                 ? static_cast<uint32_t>(rank) / static_cast<uint32_t>(hkv)
-                                 : rank / hkv;
-        if (pr64 > INT32_MAX) return it;
-        const int pr = static_cast<int>(pr64);
-        while (level >= 0) {
-          const uint32_t m = __ballot_sync(0xFFFFFFFFu, now.levels > level);
-          const int c = __popc(m);
-          if (batches == 1 && pr - before >= 8 * c) {
-            // far to go: levels from here down to the next shorter sequence's have as
-            // many, and are skipped at once, to the pair's own or past them all (one
-            // prompt of 4096 tokens, 64 levels: 57.7 us, level by level 60.6)
-            const int next = static_cast<int>(
-                __reduce_max_sync(0xFFFFFFFFu, now.levels > level ? 0 : now.levels));
-            const int skip = min((pr - before) / c, level + 1 - next);
-            before += skip * c;
-            level -= skip;
-            if (level < next) continue;
-          }
-          if (pr - before < c) {
-            uint32_t left = m;
-            for (int i = before; i < pr; ++i) left &= left - 1;
-            const int src = __ffs(left) - 1;
-            it.g = static_cast<int>(rank - pr64 * hkv);
-            it.n = __shfl_sync(0xFFFFFFFFu, now.n, src);
-            it.q0 = a.cu_q[batch * 32 + src];
-            it.tok0 = level * span;
-            break;
-          }
-          before += c;
-          if (++batch == batches) {
-            batch = 0;
-            --level;
-          }
-          if (batches > 1) {
-            now = ahead;
-            ahead = seq_at((batch + 1 == batches ? 0 : batch + 1) * 32 + lane, false);
-          }
-        }
-        if (it.g < 0) return it;
+        it.g = at.g;
+        if (at.g < 0) return it;
+        it.n = at.n;
+        it.q0 = a.cu_q[at.b];
+        it.tok0 = at.tok0;
         set_tiles<KT, C::kTiles>(it, tpc, a.causal, W);
         return it;
       };
@@ -325,19 +278,17 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
       Item it = find();
       publish(it, 0);
       for (int k = 0; it.g >= 0 && !failed; ++k) {
-        Item next;
         // K and V tiles go in the order the MMA warp takes them. Q's buffer is the
         // last item's until its last scores are there: the first K and V tile, whose
         // slots are free before that, go ahead of it. The next item is sought while
         // the ring is full
         const int loads = 2 * it.ntiles;
-        for (int j = 0; j < loads; ++j, ++slot) {
-          if (j == (k == 0 ? 0 : 2)) load_q(it, k);
-          if (j == 4) {
-            next = find();
-            publish(next, k + 1);
-          }
+        const int q_at = k == 0 ? 0 : 2;
+        for (int j = 0; j < max(loads, 5); ++j) {
+          if (j == q_at) load_q(it, k);
+          if (j == 4) publish(find(), k + 1);
           if (failed) break;
+          if (j >= loads) continue;
           const int st = slot % C::kSlots;
           if (slot >= C::kSlots &&
               !warp_wait(smem_u32(kv_empty + st), ((slot / C::kSlots) - 1) & 1, abort_s)) {
@@ -354,14 +305,10 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, 1)
                           it.q0 + it.k_lo + (j >> 1) * KT, fb);
           }
           __syncwarp();
+          ++slot;
         }
         if (failed) break;
-        if (loads == 2 && k > 0) load_q(it, k);
-        if (loads <= 4 && !failed) {
-          next = find();
-          publish(next, k + 1);
-        }
-        it = next;
+        it = items[(k + 1) & 1];
       }
       if (failed) {
         if (lane == 0) atomicOr(a.flags, PD_DEV_TIMEOUT);
