@@ -606,9 +606,10 @@ int pd_compact_tree(void* k_caches, void* v_caches, int64_t layer_bytes, int32_t
  * the codes of its earlier rows become rint(code * (old scale / want)). New
  * codes are rint(x * (1 / scale)) clamped to +-127 (NaN: 0). rint rounds to
  * nearest even. So codes are reproducible bit for bit, and a value appended
- * with scale s is off by s / 2 at most, plus half of each scale its page grows
- * to later (one past 127 * 2^60 is clamped there). Rows of the page behind the
- * new ones keep their bytes.
+ * with scale s is off by (1/2 + 2^-16) s at most (2^-16: the reciprocal and the
+ * product with it are rounded, codes reach 127), plus as much of each scale its
+ * page grows to later (one past 127 * 2^60 is clamped there). Rows of the page
+ * behind the new ones keep their bytes.
  * A page that gets rows belongs to one sequence (shared prefixes: whole pages).
  * A sequence whose counts do not fit (n_b > max_q_len, L_b < n_b, L_b beyond
  * the block table, rows beyond total_q) raises PD_DEV_BAD_SEQ_LEN and nothing of
