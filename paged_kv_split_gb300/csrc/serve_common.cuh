@@ -57,8 +57,6 @@ struct PackedArgs {
 cudaError_t launch_rope_append_int8(AppendArgs a, int head_dim, int num_sms, cudaStream_t st);
 // Decode over INT8 pages: splits, or a plan where a.plan_cta is set.
 cudaError_t launch_decode_int8(const DecodeArgs& a, int head_dim, cudaStream_t st);
-// The same on CUDA cores (splits only), for pd_decode_crosscheck.
-cudaError_t launch_decode_int8_simple(const DecodeArgs& a, int head_dim, cudaStream_t st);
 // Resident CTAs per SM of launch_decode_int8's kernel (host only).
 int int8_ctas_per_sm(int head_dim, int group);
 // pd_prefill over INT8 pages on tcgen05, head_dim 64 and 128.
