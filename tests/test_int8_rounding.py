@@ -34,4 +34,4 @@ def test_growth():
         old, new = np.float32(2.0 ** rng.uniform(-3, 0)), np.float32(2.0 ** rng.uniform(0, 1))
         got = R.quantise(codes, old / new)
         worst = max(worst, off(codes.astype(np.float64) * np.float64(old), got, new))
-    assert 0.5 < worst <= 0.5 + MORE
+    assert worst <= 0.5 + MORE
