@@ -300,9 +300,12 @@ int pd_decode_combine(const void* workspace, size_t workspace_bytes, const int32
  * expected to be faster than pd_decode with pd_plan_num_splits_for_lengths'
  * split count, 0 if not, a negative pd_status on bad arguments. Host only.
  * It compares the split planner's estimated makespan with an equal share per
- * CTA plus a measured per-tile premium of the balanced kernel (about 5 %) and
- * its per-piece cost: lengths that differ favour the balanced schedule,
- * equal lengths the split one. */
+ * CTA plus a measured per-tile premium of the balanced kernel (about 5 %; none
+ * for INT8 up to eight heads a group) and its per-piece cost: lengths that
+ * differ favour the balanced schedule, equal lengths the split one. It tries
+ * every split count on the lengths, which takes the host milliseconds for large
+ * batches (32 sequences of 1K to 4K keys 5, 64 of up to 16K 20): once a batch,
+ * for all layers, not once a call. */
 int pd_prefer_balanced(const int32_t* seq_lens, int32_t num_seqs, int32_t num_q_heads,
                        int32_t num_kv_heads, int32_t max_blocks_per_seq, int32_t block_size,
                        int32_t sliding_window, int32_t head_dim, int32_t kv_dtype,

@@ -22,16 +22,28 @@
 // head_dim 64 / 128: warps 0 and 1 take 32 keys each of the even 64-key stages, 2
 // and 3 of the odd ones, each with its own softmax state, merged at the end of a
 // piece through the stage of its last tile. head_dim 256 / 512: the warps share
-// head_dim and sum their scores through shared memory per 32-key stage. Integer
-// operations bound it (their pipe takes half an instruction a cycle), so whatever
-// is not widening is kept small: 32 keys an update, ring places counted up, a
-// maximum sought over the lanes only when one moves.
+// head_dim and sum their scores through shared memory per 32-key stage. A warp's chain
+// of a tile is long and few warps are there to hide it, so whatever is not widening is
+// kept small: 32 keys an update, ring places counted up, a maximum sought over the lanes
+// only when one moves.
 //
-// Measured: 64 sequences of 512 to 16384 keys, 64/8 heads of 128, balanced: 79.5 us
+// Measured: 64 sequences of 512 to 16384 keys, 64/8 heads of 128, balanced: 79.7 us
 // with the merge of its partials, 390 MB (4.9 TB/s; floor 57.5); this kernel alone
-// 76 us, DRAM 67% of its rate, integer pipe 45%, issue slots 44%. Equal lengths, 64 x
+// 76 us, DRAM 67% of its rate, integer pipe 45%, issue slots 44%: nothing is saturated,
+// the chain copy, widen, scores, softmax, product waits for itself. Equal lengths, 64 x
 // 4096 keys, 32/8 heads: 96 us, 5.6 TB/s. 16 keys an update, all warps on each stage:
 // 90.8 us for the first; scales before the copies: 80.7.
+//
+// The other forms, 32 sequences of 4096 keys, floors in brackets: head_dim 64, 8 kv
+// heads, 35.6 us (20): a page is 1 KB, half of head_dim 128's, at the same instructions
+// a key for masks, softmax and barriers; DRAM 50%, integer pipe 43%, issue slots 44%.
+// head_dim 256, 4 kv heads, 54 (40), 16 q heads 61; the warps meet every 32 keys (DRAM
+// 65%, issue slots 52%). head_dim 512, 2 kv heads, 51 (40) with four q heads a kv
+// head, 55 with seven, 71 with eight, whose q rows no longer leave room for a second
+// CTA an SM. 16 q heads a kv head (two column tiles): head_dim 64 67 (20), 128 73 (40);
+// 2048 keys, head_dim 256, 4 kv heads, 48 (20), 512, 8 kv heads, 137 (80): twice the
+// softmax and state a key, at 168 registers (head_dim 128 spills 20 to 100 bytes) and
+// two CTAs an SM; DRAM 38 to 49%, issue slots 34 to 39%.
 //
 // Waits are bounded (2 s): a warp that gives up raises the CTA's abort word and
 // PD_DEV_TIMEOUT; the copying warp then issues nothing more and waits for what

@@ -408,6 +408,8 @@ constexpr double kPieceOverheadBytes = 8.0 * 1024.0;
 // 89 KB a CTA), 14.2 / 18.2 / 16.4 and 18.1 / 21.2 / 20.7; 8 of 1500 (20 / 53 / 53 KB),
 // 11.2 / 14.6 / 13.9 and 9.8 / 13.3 / 13.1; 32 of 300, head_dim 128 (40 KB), 14.7 and
 // 10.5; 16 heads a group, 16 of 100 to 6000 keys, head_dim 128, 41.4 and 28.6.
+// (The splits' estimate below costs the host milliseconds for large batches, and is made
+// where the plan's bytes rule it out too.)
 constexpr double kInt8TilePremiumWide = 1.4;
 double int8_plan_bytes(int D) { return 512.0 * (D < 128 ? D : 128); }
 int prefer_balanced(const int32_t* lens, int B, int Hq, int Hkv, int mbs, int bs, int W, int D,

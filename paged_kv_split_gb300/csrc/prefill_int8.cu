@@ -17,13 +17,15 @@
 // into the operand ring. A pair of codes takes four instructions as bf16 (128 + (c mod
 // 128), less 128, or 256 for a negative code), two as f16 (int8_tile.cuh), all exact.
 //
-// Measured: 8 chunks of 512 tokens over 4096 keys, 32/8 heads of 128, 274 us (940
-// TFLOP/s; a BF16 cache's kernel 420, mma.sync tiles 1930), head_dim 64 195; 16 tokens
-// over 8000 keys 107 us, mma.sync 415; there is no size from 1 token on at which those
-// were faster. Issue slots 40%, tensor pipe 35%: the chain of a tile bounds it, copy,
-// widen, scores, softmax, product (with four widening warps 315 us where six took 297;
-// seven eighths of it left out 226). Three operand slots are what fits at head_dim
-// 128; four with a raw ring of two, or a raw ring of four, change nothing.
+// Measured: 8 chunks of 512 tokens over 4096 keys, 32/8 heads of 128, 276 us (930
+// TFLOP/s, floor 134; a BF16 cache's kernel 420, mma.sync tiles 1930), head_dim 64 198
+// (floor 67). Issue slots 43%, tensor pipe 38% (head_dim 64: 49%, 25%): the chain of a
+// tile bounds it, copy, widen, scores, softmax, product (with four widening warps 315 us
+// where six took 297; seven eighths of the widening left out 226). Three operand slots
+// are what fits at head_dim 128; four with a raw ring of two, or a raw ring of four,
+// change nothing. 16 tokens over 8000 keys take 106 us, 44 times the 2.4 us of their
+// bytes: keys are not divided among CTAs, and 8 of the 152 work (mma.sync tiles 415;
+// there is no size from 1 token on at which those were faster).
 //
 // Every wait is bounded (2 s); a role that gives up says so, and the copying warp
 // and the MMA warp wait for what they issued before the CTA ends.

@@ -34,13 +34,14 @@
 // 4096 tokens, 8/2 heads, window 1024); four tiles of 64 keys, 48: the softmax's
 // fixed part is paid for half the keys.
 //
-// Measured, 32/8 heads of 128, causal: one prompt of 8192 tokens 315 to 340 us (1750
-// TFLOP/s where the card's power allows it; tensor pipe 74% of the time, the
-// exponentials' unit 39%, issue slots 43%); 16 prompts of 64 to 2048 tokens 163 us
-// (1260): half-masked tiles and the change of items. head_dim 64, 8192 tokens, 258 us
-// (1065): a tile's chain scores, softmax, product, whose parts are each half busy.
-// head_dim 256, 8/4 heads, 4096 tokens, 58 us (1190). Many short prompts pay for whole
-// tiles: 256 of 128 tokens 127 us, 1024 of 32 tokens 196 us.
+// Measured, 32/8 heads of 128, causal: one prompt of 8192 tokens 315 to 350 us (1750 to
+// 1570 TFLOP/s: the card's power limit; tensor pipe 74% of the time, the exponentials'
+// unit 39%, issue slots 43%); 16 prompts of 64 to 2048 tokens 161 us with the rows of
+// the call before in L2, 178 without (1280, 1160): half-masked tiles and the change of
+// items. head_dim 64, 8192 tokens, 257 us (1070): a tile's chain scores, softmax,
+// product, whose parts are each half busy. head_dim 256, 8/4 heads, 4096 tokens, 58 to
+// 66 us by the card (1190 to 1040). Many short prompts pay for whole tiles: 256 of 128
+// tokens 126 us, 1024 of 32 tokens 199 us.
 //
 // Every wait is bounded (2 s); a role that gives up says so, and the copying warp
 // and the MMA warp wait for what they issued before the CTA ends.

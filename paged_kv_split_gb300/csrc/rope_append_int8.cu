@@ -13,8 +13,8 @@
 // Two kernels. A prompt's page takes 16 or 32 rows: one CTA per page and run of
 // heads holds a head's rows in registers (kLanes lanes a row, 16 elements a lane),
 // finds the maximum over the block, and writes the codes: one pass over memory,
-// which bounds it. 8945 rows of 32/8 heads of 128, 245 MB with the output rows: 47.7
-// us, 5.1 TB/s, of it 195 MB from and to DRAM (the rest stays in L2).
+// which bounds it. 8945 rows of 32/8 heads of 128, 245 MB with the output rows: 47.1
+// us, 5.2 TB/s, of it 199 MB from and to DRAM (the rest stays in L2).
 //
 // A decode step (max_q_len 1) has one row a page. It is a chain of memory latencies
 // (counts, table, scale and rows) that no bandwidth shortens, and in most steps
