@@ -636,7 +636,8 @@ int pd_rope_append_int8(const void* qkv, int64_t qkv_stride, const int32_t* cu_q
  *               k_stride / v_stride (0 = packed): parts of fused rows, say.
  *   cu_q        device int32 [num_seqs + 1]: sequence b owns rows [cu_q[b],
  *               cu_q[b+1]), its n_b tokens, n_b <= max_q_len.
- *   out         device bf16, total_q rows at t * out_stride (0 = packed).
+ *   out         device bf16, total_q rows at t * out_stride (0 = packed). May be
+ *               q (with its stride): in place. Else it overlaps none of the inputs.
  *   causal      != 0: token i sees tokens j <= i of its sequence; 0: all n_b.
  *   sliding_window  W > 0: token i sees j with i - j < W (causal; without: the
  *               last W tokens, as pd_prefill); 0 = off.

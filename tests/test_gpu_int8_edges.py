@@ -108,3 +108,22 @@ def test_decode_on_another_stream(d):
     B.pd_decode(q, k, v, tables, lens, torch.empty_like(out), num_splits=3, stream=st, **c.args())
     st.synchronize()
     assert np.array_equal(append_bits(out), want)
+
+
+@pytest.mark.parametrize("lens,hq,hkv,d", [([300, 1, 77, 130], 8, 2, 128), ([257, 90], 9, 3, 128),
+                                           ([5, 600, 64], 4, 4, 64), ([200, 31], 16, 1, 256)])
+def test_packed_in_place(lens, hq, hkv, d):
+    """The q heads of fused rows replaced by the outputs; k and v heads stay."""
+    c = PackedCase(lens, hq, hkv, d, seed=9)
+    want = c.run()
+    for crosscheck in (False, True):
+        alone = c.run(crosscheck=crosscheck)
+        rows = U.bf16_dev(c.rows)
+        before = rows.clone()
+        q, k, v = c.views(rows)
+        U.pd().pd_prefill_packed(q, k, v, U.to_dev(c.cu), q, max_q_len=max(lens), scale=c.scale,
+                                 crosscheck=crosscheck)
+        torch.cuda.synchronize()
+        assert torch.equal(q, alone)
+        assert torch.equal(rows[:, hq * d:], before[:, hq * d:])
+    assert torch.equal(want, c.run())
