@@ -463,7 +463,8 @@ __global__ void __launch_bounds__(kMmaThreads,
               if (direct) a.out[orow0 + static_cast<int64_t>(h) * D + drow(md, hh)] = f32_to_bf16(v);
               else a.ws_o[row * D + drow(md, hh)] = v;
             }
-          if (!direct && warp == 0 && r == 0) a.ws_ml[row] = make_float2(m_run[nt][j] - kWeightLog2, l_run[nt][j]);
+          if (!direct && warp == 0 && r == 0)
+            a.ws_ml[row] = make_float2(m_run[nt][j] - kWeightLog2, l_run[nt][j]);
         }
     } else {
       // the four warps' m and l by piece parity (a warp can reach the next
